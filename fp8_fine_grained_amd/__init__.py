@@ -21,8 +21,10 @@ BSCALE_128x128 = 0
 BSCALE_1x128 = 1
 OUT_BF16 = 0
 OUT_FP32 = 1
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
 
-ABI_VERSION = 14
+ABI_VERSION = 15
 EXPORTS = ("fp8_quant_act_1x128", "fp8_quant_weight_128x128", "fp8_gemm_blockscaled",
            "fp8_grouped_gemm_contiguous", "fp8_grouped_gemm_masked",
            "fp8_quant_act_1x128_bf16", "fp8_quant_weight_128x128_bf16", "fp8_requant_act_tokenwise",
@@ -30,8 +32,10 @@ EXPORTS = ("fp8_quant_act_1x128", "fp8_quant_weight_128x128", "fp8_gemm_blocksca
            "fp8_tile_weights_decode", "fp8_grouped_gemm_masked_tiled", "fp8_gemm_blockscaled_fp8mfma",
            "fp8_grouped_gemm_contiguous_fp8out", "fp8_grouped_gemm_contiguous_mx", "fp8_grouped_gemm_masked_mx",
            "fp8_quant_mx_1x32_transposed", "fp8_grouped_gemm_masked_tiled_fp8out",
-           "fp8_grouped_gemm_masked_tiled_mx", "fp8fg_status_string", "fp8fg_abi_version")
-_COMPUTE = EXPORTS[:21]
+           "fp8_grouped_gemm_masked_tiled_mx", "moe_route", "moe_route_backward", "fp8_moe_dispatch_contiguous",
+           "fp8_moe_dispatch_masked", "moe_combine", "fp8_moe_combine_backward", "fp8_swiglu", "fp8_swiglu_backward",
+           "fp8_grouped_gemm_wgrad", "fp8fg_status_string", "fp8fg_abi_version")
+_COMPUTE = EXPORTS[:-2]
 
 
 class Fp8fgError(RuntimeError):
@@ -74,6 +78,16 @@ def load_library(path=LIB_PATH):
     lib.fp8_grouped_gemm_masked_tiled_mx.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp]
     lib.fp8_grouped_gemm_contiguous_mx.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp]
     lib.fp8_grouped_gemm_masked_mx.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp]
+    f32 = ctypes.c_float
+    lib.moe_route.argtypes = [vp, i32, i64, vp, i64, i64, i64, i64, i64, i32, i32, i32, f32, vp, vp, vp]
+    lib.moe_route_backward.argtypes = [vp, i32, i64, vp, vp, i64, i64, i64, i32, i32, f32, vp, vp]
+    lib.fp8_moe_dispatch_contiguous.argtypes = [vp, i32, i64, i64, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+    lib.fp8_moe_dispatch_masked.argtypes = [vp, i32, i64, i64, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp]
+    lib.moe_combine.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, i32, vp]
+    lib.fp8_moe_combine_backward.argtypes = [vp, i32, i64, i64, vp, i32, i64, vp, vp, i64, vp, vp, i64, vp, vp, vp, vp]
+    lib.fp8_swiglu.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+    lib.fp8_swiglu_backward.argtypes = [vp, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.fp8_grouped_gemm_wgrad.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp]
     for name in _COMPUTE:
         getattr(lib, name).restype = ctypes.c_int
     lib.fp8fg_status_string.argtypes = [ctypes.c_int]
@@ -461,4 +475,235 @@ def fp8_grouped_gemm_masked_tiled(a, sa, b_tiled, sb, masked_m, out_dtype=torch.
     _check("fp8_grouped_gemm_masked_tiled", load_library().fp8_grouped_gemm_masked_tiled(
         _ptr(a), _ptr(sa), _ptr(b_tiled), _ptr(sb), _ptr(masked_m), G, M_max, N, K, _ptr(out),
         _out_dtype(out_dtype), _stream(a)))
+    return out
+
+
+# The operators around the grouped GEMMs of a mixture-of-experts layer.
+
+def _f32_or_bf16(t, name):
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return int(t.dtype == torch.bfloat16)
+
+
+def _logits(x):
+    if not x.is_cuda:
+        raise ValueError("logits must be a GPU tensor")
+    if x.dim() != 2 or x.stride(1) != 1 or (x.shape[0] > 1 and x.stride(0) < x.shape[1]):
+        raise ValueError("logits must have shape [T][E] with contiguous rows")
+    return _f32_or_bf16(x, "logits"), (x.stride(0) if x.shape[0] > 1 else x.shape[1])
+
+
+def moe_route(logits, topk, bias=None, n_groups=1, topk_groups=1, group_top=1, score=SCORE_SIGMOID, renormalize=True,
+              scale=1.0, idx=None, w=None):
+    """Experts of each token: logits f32 or bf16 [T][E] (rows may be strided) ->
+    (idx int32 [T][topk], w f32 [T][topk]).  score SCORE_SOFTMAX or SCORE_SIGMOID;
+    bias f32 [E] is added for the choice only; of n_groups groups the
+    topk_groups best (by the sum of their group_top largest scores) stay in.
+    Logits of -inf are never chosen; missing choices are -1 with weight 0."""
+    bf16, ld = _logits(logits)
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, torch.float32, (E,), "bias")
+    idx = _empty((T, topk), torch.int32, logits) if idx is None else idx
+    w = _empty((T, topk), torch.float32, logits) if w is None else w
+    _need(idx, torch.int32, (T, topk), "idx")
+    _need(w, torch.float32, (T, topk), "w")
+    _check("moe_route", load_library().moe_route(
+        _ptr(logits), bf16, ld, _ptr(bias), T, E, topk, n_groups, topk_groups, group_top, score, int(bool(renormalize)),
+        scale, _ptr(idx), _ptr(w), _stream(logits)))
+    return idx, w
+
+
+def moe_route_backward(logits, idx, dw, score=SCORE_SIGMOID, renormalize=True, scale=1.0, out=None):
+    """The gradient of moe_route's logits from dw f32 [T][topk], for the choice
+    idx: [T][E] in the logits' type."""
+    bf16, ld = _logits(logits)
+    T, E = logits.shape
+    topk = idx.shape[1]
+    _need(idx, torch.int32, (T, topk), "idx")
+    _need(dw, torch.float32, (T, topk), "dw")
+    out = _empty((T, E), logits.dtype, logits) if out is None else out
+    _need(out, logits.dtype, (T, E), "out")
+    _check("moe_route_backward", load_library().moe_route_backward(
+        _ptr(logits), bf16, ld, _ptr(idx), _ptr(dw), T, E, topk, score, int(bool(renormalize)), scale, _ptr(out),
+        _stream(logits)))
+    return out
+
+
+def moe_rows_bound(T, topk, n_experts):
+    """Rows of the contiguous layout that hold any choice of topk experts for T
+    tokens among n_experts local ones (every expert's rows padded to 128)."""
+    n = T * topk
+    return (n + 127 * min(n_experts, n)) // 128 * 128
+
+
+def fp8_moe_dispatch_contiguous(x, idx, n_experts, first=0, M_total=None, q=None, s=None):
+    """Tokens x f32 or bf16 [T][H] into the rows of their experts (idx int32
+    [T][topk]; local experts first .. first + n_experts - 1), quantized 1x128:
+    (q u8 [M_total][H], s f32 [H/128][M_total], row_of int32 [T][topk],
+    group_offsets int32 [G+1], counts int32 [G]).  M_total defaults to
+    moe_rows_bound; rows from group_offsets[G] on are not written."""
+    T, H = x.shape
+    topk = idx.shape[1]
+    _need(x, x.dtype, (T, H), "x")
+    _need(idx, torch.int32, (T, topk), "idx")
+    if M_total is None:
+        M_total = moe_rows_bound(T, topk, n_experts) if q is None else q.shape[0]
+    q = _empty((M_total, H), torch.uint8, x) if q is None else q
+    s = _empty((_nb(H), M_total), torch.float32, x) if s is None else s
+    _need(q, torch.uint8, (M_total, H), "q")
+    _need(s, torch.float32, (_nb(H), M_total), "s")
+    row_of = _empty((T, topk), torch.int32, x)
+    offsets = _empty((n_experts + 1,), torch.int32, x)
+    counts = _empty((n_experts,), torch.int32, x)
+    _check("fp8_moe_dispatch_contiguous", load_library().fp8_moe_dispatch_contiguous(
+        _ptr(x), _f32_or_bf16(x, "x"), T, H, _ptr(idx), topk, first, n_experts, M_total, _ptr(q), _ptr(s), _ptr(row_of),
+        _ptr(offsets), _ptr(counts), _stream(x)))
+    return q, s, row_of, offsets, counts
+
+
+def fp8_moe_dispatch_masked(x, idx, n_experts, M_max, first=0, q=None, s=None):
+    """fp8_moe_dispatch_contiguous in the masked layout (decode): (q u8
+    [G][M_max][H], s f32 [G][H/128][M_max], row_of int32 [T][topk] (g * M_max +
+    row), masked_m int32 [G]); rows past masked_m[g] are not written."""
+    T, H = x.shape
+    topk = idx.shape[1]
+    _need(x, x.dtype, (T, H), "x")
+    _need(idx, torch.int32, (T, topk), "idx")
+    q = _empty((n_experts, M_max, H), torch.uint8, x) if q is None else q
+    s = _empty((n_experts, _nb(H), M_max), torch.float32, x) if s is None else s
+    _need(q, torch.uint8, (n_experts, M_max, H), "q")
+    _need(s, torch.float32, (n_experts, _nb(H), M_max), "s")
+    row_of = _empty((T, topk), torch.int32, x)
+    masked_m = _empty((n_experts,), torch.int32, x)
+    _check("fp8_moe_dispatch_masked", load_library().fp8_moe_dispatch_masked(
+        _ptr(x), _f32_or_bf16(x, "x"), T, H, _ptr(idx), topk, first, n_experts, M_max, _ptr(q), _ptr(s), _ptr(row_of),
+        _ptr(masked_m), _stream(x)))
+    return q, s, row_of, masked_m
+
+
+def moe_combine(y, row_of, w=None, out_dtype=torch.bfloat16, out=None):
+    """out[t] = sum_j w[t][j] * y[row_of[t][j]] over the entries that have a row:
+    y f32 or bf16 [R][H] (or the masked [G][M_max][H]), row_of int32 [T][topk],
+    w f32 [T][topk] or None (weights of 1) -> [T][H]."""
+    T, topk = row_of.shape
+    H = y.shape[-1]
+    R = y.numel() // H if H else 0
+    _need(y, y.dtype, y.shape, "y")
+    _need(row_of, torch.int32, (T, topk), "row_of")
+    if w is not None:
+        _need(w, torch.float32, (T, topk), "w")
+    out = _empty((T, H), out_dtype, y) if out is None else out
+    _need(out, out_dtype, (T, H), "out")
+    _check("moe_combine", load_library().moe_combine(
+        _ptr(y), _f32_or_bf16(y, "y"), R, H, _ptr(row_of), _ptr(w), T, topk, _ptr(out), _out_dtype(out_dtype), _stream(y)))
+    return out
+
+
+def fp8_moe_combine_backward(dout, y, row_of, w, group_offsets, counts, q=None, s=None, dw=None):
+    """The backward pass of moe_combine in the contiguous layout: dout [T][H],
+    y [R][H] -> (q u8 [R][H], s f32 [H/128][R]: the rows' gradient
+    w[t][j] * dout[t] as a grouped GEMM's A operand; dw f32 [T][topk])."""
+    T, H = dout.shape
+    R = y.shape[0]
+    topk = row_of.shape[1]
+    G = counts.shape[0]
+    _need(dout, dout.dtype, (T, H), "dout")
+    _need(y, y.dtype, (R, H), "y")
+    _need(row_of, torch.int32, (T, topk), "row_of")
+    _need(w, torch.float32, (T, topk), "w")
+    _need(group_offsets, torch.int32, (G + 1,), "group_offsets")
+    _need(counts, torch.int32, (G,), "counts")
+    q = _empty((R, H), torch.uint8, y) if q is None else q
+    s = _empty((_nb(H), R), torch.float32, y) if s is None else s
+    dw = _empty((T, topk), torch.float32, y) if dw is None else dw
+    _need(q, torch.uint8, (R, H), "q")
+    _need(s, torch.float32, (_nb(H), R), "s")
+    _need(dw, torch.float32, (T, topk), "dw")
+    _check("fp8_moe_combine_backward", load_library().fp8_moe_combine_backward(
+        _ptr(dout), _f32_or_bf16(dout, "dout"), T, H, _ptr(y), _f32_or_bf16(y, "y"), R, _ptr(row_of), _ptr(w), topk,
+        _ptr(group_offsets), _ptr(counts), G, _ptr(q), _ptr(s), _ptr(dw), _stream(y)))
+    return q, s, dw
+
+
+def _need_rows(rows, G):
+    if rows is not None:
+        _need(rows, torch.int32, (G,), "rows")
+
+
+def fp8_swiglu(gu, rows=None, checkpoint=False, q=None, s=None, qc=None, sc=None):
+    """The gate h = g * sigmoid(g) * u of gu f32 or bf16 [M][2 I] (or the masked
+    [G][M_max][2 I]; g the first I columns, u the others), quantized 1x128:
+    (q u8 [M][I], s f32 [I/128][M]), and with checkpoint=True also the 1x128
+    quantization of gu (qc u8 [M][2 I], sc f32 [2 I/128][M]) for the backward
+    pass; a masked gu adds a leading [G] to each.  rows: int32 [1] (group_offsets[G:])
+    or int32 [G] (masked_m): the rows in use; the others are neither read nor written."""
+    lead, I = tuple(gu.shape[:-1]), gu.shape[-1] // 2
+    if gu.dim() not in (2, 3) or gu.shape[-1] % 2:
+        raise ValueError("gu must have shape [M][2 I] or [G][M_max][2 I]")
+    G, M = (1, lead[0]) if len(lead) == 1 else lead
+    _need(gu, gu.dtype, gu.shape, "gu")
+    _need_rows(rows, G)
+    ss = lead[:-1] + (_nb(I), M)
+    q = _empty(lead + (I,), torch.uint8, gu) if q is None else q
+    s = _empty(ss, torch.float32, gu) if s is None else s
+    _need(q, torch.uint8, lead + (I,), "q")
+    _need(s, torch.float32, ss, "s")
+    if checkpoint:
+        cs = lead[:-1] + (2 * _nb(I), M)
+        qc = _empty(gu.shape, torch.uint8, gu) if qc is None else qc
+        sc = _empty(cs, torch.float32, gu) if sc is None else sc
+        _need(qc, torch.uint8, gu.shape, "qc")
+        _need(sc, torch.float32, cs, "sc")
+    elif qc is not None or sc is not None:
+        raise ValueError("qc and sc are written with checkpoint=True only")
+    _check("fp8_swiglu", load_library().fp8_swiglu(
+        _ptr(gu), _f32_or_bf16(gu, "gu"), G, M, I, _ptr(rows), _ptr(q), _ptr(s), _ptr(qc), _ptr(sc), _stream(gu)))
+    return (q, s, qc, sc) if checkpoint else (q, s)
+
+
+def fp8_swiglu_backward(qc, sc, dh, rows=None, out=None):
+    """The backward pass of fp8_swiglu from its checkpoint (qc u8 [M][2 I], sc f32
+    [2 I/128][M]) and dh f32 or bf16 [M][I]: (q u8 [M][2 I], s f32 [2 I/128][M],
+    qt u8 [2 I][M], st f32 [M/128][2 I], qh u8 [I][M], sh f32 [M/128][I]) -- the
+    gradient of gu along its channels and along its rows, and h along its rows.
+    out: the six buffers to write."""
+    M, I = dh.shape
+    _need(qc, torch.uint8, (M, 2 * I), "qc")
+    _need(sc, torch.float32, (2 * _nb(I), M), "sc")
+    _need(dh, dh.dtype, (M, I), "dh")
+    _need_rows(rows, 1)
+    shapes = ((torch.uint8, (M, 2 * I), "q"), (torch.float32, (2 * _nb(I), M), "s"), (torch.uint8, (2 * I, M), "qt"),
+              (torch.float32, (_nb(M), 2 * I), "st"), (torch.uint8, (I, M), "qh"), (torch.float32, (_nb(M), I), "sh"))
+    out = tuple(_empty(shape, dtype, dh) for dtype, shape, _ in shapes) if out is None else tuple(out)
+    if len(out) != 6:
+        raise ValueError("out must hold six tensors")
+    for t, (dtype, shape, name) in zip(out, shapes):
+        _need(t, dtype, shape, name)
+    _check("fp8_swiglu_backward", load_library().fp8_swiglu_backward(
+        _ptr(qc), _ptr(sc), _ptr(dh), _f32_or_bf16(dh, "dh"), M, I, _ptr(rows), *(_ptr(t) for t in out), _stream(dh)))
+    return out
+
+
+def fp8_grouped_gemm_wgrad(a, sa, b, sb, group_offsets, out=None, accumulate=False):
+    """The experts' weight gradients out[g] = sum over expert g's rows r of
+    a[:, r] b[:, r]^T (FP32 [G][M][N]): a u8 [M][R] / sa f32 [R/128][M], b u8
+    [N][R] / sb f32 [R/128][N] (1x128 along the rows), group_offsets device int32
+    [G+1].  accumulate=True adds to out."""
+    M, R = a.shape
+    N = b.shape[0]
+    G = group_offsets.shape[0] - 1
+    _need(a, torch.uint8, (M, R), "a")
+    _need(sa, torch.float32, (_nb(R), M), "sa")
+    _need(b, torch.uint8, (N, R), "b")
+    _need(sb, torch.float32, (_nb(R), N), "sb")
+    _need(group_offsets, torch.int32, (G + 1,), "group_offsets")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    out = _empty((G, M, N), torch.float32, a) if out is None else out
+    _need(out, torch.float32, (G, M, N), "out")
+    _check("fp8_grouped_gemm_wgrad", load_library().fp8_grouped_gemm_wgrad(
+        _ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(group_offsets), G, M, N, R, _ptr(out), int(bool(accumulate)),
+        _stream(a)))
     return out

@@ -7,7 +7,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfp8fg.so")
-SOURCES = ["api.hip", "quant.hip", "gemm.hip"]
+SOURCES = ["api.hip", "quant.hip", "gemm.hip", "moe.hip", "gate.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -366,4 +366,182 @@ int fp8_grouped_gemm_masked_tiled(const uint8_t* a, const float* sa, const uint8
                                                       static_cast<hipStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------------------
+// mixture-of-experts operators
+
+constexpr int64_t kMaxTopk = 16, kMaxLocalExperts = 256, kMaxExperts = 1024;
+
+static inline bool flag(int f) { return f == 0 || f == 1; }
+static inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// blocks of a launch that needs `n` of them
+static inline bool grid_fits(int64_t n) { return n <= kMaxDim; }
+
+// the checks that both routing calls share
+static int route_args(int64_t ld, int64_t T, int64_t E, int64_t topk, int logits_bf16, int score, int renormalize) {
+    if (T < 0 || E < 1 || topk < 1 || topk > E || ld < E) return FP8FG_ERR_SHAPE;
+    if (!flag(logits_bf16) || !flag(renormalize) || (score != FP8FG_SCORE_SOFTMAX && score != FP8FG_SCORE_SIGMOID))
+        return FP8FG_ERR_UNSUPPORTED;
+    if (E > kMaxExperts || topk > kMaxTopk || T > kMaxDim || ld > kMaxDim) return FP8FG_ERR_UNSUPPORTED;
+    return FP8FG_OK;
+}
+
+int moe_route(const void* logits, int logits_bf16, int64_t ld, const float* bias, int64_t T, int64_t E, int64_t topk,
+              int64_t n_groups, int64_t topk_groups, int group_top, int score, int renormalize, float scale,
+              int32_t* idx, float* w, void* stream) {
+    if (T > 0 && (!logits || !idx || !w)) return FP8FG_ERR_NULL;
+    if (const int e = route_args(ld, T, E, topk, logits_bf16, score, renormalize)) return e;
+    if (n_groups < 1 || topk_groups < 1 || topk_groups > n_groups || E % n_groups != 0 ||
+        topk > topk_groups * (E / n_groups))
+        return FP8FG_ERR_SHAPE;
+    if (!aligned16(logits) || !aligned16(bias) || !aligned16(idx) || !aligned16(w)) return FP8FG_ERR_ALIGN;
+    if (group_top != 1 && group_top != 2) return FP8FG_ERR_UNSUPPORTED;
+    int64_t pow2 = 1;
+    while (pow2 < n_groups && pow2 < 32) pow2 *= 2;
+    if (pow2 > 16 || (E / n_groups) * pow2 > kMaxExperts) return FP8FG_ERR_UNSUPPORTED;
+    if (T == 0) return FP8FG_OK;
+    const fp8fg::RouteCall c{logits, logits_bf16, ld, T, E, topk, n_groups, topk_groups, group_top,
+                             score == FP8FG_SCORE_SIGMOID, renormalize, scale, bias, idx, w};
+    return hip_status(fp8fg::launch_route(c, static_cast<hipStream_t>(stream)));
+}
+
+int moe_route_backward(const void* logits, int logits_bf16, int64_t ld, const int32_t* idx, const float* dw, int64_t T,
+                       int64_t E, int64_t topk, int score, int renormalize, float scale, void* dlogits, void* stream) {
+    if (T > 0 && (!logits || !idx || !dw || !dlogits)) return FP8FG_ERR_NULL;
+    if (const int e = route_args(ld, T, E, topk, logits_bf16, score, renormalize)) return e;
+    if (!aligned16(logits) || !aligned16(idx) || !aligned16(dw) || !aligned16(dlogits)) return FP8FG_ERR_ALIGN;
+    if (T == 0) return FP8FG_OK;
+    const fp8fg::RouteCall c{logits, logits_bf16, ld, T, E, topk, 1, 1, 1, score == FP8FG_SCORE_SIGMOID, renormalize,
+                             scale, nullptr, const_cast<int32_t*>(idx), nullptr};
+    return hip_status(fp8fg::launch_route_backward(c, dw, dlogits, static_cast<hipStream_t>(stream)));
+}
+
+// sizes of [T][H] tokens with topk entries each, G local experts
+static int rows_args(int64_t T, int64_t H, int64_t topk, int64_t G, int64_t R) {
+    if (T < 0 || H < 0 || G < 0 || R < 0 || topk < 1) return FP8FG_ERR_SHAPE;
+    if (topk > kMaxTopk || G > kMaxLocalExperts) return FP8FG_ERR_UNSUPPORTED;
+    if (T > kMaxDim / topk || H > kMaxDim || R > kMaxDim) return FP8FG_ERR_UNSUPPORTED;
+    if (H > 0 && (T > kMaxElems / H || R > kMaxElems / H)) return FP8FG_ERR_UNSUPPORTED;
+    // one wave per token and 512 channels at the most
+    if (!grid_fits(T * ((H + 511) / 512) + 127 * G)) return FP8FG_ERR_UNSUPPORTED;
+    return FP8FG_OK;
+}
+
+// the local experts' index range: any, as long as it can be formed
+static inline bool first_ok(int64_t first) { return first >= 0 && first <= kMaxDim - kMaxLocalExperts; }
+
+int fp8_moe_dispatch_contiguous(const void* x, int x_bf16, int64_t T, int64_t H, const int32_t* idx, int64_t topk,
+                                int64_t first, int64_t G, int64_t M_total, uint8_t* q, float* s, int32_t* row_of,
+                                int32_t* group_offsets, int32_t* counts, void* stream) {
+    if (G > 0 && (!group_offsets || !counts)) return FP8FG_ERR_NULL;
+    if (G > 0 && T > 0 && (!idx || !row_of || (H > 0 && (!x || !q || !s)))) return FP8FG_ERR_NULL;
+    if (H % 16 != 0 || M_total % 128 != 0) return FP8FG_ERR_SHAPE;
+    if (const int e = rows_args(T, H, topk, G, M_total)) return e;
+    const int64_t n = T * topk;
+    if (M_total < (n + 127 * (G < n ? G : n)) / 128 * 128) return FP8FG_ERR_SHAPE;
+    if (!first_ok(first)) return FP8FG_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(idx) || !aligned16(q) || !aligned16(s) || !aligned16(row_of) ||
+        !aligned16(group_offsets) || !aligned16(counts))
+        return FP8FG_ERR_ALIGN;
+    if (!flag(x_bf16)) return FP8FG_ERR_UNSUPPORTED;
+    if (G == 0) return FP8FG_OK;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (const hipError_t e = fp8fg::launch_rows_layout(idx, n, first, G, 0, row_of, group_offsets, counts, st)) return hip_status(e);
+    if (T == 0 || H == 0) return FP8FG_OK;
+    return hip_status(fp8fg::launch_dispatch_rows(x, x_bf16, T, H, row_of, topk, M_total, M_total, group_offsets, counts,
+                                                  G, q, s, st));
+}
+
+int fp8_moe_dispatch_masked(const void* x, int x_bf16, int64_t T, int64_t H, const int32_t* idx, int64_t topk,
+                            int64_t first, int64_t G, int64_t M_max, uint8_t* q, float* s, int32_t* row_of,
+                            int32_t* masked_m, void* stream) {
+    if (G > 0 && !masked_m) return FP8FG_ERR_NULL;
+    if (G > 0 && T > 0 && (!idx || !row_of || (H > 0 && (!x || !q || !s)))) return FP8FG_ERR_NULL;
+    if (H % 16 != 0 || M_max < 1) return FP8FG_ERR_SHAPE;
+    if (G > 0 && M_max > kMaxDim / G) return FP8FG_ERR_UNSUPPORTED;
+    if (const int e = rows_args(T, H, topk, G, G > 0 ? G * M_max : 0)) return e;
+    if (!first_ok(first)) return FP8FG_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(idx) || !aligned16(q) || !aligned16(s) || !aligned16(row_of) || !aligned16(masked_m))
+        return FP8FG_ERR_ALIGN;
+    if (!flag(x_bf16)) return FP8FG_ERR_UNSUPPORTED;
+    if (G == 0) return FP8FG_OK;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (const hipError_t e = fp8fg::launch_rows_layout(idx, T * topk, first, G, M_max, row_of, nullptr, masked_m, st))
+        return hip_status(e);
+    if (T == 0 || H == 0) return FP8FG_OK;
+    return hip_status(fp8fg::launch_dispatch_rows(x, x_bf16, T, H, row_of, topk, G * M_max, M_max, nullptr, nullptr, G, q,
+                                                  s, st));
+}
+
+int moe_combine(const void* y, int y_bf16, int64_t R, int64_t H, const int32_t* row_of, const float* w, int64_t T,
+                int64_t topk, void* out, int out_dtype, void* stream) {
+    if (T > 0 && H > 0 && (!row_of || !out || (R > 0 && !y))) return FP8FG_ERR_NULL;
+    if (H % 8 != 0) return FP8FG_ERR_SHAPE;
+    if (const int e = rows_args(T, H, topk, 0, R)) return e;
+    if (!aligned16(y) || !aligned16(row_of) || !aligned16(w) || !aligned16(out)) return FP8FG_ERR_ALIGN;
+    if (!flag(y_bf16) || !valid_out(out_dtype)) return FP8FG_ERR_UNSUPPORTED;
+    if (T == 0 || H == 0) return FP8FG_OK;
+    return hip_status(fp8fg::launch_combine(y, y_bf16, R, H, row_of, w, T, topk, out, out_dtype == FP8FG_OUT_FP32,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+int fp8_moe_combine_backward(const void* dout, int dout_bf16, int64_t T, int64_t H, const void* y, int y_bf16,
+                             int64_t R, const int32_t* row_of, const float* w, int64_t topk,
+                             const int32_t* group_offsets, const int32_t* counts, int64_t G, uint8_t* q, float* s,
+                             float* dw, void* stream) {
+    if (T > 0 && (!row_of || !w || !dw || (H > 0 && !dout))) return FP8FG_ERR_NULL;
+    if (R > 0 && H > 0 && (!y || !q || !s)) return FP8FG_ERR_NULL;
+    if (G > 0 && (!group_offsets || !counts)) return FP8FG_ERR_NULL;
+    if (H % 16 != 0) return FP8FG_ERR_SHAPE;
+    if (const int e = rows_args(T, H, topk, G, R)) return e;
+    if (!aligned16(dout) || !aligned16(y) || !aligned16(row_of) || !aligned16(w) || !aligned16(group_offsets) ||
+        !aligned16(counts) || !aligned16(q) || !aligned16(s) || !aligned16(dw))
+        return FP8FG_ERR_ALIGN;
+    if (!flag(dout_bf16) || !flag(y_bf16)) return FP8FG_ERR_UNSUPPORTED;
+    if (T == 0 && (G == 0 || R == 0)) return FP8FG_OK;
+    return hip_status(fp8fg::launch_combine_backward(dout, dout_bf16, T, H, y, y_bf16, R, row_of, w, topk, group_offsets,
+                                                     counts, G, q, s, dw, static_cast<hipStream_t>(stream)));
+}
+
+int fp8_swiglu(const void* gu, int gu_bf16, int64_t G, int64_t M, int64_t I, const int32_t* rows, uint8_t* q, float* s,
+               uint8_t* qc, float* sc, void* stream) {
+    if (G > 0 && M > 0 && I > 0 && (!gu || !q || !s || !qc != !sc)) return FP8FG_ERR_NULL;
+    if (G < 0 || M < 0 || I < 0 || I % 128 != 0) return FP8FG_ERR_SHAPE;
+    if (!aligned16(gu) || !aligned16(q) || !aligned16(s) || !aligned16(qc) || !aligned16(sc) || !aligned4(rows))
+        return FP8FG_ERR_ALIGN;
+    if (!flag(gu_bf16) || G > 65535 || M > kMaxDim || I > kMaxDim / 2) return FP8FG_ERR_UNSUPPORTED;
+    if (G == 0 || M == 0 || I == 0) return FP8FG_OK;
+    if (M > kMaxElems / (2 * I) / G) return FP8FG_ERR_UNSUPPORTED;
+    return hip_status(fp8fg::launch_swiglu(gu, gu_bf16, G, M, I, rows, q, s, qc, sc, static_cast<hipStream_t>(stream)));
+}
+
+int fp8_swiglu_backward(const uint8_t* qc, const float* sc, const void* dh, int dh_bf16, int64_t M, int64_t I,
+                        const int32_t* rows, uint8_t* q, float* s, uint8_t* qt, float* st, uint8_t* qh, float* sh,
+                        void* stream) {
+    if (M > 0 && I > 0 && (!qc || !sc || !dh || !q || !s || !qt || !st || !qh || !sh)) return FP8FG_ERR_NULL;
+    if (M < 0 || I < 0 || I % 128 != 0 || M % 16 != 0) return FP8FG_ERR_SHAPE;
+    if (!aligned16(qc) || !aligned16(sc) || !aligned16(dh) || !aligned16(q) || !aligned16(s) || !aligned16(qt) ||
+        !aligned16(st) || !aligned16(qh) || !aligned16(sh) || !aligned4(rows))
+        return FP8FG_ERR_ALIGN;
+    if (!flag(dh_bf16) || M > int64_t(128) * 65535 || I > kMaxDim / 2) return FP8FG_ERR_UNSUPPORTED;
+    if (M == 0 || I == 0) return FP8FG_OK;
+    if (M > kMaxElems / (2 * I)) return FP8FG_ERR_UNSUPPORTED;
+    return hip_status(fp8fg::launch_swiglu_backward(qc, sc, dh, dh_bf16, M, I, rows, q, s, qt, st, qh, sh,
+                                                    static_cast<hipStream_t>(stream)));
+}
+
+int fp8_grouped_gemm_wgrad(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb,
+                           const int32_t* group_offsets, int64_t G, int64_t M, int64_t N, int64_t R, float* c,
+                           int accumulate, void* stream) {
+    if (G > 0 && M > 0 && N > 0 && (!c || !group_offsets || (R > 0 && (!a || !sa || !b || !sb)))) return FP8FG_ERR_NULL;
+    if (G < 0 || M < 0 || N < 0 || R < 0 || R % 128 != 0 || N % 16 != 0) return FP8FG_ERR_SHAPE;
+    if (!aligned16(a) || !aligned16(sa) || !aligned16(b) || !aligned16(sb) || !aligned16(c) || !aligned16(group_offsets))
+        return FP8FG_ERR_ALIGN;
+    if (!flag(accumulate) || M > kMaxDim || N > kMaxDim || R > kMaxDim || G > kMaxDim - 1) return FP8FG_ERR_UNSUPPORTED;
+    if (G == 0 || M == 0 || N == 0) return FP8FG_OK;
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+    if (G > kMaxDim / tiles) return FP8FG_ERR_UNSUPPORTED;
+    fp8fg::GemmArgs args{a, sa, b, sb, c, group_offsets, M, N, R, G, nullptr, accumulate};
+    return hip_status(fp8fg::launch_gemm(0, fp8fg::GemmMode::Wgrad, 1, 1, args, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

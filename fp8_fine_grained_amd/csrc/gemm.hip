@@ -125,6 +125,7 @@ struct Tile {
     const uint8_t* B;
     const float* SB;
     int64_t g;            // the tile's expert (0 in the dense layout)
+    int64_t k_len;        // the contraction's length (Wgrad layout: the expert's rows, from A and B on)
     int bn;
     bool live;
 };
@@ -180,6 +181,22 @@ __device__ __forceinline__ int64_t masked_pair_by_work(const GemmArgs& args, int
     return -1;
 }
 
+// Wgrad layout: the p-th expert in order of decreasing rows (its contraction's
+// length), ties by index, so that the longest tiles start first.  One lane per
+// expert; past 64 experts the natural order is kept.
+__device__ __forceinline__ int64_t wgrad_expert_by_work(const GemmArgs& args, int64_t p) {
+    if (args.G > 64) return p;
+    const int lane = threadIdx.x & 63, G = int(args.G);
+    const int len = lane < G ? args.aux[lane + 1] - args.aux[lane] : -1;
+    int rank = 0;
+    for (int j = 0; j < G; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        rank += (other > len || (other == len && j < lane)) ? 1 : 0;
+    }
+    const uint64_t at = __builtin_amdgcn_ballot_w64(lane < G && rank == int(p));
+    return at ? int64_t(__builtin_ctzll(at)) : p;
+}
+
 // tile -> operands; n-tiles cover columns [0, n_ext) (n_ext < 0: all N)
 template <class C, int MODE>
 __device__ __forceinline__ Tile map_tile(const GemmArgs& args, int64_t tile, int64_t n_ext = -1) {
@@ -187,6 +204,13 @@ __device__ __forceinline__ Tile map_tile(const GemmArgs& args, int64_t tile, int
     Tile t;
     const int n_tiles = int(((n_ext < 0 ? args.N : n_ext) + BN - 1) / BN);   // a last partial n-tile when N % BN != 0
     const int64_t kbs = (args.K + BK - 1) / BK;
+    constexpr bool GRID = MODE == int(GemmMode::Dense) || MODE == int(GemmMode::Wgrad);   // whole M x N grids of tiles
+    int64_t wg = 0;
+    if (MODE == int(GemmMode::Wgrad)) {
+        const int64_t per = ((args.M + BM - 1) / BM) * n_tiles;
+        wg = wgrad_expert_by_work(args, tile / per);
+        tile %= per;
+    }
     if (MODE == int(GemmMode::Masked) && args.xcds > 1) {
         // Workgroup w runs on XCD w mod xcds (round-robin dispatch).  Give each
         // XCD whole (expert, m-tile) pairs -- ranks x, x + xcds, ... -- so the
@@ -195,7 +219,7 @@ __device__ __forceinline__ Tile map_tile(const GemmArgs& args, int64_t tile, int
         const int64_t x = tile % args.xcds, j = tile / args.xcds;
         tile = (x + args.xcds * (j / n_tiles)) * n_tiles + j % n_tiles;
     }
-    if (MODE == int(GemmMode::Dense) && args.xcds > 1 && tile < ((args.M + BM - 1) / BM) * n_tiles) {
+    if (GRID && args.xcds > 1 && tile < ((args.M + BM - 1) / BM) * n_tiles) {
         // Workgroup w runs on XCD w mod xcds, and the workgroups of one XCD
         // start in order of w.  XCD x takes the x-th run of Q = T / xcds
         // consecutive tiles (T tiles in all; the last T mod xcds keep their
@@ -228,10 +252,25 @@ __device__ __forceinline__ Tile map_tile(const GemmArgs& args, int64_t tile, int
     t.c_base = 0;
     t.live = true;
     t.lda_s = args.M;
+    t.k_len = args.K;
     int64_t g = 0;
-    if (MODE == int(GemmMode::Dense)) {
+    if (GRID) {
         t.m0 = tile * BM;
         t.rows_valid = args.M;
+        if (MODE == int(GemmMode::Wgrad)) {
+            // expert g's rows [lo, hi) of the contraction axis, whole 128-row
+            // groups; operands are [M][K] and [N][K] with K all experts' rows
+            g = wg;
+            int64_t lo = args.aux[g], hi = args.aux[g + 1];
+            lo = (lo < 0 ? 0 : lo > args.K ? args.K : lo) / BK * BK;
+            hi = (hi < lo ? lo : hi > args.K ? args.K : hi) / BK * BK;
+            t.k_len = hi - lo;
+            t.A += lo;
+            t.B += lo;
+            t.SA += lo / BK * args.M;
+            t.SB += lo / BK * args.N;
+            t.c_base = g * args.M * args.N;
+        }
     } else if (MODE == int(GemmMode::Contig)) {
         // walk the groups, counting ceil(rows / BM) tiles per group, until the
         // tile's index falls inside one; the grid is sized M_total/BM + G, an
@@ -269,7 +308,7 @@ __device__ __forceinline__ Tile map_tile(const GemmArgs& args, int64_t tile, int
     }
     t.g = g;
     if (t.m0 >= t.rows_valid) t.live = false;
-    if (MODE != int(GemmMode::Dense)) {
+    if (!GRID) {
         t.B += g * args.N * args.K;
         t.SB += g * ((args.N + 127) / 128) * kbs;   // 128x128 scales [G][ceil(N/128)][ceil(K/128)]
     }
@@ -329,7 +368,7 @@ struct Copier {
 
 template <class C, int BSCALE_1x128>
 __device__ __forceinline__ Copier<C> make_copier(const Tile& t, int wave, int lane, int64_t K, int64_t N,
-                                                 int64_t n0) {
+                                                 int64_t n0, int64_t pitch) {
     typedef Stage<C> S;
     Copier<C> c;
     c.K = K;
@@ -341,7 +380,7 @@ __device__ __forceinline__ Copier<C> make_copier(const Tile& t, int wave, int la
         const int chunk = slot ^ ((r >> 1) & 7);
         int64_t row = t.m0 + r;
         if (row >= t.rows_valid) row = t.rows_valid - 1;      // clamp: loaded, never stored
-        c.a_row[i] = t.A + row * K;
+        c.a_row[i] = t.A + row * pitch;
         c.a_c16[i] = chunk * 16;
         c.a_lds[i] = int(offsetof(S, a)) + r0 * BK;
     }
@@ -350,7 +389,7 @@ __device__ __forceinline__ Copier<C> make_copier(const Tile& t, int wave, int la
         const int r0 = (wave * C::B_PER_WAVE + i) * 8, r = r0 + sub;
         const int chunk = slot ^ ((r >> 1) & 7);
         const int64_t brow = n0 + r < N ? n0 + r : N - 1;       // clamp: loaded, never stored
-        c.b_row[i] = t.B + brow * K;
+        c.b_row[i] = t.B + brow * pitch;
         c.b_c16[i] = chunk * 16;
         c.b_lds[i] = int(offsetof(S, b)) + r0 * BK;
     }
@@ -566,7 +605,9 @@ __device__ __forceinline__ void store_bf16_rows64(uint16_t* p, int64_t ldc, int 
 // the lanes with l % 16 = i columns 16 p .. 16 p + 15 of tile row i in one
 // chunk and of row i + 16 in the other: each store writes 64 contiguous bytes
 // of 16 rows, not 32 bytes of 32.  p points at the tile's row 0, column 0;
-// `rows` of its rows exist.  Every lane of the wave must take part.
+// `rows` of its rows exist.  Every lane of the wave must take part.  ADD: the
+// values are added to what C holds.
+template <bool ADD = false>
 __device__ __forceinline__ void store_f32_rows64(float* p, int64_t ldc, int lane, int64_t rows, v4f (&v)[4]) {
     const int i = lane & 15, col = 4 * (lane >> 5) + 8 * ((lane >> 4) & 1);
 #pragma unroll
@@ -579,8 +620,15 @@ __device__ __forceinline__ void store_f32_rows64(float* p, int64_t ldc, int lane
             x[q] = sw[0];
             y[q] = sw[1];
         }
-        if (i < rows) st<u32x4>(p + i * ldc + 16 * pr + col, u32x4{x[0], x[1], x[2], x[3]});
-        if (i + 16 < rows) st<u32x4>(p + (i + 16) * ldc + 16 * pr + col, u32x4{y[0], y[1], y[2], y[3]});
+        float* c0 = p + i * ldc + 16 * pr + col;
+        float* c1 = c0 + 16 * ldc;
+        u32x4 s0 = u32x4{x[0], x[1], x[2], x[3]}, s1 = u32x4{y[0], y[1], y[2], y[3]};
+        if (ADD) {
+            if (i < rows) s0 = __builtin_bit_cast(u32x4, __builtin_bit_cast(v4f, s0) + ld<v4f>(c0));
+            if (i + 16 < rows) s1 = __builtin_bit_cast(u32x4, __builtin_bit_cast(v4f, s1) + ld<v4f>(c1));
+        }
+        if (i < rows) st<u32x4>(c0, s0);
+        if (i + 16 < rows) st<u32x4>(c1, s1);
     }
 }
 
@@ -601,11 +649,12 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& args) {
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-    const int64_t N = args.N, K = args.K, kbs = (K + BK - 1) / BK;   // the last K-block may be partial
     const Tile t = map_tile<C, MODE>(args, blockIdx.x);
     if (!t.live) return;
+    const int64_t N = args.N, K = MODE == int(GemmMode::Wgrad) ? t.k_len : args.K;
+    const int64_t kbs = (K + BK - 1) / BK;   // the last K-block may be partial
     const int64_t n0 = int64_t(t.bn) * C::BN;
-    const Copier<C> cp = make_copier<C, BSCALE_1x128>(t, wave, lane, K, N, n0);
+    const Copier<C> cp = make_copier<C, BSCALE_1x128>(t, wave, lane, K, N, n0, args.K);
     // 32-row m-tiles of this wave that hold valid rows (0 .. FM)
     const int64_t wrow0 = t.m0 + wm * FM * 32;
     const int64_t left = t.rows_valid - wrow0;
@@ -693,7 +742,13 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& args) {
                 const v4f v = v4f{acc[mi][ni][4 * j], acc[mi][ni][4 * j + 1], acc[mi][ni][4 * j + 2],
                                   acc[mi][ni][4 * j + 3]};
                 if (OUT_FP32) {
-                    if (8 * j + 4 * hh < cols) st<v4f>(static_cast<float*>(args.c) + t.c_base + m * N + col0 + 8 * j + 4 * hh, v);
+                    float* c = static_cast<float*>(args.c) + t.c_base + m * N + col0 + 8 * j + 4 * hh;
+                    if (8 * j + 4 * hh < cols) {
+                        if (MODE == int(GemmMode::Wgrad) && args.accumulate)
+                            st<v4f>(c, v + ld<v4f>(c));
+                        else
+                            st<v4f>(c, v);
+                    }
                 } else {
                     bf16_words(v, d[j]);
                 }
@@ -1272,7 +1327,7 @@ struct IlCopier {
 
 template <class W, int CW, bool BS1 = false>
 __device__ __forceinline__ IlCopier<W, CW> make_il_copier(const Tile& t, int wave, int lane, int64_t K, int64_t N,
-                                                          int64_t n0) {
+                                                          int64_t n0, int64_t pitch) {
     typedef WStage<W> S;
     typedef IlCopier<W, CW> C;
     C c;
@@ -1281,8 +1336,8 @@ __device__ __forceinline__ IlCopier<W, CW> make_il_copier(const Tile& t, int wav
     const int cw = c.copier ? wave : 0;     // non-copying waves set up (unused) offsets of wave 0
     const int sub = lane >> 2, slot = lane & 3;
     const int64_t tile_rows = t.rows_valid - t.m0 < W::BM ? t.rows_valid - t.m0 : W::BM;   // >= 1
-    c.ra = make_rsrc(t.A + t.m0 * K, uint32_t(tile_rows * K));
-    c.rb = make_rsrc(t.B + n0 * K, uint32_t(W::BN * K));
+    c.ra = make_rsrc(t.A + t.m0 * pitch, uint32_t((tile_rows - 1) * pitch + K));
+    c.rb = make_rsrc(t.B + n0 * pitch, uint32_t((W::BN - 1) * pitch + K));
     // row r = r0 + sub of a piece holds the lane's chunk at slot ^ ((r >> 2) & 3),
     // and with r0 % 16 == 0 (sub < 16) that is slot ^ ((sub >> 2) & 3) in every piece
     static_assert(W::ROWS_PER_PIECE % 16 == 0, "one swizzle phase per piece");
@@ -1291,16 +1346,16 @@ __device__ __forceinline__ IlCopier<W, CW> make_il_copier(const Tile& t, int wav
     for (int i = 0; i < C::AP; ++i) {
         const int r0 = (cw * C::AP + i) * W::ROWS_PER_PIECE, r = r0 + sub;
         const int64_t row = r < tile_rows ? r : tile_rows - 1;      // clamp: loaded, never stored
-        c.va[i] = uint32_t(row * K + c.c16);
+        c.va[i] = uint32_t(row * pitch + c.c16);
         c.a_lds[i] = int(offsetof(S, a)) + r0 * W::KS;
     }
 #pragma unroll
     for (int i = 0; i < C::BP; ++i) {
         const int r0 = (cw * C::BP + i) * W::ROWS_PER_PIECE, r = r0 + sub;
-        if (i == 0) c.vb0 = uint32_t(int64_t(r) * K + c.c16);
+        if (i == 0) c.vb0 = uint32_t(int64_t(r) * pitch + c.c16);
         c.b_lds[i] = int(offsetof(S, b)) + r0 * W::KS;
     }
-    c.b_step = uint32_t(W::ROWS_PER_PIECE * K);
+    c.b_step = uint32_t(W::ROWS_PER_PIECE * pitch);
     const int64_t kbs = (K + BK - 1) / BK;
     if (wave < W::A_SCALE_WAVES) {        // A scales of rows 64 wave .. +63 (clamped)
         const int64_t rr = int64_t(wave) * 64 + lane;
@@ -1861,10 +1916,12 @@ __device__ __forceinline__ void il_kloop(uint8_t* lds_raw, WStage<W>* ring, cons
 
 // BS1: B is 1x128-scaled (one scale per column and K-block, [K/128][N]: the
 // Wgrad operand); dense layout, BF16 / FP32 out.
-template <class W, int OUT, int MODE, bool BS1 = false>
-__device__ __forceinline__ void gemm_wide_il_body(const GemmArgs& args, uint8_t* lds_raw, int64_t tile, int64_t n_ext) {
-    static_assert(MODE != int(GemmMode::Masked), "dense and contiguous layouts");
-    static_assert(!BS1 || (OUT != 2 && MODE == int(GemmMode::Dense)), "1x128 B: dense, BF16 / FP32 out");
+// K: the contraction's length from t.A and t.B on, whose rows are `pitch`
+// bytes apart; add: the FP32 result is added to C.
+template <class W, int OUT, bool BS1 = false, bool ADD = false>
+__device__ __forceinline__ void wide_il_tile(const GemmArgs& args, uint8_t* lds_raw, const Tile& t, int64_t K,
+                                             int64_t pitch, bool add) {
+    static_assert(!BS1 || OUT != 2, "1x128 B: BF16 / FP32 out");
     typedef WStage<W> S;
     constexpr int FM = W::FM, FN = W::FN, STAGES = W::STAGES;
     constexpr uint32_t kZeroLine = STAGES * sizeof(S);
@@ -1873,12 +1930,10 @@ __device__ __forceinline__ void gemm_wide_il_body(const GemmArgs& args, uint8_t*
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / W::WAVES_N, wn = wave % W::WAVES_N;
-    const int64_t N = args.N, K = args.K;
+    const int64_t N = args.N;
     const int halves = int(2 * ((K + BK - 1) / BK));
-    const Tile t = map_tile<W, MODE>(args, tile, n_ext);
-    if (!t.live) return;
     const int64_t n0 = int64_t(t.bn) * W::BN;
-    const IlCopier<W, IL_COPY_WAVES> cp = make_il_copier<W, IL_COPY_WAVES, BS1>(t, wave, lane, K, N, n0);
+    const IlCopier<W, IL_COPY_WAVES> cp = make_il_copier<W, IL_COPY_WAVES, BS1>(t, wave, lane, K, N, n0, pitch);
     const int64_t wrow0 = t.m0 + wm * FM * 32;
     const bool live = wrow0 < t.rows_valid;   // uniform
     const int r = lane & 31, h = lane >> 5;
@@ -2022,10 +2077,53 @@ __device__ __forceinline__ void gemm_wide_il_body(const GemmArgs& args, uint8_t*
                     if (BS1)   // the columns' last mantissa parts
                         v[j] = v[j] * ld<v4f>(lds_raw + cl + 1024u + uint32_t((ni * 32 + 8 * j + 4 * h) * 4));
                 }
-                store_f32_rows64(static_cast<float*>(args.c) + t.c_base + m0 * N + n0 + wn * FN * 32 + ni * 32, N, lane,
-                                 t.rows_valid - m0, v);
+                float* c = static_cast<float*>(args.c) + t.c_base + m0 * N + n0 + wn * FN * 32 + ni * 32;
+                if (ADD && add)
+                    store_f32_rows64<true>(c, N, lane, t.rows_valid - m0, v);
+                else
+                    store_f32_rows64(c, N, lane, t.rows_valid - m0, v);
             }
         }
+    }
+}
+
+template <class W, int OUT, int MODE, bool BS1 = false>
+__device__ __forceinline__ void gemm_wide_il_body(const GemmArgs& args, uint8_t* lds_raw, int64_t tile, int64_t n_ext) {
+    static_assert(MODE == int(GemmMode::Dense) || (MODE == int(GemmMode::Contig) && !BS1), "dense and contiguous layouts");
+    const Tile t = map_tile<W, MODE>(args, tile, n_ext);
+    if (!t.live) return;
+    wide_il_tile<W, OUT, BS1>(args, lds_raw, t, args.K, args.K, false);
+}
+
+// The experts' weight gradients: C[g][M][N] = sum over expert g's rows of
+// a_row b_row^T, the contraction running over a part [lo, hi) of the operands'
+// common axis.  A contraction longer than WGRAD_BLOCKS K-blocks runs in pieces of that
+// many, each adding its FP32 sum to C: one accumulator stays inside the 2^-14
+// S contract only up to kWideB1MaxKBlocks of them.  An expert without rows
+// gets zeros.
+constexpr int64_t WGRAD_BLOCKS = 64;
+template <class W>
+__device__ __forceinline__ void gemm_wide_wgrad_body(const GemmArgs& args, uint8_t* lds_raw) {
+    Tile t = map_tile<W, int(GemmMode::Wgrad)>(args, blockIdx.x);
+    if (!t.live) return;
+    if (t.k_len == 0) {
+        if (args.accumulate) return;
+        float* c = static_cast<float*>(args.c) + t.c_base + t.m0 * args.N + int64_t(t.bn) * W::BN;
+        for (int64_t i = threadIdx.x; i < W::BM * (W::BN / 4); i += W::THREADS) {
+            const int64_t m = i / (W::BN / 4);
+            if (t.m0 + m < t.rows_valid) st<v4f>(c + m * args.N + (i % (W::BN / 4)) * 4, v4f{0.f, 0.f, 0.f, 0.f});
+        }
+        return;
+    }
+    for (int64_t k0 = 0; k0 < t.k_len; k0 += WGRAD_BLOCKS * BK) {
+        const int64_t left = t.k_len - k0;
+        if (k0 > 0) __syncthreads();      // every wave has read its last fragments before the ring is refilled
+        wide_il_tile<W, 1, true, true>(args, lds_raw, t, left < WGRAD_BLOCKS * BK ? left : WGRAD_BLOCKS * BK, args.K,
+                                       k0 > 0 || args.accumulate);
+        t.A += WGRAD_BLOCKS * BK;
+        t.B += WGRAD_BLOCKS * BK;
+        t.SA += WGRAD_BLOCKS * args.M;
+        t.SB += WGRAD_BLOCKS * args.N;
     }
 }
 
@@ -2364,7 +2462,8 @@ __global__ __launch_bounds__(MxTile::THREADS) void gemm_mxbs_o1_dense(GemmArgs a
     X(big_e1_b0_o0_dense, 0, 4, 2, 2, 2, 3, 1, 0, 0, 0)                    \
     X(big_e1_b0_o1_dense, 0, 4, 2, 2, 2, 3, 1, 0, 1, 0)                    \
     X(big_e1_b1_o0_dense, 0, 4, 2, 2, 2, 3, 1, 1, 0, 0)                    \
-    X(big_e1_b1_o1_dense, 0, 4, 2, 2, 2, 3, 1, 1, 1, 0)
+    X(big_e1_b1_o1_dense, 0, 4, 2, 2, 2, 3, 1, 1, 1, 0)                    \
+    X(big_e0_b1_o1_wgrad, 0, 4, 2, 2, 2, 3, 0, 1, 1, 3)
 
 #define FP8FG_DEFINE_KERNEL(NAME, TILE, WM, WN, FM, FN, ST, E, BS, OF, MODE)                  \
     __global__ __launch_bounds__(kThreads) void gemm_##NAME(GemmArgs args) {                  \
@@ -2415,7 +2514,13 @@ __global__ __launch_bounds__(WideTile::THREADS) void gemm_wide_b1_o1_dense(GemmA
     __shared__ __align__(16) uint8_t lds[wide_lds_bytes<WideTile, true>()];
     gemm_wide_il_body<WideTile, 1, int(GemmMode::Dense), true>(args, lds, blockIdx.x, -1);
 }
-const KernelEntry kWideB1Kernels[] = {{gemm_wide_b1_o0_dense, 2, 0, 1, 0, int(GemmMode::Dense), WideTile::THREADS},
+// the experts' weight gradients
+__global__ __launch_bounds__(WideTile::THREADS) void gemm_wide_b1_o1_wgrad(GemmArgs args) {
+    __shared__ __align__(16) uint8_t lds[wide_lds_bytes<WideTile, true>()];
+    gemm_wide_wgrad_body<WideTile>(args, lds);
+}
+const KernelEntry kWideB1Kernels[] = {{gemm_wide_b1_o1_wgrad, 2, 0, 1, 1, int(GemmMode::Wgrad), WideTile::THREADS},
+                                      {gemm_wide_b1_o0_dense, 2, 0, 1, 0, int(GemmMode::Dense), WideTile::THREADS},
                                       {gemm_wide_b1_o1_dense, 2, 0, 1, 1, int(GemmMode::Dense), WideTile::THREADS}};
 
 
@@ -3002,7 +3107,7 @@ int64_t tile_count(GemmMode mode, const GemmArgs& args) {
     const int64_t n_tiles = (args.N + C::BN - 1) / C::BN;
     if (mode == GemmMode::Masked) return args.G * ((args.M + C::BM - 1) / C::BM) * n_tiles;
     if (mode == GemmMode::Contig) return (args.M / C::BM + args.G) * n_tiles;
-    return ((args.M + C::BM - 1) / C::BM) * n_tiles;
+    return ((args.M + C::BM - 1) / C::BM) * n_tiles * (mode == GemmMode::Wgrad ? args.G : 1);
 }
 
 // The wide kernel addresses its operands through buffer descriptors with
@@ -3030,6 +3135,15 @@ bool wide_b1_fits(const GemmArgs& args) {
     const int64_t kbs = (args.K + BK - 1) / BK;
     if (args.N % WideTile::BN != 0 || kbs > kWideB1MaxKBlocks) return false;
     return kbs * args.M * 4 <= int64_t(0xFFFFFFFF) && kbs * args.N * 4 <= int64_t(0xFFFFFFFF);
+}
+
+// The experts' weight gradients on the wide kernel: 256-wide n-tiles, and the
+// byte ranges of a 256-row slice of an operand (rows K apart) and of the scales
+// of one piece of the contraction below 4 GiB.
+bool wide_wgrad_fits(const GemmArgs& args) {
+    const int64_t rows = args.M > args.N ? args.M : args.N;
+    return args.N % WideTile::BN == 0 && 256 * args.K <= int64_t(0xFFFFFFFF) &&
+           WGRAD_BLOCKS * rows * 4 <= int64_t(0xFFFFFFFF);
 }
 
 // gfx950 (MI350 series): eight XCDs, each with its own L2
@@ -3118,7 +3232,9 @@ hipError_t dispatch(int engine, GemmMode mode, int bscale_1x128, int out_fp32, c
     // 256 x 128 tiles otherwise.  The FP8 output mode exists only in the wide
     // exact kernel (its entry point checks that it fits).
     const bool wide = out_fp32 == 2 ||
-                      (engine == 0 && (bscale_1x128 ? mode == GemmMode::Dense && wide_b1_fits(args) : wide_fits(args)));
+                      (engine == 0 && (mode == GemmMode::Wgrad ? wide_wgrad_fits(args)
+                                       : bscale_1x128          ? mode == GemmMode::Dense && wide_b1_fits(args)
+                                                               : wide_fits(args)));
     if (out_fp32 == 2) engine = 0;
     int tile = 0;
     if (mode == GemmMode::Masked && args.M <= 128)
@@ -3136,7 +3252,7 @@ hipError_t dispatch(int engine, GemmMode mode, int bscale_1x128, int out_fp32, c
                                    : tile == 1 ? DecodeTile::BM
                                    : tile == 2 ? WideTile::BM
                                                : WideDecodeTile::BM);
-    else if (mode == GemmMode::Dense)
+    else if (mode == GemmMode::Dense || mode == GemmMode::Wgrad)
         a.xcds = kXcds;
     for (const KernelEntry* table : {kKernels, kWideKernels, kWideB1Kernels}) {
         const size_t count = table == kKernels       ? sizeof(kKernels) / sizeof(kKernels[0])

@@ -34,7 +34,7 @@ hipError_t launch_quant_fprop(const void* x, int x_bf16, int64_t M, const void* 
 hipError_t launch_quant_weight(const void* w, int bf16, int64_t N, int64_t K, int transpose_out, uint8_t* q,
                                float* s, hipStream_t stream);
 
-enum class GemmMode : int { Dense = 0, Contig = 1, Masked = 2 };
+enum class GemmMode : int { Dense = 0, Contig = 1, Masked = 2, Wgrad = 3 };
 
 struct GemmArgs {
     const uint8_t* a;       // A codes (group 0)
@@ -42,11 +42,12 @@ struct GemmArgs {
     const uint8_t* b;       // B codes (group 0)
     const float* sb;        // B scales
     void* c;                // output (group 0)
-    const int32_t* aux;     // group_offsets (contiguous) or masked_m (masked)
-    int64_t M;              // rows: dense M, contiguous M_total, masked M_max (per group)
+    const int32_t* aux;     // group_offsets (contiguous, wgrad) or masked_m (masked)
+    int64_t M;              // rows: dense M, contiguous M_total, masked M_max (per group), wgrad M (per group)
     int64_t N, K;
     int64_t G;              // groups (1 for dense)
     float* cs;              // output scales [N/128][M] of the FP8 output mode (else unused)
+    int accumulate = 0;     // wgrad: add to C instead of writing it
     int xcds = 1;           // XCDs whose L2s the tile order groups tiles for (1: the plain order)
 };
 
@@ -64,5 +65,40 @@ hipError_t launch_gemm_masked_tiled(int out_fp32, const GemmArgs& args, hipStrea
 // [G][N][K] codes -> the decode-tiled layout (N % 256 == 0, K % 64 == 0)
 hipError_t launch_tile_weights_decode(const uint8_t* q, int64_t G, int64_t N, int64_t K, uint8_t* out,
                                       hipStream_t stream);
+
+// ---- moe.hip ----
+struct RouteCall {
+    const void* x;          // logits [T][E], rows ld elements apart; fp32, or bf16 bits when bf16 != 0
+    int bf16;
+    int64_t ld, T, E, topk, n_groups, topk_groups;
+    int group_top, sigmoid, renorm;
+    float scale;
+    const float* bias;      // may be null
+    int32_t* idx;           // [T][topk]
+    float* w;               // [T][topk]
+};
+hipError_t launch_route(const RouteCall& call, hipStream_t stream);
+// dx: [T][E] in the logits' type; call.idx is read, call.w and call.bias are not used
+hipError_t launch_route_backward(const RouteCall& call, const float* dw, void* dx, hipStream_t stream);
+// m_max 0: contiguous layout (offsets [G + 1] written); else masked (offsets null)
+hipError_t launch_rows_layout(const int32_t* idx, int64_t n, int64_t first, int64_t G, int64_t m_max, int32_t* row_of,
+                              int32_t* offsets, int32_t* counts, hipStream_t stream);
+// rows_per: rows of one scale array; offsets null: no padding rows to clear
+hipError_t launch_dispatch_rows(const void* x, int bf16, int64_t T, int64_t H, const int32_t* row_of, int64_t topk,
+                                int64_t R, int64_t rows_per, const int32_t* offsets, const int32_t* counts, int64_t G,
+                                uint8_t* q, float* s, hipStream_t stream);
+hipError_t launch_combine(const void* y, int y_bf16, int64_t R, int64_t H, const int32_t* row_of, const float* w,
+                          int64_t T, int64_t topk, void* out, int out_fp32, hipStream_t stream);
+hipError_t launch_combine_backward(const void* dout, int dout_bf16, int64_t T, int64_t H, const void* y, int y_bf16,
+                                   int64_t R, const int32_t* row_of, const float* w, int64_t topk,
+                                   const int32_t* offsets, const int32_t* counts, int64_t G, uint8_t* q, float* s,
+                                   float* dw, hipStream_t stream);
+
+// ---- gate.hip ----
+hipError_t launch_swiglu(const void* gu, int bf16, int64_t G, int64_t M, int64_t I, const int32_t* rows, uint8_t* q,
+                         float* s, uint8_t* qc, float* sc, hipStream_t stream);
+hipError_t launch_swiglu_backward(const uint8_t* qc, const float* sc, const void* dh, int bf16, int64_t M, int64_t I,
+                                  const int32_t* rows, uint8_t* q, float* s, uint8_t* qt, float* st, uint8_t* qh,
+                                  float* sh, hipStream_t stream);
 
 }  // namespace fp8fg

@@ -1,0 +1,706 @@
+// The operators around the grouped GEMMs of a mixture-of-experts layer
+// (gfx950): the router's choice of experts and its gradient, the tokens' rows
+// quantized into the layouts the grouped GEMMs read, and the weighted sum that
+// brings the rows back, with its backward pass.
+#include "device_common.hpp"
+#include "launch.hpp"
+
+#include <math.h>
+
+namespace fp8fg {
+
+namespace moe_detail {
+
+// ---------------------------------------------------------------------------
+// Loads of N consecutive elements (the address 16-byte aligned) as fp32
+template <int N>
+__device__ __forceinline__ void load_n(const float* p, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const v4f a = ld<v4f>(p + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i + j] = a[j];
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_n(const uint16_t* p, float (&v)[N]) {
+    if constexpr (N == 4) {
+        const u32x2_t a = ld<u32x2_t>(p);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            v[2 * j] = __uint_as_float(a[j] << 16);
+            v[2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8) {
+            const u32x4 a = ld<u32x4>(p + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[i + 2 * j] = __uint_as_float(a[j] << 16);
+                v[i + 2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
+            }
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_n(float* p, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) st<v4f>(p + i, v4f{v[i], v[i + 1], v[i + 2], v[i + 3]});
+}
+template <int N>
+__device__ __forceinline__ void store_n(uint16_t* p, const float (&v)[N]) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
+    if constexpr (N == 4) {
+        st<u32x2_t>(p, u32x2_t{w[0], w[1]});
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; i += 4) st<u32x4>(p + 2 * i, u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]});
+    }
+}
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = uint16_t(bf16_bits(v)); }
+
+// reductions over segments of L lanes (L a power of two), every lane gets the result
+template <int L>
+__device__ __forceinline__ uint32_t seg_max(uint32_t v) {
+#pragma unroll
+    for (int o = L / 2; o >= 1; o >>= 1) {
+        const uint32_t t = __shfl_xor(v, o, 64);
+        v = t > v ? t : v;
+    }
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float seg_max(float v) {
+#pragma unroll
+    for (int o = L / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float seg_sum(float v) {
+#pragma unroll
+    for (int o = L / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// Routing.  s = sigmoid(x) or softmax(x) over the row, c = s + bias; a group
+// of experts scores the sum of its group_top (1 or 2) largest c; the
+// topk_groups best groups keep their experts, and the topk largest c among
+// them are chosen, equal ones by the lowest index.  An expert with c = -inf
+// (a logit of -inf) is never chosen; where fewer than topk remain the index
+// is -1 and the weight 0.  Weights are scale * s, divided by their sum when
+// renormalised.
+//
+// LPT lanes hold a token's row; a lane owns V consecutive experts of one
+// group (groups rounded up to a power of two of lane runs), so ascending
+// lanes are ascending experts and ties fall to the lowest lane.  Scores are
+// compared as order-preserving unsigned integers, 0 for an expert that cannot
+// be chosen; everything stays in registers.
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+constexpr float kNegInf = -__builtin_inff();
+
+__device__ __forceinline__ float sigmoidf(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// A chosen expert's score up to a factor that all the chosen share, for
+// renormalised weights: where the largest of them (at logit ms) comes near
+// FP32's smallest normal, sigmoid(x) is exp(x) to FP32's accuracy.
+__device__ __forceinline__ float chosen_sigmoid(float x, float ms) { return ms < -80.0f ? expf(x - ms) : sigmoidf(x); }
+
+struct RouteArgs {
+    int64_t T, ld;
+    int E, topk, groups, gs, lpg, topk_groups, group_top, sigmoid, renorm, vec;
+    float scale;
+};
+
+// V consecutive logits of a row from element `at` on (n of them exist; the others -inf)
+template <int V, class T>
+__device__ __forceinline__ void load_logits(const T* row, int at, int n, int vec, float (&v)[V]) {
+    if (vec && n == V) {
+        load_n<V>(row + at, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = j < n ? f32_of(row[at + j]) : kNegInf;
+    }
+}
+
+template <class T, int LPT, int V>
+__global__ __launch_bounds__(256) void route(const T* __restrict__ x, const float* __restrict__ bias, RouteArgs a,
+                                             int32_t* __restrict__ idx, float* __restrict__ w) {
+    const int lane = threadIdx.x & 63, sl = lane & (LPT - 1), seg0 = lane & ~(LPT - 1);
+    const int64_t token = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LPT;
+    const bool there = token < a.T;
+    const int g = sl / a.lpg, p = sl - g * a.lpg;
+    const int left = a.gs - p * V, n = !there || g >= a.groups || left < 0 ? 0 : (left < V ? left : V);
+    const int e0 = g * a.gs + p * V;
+    const T* row = x + (there ? token : 0) * a.ld;
+    float v[V];
+    load_logits<V>(row, e0, n, a.vec, v);
+    float m = 0.0f, inv = 0.0f;
+    if (!a.sigmoid) {
+        m = kNegInf;
+#pragma unroll
+        for (int j = 0; j < V; ++j) m = fmaxf(m, v[j]);
+        m = seg_max<LPT>(m);
+        if (m == kNegInf) m = 0.0f;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum += expf(v[j] - m);
+        sum = seg_sum<LPT>(sum);
+        inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    }
+    uint32_t key[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        float c = a.sigmoid ? sigmoidf(v[j]) : expf(v[j] - m) * inv;
+        if (bias) c += j < n ? bias[e0 + j] : 0.0f;
+        key[j] = (v[j] == kNegInf || c == kNegInf) ? 0u : ordered(c);
+    }
+    if (a.topk_groups < a.groups) {
+        uint32_t k1 = 0, k2 = 0;       // the two largest keys of the lane, then of its group
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const uint32_t lo = key[j] < k1 ? key[j] : k1;
+            k1 = key[j] > k1 ? key[j] : k1;
+            k2 = lo > k2 ? lo : k2;
+        }
+        for (int o = 1; o < a.lpg; o <<= 1) {
+            const uint32_t t1 = __shfl_xor(k1, o, 64), t2 = __shfl_xor(k2, o, 64);
+            const uint32_t lo = t1 < k1 ? t1 : k1, hi2 = t2 > k2 ? t2 : k2;
+            k1 = t1 > k1 ? t1 : k1;
+            k2 = lo > hi2 ? lo : hi2;
+        }
+        uint32_t gk = k1;
+        if (a.group_top == 2 && k2 != 0) {
+            const float sum = unordered(k1) + unordered(k2);
+            gk = sum == kNegInf ? 1u : ordered(sum);
+        }
+        int rank = 0;
+        for (int q = 0; q < a.groups; ++q) {
+            const uint32_t o = __shfl(gk, seg0 + q * a.lpg, 64);
+            rank += (o > gk || (o == gk && q < g)) ? 1 : 0;
+        }
+        if (rank >= a.topk_groups) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) key[j] = 0u;
+        }
+    }
+    int mine = -1;                     // lane i < topk keeps the i-th choice
+    for (int i = 0; i < a.topk; ++i) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) best = key[j] > best ? key[j] : best;
+        const uint32_t top = seg_max<LPT>(best);
+        uint64_t who = __builtin_amdgcn_ballot_w64(best == top && top != 0u);
+        if (LPT < 64) who = (who >> seg0) & ((uint64_t(1) << (LPT & 63)) - 1);
+        const int owner = who ? int(__builtin_ctzll(who)) : -1;
+        int at = 0;
+#pragma unroll
+        for (int j = V - 1; j >= 0; --j) at = key[j] == best ? j : at;
+        const int e = __shfl(e0 + at, seg0 + (owner < 0 ? 0 : owner), 64);
+        if (sl == owner) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) key[j] = j == at ? 0u : key[j];
+        }
+        if (sl == i && owner >= 0) mine = e;
+    }
+    const float xs = mine >= 0 ? f32_of(row[mine]) : kNegInf;
+    float wt;
+    if (a.sigmoid) {
+        const float ms = a.renorm ? seg_max<LPT>(xs) : 0.0f;
+        wt = mine >= 0 ? chosen_sigmoid(xs, ms) : 0.0f;
+        if (a.renorm) {
+            const float sum = seg_sum<LPT>(wt);
+            wt = sum > 0.0f ? wt / sum : 0.0f;
+        }
+    } else if (a.renorm) {             // a softmax over the chosen alone: relative to their own maximum
+        const float ms = seg_max<LPT>(xs);
+        wt = mine >= 0 ? expf(xs - ms) : 0.0f;
+        const float sum = seg_sum<LPT>(wt);
+        wt = sum > 0.0f ? wt / sum : 0.0f;
+    } else {
+        wt = mine >= 0 ? expf(xs - m) * inv : 0.0f;
+    }
+    if (there && sl < a.topk) {
+        idx[token * a.topk + sl] = mine;
+        w[token * a.topk + sl] = wt * a.scale;
+    }
+}
+
+// The gradient of the logits.  With p_i = s_i / v (v the sum over the chosen)
+// and d_i = sum_j (g_i - g_j) p_j, renormalised weights give
+//   softmax dx_i = scale p_i d_i,   sigmoid dx_i = scale p_i (1 - s_i) d_i
+// for the chosen and 0 for the others; otherwise sigmoid dx_i = scale g_i s_i
+// (1 - s_i) and softmax dx_e = s_e (scale g_e [e chosen] - scale sum_j g_j s_j)
+// for every expert.  The differences g_i - g_j keep a single renormalised
+// weight's gradient exactly 0.
+template <class T, int LPT, int V>
+__global__ __launch_bounds__(256) void route_backward(const T* __restrict__ x, const int32_t* __restrict__ idx,
+                                                      const float* __restrict__ dw, RouteArgs a, T* __restrict__ dx) {
+    const int lane = threadIdx.x & 63, sl = lane & (LPT - 1), seg0 = lane & ~(LPT - 1);
+    const int64_t token = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LPT;
+    const bool there = token < a.T;
+    const int64_t tk = there ? token : 0;
+    const T* row = x + tk * a.ld;
+    const int e0 = sl * V, left = a.E - e0, n = !there || left < 0 ? 0 : (left < V ? left : V);
+    const bool dense = !a.sigmoid && !a.renorm;
+    float v[V], m = 0.0f, inv = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = 0.0f;
+    if (dense) {
+        load_logits<V>(row, e0, n, a.vec, v);
+        m = kNegInf;
+#pragma unroll
+        for (int j = 0; j < V; ++j) m = fmaxf(m, v[j]);
+        m = seg_max<LPT>(m);
+        if (m == kNegInf) m = 0.0f;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum += expf(v[j] - m);
+        sum = seg_sum<LPT>(sum);
+        inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    }
+    int mine = -1;
+    float g = 0.0f;
+    if (there && sl < a.topk) {
+        mine = idx[token * a.topk + sl];
+        if (mine >= a.E) mine = -1;
+        if (mine >= 0) g = dw[token * a.topk + sl] * a.scale;
+    }
+    const float xs = mine >= 0 ? f32_of(row[mine]) : kNegInf;
+    float c = 0.0f, D = 0.0f;          // the chosen expert's own term; the sum over the chosen
+    if (a.renorm) {
+        const float ms = seg_max<LPT>(xs);
+        float p = mine < 0 ? 0.0f : a.sigmoid ? chosen_sigmoid(xs, ms) : expf(xs - ms);
+        const float sum = seg_sum<LPT>(p);
+        p = sum > 0.0f ? p / sum : 0.0f;
+        float d = 0.0f;
+        for (int j = 0; j < a.topk; ++j) {
+            const float gj = __shfl(g, seg0 + j, 64), pj = __shfl(p, seg0 + j, 64);
+            d += (g - gj) * pj;
+        }
+        c = p * d;
+        if (a.sigmoid && mine >= 0) c *= sigmoidf(-xs);
+    } else if (a.sigmoid) {
+        c = mine >= 0 ? g * sigmoidf(xs) * sigmoidf(-xs) : 0.0f;
+    } else {
+        c = mine >= 0 ? g * (expf(xs - m) * inv) : 0.0f;
+        D = seg_sum<LPT>(c);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = dense ? -(expf(v[j] - m) * inv) * D : 0.0f;
+    for (int i = 0; i < a.topk; ++i) {
+        const int e = __shfl(mine, seg0 + i, 64);
+        const float ci = __shfl(c, seg0 + i, 64);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] += e0 + j == e ? ci : 0.0f;
+    }
+    T* out = dx + tk * a.E + e0;
+    if (n == V && a.E % V == 0) {
+        store_n<V>(out, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j < n) store1(out + j, v[j]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The row of every (token, choice) of the local experts first .. first + G - 1,
+// in the order of the entries (stable, no atomics on the result), the experts'
+// counts and, in the contiguous layout (m_max = 0), their offsets rounded up
+// to 128 rows; in the masked layout expert g owns rows g m_max .. and entries
+// past m_max have no row.
+//
+// One workgroup per `chunk` entries.  It counts every expert's entries before
+// its chunk and in all (32 counters per expert, one per lane pair, so that
+// the lanes of a wave never meet on an address), then ranks its own chunk
+// 1024 entries at a time: the lanes of a wave with the same expert find each
+// other with one ballot per bit of the index, the waves' counts are summed in
+// order.  No workgroup waits for another.
+constexpr int kMaxLocal = 256;
+
+__global__ __launch_bounds__(1024) void rows_layout(const int32_t* __restrict__ idx, int64_t n, int first, int G,
+                                                    int64_t chunk, int64_t m_max, int32_t* __restrict__ row_of,
+                                                    int32_t* __restrict__ offsets, int32_t* __restrict__ counts) {
+    __shared__ uint32_t hist[kMaxLocal * 32];
+    __shared__ uint32_t wave_count[16][kMaxLocal];
+    __shared__ uint32_t base[kMaxLocal];       // rows of the expert before the current entry
+    __shared__ uint32_t start[kMaxLocal + 1];  // first row of the expert
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int64_t lo = int64_t(blockIdx.x) * chunk, hi = lo + chunk < n ? lo + chunk : n;
+    for (int i = t; i < G * 32; i += 1024) hist[i] = 0;
+    __syncthreads();
+    auto count = [&](int64_t from, int64_t to) {
+        for (int64_t i = from + t; i < to; i += 1024) {
+            const uint32_t e = uint32_t(idx[i]) - uint32_t(first);
+            if (e < uint32_t(G)) atomicAdd(&hist[e * 32 + (lane & 31)], 1u);
+        }
+        __syncthreads();
+    };
+    auto total = [&](int e) {
+        uint32_t c = 0;
+        for (int i = 0; i < 32; ++i) c += hist[e * 32 + ((i + e) & 31)];
+        return c;
+    };
+    count(0, lo);
+    if (t < G) base[t] = total(t);
+    __syncthreads();
+    count(lo, n);
+    if (t < G) {
+        const uint32_t c = total(t);
+        start[t + 1] = m_max ? 0u : (c + 127u) / 128u * 128u;
+        if (blockIdx.x == 0) counts[t] = int32_t(m_max && c > uint64_t(m_max) ? uint32_t(m_max) : c);
+    }
+    if (t == 0) start[0] = 0;
+    __syncthreads();
+    if (t == 0)
+        for (int e = 0; e < G; ++e) start[e + 1] = m_max ? uint32_t((e + 1) * m_max) : start[e] + start[e + 1];
+    __syncthreads();
+    if (blockIdx.x == 0 && offsets)
+        for (int i = t; i <= G; i += 1024) offsets[i] = int32_t(start[i]);
+    for (int64_t at = lo; at < hi; at += 1024) {
+        for (int i = t; i < 16 * kMaxLocal; i += 1024) wave_count[i / kMaxLocal][i % kMaxLocal] = 0;
+        __syncthreads();
+        const int64_t i = at + t;
+        const uint32_t e0 = i < hi ? uint32_t(idx[i]) - uint32_t(first) : uint32_t(G);
+        const bool mine = e0 < uint32_t(G);
+        const uint32_t e = mine ? e0 : uint32_t(G);
+        uint64_t same = ~uint64_t(0);
+        for (int b = 0; (1 << b) <= G; ++b) {
+            const uint64_t set = __builtin_amdgcn_ballot_w64((e >> b) & 1);
+            same &= ((e >> b) & 1) ? set : ~set;
+        }
+        const uint32_t before = uint32_t(__builtin_popcountll(same & ((uint64_t(1) << lane) - 1)));
+        if (mine && before == 0) wave_count[wave][e] = uint32_t(__builtin_popcountll(same));
+        __syncthreads();
+        if (t < G) {
+            uint32_t run = base[t];
+            for (int k = 0; k < 16; ++k) {
+                const uint32_t c = wave_count[k][t];
+                wave_count[k][t] = run;
+                run += c;
+            }
+            base[t] = run;
+        }
+        __syncthreads();
+        if (i < hi) {
+            int32_t row = -1;
+            if (mine) {
+                const uint32_t rank = wave_count[wave][e] + before;
+                if (!m_max || rank < uint64_t(m_max)) row = int32_t(start[e] + rank);
+            }
+            row_of[i] = row;
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A token's row quantized 1x128 and written to its rows.  A wave takes 1024
+// channels of one token: 16 per lane, eight lanes to a 128-group, so one
+// store instruction writes 1 KB of a row.
+constexpr int kChan = 16, kWaveChan = 64 * kChan;
+
+struct RowsOut {
+    uint8_t* q;
+    float* s;
+    int64_t H, kbs, rows_per;      // rows_per: rows of one scale array (M_total, or M_max of an expert)
+    __device__ __forceinline__ float* scale(int64_t row, int64_t kb) const {
+        const int64_t b = row / rows_per;
+        return s + (b * kbs + kb) * rows_per + (row - b * rows_per);
+    }
+};
+
+__device__ __forceinline__ u32x4 encode16(const float (&v)[kChan], float& sc) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChan; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 64));
+    sc = amax / 448.0f;
+    const float rc = 1.0f / sc;
+    u32x4 c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = encode4(v4f{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}, sc, rc);
+    return c;
+}
+
+// zero rows [counts[g], padded count) of every expert: wave p = (expert, row)
+__device__ __forceinline__ void zero_padding(int64_t p, const int32_t* offsets, const int32_t* counts, int64_t R,
+                                             const RowsOut& o, int lane) {
+    const int64_t g = p / 127, row = int64_t(offsets[g]) + counts[g] + p % 127;
+    if (row < 0 || row >= offsets[g + 1] || row >= R) return;
+    for (int64_t c = lane * 16; c < o.H; c += 1024) st<u32x4>(o.q + row * o.H + c, u32x4{0u, 0u, 0u, 0u});
+    for (int64_t kb = lane; kb < o.kbs; kb += 64) *o.scale(row, kb) = 0.0f;
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void dispatch_rows(const T* __restrict__ x, const int32_t* __restrict__ row_of,
+                                                     int64_t T_, int topk, int64_t chunks, RowsOut o,
+                                                     const int32_t* __restrict__ offsets,
+                                                     const int32_t* __restrict__ counts, int64_t G, int64_t R) {
+    const int lane = threadIdx.x & 63;
+    const int64_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + int64_t(blockIdx.x) * 4;
+    if (w >= T_ * chunks) {
+        if (offsets && w - T_ * chunks < 127 * G) zero_padding(w - T_ * chunks, offsets, counts, R, o, lane);
+        return;
+    }
+    const int64_t token = w / chunks, c = w - token * chunks;
+    const int64_t ch = c * kWaveChan + lane * kChan;
+    float v[kChan];
+#pragma unroll
+    for (int i = 0; i < kChan; ++i) v[i] = 0.0f;
+    if (ch < o.H) load_n<kChan>(x + token * o.H + ch, v);
+    float sc;
+    const u32x4 code = encode16(v, sc);
+    const int32_t* rows = row_of + token * topk;
+    for (int j = 0; j < topk; ++j) {
+        const int64_t r = rows[j];
+        if (r >= 0 && ch < o.H) st<u32x4>(o.q + r * o.H + ch, code);
+    }
+    const int64_t kb = c * 8 + (lane >> 3);
+    if (kb < o.kbs)
+        for (int j = lane & 7; j < topk; j += 8) {
+            const int64_t r = rows[j];
+            if (r >= 0) *o.scale(r, kb) = sc;
+        }
+}
+
+// ---------------------------------------------------------------------------
+// out_t = sum_j w_tj y[row_tj], in the order of the choices, in FP32.  A wave
+// takes 512 channels of one token, eight per lane.
+template <class TY, class TO>
+__global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t R, int64_t H,
+                                               const int32_t* __restrict__ row_of, const float* __restrict__ wts,
+                                               int64_t T_, int topk, int64_t chunks, TO* __restrict__ out) {
+    const int lane = threadIdx.x & 63;
+    const int64_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + int64_t(blockIdx.x) * 4;
+    if (w >= T_ * chunks) return;
+    const int64_t token = w / chunks, ch = (w - token * chunks) * 512 + lane * 8;
+    if (ch >= H) return;
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+    for (int j = 0; j < topk; ++j) {
+        const int64_t r = row_of[token * topk + j];
+        if (r < 0 || r >= R) continue;
+        const float wt = wts ? wts[token * topk + j] : 1.0f;
+        float v[8];
+        load_n<8>(y + r * H + ch, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(wt, v[i], acc[i]);
+    }
+    store_n<8>(out + token * H + ch, acc);
+}
+
+// ---------------------------------------------------------------------------
+// The backward pass of combine: dw_tj = <dout_t, y[row_tj]> in FP32, and the
+// rows dy = w_tj Q(dout_t), where Q is the 1x128 quantization of dout_t: every
+// row of a token shares its codes, and its scales are |w| times the token's
+// (the sign of w goes into the codes).  A workgroup per token.
+template <class TD, class TY>
+__global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ dout, const TY* __restrict__ y,
+                                                        const int32_t* __restrict__ row_of,
+                                                        const float* __restrict__ wts, int64_t T_, int topk, RowsOut o,
+                                                        const int32_t* __restrict__ offsets,
+                                                        const int32_t* __restrict__ counts, int64_t G, int64_t R,
+                                                        float* __restrict__ dw) {
+    __shared__ float part[4][16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t token = blockIdx.x;
+    if (token >= T_) {
+        const int64_t p = (token - T_) * 4 + wave;
+        if (p < 127 * G) zero_padding(p, offsets, counts, R, o, lane);
+        return;
+    }
+    const int32_t* rows = row_of + token * topk;
+    float dot[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) dot[j] = 0.0f;
+    const int64_t chunks = (o.H + kWaveChan - 1) / kWaveChan;
+    for (int64_t c = wave; c < chunks; c += 4) {
+        const int64_t ch = c * kWaveChan + lane * kChan;
+        float v[kChan];
+#pragma unroll
+        for (int i = 0; i < kChan; ++i) v[i] = 0.0f;
+        if (ch < o.H) load_n<kChan>(dout + token * o.H + ch, v);
+        float sc;
+        const u32x4 code = encode16(v, sc);
+        const int64_t kb = c * 8 + (lane >> 3);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (j >= topk) break;
+            const int64_t r = rows[j];
+            if (r < 0 || r >= R) continue;
+            const float wt = wts[token * topk + j];
+            if (ch < o.H) {
+                float u[kChan];
+                load_n<kChan>(y + r * o.H + ch, u);
+#pragma unroll
+                for (int i = 0; i < kChan; ++i) dot[j] = fmaf(v[i], u[i], dot[j]);
+                const uint32_t flip = wt < 0.0f ? 0x80808080u : 0u;
+                st<u32x4>(o.q + r * o.H + ch, u32x4{code[0] ^ flip, code[1] ^ flip, code[2] ^ flip, code[3] ^ flip});
+            }
+            if ((lane & 7) == 0 && kb < o.kbs) *o.scale(r, kb) = sc * fabsf(wt);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        if (j >= topk) break;
+        dot[j] = seg_sum<64>(dot[j]);
+        if (lane == 0) part[wave][j] = dot[j];
+    }
+    __syncthreads();
+    const int j = threadIdx.x;
+    if (j < topk) dw[token * topk + j] = part[0][j] + part[1][j] + part[2][j] + part[3][j];
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+inline int pow2_at_least(int64_t n) {
+    int p = 1;
+    while (p < n) p *= 2;
+    return p;
+}
+constexpr int64_t kGridMax = 0x7FFFFFFF;
+
+template <class T, int LPT, int V>
+hipError_t run_route(const void* x, const float* bias, const RouteArgs& a, int32_t* idx, float* w, hipStream_t stream) {
+    const int64_t blocks = (a.T + 256 / LPT - 1) / (256 / LPT);
+    return launch_kernel(route<T, LPT, V>, dim3(unsigned(blocks)), dim3(256), stream, static_cast<const T*>(x), bias, a, idx, w);
+}
+template <class T, int LPT, int V>
+hipError_t run_route_backward(const void* x, const int32_t* idx, const float* dw, const RouteArgs& a, void* dx,
+                              hipStream_t stream) {
+    const int64_t blocks = (a.T + 256 / LPT - 1) / (256 / LPT);
+    return launch_kernel(route_backward<T, LPT, V>, dim3(unsigned(blocks)), dim3(256), stream,
+                         static_cast<const T*>(x), idx, dw, a, static_cast<T*>(dx));
+}
+
+}  // namespace moe_detail
+
+using namespace moe_detail;
+
+hipError_t launch_route(const RouteCall& c, hipStream_t stream) {
+    RouteArgs a{c.T, c.ld, int(c.E), int(c.topk), int(c.n_groups), int(c.E / c.n_groups), 0, int(c.topk_groups), c.group_top,
+                c.sigmoid, c.renorm, 0, c.scale};
+    const int ng = pow2_at_least(c.n_groups);
+    const int el = c.bf16 ? 2 : 4;
+    // 16 lanes per token (four tokens per wave) where a lane's share is at
+    // most 16 experts, else the whole wave
+    const int lpt = (a.gs + 16 / ng - 1) / (16 / ng) <= 16 ? 16 : 64;
+    a.lpg = lpt / ng;
+    const int need = (a.gs + a.lpg - 1) / a.lpg, v = need <= 4 ? 4 : need <= 8 ? 8 : 16;
+    const int unit = v * el < 16 ? v * el : 16;
+    a.vec = (c.ld * el) % unit == 0 && (int64_t(a.gs) * el) % unit == 0;
+#define FP8FG_ROUTE(T, L, V) \
+    if (lpt == L && v == V) return run_route<T, L, V>(c.x, c.bias, a, c.idx, c.w, stream);
+#define FP8FG_ROUTES(T) \
+    FP8FG_ROUTE(T, 16, 4) FP8FG_ROUTE(T, 16, 8) FP8FG_ROUTE(T, 16, 16) FP8FG_ROUTE(T, 64, 4) FP8FG_ROUTE(T, 64, 8) FP8FG_ROUTE(T, 64, 16)
+    if (c.bf16) {
+        FP8FG_ROUTES(uint16_t)
+    } else {
+        FP8FG_ROUTES(float)
+    }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_route_backward(const RouteCall& c, const float* dw, void* dx, hipStream_t stream) {
+    RouteArgs a{c.T, c.ld, int(c.E), int(c.topk), 1, int(c.E), 0, 1, 1, c.sigmoid, c.renorm, 0, c.scale};
+    const int el = c.bf16 ? 2 : 4;
+    const int lpt = c.E <= 256 ? 16 : 64;
+    const int need = (a.E + lpt - 1) / lpt, v = need <= 4 ? 4 : need <= 8 ? 8 : 16;
+    const int unit = v * el < 16 ? v * el : 16;
+    a.vec = (c.ld * el) % unit == 0;
+#define FP8FG_ROUTE_B(T, L, V) \
+    if (lpt == L && v == V) return run_route_backward<T, L, V>(c.x, c.idx, dw, a, dx, stream);
+#define FP8FG_ROUTES_B(T) \
+    FP8FG_ROUTE_B(T, 16, 4) FP8FG_ROUTE_B(T, 16, 8) FP8FG_ROUTE_B(T, 16, 16) FP8FG_ROUTE_B(T, 64, 8) FP8FG_ROUTE_B(T, 64, 16)
+    if (c.bf16) {
+        FP8FG_ROUTES_B(uint16_t)
+    } else {
+        FP8FG_ROUTES_B(float)
+    }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_rows_layout(const int32_t* idx, int64_t n, int64_t first, int64_t G, int64_t m_max, int32_t* row_of,
+                              int32_t* offsets, int32_t* counts, hipStream_t stream) {
+    int64_t chunk = 1024, blocks = (n + chunk - 1) / chunk;
+    if (blocks > 256) {
+        chunk = (n + 256 * 1024 - 1) / (256 * 1024) * 1024;
+        blocks = (n + chunk - 1) / chunk;
+    }
+    if (blocks == 0) blocks = 1;       // no entries: the counts and offsets are still written
+    return launch_kernel(rows_layout, dim3(unsigned(blocks)), dim3(1024), stream, idx, n, int(first), int(G), chunk, m_max,
+                         row_of, offsets, counts);
+}
+
+hipError_t launch_dispatch_rows(const void* x, int bf16, int64_t T, int64_t H, const int32_t* row_of, int64_t topk,
+                                int64_t R, int64_t rows_per, const int32_t* offsets, const int32_t* counts, int64_t G,
+                                uint8_t* q, float* s, hipStream_t stream) {
+    const RowsOut o{q, s, H, (H + kBlock - 1) / kBlock, rows_per};
+    const int64_t chunks = (H + kWaveChan - 1) / kWaveChan;
+    const int64_t waves = T * chunks + (offsets ? 127 * G : 0), blocks = (waves + 3) / 4;
+    if (bf16)
+        return launch_kernel(dispatch_rows<uint16_t>, dim3(unsigned(blocks)), dim3(256), stream,
+                             static_cast<const uint16_t*>(x), row_of, T, int(topk), chunks, o, offsets, counts, G, R);
+    return launch_kernel(dispatch_rows<float>, dim3(unsigned(blocks)), dim3(256), stream, static_cast<const float*>(x),
+                         row_of, T, int(topk), chunks, o, offsets, counts, G, R);
+}
+
+template <class TY, class TO>
+static hipError_t run_combine(const void* y, int64_t R, int64_t H, const int32_t* row_of, const float* w, int64_t T,
+                              int64_t topk, void* out, hipStream_t stream) {
+    const int64_t chunks = (H + 511) / 512, blocks = (T * chunks + 3) / 4;
+    return launch_kernel(combine<TY, TO>, dim3(unsigned(blocks)), dim3(256), stream, static_cast<const TY*>(y), R, H,
+                         row_of, w, T, int(topk), chunks, static_cast<TO*>(out));
+}
+
+hipError_t launch_combine(const void* y, int y_bf16, int64_t R, int64_t H, const int32_t* row_of, const float* w,
+                          int64_t T, int64_t topk, void* out, int out_fp32, hipStream_t stream) {
+    if (y_bf16)
+        return out_fp32 ? run_combine<uint16_t, float>(y, R, H, row_of, w, T, topk, out, stream)
+                        : run_combine<uint16_t, uint16_t>(y, R, H, row_of, w, T, topk, out, stream);
+    return out_fp32 ? run_combine<float, float>(y, R, H, row_of, w, T, topk, out, stream)
+                    : run_combine<float, uint16_t>(y, R, H, row_of, w, T, topk, out, stream);
+}
+
+template <class TD, class TY>
+static hipError_t run_combine_backward(const void* dout, int64_t T, int64_t H, const void* y, int64_t R,
+                                       const int32_t* row_of, const float* w, int64_t topk, const int32_t* offsets,
+                                       const int32_t* counts, int64_t G, uint8_t* q, float* s, float* dw,
+                                       hipStream_t stream) {
+    const RowsOut o{q, s, H, (H + kBlock - 1) / kBlock, R};
+    const int64_t blocks = T + (127 * G + 3) / 4;
+    return launch_kernel(combine_backward<TD, TY>, dim3(unsigned(blocks)), dim3(256), stream,
+                         static_cast<const TD*>(dout), static_cast<const TY*>(y), row_of, w, T, int(topk), o, offsets,
+                         counts, G, R, dw);
+}
+
+hipError_t launch_combine_backward(const void* dout, int dout_bf16, int64_t T, int64_t H, const void* y, int y_bf16,
+                                   int64_t R, const int32_t* row_of, const float* w, int64_t topk,
+                                   const int32_t* offsets, const int32_t* counts, int64_t G, uint8_t* q, float* s,
+                                   float* dw, hipStream_t stream) {
+#define FP8FG_CB(D, Y) return run_combine_backward<D, Y>(dout, T, H, y, R, row_of, w, topk, offsets, counts, G, q, s, dw, stream)
+    if (dout_bf16) {
+        if (y_bf16) FP8FG_CB(uint16_t, uint16_t);
+        FP8FG_CB(uint16_t, float);
+    }
+    if (y_bf16) FP8FG_CB(float, uint16_t);
+    FP8FG_CB(float, float);
+#undef FP8FG_CB
+}
+
+}  // namespace fp8fg

@@ -71,7 +71,7 @@
 extern "C" {
 #endif
 
-#define FP8FG_ABI_VERSION 14
+#define FP8FG_ABI_VERSION 15
 
 enum fp8fg_status {
     FP8FG_OK = 0,
@@ -88,6 +88,8 @@ enum fp8fg_bscale {
     FP8FG_BSCALE_128x128 = 0,    /* sb f32 [N/128][K/128]   (weights: Fprop, Dgrad) */
     FP8FG_BSCALE_1x128 = 1       /* sb f32 [K/128][N]       (token-wise operand: Wgrad) */
 };
+
+enum fp8fg_score { FP8FG_SCORE_SOFTMAX = 0, FP8FG_SCORE_SIGMOID = 1 };
 
 /*
  * Online 1x128 activation quantization.
@@ -400,6 +402,183 @@ int fp8_grouped_gemm_masked_tiled_mx(const uint8_t* a, const uint8_t* ea, const 
 int fp8_grouped_gemm_masked_tiled_fp8out(const uint8_t* a, const float* sa, const uint8_t* b_tiled, const float* sb,
                                          const int32_t* masked_m, int64_t G, int64_t M_max,
                                          int64_t N, int64_t K, uint8_t* q, float* s, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The operators around the grouped GEMMs of a mixture-of-experts layer.
+ *   forward:   moe_route -> fp8_moe_dispatch_contiguous (or _masked: decode)
+ *              -> grouped GEMM (gate+up) -> fp8_swiglu -> grouped GEMM (down)
+ *              -> moe_combine
+ *   backward:  fp8_moe_combine_backward -> grouped GEMM (down, transposed
+ *              weights) -> fp8_swiglu_backward -> grouped GEMM (gate+up,
+ *              transposed weights) -> moe_combine without weights (the
+ *              gradient of the tokens) and moe_route_backward; the weight
+ *              gradients by fp8_grouped_gemm_wgrad.
+ * All of them are deterministic: no atomics on results, sums in a fixed
+ * order, FP32 throughout.  Type flags (x_bf16, ...) are 0 for f32, 1 for bf16
+ * bit patterns (u16).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Routing.  logits: [T][E], f32 or bf16, rows ld elements apart (ld >= E).
+ *   s = sigmoid(x) or softmax(x) over the row (score: fp8fg_score),
+ *   c = s + bias      (bias f32 [E], NULL for none: the correction that
+ *                      balances the experts' load; it only steers the choice).
+ * The E experts form n_groups equal groups of consecutive ones.  A group
+ * scores the sum of its group_top (1 or 2) largest c; the topk_groups best
+ * groups stay in (all of them when topk_groups = n_groups), and the topk
+ * largest c among their experts are chosen, in decreasing order.  Equal
+ * scores go to the lowest index, for groups and experts alike; scores are
+ * compared in FP32.  An expert whose logit, or c, is -inf is never chosen and
+ * adds nothing to its group's score; where fewer than topk experts can be
+ * chosen the index is -1 and the weight 0 (a row of -inf, a padding token,
+ * chooses nothing).  A NaN or +inf logit gives unspecified weights and an
+ * unspecified choice, with every index still in [-1, E).
+ *   idx: int32 [T][topk];  w: f32 [T][topk] = scale * s_idx, divided by the
+ *   sum of the chosen s when renormalize = 1 (weights whose scores are all too
+ *   small for FP32 keep their ratios).
+ * Requires 1 <= topk <= 16, topk <= topk_groups * (E / n_groups),
+ * E % n_groups == 0, 1 <= topk_groups <= n_groups <= 16, and
+ * (E / n_groups) * P <= 1024, P the power of two from n_groups on.
+ */
+int moe_route(const void* logits, int logits_bf16, int64_t ld, const float* bias, int64_t T, int64_t E, int64_t topk,
+              int64_t n_groups, int64_t topk_groups, int group_top, int score, int renormalize, float scale,
+              int32_t* idx, float* w, void* stream);
+
+/*
+ * The gradient of the logits from dw (f32 [T][topk], the gradient of w), for
+ * the choice idx (entries outside [0, E) contribute nothing; the choice itself
+ * and the bias have no gradient).  With g_i = scale * dw_i, S the chosen
+ * experts, p_i = s_i / sum_S s and d_i = sum_j (g_i - g_j) p_j:
+ *   renormalize = 1: softmax dx_i = p_i d_i, sigmoid dx_i = p_i (1 - s_i) d_i
+ *     for i in S, 0 elsewhere;
+ *   renormalize = 0: sigmoid dx_i = g_i s_i (1 - s_i) for i in S, 0 elsewhere;
+ *     softmax dx_e = s_e ((g_e if e in S) - sum_S g_j s_j) for every expert.
+ * dlogits: [T][E] in the logits' type, rows E apart.  Requires E <= 1024,
+ * 1 <= topk <= 16 and topk <= E.
+ */
+int moe_route_backward(const void* logits, int logits_bf16, int64_t ld, const int32_t* idx, const float* dw, int64_t T,
+                       int64_t E, int64_t topk, int score, int renormalize, float scale, void* dlogits, void* stream);
+
+/*
+ * The tokens' rows in the contiguous layout, quantized.
+ * x: [T][H], f32 or bf16;  idx: int32 [T][topk], experts of each token (as
+ * moe_route gives them).  The local experts are first .. first + G - 1;
+ * entries outside (experts elsewhere, -1) have no row.
+ *   counts: int32 [G], entries per expert;
+ *   group_offsets: int32 [G+1], the experts' first rows: every count rounded
+ *     up to a multiple of 128 (as fp8_grouped_gemm_contiguous reads them; its
+ *     last entry, at most M_total, is the number of rows in use);
+ *   row_of: int32 [T][topk], the row of each entry, or -1.  An expert's rows
+ *     are its entries in their order in idx.
+ *   q: u8 [M_total][H], s: f32 [H/128][M_total]: row row_of[t][j] holds the
+ *     1x128 quantization of x[t] (exactly fp8_quant_act_1x128's; each token
+ *     is quantized once, whatever its number of rows).  Rows from an expert's
+ *     count to the next offset are zero (codes and scales); rows from
+ *     group_offsets[G] on are not written.
+ * Requires H % 16 == 0, 1 <= topk <= 16, 1 <= G <= 256 (G = 0: a no-op),
+ * M_total % 128 == 0 and M_total >= the bound that holds any choice:
+ * (n + 127 * min(G, n)) / 128 * 128 with n = T * topk; M_total < 2^31.
+ * T = 0 writes the (zero) counts and offsets.
+ */
+int fp8_moe_dispatch_contiguous(const void* x, int x_bf16, int64_t T, int64_t H, const int32_t* idx, int64_t topk,
+                                int64_t first, int64_t G, int64_t M_total, uint8_t* q, float* s, int32_t* row_of,
+                                int32_t* group_offsets, int32_t* counts, void* stream);
+
+/*
+ * The same in the masked layout (decode): expert first + g owns rows
+ * g * M_max .. of q u8 [G][M_max][H] and s f32 [G][H/128][M_max];
+ * masked_m: int32 [G], its entries, at most M_max (as fp8_grouped_gemm_masked
+ * reads them).  row_of holds g * M_max + r, r the entry's place among the
+ * expert's; entries beyond M_max have no row (-1).  Rows at or beyond
+ * masked_m[g] are not written.  Requires H % 16 == 0, 1 <= topk <= 16,
+ * G <= 256, M_max >= 1, G * M_max < 2^31.
+ */
+int fp8_moe_dispatch_masked(const void* x, int x_bf16, int64_t T, int64_t H, const int32_t* idx, int64_t topk,
+                            int64_t first, int64_t G, int64_t M_max, uint8_t* q, float* s, int32_t* row_of,
+                            int32_t* masked_m, void* stream);
+
+/*
+ * The experts' rows back to their tokens:
+ *   out[t] = sum_j w[t][j] * y[row_of[t][j]]   over the entries that have a
+ * row (row_of outside [0, R) has none; a token without rows gets 0), in the
+ * order of j, FP32 sums.  y: [R][H] f32 or bf16 (R = M_total, or G * M_max of
+ * the masked layout); w: f32 [T][topk], or NULL for weights of 1 (the
+ * backward pass of the dispatch); out: [T][H] per out_dtype (fp8fg_out).
+ * Requires H % 8 == 0, 1 <= topk <= 16.
+ */
+int moe_combine(const void* y, int y_bf16, int64_t R, int64_t H, const int32_t* row_of, const float* w, int64_t T,
+                int64_t topk, void* out, int out_dtype, void* stream);
+
+/*
+ * The backward pass of moe_combine in the contiguous layout.
+ * dout: [T][H], y: [R][H] (f32 or bf16 each); row_of, w, group_offsets,
+ * counts as the forward pass had them.
+ *   dw: f32 [T][topk] = <dout[t], y[row_of[t][j]]> (0 without a row);
+ *   q: u8 [R][H], s: f32 [H/128][R]: the gradient w[t][j] * dout[t] of the
+ *     rows as a grouped GEMM's A operand: row row_of[t][j] holds the 1x128 codes
+ *     of dout[t] (sign-flipped where w < 0) with the scales RN32(|w| * scale),
+ *     so a token is quantized once.  Padding rows are zero and rows from
+ *     group_offsets[G] on are not written, as in the dispatch.
+ * Requires H % 16 == 0, 1 <= topk <= 16, G <= 256.
+ */
+int fp8_moe_combine_backward(const void* dout, int dout_bf16, int64_t T, int64_t H, const void* y, int y_bf16,
+                             int64_t R, const int32_t* row_of, const float* w, int64_t topk,
+                             const int32_t* group_offsets, const int32_t* counts, int64_t G, uint8_t* q, float* s,
+                             float* dw, void* stream);
+
+/*
+ * The gate between an expert's two products, with its 8-bit checkpoint.
+ * gu: [G][M][2 I], f32 or bf16: gate g = columns [0, I), up u = [I, 2 I).
+ *   q: u8 [G][M][I], s: f32 [G][I/128][M]: the 1x128 quantization of
+ *     h = g * sigmoid(g) * u (FP32), the A operand of the second product;
+ *   qc: u8 [G][M][2 I], sc: f32 [G][2 I/128][M]: the 1x128 quantization of gu
+ *     itself (exactly fp8_quant_act_1x128's), the checkpoint that
+ *     fp8_swiglu_backward starts from; both NULL to leave it out (inference).
+ * rows: int32 [G] (4-byte aligned), or NULL for all rows: only rows
+ * r < rows[g] of buffer g are read and written.  The contiguous layout is G = 1 with
+ * rows = &group_offsets[G]; the masked one rows = masked_m.
+ * Requires I % 128 == 0, G <= 65535; h must be finite.
+ */
+int fp8_swiglu(const void* gu, int gu_bf16, int64_t G, int64_t M, int64_t I, const int32_t* rows, uint8_t* q, float* s,
+               uint8_t* qc, float* sc, void* stream);
+
+/*
+ * Its backward pass from the checkpoint (qc u8 [M][2 I], sc f32 [2 I/128][M],
+ * contiguous layout) and dh ([M][I], f32 or bf16).  With g, u the decoded
+ * checkpoint and sg = sigmoid(g):
+ *   du = dh * g * sg,  dg = dh * u * sg * (1 + g * (1 - sg)),  h = g * sg * u,
+ * formed in FP32 and quantized 1x128 once in each layout that the products read:
+ *   q:  u8 [M][2 I],  s:  f32 [2 I/128][M]   (dg, du) along the channels
+ *   qt: u8 [2 I][M],  st: f32 [M/128][2 I]   (dg, du) along the rows, transposed
+ *   qh: u8 [I][M],    sh: f32 [M/128][I]     h along the rows, transposed
+ * -- the A operand of the gate+up product's Dgrad, and the operands of
+ * the gate+up and down products' weight gradients.
+ * rows: int32 [1], or NULL: rows from rows[0] on count as zero; their rows of
+ * q and s, and the 128-row groups of qt and qh that lie wholly past them, are
+ * not written.  Requires I % 128 == 0, M % 16 == 0, M <= 128 * 65535.
+ */
+int fp8_swiglu_backward(const uint8_t* qc, const float* sc, const void* dh, int dh_bf16, int64_t M, int64_t I,
+                        const int32_t* rows, uint8_t* q, float* s, uint8_t* qt, float* st, uint8_t* qh, float* sh,
+                        void* stream);
+
+/*
+ * The experts' weight gradients:
+ *   c[g][M][N] (+)= sum over rows r of expert g of a[:, r] b[:, r]^T,
+ * a: u8 [M][R], sa f32 [R/128][M];  b: u8 [N][R], sb f32 [R/128][N]: operands
+ * quantized 1x128 along the rows, transposed (fp8_requant_act_tokenwise of a
+ * checkpoint, fp8_swiglu_backward's qt and qh, fp8_quant_act_1x128 with
+ * transpose_out = 1); R all experts' rows, M the output and N the input
+ * channels of the weight.
+ * group_offsets: DEVICE int32 [G+1] as for fp8_grouped_gemm_contiguous (entries
+ * are clamped to [0, R] and rounded down to multiples of 128).  An expert
+ * without rows gets zeros.  c: FP32 [G][M][N]; accumulate = 1 adds to it
+ * (gradient accumulation) instead of writing it.  The accuracy contract and
+ * engine are fp8_gemm_blockscaled's (2^-14 * S), for any number of rows.
+ * Requires R % 128 == 0, N % 16 == 0; M, N, R < 2^31.
+ */
+int fp8_grouped_gemm_wgrad(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb,
+                           const int32_t* group_offsets, int64_t G, int64_t M, int64_t N, int64_t R, float* c,
+                           int accumulate, void* stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fp8fg_status_string(int status);
