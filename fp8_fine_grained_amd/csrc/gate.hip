@@ -5,62 +5,12 @@
 //
 // sigmoid(g) = 1 / (1 + exp(-g));  with dh the gradient of h:
 //   du = dh g sigmoid(g),   dg = dh u sigmoid(g) (1 + g (1 - sigmoid(g))).
-#include "device_common.hpp"
+#include "elementwise.hpp"
 #include "launch.hpp"
-
-#include <math.h>
 
 namespace fp8fg {
 
 namespace gate_detail {
-
-__device__ __forceinline__ float sigmoidf(float x) { return 1.0f / (1.0f + expf(-x)); }
-
-template <int N>
-__device__ __forceinline__ void load_once(const float* p, float (&v)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const v4f a = ld_once<v4f>(p + i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i + j] = a[j];
-    }
-}
-template <int N>
-__device__ __forceinline__ void load_once(const uint16_t* p, float (&v)[N]) {
-    if constexpr (N == 4) {
-        const u32x2_t a = ld_once<u32x2_t>(p);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            v[2 * j] = __uint_as_float(a[j] << 16);
-            v[2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 8) {
-            const u32x4 a = ld_once<u32x4>(p + i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[i + 2 * j] = __uint_as_float(a[j] << 16);
-                v[i + 2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
-            }
-        }
-    }
-}
-
-// 16 values of a lane, eight lanes to a 128-group: the group's scale and the lane's codes
-__device__ __forceinline__ u32x4 encode16(const float (&v)[16], float& sc) {
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
-#pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 64));
-    sc = amax / 448.0f;
-    const float rc = 1.0f / sc;
-    u32x4 c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = encode4(v4f{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}, sc, rc);
-    return c;
-}
 
 // A workgroup takes 32 rows of one 128-channel group: eight lanes per row.
 // Row r of buffer blockIdx.z exists when r < rows[blockIdx.z] (rows may be
@@ -76,10 +26,10 @@ __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t 
     for (int64_t m = int64_t(blockIdx.y) * 32 + (threadIdx.x >> 3); m < end; m += int64_t(gridDim.y) * 32) {
         const T* row = gu + (b * M + m) * 2 * I + ch;
         float g[16], u[16], h[16];
-        load_once<16>(row, g);
-        load_once<16>(row + I, u);
+        load_n<16, true>(row, g);
+        load_n<16, true>(row + I, u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) h[i] = g[i] * sigmoidf(g[i]) * u[i];
+        for (int i = 0; i < 16; ++i) h[i] = g[i] * sigmoid_fast(g[i]) * u[i];
         float a;
         const u32x4 ch_code = encode16(h, a);
         st<u32x4>(q + (b * M + m) * I + ch, ch_code);
@@ -101,112 +51,152 @@ __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t 
 // The backward pass of a 128-row x 128-channel tile: the checkpoint decoded,
 // dg, du and h formed once in registers, and quantized along the channels
 // (dg, du: the next product's A operand) and along the rows, transposed (dg,
-// du, h: the operands of the two weight gradients).  A thread holds eight
-// rows of four channels; a row's 128 channels lie in 32 lanes, a channel's
-// rows in 16 threads, whose maxima meet in LDS.  The transposed codes pass
-// through LDS so that whole 128-byte row segments are written.
+// du, h: the operands of the two weight gradients).  A thread holds four rows
+// of eight channels, so that a row's 128 channels are one 16-lane row (its
+// maximum by DPP) and a channel's four rows one word of transposed codes.  A
+// channel's maxima over a wave's 16 rows meet by swaps that reduce two values into one
+// register each time, over the eight waves in LDS.  The transposed codes pass through
+// LDS so that whole 128-byte row segments are written.
 constexpr int kTileThreads = 512;
 
+// the word of rows 4 row4 .. + 3 of channel ch in a tile of transposed codes:
+// 16-byte pieces swapped by channel run, and odd and even channels by halves,
+// so that a wave's stores (16 channel runs x 4 words) meet 64 different banks
+__device__ __forceinline__ int code_word(int ch, int row4) {
+    return (ch ^ ((ch >> 6) & 1)) * 32 + (((row4 >> 2) ^ ((ch >> 3) & 7)) << 2) + (row4 & 3);
+}
+
 template <class T>
-__global__ __launch_bounds__(kTileThreads) void swiglu_backward(
+__global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
     const uint8_t* __restrict__ qc, const float* __restrict__ sc, const T* __restrict__ dh, int64_t M, int64_t I,
     const int32_t* __restrict__ rows, uint8_t* __restrict__ q, float* __restrict__ s, uint8_t* __restrict__ qt,
     float* __restrict__ st_, uint8_t* __restrict__ qh, float* __restrict__ sh) {
-    __shared__ float part[3][16][kBlock];
-    __shared__ float col[3][kBlock];
-    __shared__ __align__(16) uint8_t codes[kBlock][kBlock + 16];
-    const int t = threadIdx.x, c4 = (t & 31) * 4, r8 = (t >> 5) * 8;
+    __shared__ float part[8][3 * kBlock];
+    __shared__ __align__(16) float gs[3 * kBlock], gr[3 * kBlock];      // the channels' groups
+    __shared__ __align__(16) uint32_t codes[3][kBlock * kBlock / 4];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, c8 = (t & 15) * 8, r4 = (t >> 4) * 4;
     const int64_t nb = I / kBlock, kb = blockIdx.x, mb = blockIdx.y;
     int64_t end = rows ? int64_t(rows[0]) : M;
     end = end < M ? end : M;
     if (mb * kBlock >= end) return;
-    const int64_t ch = kb * kBlock + c4;
-    float d[3][8][4];              // dg, du, h
+    const int64_t ch = kb * kBlock + c8, m0 = mb * kBlock + r4;
+    float d[3][4][8];              // dg, du, h
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t m = mb * kBlock + r8 + i;
-        if (m < end) {
-            const uint32_t wg = ld<uint32_t>(qc + m * 2 * I + ch), wu = ld<uint32_t>(qc + m * 2 * I + I + ch);
-            const float fg = sc[kb * M + m], fu = sc[(nb + kb) * M + m];
-            float e[4];
-            load_once<4>(dh + m * I + ch, e);
-            const v2f g01 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wg, 1.0f, false);
-            const v2f g23 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wg, 1.0f, true);
-            const v2f u01 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wu, 1.0f, false);
-            const v2f u23 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wu, 1.0f, true);
-            const float gg[4] = {g01[0] * fg, g01[1] * fg, g23[0] * fg, g23[1] * fg};
-            const float uu[4] = {u01[0] * fu, u01[1] * fu, u23[0] * fu, u23[1] * fu};
+    for (int i = 0; i < 4; ++i) {
+        const bool live = m0 + i < end;
+        const int64_t m = live ? m0 + i : end - 1;     // rows past the end: loaded, then zero
+        const u32x2_t wg = ld_once<u32x2_t>(qc + m * 2 * I + ch), wu = ld_once<u32x2_t>(qc + m * 2 * I + I + ch);
+        const float fg = sc[kb * M + m], fu = live ? sc[(nb + kb) * M + m] : 0.0f;
+        float e[8];
+        load_n<8, true>(dh + m * I + ch, e);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float sg = sigmoidf(gg[j]);
-                d[0][i][j] = e[j] * uu[j] * (sg * (1.0f + gg[j] * (1.0f - sg)));
-                d[1][i][j] = e[j] * (gg[j] * sg);
-                d[2][i][j] = gg[j] * sg * uu[j];
+        for (int p = 0; p < 4; ++p) {
+            const v2f g2 = (p & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wg[p >> 1], 1.0f, true)
+                                   : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wg[p >> 1], 1.0f, false);
+            const v2f u2 = (p & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wu[p >> 1], 1.0f, true)
+                                   : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wu[p >> 1], 1.0f, false);
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const int j = 2 * p + o;
+                const float g = g2[o] * fg, u = u2[o] * fu;
+                const float dhj = live ? e[j] : 0.0f;
+                const float sg = sigmoid_fast(g), si = g * sg;
+                d[0][i][j] = dhj * u * (sg * __builtin_fmaf(g, 1.0f - sg, 1.0f));
+                d[1][i][j] = dhj * si;
+                d[2][i][j] = si * u;
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d[k][i][j] = 0.0f;
         }
+    }
+    // the channels' maxima over the wave's rows
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        float a[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            a[j] = fmaxf(fmaxf(fabsf(d[k][0][j]), fabsf(d[k][1][j])), fmaxf(fabsf(d[k][2][j]), fabsf(d[k][3][j])));
+        // halves: a[i] then holds channel 2 i on lanes 0..31 and 2 i + 1 on the others
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(a[2 * i]), __float_as_uint(a[2 * i + 1]), false, false);
+            const uint32_t lo = w[0], hi = w[1];
+            a[i] = fmaxf(__uint_as_float(lo), __uint_as_float(hi));
+        }
+        // 16-lane rows: a[i] holds what a[2 i] held on even rows and a[2 i + 1] on odd ones
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[2 * i]), __float_as_uint(a[2 * i + 1]), false, false);
+            const uint32_t lo = w[0], hi = w[1];
+            part[wave][k * kBlock + c8 + 2 * (2 * i + ((lane >> 4) & 1)) + (lane >> 5)] =
+                fmaxf(__uint_as_float(lo), __uint_as_float(hi));
+        }
+        __builtin_amdgcn_sched_barrier(0);      // one of the three at a time: their registers would not fit
+    }
+    __syncthreads();
+    if (t < 3 * kBlock) {
+        float a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a = fmaxf(a, part[i][t]);
+        const Group g = make_group(a);
+        gs[t] = a = g.s;
+        gr[t] = g.r;
+        if (t < 2 * kBlock)
+            st_[mb * 2 * I + (t >> 7) * I + kb * kBlock + (t & 127)] = a;
+        else
+            sh[mb * I + kb * kBlock + (t & 127)] = a;
     }
     // along the channels
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) {
+        float a[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t m = mb * kBlock + r8 + i;
-            const v4f v = v4f{d[k][i][0], d[k][i][1], d[k][i][2], d[k][i][3]};
-            const float a = halfwave_max(abs_max4(v)) / 448.0f;
-            const uint32_t w = encode4(v, a, 1.0f / a);
-            if (m < end) {
-                st<uint32_t>(q + m * 2 * I + k * I + ch, w);
-                if (c4 == 0) s[(k * nb + kb) * M + m] = a;
+        for (int i = 0; i < 4; ++i) {
+            a[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[i] = fmaxf(a[i], fabsf(d[k][i][j]));
+            const Group g = make_group(lanes_max<16>(a[i]));
+            a[i] = g.s;
+            uint32_t w[2];
+            encode_run<2>(d[k][i], g, w);
+            if (m0 + i < end) st<u32x2_t>(q + (m0 + i) * 2 * I + k * I + ch, u32x2_t{w[0], w[1]});
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (c8 == 0) {
+            float* p = s + (k * nb + kb) * M + m0;
+            if (m0 + 4 <= end) {
+                st<v4f>(p, v4f{a[0], a[1], a[2], a[3]});
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (m0 + i < end) p[i] = a[i];
             }
         }
+    }
+    __syncthreads();
     // along the rows
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
+    for (int k = 0; k < 3; ++k) {
+        float r[8];
+        load_n<8>(gr + k * kBlock + c8, r);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float a = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(d[k][i][j]));
-            part[k][t >> 5][c4 + j] = a;
+        for (int j = 0; j < 8; ++j) {
+            const int c = c8 + j;
+            const float x[4] = {d[k][0][j], d[k][1][j], d[k][2][j], d[k][3][j]};
+            uint32_t w[1];
+            encode_run<1>(x, Group{gs[k * kBlock + c], r[j]}, w);
+            codes[k][code_word(c, r4 >> 2)] = w[0];
+            if (j & 1) __builtin_amdgcn_sched_barrier(0);
         }
-    __syncthreads();
-    if (t < 3 * kBlock) {
-        const int k = t / kBlock, c = t % kBlock;
-        float a = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) a = fmaxf(a, part[k][i][c]);
-        a /= 448.0f;
-        col[k][c] = a;
-        if (k < 2)
-            st_[mb * 2 * I + k * I + kb * kBlock + c] = a;
-        else
-            sh[mb * I + kb * kBlock + c] = a;
     }
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float a = col[k][c4 + j], r = 1.0f / a;
-            u32x2_t w;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                w[i] = encode4(v4f{d[k][4 * i][j], d[k][4 * i + 1][j], d[k][4 * i + 2][j], d[k][4 * i + 3][j]}, a, r);
-            st<u32x2_t>(&codes[c4 + j][r8], w);
-        }
-        __syncthreads();
         uint8_t* out = k < 2 ? qt + (k * I + kb * kBlock) * M : qh + kb * kBlock * M;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int piece = t + kTileThreads * i;          // 128 channels x 8 pieces of 16 rows
             const int c = piece >> 3, off = (piece & 7) * 16;
             if (mb * kBlock + off < M)                        // M % 16 == 0: whole pieces
-                st<u32x4>(out + c * M + mb * kBlock + off, ld<u32x4>(&codes[c][off]));
+                st<u32x4>(out + c * M + mb * kBlock + off, ld<u32x4>(&codes[k][code_word(c, off >> 2)]));
         }
     }
 }

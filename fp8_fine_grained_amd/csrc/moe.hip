@@ -2,7 +2,7 @@
 // (gfx950): the router's choice of experts and its gradient, the tokens' rows
 // quantized into the layouts the grouped GEMMs read, and the weighted sum that
 // brings the rows back, with its backward pass.
-#include "device_common.hpp"
+#include "elementwise.hpp"
 #include "launch.hpp"
 
 #include <math.h>
@@ -10,81 +10,6 @@
 namespace fp8fg {
 
 namespace moe_detail {
-
-// ---------------------------------------------------------------------------
-// Loads of N consecutive elements (the address 16-byte aligned) as fp32
-template <int N>
-__device__ __forceinline__ void load_n(const float* p, float (&v)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const v4f a = ld<v4f>(p + i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i + j] = a[j];
-    }
-}
-template <int N>
-__device__ __forceinline__ void load_n(const uint16_t* p, float (&v)[N]) {
-    if constexpr (N == 4) {
-        const u32x2_t a = ld<u32x2_t>(p);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            v[2 * j] = __uint_as_float(a[j] << 16);
-            v[2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 8) {
-            const u32x4 a = ld<u32x4>(p + i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[i + 2 * j] = __uint_as_float(a[j] << 16);
-                v[i + 2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
-            }
-        }
-    }
-}
-template <int N>
-__device__ __forceinline__ void store_n(float* p, const float (&v)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) st<v4f>(p + i, v4f{v[i], v[i + 1], v[i + 2], v[i + 3]});
-}
-template <int N>
-__device__ __forceinline__ void store_n(uint16_t* p, const float (&v)[N]) {
-    uint32_t w[N / 2];
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) w[i] = bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
-    if constexpr (N == 4) {
-        st<u32x2_t>(p, u32x2_t{w[0], w[1]});
-    } else {
-#pragma unroll
-        for (int i = 0; i < N / 2; i += 4) st<u32x4>(p + 2 * i, u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]});
-    }
-}
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = uint16_t(bf16_bits(v)); }
-
-// reductions over segments of L lanes (L a power of two), every lane gets the result
-template <int L>
-__device__ __forceinline__ uint32_t seg_max(uint32_t v) {
-#pragma unroll
-    for (int o = L / 2; o >= 1; o >>= 1) {
-        const uint32_t t = __shfl_xor(v, o, 64);
-        v = t > v ? t : v;
-    }
-    return v;
-}
-template <int L>
-__device__ __forceinline__ float seg_max(float v) {
-#pragma unroll
-    for (int o = L / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-    return v;
-}
-template <int L>
-__device__ __forceinline__ float seg_sum(float v) {
-#pragma unroll
-    for (int o = L / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
-}
 
 // ---------------------------------------------------------------------------
 // Routing.  s = sigmoid(x) or softmax(x) over the row, c = s + bias; a group
@@ -150,12 +75,12 @@ __global__ __launch_bounds__(256) void route(const T* __restrict__ x, const floa
         m = kNegInf;
 #pragma unroll
         for (int j = 0; j < V; ++j) m = fmaxf(m, v[j]);
-        m = seg_max<LPT>(m);
+        m = lanes_max<LPT>(m);
         if (m == kNegInf) m = 0.0f;
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) sum += expf(v[j] - m);
-        sum = seg_sum<LPT>(sum);
+        sum = lanes_sum<LPT>(sum);
         inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
     uint32_t key[V];
@@ -199,7 +124,7 @@ __global__ __launch_bounds__(256) void route(const T* __restrict__ x, const floa
         uint32_t best = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) best = key[j] > best ? key[j] : best;
-        const uint32_t top = seg_max<LPT>(best);
+        const uint32_t top = lanes_max<LPT>(best);
         uint64_t who = __builtin_amdgcn_ballot_w64(best == top && top != 0u);
         if (LPT < 64) who = (who >> seg0) & ((uint64_t(1) << (LPT & 63)) - 1);
         const int owner = who ? int(__builtin_ctzll(who)) : -1;
@@ -216,16 +141,16 @@ __global__ __launch_bounds__(256) void route(const T* __restrict__ x, const floa
     const float xs = mine >= 0 ? f32_of(row[mine]) : kNegInf;
     float wt;
     if (a.sigmoid) {
-        const float ms = a.renorm ? seg_max<LPT>(xs) : 0.0f;
+        const float ms = a.renorm ? lanes_max<LPT>(xs) : 0.0f;
         wt = mine >= 0 ? chosen_sigmoid(xs, ms) : 0.0f;
         if (a.renorm) {
-            const float sum = seg_sum<LPT>(wt);
+            const float sum = lanes_sum<LPT>(wt);
             wt = sum > 0.0f ? wt / sum : 0.0f;
         }
     } else if (a.renorm) {             // a softmax over the chosen alone: relative to their own maximum
-        const float ms = seg_max<LPT>(xs);
+        const float ms = lanes_max<LPT>(xs);
         wt = mine >= 0 ? expf(xs - ms) : 0.0f;
-        const float sum = seg_sum<LPT>(wt);
+        const float sum = lanes_sum<LPT>(wt);
         wt = sum > 0.0f ? wt / sum : 0.0f;
     } else {
         wt = mine >= 0 ? expf(xs - m) * inv : 0.0f;
@@ -261,12 +186,12 @@ __global__ __launch_bounds__(256) void route_backward(const T* __restrict__ x, c
         m = kNegInf;
 #pragma unroll
         for (int j = 0; j < V; ++j) m = fmaxf(m, v[j]);
-        m = seg_max<LPT>(m);
+        m = lanes_max<LPT>(m);
         if (m == kNegInf) m = 0.0f;
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) sum += expf(v[j] - m);
-        sum = seg_sum<LPT>(sum);
+        sum = lanes_sum<LPT>(sum);
         inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
     int mine = -1;
@@ -279,9 +204,9 @@ __global__ __launch_bounds__(256) void route_backward(const T* __restrict__ x, c
     const float xs = mine >= 0 ? f32_of(row[mine]) : kNegInf;
     float c = 0.0f, D = 0.0f;          // the chosen expert's own term; the sum over the chosen
     if (a.renorm) {
-        const float ms = seg_max<LPT>(xs);
+        const float ms = lanes_max<LPT>(xs);
         float p = mine < 0 ? 0.0f : a.sigmoid ? chosen_sigmoid(xs, ms) : expf(xs - ms);
-        const float sum = seg_sum<LPT>(p);
+        const float sum = lanes_sum<LPT>(p);
         p = sum > 0.0f ? p / sum : 0.0f;
         float d = 0.0f;
         for (int j = 0; j < a.topk; ++j) {
@@ -294,7 +219,7 @@ __global__ __launch_bounds__(256) void route_backward(const T* __restrict__ x, c
         c = mine >= 0 ? g * sigmoidf(xs) * sigmoidf(-xs) : 0.0f;
     } else {
         c = mine >= 0 ? g * (expf(xs - m) * inv) : 0.0f;
-        D = seg_sum<LPT>(c);
+        D = lanes_sum<LPT>(c);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = dense ? -(expf(v[j] - m) * inv) * D : 0.0f;
@@ -421,20 +346,6 @@ struct RowsOut {
     }
 };
 
-__device__ __forceinline__ u32x4 encode16(const float (&v)[kChan], float& sc) {
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kChan; ++i) amax = fmaxf(amax, fabsf(v[i]));
-#pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 64));
-    sc = amax / 448.0f;
-    const float rc = 1.0f / sc;
-    u32x4 c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = encode4(v4f{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}, sc, rc);
-    return c;
-}
-
 // zero rows [counts[g], padded count) of every expert: wave p = (expert, row)
 __device__ __forceinline__ void zero_padding(int64_t p, const int32_t* offsets, const int32_t* counts, int64_t R,
                                              const RowsOut& o, int lane) {
@@ -557,7 +468,7 @@ __global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ d
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         if (j >= topk) break;
-        dot[j] = seg_sum<64>(dot[j]);
+        dot[j] = lanes_sum<64>(dot[j]);
         if (lane == 0) part[wave][j] = dot[j];
     }
     __syncthreads();

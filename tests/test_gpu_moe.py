@@ -266,6 +266,32 @@ def test_dispatch_special_entries():
         fp8.fp8_moe_dispatch_contiguous(x, dev(idx), 4, M_total=128)
 
 
+def test_dispatch_encodes_every_rounding_boundary():
+    """Values within two FP32 steps of every boundary between E4M3 codes, at scales from subnormal to near
+    overflow, and signed zeros: codes and scales bit for bit."""
+    rng = np.random.default_rng(12)
+    m = np.concatenate([np.arange(0, 16) / 16 * 2.0 ** -6, *[2.0 ** e * (1 + np.arange(16) / 16) for e in range(-6, 9)]])
+    m = m[m < 448]                                         # codes and the midpoints between them
+    scales = np.concatenate([2.0 ** rng.uniform(-40, 40, 24), 2.0 ** rng.uniform(-135, -75, 12), 2.0 ** rng.uniform(75, 118, 12), [2.0 ** -149, 1.0]])
+    rows = []
+    for s in scales.astype(np.float32):
+        for shift in range(-2, 3):
+            v = (m * np.float64(s)).astype(np.float32)
+            v = (v.view(np.int32) + np.int32(shift) * (v > 0).astype(np.int32)).view(np.float32) * rng.choice([-1, 1], m.size).astype(np.float32)
+            v = np.concatenate([v, np.zeros(-m.size % 127, np.float32)]).reshape(-1, 127)
+            top = np.full((v.shape[0], 1), np.float32(448.0) * s, np.float32)
+            rows.append(np.concatenate([top, v], axis=1))
+    x = np.concatenate(rows).astype(np.float32)
+    x[::7, 5] = -0.0
+    x = x[np.all(np.isfinite(x), axis=1)]
+    T = x.shape[0]
+    q, s, row, off, cnt = fp8.fp8_moe_dispatch_contiguous(dev(x), dev(np.zeros((T, 1), np.int32)), 1)
+    eq, es = quant.quant_act_1x128(x)
+    bad = np.argwhere(host(q)[:T] != eq)
+    assert bad.size == 0, (len(bad), bad[:3].tolist(), x[tuple(bad[0])], es[0, bad[0][0]])
+    assert same_bits(host(s)[:, :T], es)
+
+
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("T,H,topk,R", [(1, 8, 1, 1), (7, 264, 3, 20), (65, 1040, 8, 512), (300, 512, 16, 700), (4, 7168, 8, 40)])
 def test_combine(T, H, topk, R, out):
