@@ -102,78 +102,75 @@ __device__ __forceinline__ T lanes_max(T v) { return lanes_reduce<L>(v, MaxOp())
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) { return lanes_reduce<L>(v, SumOp()); }
 
-// exp(x), for x up to 87 (beyond that it saturates near 2^126; below -87 it
-// reaches 0): 2^(x log2 e) with the product's low part put back, so that the
-// result is within about two roundings of exp(x).
-__device__ __forceinline__ float exp_fast(float x) {
-    constexpr float kHi = 0x1.715476p+0f, kLo = 0x1.4ae0c0p-26f;      // log2 e
-    const float t = fminf(x * kHi, 126.0f);
+// 1 / (1 + exp(-x)), within about two roundings.  exp is 2^(-x log2 e) with the
+// product's low part put back; the reciprocal's one Newton step takes the
+// place of an IEEE division.  x is clamped where the result is 1 to FP32's last bit,
+// or below FP32's smallest normal.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+    constexpr float kHi = -0x1.715476p+0f, kLo = -0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;      // -log2 e, ln 2
+    x = __builtin_amdgcn_fmed3f(x, -88.0f, 100.0f);
+    const float t = x * kHi;
     const float lo = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -t));
     const float e = __builtin_amdgcn_exp2f(t);
-    return __builtin_fmaf(e, fmaxf(fminf(lo, 1.0f), -1.0f) * 0x1.62e430p-1f, e);
-}
-
-// 1 / (1 + exp(-x)), within about two roundings: the reciprocal's one Newton
-// step takes the place of an IEEE division
-__device__ __forceinline__ float sigmoid_fast(float x) {
-    const float d = 1.0f + exp_fast(-x);
+    const float d = 1.0f + __builtin_fmaf(e, lo * kLn2, e);
     const float r = __builtin_amdgcn_rcpf(d);
     return __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);
 }
 
-// A quantization group: its scale s = RN32(amax / 448), and r for its
-// quotients: RN32(1 / s) for scales in [2^-80, 2^80].  Outside, -RN32(1 / (s k))
-// with the power of two k = far_factor(s) that brings s there; 0 for s == 0 (every
-// element so small that its code is a signed zero).
+// A quantization group: its scale s = RN32(amax / 448), and the ends lo, hi of
+// a bracket of its reciprocal, r (1 -+ 2^-21) with r = RN32(1 / s).  Scales
+// outside [2^-80, 2^80] get ends of opposite signs, which never agree; s == 0 (every
+// element so small that its code is a signed zero) gets 0 and 0.
 struct Group {
-    float s, r;
+    float s, lo, hi;
 };
+// the power of two that brings a far scale back, 1 for the others
 __device__ __forceinline__ float far_factor(float s) { return s < 0x1p-80f ? 0x1p64f : s > 0x1p80f ? 0x1p-64f : 1.0f; }
 __device__ __forceinline__ Group make_group(float amax) {
     Group g;
     g.s = amax / 448.0f;
-    const float k = far_factor(g.s);
-    g.r = 1.0f / (g.s * k);
-    if (k != 1.0f) g.r = g.s == 0.0f ? 0.0f : -g.r;
+    const float k = far_factor(g.s), r = 1.0f / (g.s * k);
+    g.lo = g.s == 0.0f ? 0.0f : r * (1.0f - 0x1p-21f);
+    g.hi = g.s == 0.0f ? 0.0f : r * (k != 1.0f ? -1.0f : 1.0f + 0x1p-21f);
     return g;
 }
 
 // Codes of RN32(x / s) for 4 N elements of a group, bit for bit as encode4
 // gives them.
 //
-// y = RN32(x * r) lies within 3 units in the last place of the quotient rounded
-// to FP32 (two roundings of 2^-24, and the quotient's own).  The values at which
-// E4M3 changes its code have at most five significant bits, so their FP32
-// patterns end in 19 zeros: where no y's pattern is within 4 of a multiple of
-// 2^19, y and the quotient have the same codes.  One shifted add per
-// element tells (the 19 low bits come to the top).  Otherwise (2^-16 of the
-// elements, and zeros) every quotient is formed: with r the rounded reciprocal of
-// t = s k, one remainder step makes y faithful and a second one correctly
+// The quotient rounded to FP32 lies between x lo and x hi (each end is 2^-21 away,
+// its own roundings and the quotient's together less than 2^-22), and rounding
+// to E4M3 is monotone: where both ends have the same code it is the quotient's.
+// That is two products and one conversion per element.  Otherwise (2^-16 of
+// the elements) every quotient is formed: with r the rounded reciprocal of
+// t = s k, one remainder step makes x r faithful and a second one correctly
 // rounded (Markstein's theorem on division by a correctly rounded
-// reciprocal; the remainders x k - y t are exact).
+// reciprocal; the remainders x k - y t are exact).  A zero's sign does not
+// survive the remainder and is put back.
 template <int N>
 __device__ __forceinline__ void encode_run(const float (&x)[4 * N], const Group& g, uint32_t (&code)[N]) {
-    float y[4 * N];
-    uint32_t near = ~0u;
+    uint32_t differ = 0;
 #pragma unroll
-    for (int i = 0; i < 4 * N; ++i) {
-        y[i] = x[i] * g.r;
-        const uint32_t t = (__float_as_uint(y[i]) + 4u) << 13;
-        near = t < near ? t : near;
+    for (int i = 0; i < N; ++i) {
+        code[i] = cvt4(x[4 * i] * g.lo, x[4 * i + 1] * g.lo, x[4 * i + 2] * g.lo, x[4 * i + 3] * g.lo);
+        differ |= code[i] ^ cvt4(x[4 * i] * g.hi, x[4 * i + 1] * g.hi, x[4 * i + 2] * g.hi, x[4 * i + 3] * g.hi);
     }
-    if (near < (9u << 13) || g.r < 0.0f) {
-        const float k = far_factor(g.s), t = g.s * k, r = fabsf(g.r);
+    if (differ) {
+        const float k = far_factor(g.s), t = g.s * k, r = 1.0f / t;
 #pragma unroll
-        for (int i = 0; i < 4 * N; ++i) {
-            const float xs = x[i] * k;
-            y[i] = xs * r;
-            y[i] = __builtin_fmaf(__builtin_fmaf(-y[i], t, xs), r, y[i]);
-            y[i] = __builtin_fmaf(__builtin_fmaf(-y[i], t, xs), r, y[i]);
-            y[i] = copysignf(y[i], x[i]);      // a zero's sign does not survive the remainder
+        for (int i = 0; i < N; ++i) {
+            float y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float xs = x[4 * i + j] * k;
+                y[j] = xs * r;
+                y[j] = __builtin_fmaf(__builtin_fmaf(-y[j], t, xs), r, y[j]);
+                y[j] = __builtin_fmaf(__builtin_fmaf(-y[j], t, xs), r, y[j]);
+                y[j] = copysignf(y[j], x[4 * i + j]);
+            }
+            code[i] = cvt4(y[0], y[1], y[2], y[3]);
         }
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) code[i] = cvt4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
 }
 
 // 16 consecutive values of a lane, eight lanes to a 128-group: the group's

@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
     const int32_t* __restrict__ rows, uint8_t* __restrict__ q, float* __restrict__ s, uint8_t* __restrict__ qt,
     float* __restrict__ st_, uint8_t* __restrict__ qh, float* __restrict__ sh) {
     __shared__ float part[8][3 * kBlock];
-    __shared__ __align__(16) float gs[3 * kBlock], gr[3 * kBlock];      // the channels' groups
+    __shared__ __align__(16) float gs[3 * kBlock], glo[3 * kBlock], ghi[3 * kBlock];      // the channels' groups
     __shared__ __align__(16) uint32_t codes[3][kBlock * kBlock / 4];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, c8 = (t & 15) * 8, r4 = (t >> 4) * 4;
     const int64_t nb = I / kBlock, kb = blockIdx.x, mb = blockIdx.y;
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
         const bool live = m0 + i < end;
         const int64_t m = live ? m0 + i : end - 1;     // rows past the end: loaded, then zero
         const u32x2_t wg = ld_once<u32x2_t>(qc + m * 2 * I + ch), wu = ld_once<u32x2_t>(qc + m * 2 * I + I + ch);
-        const float fg = sc[kb * M + m], fu = live ? sc[(nb + kb) * M + m] : 0.0f;
+        const float fg = live ? sc[kb * M + m] : 0.0f, fu = live ? sc[(nb + kb) * M + m] : 0.0f;
         float e[8];
         load_n<8, true>(dh + m * I + ch, e);
 #pragma unroll
@@ -99,10 +99,9 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
             for (int o = 0; o < 2; ++o) {
                 const int j = 2 * p + o;
                 const float g = g2[o] * fg, u = u2[o] * fu;
-                const float dhj = live ? e[j] : 0.0f;
                 const float sg = sigmoid_fast(g), si = g * sg;
-                d[0][i][j] = dhj * u * (sg * __builtin_fmaf(g, 1.0f - sg, 1.0f));
-                d[1][i][j] = dhj * si;
+                d[0][i][j] = e[j] * u * (sg * __builtin_fmaf(g, 1.0f - sg, 1.0f));
+                d[1][i][j] = e[j] * si;
                 d[2][i][j] = si * u;
             }
         }
@@ -138,7 +137,8 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
         for (int i = 0; i < 8; ++i) a = fmaxf(a, part[i][t]);
         const Group g = make_group(a);
         gs[t] = a = g.s;
-        gr[t] = g.r;
+        glo[t] = g.lo;
+        ghi[t] = g.hi;
         if (t < 2 * kBlock)
             st_[mb * 2 * I + (t >> 7) * I + kb * kBlock + (t & 127)] = a;
         else
@@ -175,14 +175,15 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
     // along the rows
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        float r[8];
-        load_n<8>(gr + k * kBlock + c8, r);
+        float lo[8], hi[8];
+        load_n<8>(glo + k * kBlock + c8, lo);
+        load_n<8>(ghi + k * kBlock + c8, hi);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = c8 + j;
             const float x[4] = {d[k][0][j], d[k][1][j], d[k][2][j], d[k][3][j]};
             uint32_t w[1];
-            encode_run<1>(x, Group{gs[k * kBlock + c], r[j]}, w);
+            encode_run<1>(x, Group{gs[k * kBlock + c], lo[j], hi[j]}, w);
             codes[k][code_word(c, r4 >> 2)] = w[0];
             if (j & 1) __builtin_amdgcn_sched_barrier(0);
         }
