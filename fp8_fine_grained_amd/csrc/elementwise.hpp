@@ -117,73 +117,126 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
     return __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);
 }
 
-// A quantization group: its scale s = RN32(amax / 448), and the ends lo, hi of
-// a bracket of its reciprocal, r (1 -+ 2^-21) with r = RN32(1 / s).  Scales
-// outside [2^-80, 2^80] get ends of opposite signs, which never agree; s == 0 (every
-// element so small that its code is a signed zero) gets 0 and 0.
-struct Group {
-    float s, lo, hi;
-};
-// the power of two that brings a far scale back, 1 for the others
-__device__ __forceinline__ float far_factor(float s) { return s < 0x1p-80f ? 0x1p64f : s > 0x1p80f ? 0x1p-64f : 1.0f; }
-__device__ __forceinline__ Group make_group(float amax) {
-    Group g;
-    g.s = amax / 448.0f;
-    const float k = far_factor(g.s), r = 1.0f / (g.s * k);
-    g.lo = g.s == 0.0f ? 0.0f : r * (1.0f - 0x1p-21f);
-    g.hi = g.s == 0.0f ? 0.0f : r * (k != 1.0f ? -1.0f : 1.0f + 0x1p-21f);
-    return g;
+// RN32(a / 448): the product with RN32(1 / 448) corrected once by its exact
+// remainder.  A normal a / 448 is never within 1/896 of a last place of the middle
+// between two floats (448 = 7 * 64), far more than the corrected value's
+// error; subnormal ones can be exact ties and are divided.
+__device__ __forceinline__ float scale_of(float a) {
+    if (a < 0x1p-116f) return a / 448.0f;
+    const float y = a * (1.0f / 448.0f);
+    return __builtin_fmaf(__builtin_fmaf(-448.0f, y, a), 1.0f / 448.0f, y);
 }
 
-// Codes of RN32(x / s) for 4 N elements of a group, bit for bit as encode4
-// gives them.
-//
-// The quotient rounded to FP32 lies between x lo and x hi (each end is 2^-21 away,
-// its own roundings and the quotient's together less than 2^-22), and rounding
-// to E4M3 is monotone: where both ends have the same code it is the quotient's.
-// That is two products and one conversion per element.  Otherwise (2^-16 of
-// the elements) every quotient is formed: with r the rounded reciprocal of
-// t = s k, one remainder step makes x r faithful and a second one correctly
-// rounded (Markstein's theorem on division by a correctly rounded
-// reciprocal; the remainders x k - y t are exact).  A zero's sign does not
-// survive the remainder and is put back.
+// Scales outside [2^-80, 2^80) (0 among them) and the power of two that brings
+// a far one near: quotients by far scales are formed from scaled operands
+__device__ __forceinline__ bool far_scale(float s) { return __float_as_uint(s) - 0x17800000u >= 0x50000000u; }
+__device__ __forceinline__ float far_factor(float s) { return s < 1.0f ? 0x1p64f : 0x1p-64f; }
+
+// E4M3 codes of RN32(x / s) for 4 N elements of a group, by exact quotients: with
+// r the rounded reciprocal of s (of s k, and x k, for a far scale), one remainder step
+// makes x r faithful and a second one correctly rounded (Markstein's theorem on
+// division by a correctly rounded reciprocal; the remainders are exact).  A
+// zero's sign does not survive the remainder and is put back.  A subnormal scale
+// can be a third below amax / 448: the quotient saturates.
 template <int N>
-__device__ __forceinline__ void encode_run(const float (&x)[4 * N], const Group& g, uint32_t (&code)[N]) {
-    uint32_t differ = 0;
+__device__ __forceinline__ void encode_exact(const float (&x)[4 * N], float s, uint32_t (&code)[N]) {
+    const float k = far_scale(s) ? far_factor(s) : 1.0f, t = s * k, r = s == 0.0f ? 0.0f : 1.0f / t;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        code[i] = cvt4(x[4 * i] * g.lo, x[4 * i + 1] * g.lo, x[4 * i + 2] * g.lo, x[4 * i + 3] * g.lo);
-        differ |= code[i] ^ cvt4(x[4 * i] * g.hi, x[4 * i + 1] * g.hi, x[4 * i + 2] * g.hi, x[4 * i + 3] * g.hi);
-    }
-    if (differ) {
-        const float k = far_factor(g.s), t = g.s * k, r = 1.0f / t;
+        float y[4];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float xs = x[4 * i + j] * k;
-                y[j] = xs * r;
-                y[j] = __builtin_fmaf(__builtin_fmaf(-y[j], t, xs), r, y[j]);
-                y[j] = __builtin_fmaf(__builtin_fmaf(-y[j], t, xs), r, y[j]);
-                y[j] = copysignf(y[j], x[4 * i + j]);
-            }
-            code[i] = cvt4(y[0], y[1], y[2], y[3]);
+        for (int j = 0; j < 4; ++j) {
+            const float xs = x[4 * i + j] * k;
+            y[j] = xs * r;
+            y[j] = __builtin_fmaf(__builtin_fmaf(-y[j], t, xs), r, y[j]);
+            y[j] = __builtin_fmaf(__builtin_fmaf(-y[j], t, xs), r, y[j]);
+            y[j] = copysignf(fminf(fabsf(y[j]), 448.0f), x[4 * i + j]);
         }
+        code[i] = cvt4(y[0], y[1], y[2], y[3]);
     }
 }
 
+// The codes of a group's elements, bit for bit as encode4 gives them.  FP32
+// elements: a bracket [lo, hi] = r (1 -+ 2^-21) of the reciprocal.  RN32(x / s)
+// lies between x lo and x hi (the roundings of r, of the products and of the quotient
+// are together less than 2^-22), and rounding to E4M3 is monotone: where both
+// ends have the same code it is the quotient's.  That is two products
+// and one conversion per element; the others (2^-16 of them, exact ties
+// above all) take encode_exact.  Far scales get ends of opposite signs, which never
+// agree.
+struct Bracket {
+    float s, lo, hi;
+    __device__ __forceinline__ explicit Bracket(float amax) : s(scale_of(amax)) {
+        const float r = __builtin_amdgcn_rcpf(s);
+        const bool far = far_scale(s);
+        lo = far ? 1.0f : r * (1.0f - 0x1p-21f);
+        hi = far ? -1.0f : r * (1.0f + 0x1p-21f);
+    }
+    __device__ __forceinline__ Bracket(float s_, float lo_, float hi_) : s(s_), lo(lo_), hi(hi_) {}
+    template <int N>
+    __device__ __forceinline__ void encode(const float (&x)[4 * N], uint32_t (&code)[N]) const {
+        uint32_t differ = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            code[i] = cvt4(x[4 * i] * lo, x[4 * i + 1] * lo, x[4 * i + 2] * lo, x[4 * i + 3] * lo);
+            differ |= code[i] ^ cvt4(x[4 * i] * hi, x[4 * i + 1] * hi, x[4 * i + 2] * hi, x[4 * i + 3] * hi);
+        }
+        if (differ) encode_exact<N>(x, s, code);
+    }
+};
+
+// BF16 elements: exact ties between codes are common (ratios of 8-bit numbers:
+// every seventh maximum makes one element in sixteen a tie), so a branch on them
+// would be taken by most waves.  The quotient itself is formed instead, from the
+// reciprocal in two parts r + rl, r below 1 / s so that a zero keeps its sign:
+// x rl + x r, one rounding, is within 2^-40 of x / s before it.  That decides
+// the code: x = X 2^i and s = RN32(A 2^j / 448) with 8-bit X and A put x / s at
+// least 2^-32 away from the middle of a code boundary and its FP32 neighbour, where
+// RN32 would turn (the low bits of A / 7 repeat 001, 010 or 100, or are zero).
+struct Ratio {
+    float s, r, rl;
+    __device__ __forceinline__ explicit Ratio(float amax) : s(scale_of(amax)) {
+        r = __builtin_amdgcn_rcpf(s);
+        r = __builtin_fmaf(r, -0x1p-22f, r);
+        rl = r * __builtin_fmaf(-s, r, 1.0f);
+    }
+    template <int N>
+    __device__ __forceinline__ void encode(const float (&x)[4 * N], uint32_t (&code)[N]) const {
+        if (far_scale(s)) {
+            encode_exact<N>(x, s, code);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = __builtin_fmaf(x[4 * i + j], r, x[4 * i + j] * rl);
+                code[i] = cvt4(y[0], y[1], y[2], y[3]);
+            }
+        }
+    }
+};
+
 // 16 consecutive values of a lane, eight lanes to a 128-group: the group's
-// scale and the lane's codes
+// scale and the lane's codes (G: Bracket, or Ratio for values that are BF16)
+template <class G>
 __device__ __forceinline__ u32x4 encode16(const float (&v)[16], float& sc) {
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
-    const Group g = make_group(lanes_max<8>(amax));
+    const G g(lanes_max<8>(amax));
     sc = g.s;
     uint32_t c[4];
-    encode_run<4>(v, g, c);
+    g.template encode<4>(v, c);
     return u32x4{c[0], c[1], c[2], c[3]};
 }
+// the encoding of values read as T
+template <class T>
+struct encoder_of {
+    typedef Bracket type;
+};
+template <>
+struct encoder_of<uint16_t> {
+    typedef Ratio type;
+};
 
 }  // namespace fp8fg

@@ -14,35 +14,37 @@ namespace gate_detail {
 
 // A workgroup takes 32 rows of one 128-channel group: eight lanes per row.
 // Row r of buffer blockIdx.z exists when r < rows[blockIdx.z] (rows may be
-// null: all of them).
+// null: all of them).  Offsets within the 32 rows fit 32 bits.
 template <class T>
 __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t M, int64_t I,
                                               const int32_t* __restrict__ rows, uint8_t* __restrict__ q,
                                               float* __restrict__ s, uint8_t* __restrict__ qc, float* __restrict__ sc) {
+    typedef typename encoder_of<T>::type Enc;
     const int64_t b = blockIdx.z, kb = blockIdx.x, nb = I / kBlock;
     int64_t end = rows ? int64_t(rows[b]) : M;
     end = end < M ? end : M;
-    const int64_t ch = kb * kBlock + (threadIdx.x & 7) * 16;
-    for (int64_t m = int64_t(blockIdx.y) * 32 + (threadIdx.x >> 3); m < end; m += int64_t(gridDim.y) * 32) {
-        const T* row = gu + (b * M + m) * 2 * I + ch;
+    const uint32_t r = threadIdx.x >> 3, c16 = (threadIdx.x & 7) * 16, in = r * uint32_t(I) + c16;
+    for (int64_t m0 = int64_t(blockIdx.y) * 32; m0 < end; m0 += int64_t(gridDim.y) * 32) {
+        if (m0 + r >= end) return;
+        const T* row = gu + (b * M + m0) * 2 * I + kb * kBlock;
         float g[16], u[16], h[16];
-        load_n<16, true>(row, g);
-        load_n<16, true>(row + I, u);
+        load_n<16, true>(row + (in + r * uint32_t(I)), g);
+        load_n<16, true>(row + I + (in + r * uint32_t(I)), u);
 #pragma unroll
         for (int i = 0; i < 16; ++i) h[i] = g[i] * sigmoid_fast(g[i]) * u[i];
         float a;
-        const u32x4 ch_code = encode16(h, a);
-        st<u32x4>(q + (b * M + m) * I + ch, ch_code);
-        if ((threadIdx.x & 7) == 0) s[(b * nb + kb) * M + m] = a;
+        const u32x4 codes = encode16<Bracket>(h, a);
+        st<u32x4>(q + (b * M + m0) * I + kb * kBlock + in, codes);
+        if (c16 == 0) s[(b * nb + kb) * M + m0 + r] = a;
         if (qc) {
             float sg, su;
-            const u32x4 cg = encode16(g, sg), cu = encode16(u, su);
-            uint8_t* c = qc + (b * M + m) * 2 * I + ch;
-            st<u32x4>(c, cg);
-            st<u32x4>(c + I, cu);
-            if ((threadIdx.x & 7) == 0) {
-                sc[(b * 2 * nb + kb) * M + m] = sg;
-                sc[(b * 2 * nb + nb + kb) * M + m] = su;
+            const u32x4 cg = encode16<Enc>(g, sg), cu = encode16<Enc>(u, su);
+            uint8_t* c = qc + (b * M + m0) * 2 * I + kb * kBlock;
+            st<u32x4>(c + (in + r * uint32_t(I)), cg);
+            st<u32x4>(c + I + (in + r * uint32_t(I)), cu);
+            if (c16 == 0) {
+                sc[(b * 2 * nb + kb) * M + m0 + r] = sg;
+                sc[(b * 2 * nb + nb + kb) * M + m0 + r] = su;
             }
         }
     }
@@ -135,7 +137,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
         float a = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) a = fmaxf(a, part[i][t]);
-        const Group g = make_group(a);
+        const Bracket g(a);
         gs[t] = a = g.s;
         glo[t] = g.lo;
         ghi[t] = g.hi;
@@ -153,10 +155,10 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
             a[i] = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) a[i] = fmaxf(a[i], fabsf(d[k][i][j]));
-            const Group g = make_group(lanes_max<16>(a[i]));
+            const Bracket g(lanes_max<16>(a[i]));
             a[i] = g.s;
             uint32_t w[2];
-            encode_run<2>(d[k][i], g, w);
+            g.encode<2>(d[k][i], w);
             if (m0 + i < end) st<u32x2_t>(q + (m0 + i) * 2 * I + k * I + ch, u32x2_t{w[0], w[1]});
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -183,7 +185,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
             const int c = c8 + j;
             const float x[4] = {d[k][0][j], d[k][1][j], d[k][2][j], d[k][3][j]};
             uint32_t w[1];
-            encode_run<1>(x, Group{gs[k * kBlock + c], lo[j], hi[j]}, w);
+            Bracket(gs[k * kBlock + c], lo[j], hi[j]).encode<1>(x, w);
             codes[k][code_word(c, r4 >> 2)] = w[0];
             if (j & 1) __builtin_amdgcn_sched_barrier(0);
         }

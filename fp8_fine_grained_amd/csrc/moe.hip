@@ -373,7 +373,7 @@ __global__ __launch_bounds__(256) void dispatch_rows(const T* __restrict__ x, co
     for (int i = 0; i < kChan; ++i) v[i] = 0.0f;
     if (ch < o.H) load_n<kChan>(x + token * o.H + ch, v);
     float sc;
-    const u32x4 code = encode16(v, sc);
+    const u32x4 code = encode16<typename encoder_of<T>::type>(v, sc);
     const int32_t* rows = row_of + token * topk;
     for (int j = 0; j < topk; ++j) {
         const int64_t r = rows[j];
@@ -446,7 +446,7 @@ __global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ d
         for (int i = 0; i < kChan; ++i) v[i] = 0.0f;
         if (ch < o.H) load_n<kChan>(dout + token * o.H + ch, v);
         float sc;
-        const u32x4 code = encode16(v, sc);
+        const u32x4 code = encode16<typename encoder_of<TD>::type>(v, sc);
         const int64_t kb = c * 8 + (lane >> 3);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {

@@ -292,6 +292,43 @@ def test_dispatch_encodes_every_rounding_boundary():
     assert same_bits(host(s)[:, :T], es)
 
 
+def test_dispatch_encodes_every_bf16_ratio():
+    """BF16 activations: every 8-bit significand against every 8-bit maximum, over E4M3's range and below it."""
+    rows = []
+    m = np.arange(128, 256, dtype=np.float32)
+    for e in range(0, 20):
+        v = m * np.float32(2.0 ** -e)
+        for part in (v[:64], v[64:]):
+            for a in m:
+                rows.append(np.concatenate([[a if e else 255.0], part * np.where(np.arange(64) % 2, -1, 1), np.zeros(63)]))
+    x = np.array(rows, np.float32) * 2.0 ** -7
+    x[5, 70], x[6, 71] = -0.0, np.float32(-2.0 ** -120)
+    x[100:200] *= np.float32(2.0 ** -100)                   # scales below 2^-80, and above 2^80
+    x[300:400] *= np.float32(2.0 ** 100)
+    T = x.shape[0]
+    t, vals = rounded(x, True)
+    assert np.array_equal(vals, x)
+    q, s, row, off, cnt = fp8.fp8_moe_dispatch_contiguous(t, dev(np.zeros((T, 1), np.int32)), 1)
+    eq, es = quant.quant_act_1x128(x)
+    assert np.array_equal(host(q)[:T], eq) and same_bits(host(s)[:, :T], es)
+
+
+def test_dispatch_scales_of_every_kind():
+    """Scales RN32(amax / 448) from subnormal maxima to the largest."""
+    rng = np.random.default_rng(15)
+    bits = np.concatenate([rng.integers(1, 0x7F800000, 20000), rng.integers(1, 0x04000000, 4000), np.arange(1, 2000),
+                           0x3F800000 + 1198 * np.arange(7000)]).astype(np.uint32)
+    x = np.zeros((bits.size, 16), np.float32)
+    x[:, 3] = bits.view(np.float32)
+    x[:, 7] = -x[:, 3] * np.float32(0.37)
+    T = x.shape[0]
+    q, s, row, off, cnt = fp8.fp8_moe_dispatch_contiguous(dev(x), dev(np.zeros((T, 1), np.int32)), 1)
+    eq, es = quant.quant_act_1x128(x)
+    assert same_bits(host(s)[:, :T], es)
+    bad = np.argwhere(host(q)[:T] != eq)
+    assert bad.size == 0, (len(bad), bad[:3].tolist(), x[bad[0][0], [3, 7]], host(q)[bad[0][0]], eq[bad[0][0]])
+
+
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("T,H,topk,R", [(1, 8, 1, 1), (7, 264, 3, 20), (65, 1040, 8, 512), (300, 512, 16, 700), (4, 7168, 8, 40)])
 def test_combine(T, H, topk, R, out):
