@@ -508,8 +508,8 @@ int fp8_swiglu(const void* gu, int gu_bf16, int64_t G, int64_t M, int64_t I, con
     if (G < 0 || M < 0 || I < 0 || I % 128 != 0) return FP8FG_ERR_SHAPE;
     if (!aligned16(gu) || !aligned16(q) || !aligned16(s) || !aligned16(qc) || !aligned16(sc) || !aligned4(rows))
         return FP8FG_ERR_ALIGN;
-    // the kernel's offsets within 32 rows fit 32 bits
-    if (!flag(gu_bf16) || G > 65535 || M > kMaxDim || I > (int64_t(1) << 25)) return FP8FG_ERR_UNSUPPORTED;
+    // the kernels' offsets within a tile fit 32 bits
+    if (!flag(gu_bf16) || G > 65535 || M > kMaxDim || I > (int64_t(1) << 23)) return FP8FG_ERR_UNSUPPORTED;
     if (G == 0 || M == 0 || I == 0) return FP8FG_OK;
     if (M > kMaxElems / (2 * I) / G) return FP8FG_ERR_UNSUPPORTED;
     return hip_status(fp8fg::launch_swiglu(gu, gu_bf16, G, M, I, rows, q, s, qc, sc, static_cast<hipStream_t>(stream)));
@@ -523,7 +523,7 @@ int fp8_swiglu_backward(const uint8_t* qc, const float* sc, const void* dh, int 
     if (!aligned16(qc) || !aligned16(sc) || !aligned16(dh) || !aligned16(q) || !aligned16(s) || !aligned16(qt) ||
         !aligned16(st) || !aligned16(qh) || !aligned16(sh) || !aligned4(rows))
         return FP8FG_ERR_ALIGN;
-    if (!flag(dh_bf16) || M > int64_t(128) * 65535 || I > (int64_t(1) << 25)) return FP8FG_ERR_UNSUPPORTED;
+    if (!flag(dh_bf16) || M > int64_t(128) * 65535 || I > (int64_t(1) << 23)) return FP8FG_ERR_UNSUPPORTED;
     if (M == 0 || I == 0) return FP8FG_OK;
     if (M > kMaxElems / (2 * I)) return FP8FG_ERR_UNSUPPORTED;
     return hip_status(fp8fg::launch_swiglu_backward(qc, sc, dh, dh_bf16, M, I, rows, q, s, qt, st, qh, sh,

@@ -117,12 +117,18 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
     return __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);
 }
 
-// RN32(a / 448): the product with RN32(1 / 448) corrected once by its exact
-// remainder.  A normal a / 448 is never within 1/896 of a last place of the middle
-// between two floats (448 = 7 * 64), far more than the corrected value's
-// error; subnormal ones can be exact ties and are divided.
-__device__ __forceinline__ float scale_of(float a) {
-    if (a < 0x1p-116f) return a / 448.0f;
+// cvt4 without clearing its result first: the conversion of a pair keeps the
+// other half of its destination, which the second pair then overwrites
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, __builtin_bit_cast(int, a), false);
+    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
+}
+
+// RN32(a / 448) for results from 2^-80 on: the product with RN32(1 / 448)
+// corrected once by its exact remainder.  a / 448 is never within 1/896 of a last
+// place of the middle between two normal floats (448 = 7 * 64), far more than
+// the corrected value's error.  (Subnormal results can be exact ties.)
+__device__ __forceinline__ float scale_near(float a) {
     const float y = a * (1.0f / 448.0f);
     return __builtin_fmaf(__builtin_fmaf(-448.0f, y, a), 1.0f / 448.0f, y);
 }
@@ -166,11 +172,15 @@ __device__ __forceinline__ void encode_exact(const float (&x)[4 * N], float s, u
 // agree.
 struct Bracket {
     float s, lo, hi;
-    __device__ __forceinline__ explicit Bracket(float amax) : s(scale_of(amax)) {
+    __device__ __forceinline__ explicit Bracket(float amax) : s(scale_near(amax)) {
         const float r = __builtin_amdgcn_rcpf(s);
-        const bool far = far_scale(s);
-        lo = far ? 1.0f : r * (1.0f - 0x1p-21f);
-        hi = far ? -1.0f : r * (1.0f + 0x1p-21f);
+        lo = r * (1.0f - 0x1p-21f);
+        hi = r * (1.0f + 0x1p-21f);
+        if (far_scale(s)) {
+            s = amax / 448.0f;
+            lo = 1.0f;
+            hi = -1.0f;
+        }
     }
     __device__ __forceinline__ Bracket(float s_, float lo_, float hi_) : s(s_), lo(lo_), hi(hi_) {}
     template <int N>
@@ -178,8 +188,8 @@ struct Bracket {
         uint32_t differ = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            code[i] = cvt4(x[4 * i] * lo, x[4 * i + 1] * lo, x[4 * i + 2] * lo, x[4 * i + 3] * lo);
-            differ |= code[i] ^ cvt4(x[4 * i] * hi, x[4 * i + 1] * hi, x[4 * i + 2] * hi, x[4 * i + 3] * hi);
+            code[i] = codes4(x[4 * i] * lo, x[4 * i + 1] * lo, x[4 * i + 2] * lo, x[4 * i + 3] * lo);
+            differ |= code[i] ^ codes4(x[4 * i] * hi, x[4 * i + 1] * hi, x[4 * i + 2] * hi, x[4 * i + 3] * hi);
         }
         if (differ) encode_exact<N>(x, s, code);
     }
@@ -195,10 +205,11 @@ struct Bracket {
 // RN32 would turn (the low bits of A / 7 repeat 001, 010 or 100, or are zero).
 struct Ratio {
     float s, r, rl;
-    __device__ __forceinline__ explicit Ratio(float amax) : s(scale_of(amax)) {
+    __device__ __forceinline__ explicit Ratio(float amax) : s(scale_near(amax)) {
         r = __builtin_amdgcn_rcpf(s);
         r = __builtin_fmaf(r, -0x1p-22f, r);
         rl = r * __builtin_fmaf(-s, r, 1.0f);
+        if (far_scale(s)) s = amax / 448.0f;
     }
     template <int N>
     __device__ __forceinline__ void encode(const float (&x)[4 * N], uint32_t (&code)[N]) const {
@@ -210,7 +221,7 @@ struct Ratio {
                 float y[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[j] = __builtin_fmaf(x[4 * i + j], r, x[4 * i + j] * rl);
-                code[i] = cvt4(y[0], y[1], y[2], y[3]);
+                code[i] = codes4(y[0], y[1], y[2], y[3]);
             }
         }
     }

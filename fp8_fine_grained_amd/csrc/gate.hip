@@ -61,12 +61,24 @@ __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t 
 // LDS so that whole 128-byte row segments are written.
 constexpr int kTileThreads = 512;
 
-// the word of rows 4 row4 .. + 3 of channel ch in a tile of transposed codes:
-// 16-byte pieces swapped by channel run, and odd and even channels by halves,
-// so that a wave's stores (16 channel runs x 4 words) meet 64 different banks
-__device__ __forceinline__ int code_word(int ch, int row4) {
+// The transposed codes of a tile in LDS: word row4 of channel ch (rows 4 row4
+// .. + 3), the 16-byte pieces of a channel swapped by channel run and odd and even
+// channels by halves, so that a wave's stores (16 channel runs x 4 words) meet
+// 64 different banks
+__device__ __forceinline__ uint32_t code_word(uint32_t ch, uint32_t row4) {
     return (ch ^ ((ch >> 6) & 1)) * 32 + (((row4 >> 2) ^ ((ch >> 3) & 7)) << 2) + (row4 & 3);
 }
+
+template <class T>
+struct GateRow {                   // a thread's eight channels of a row, as loaded
+    u32x2_t g, u;
+    u32x4 dh[sizeof(T) == 4 ? 2 : 1];
+    float sg, su;
+};
+__device__ __forceinline__ float dh_of(const u32x4 (&w)[1], int j) {
+    return __uint_as_float((j & 1) ? w[0][j >> 1] & 0xFFFF0000u : w[0][j >> 1] << 16);
+}
+__device__ __forceinline__ float dh_of(const u32x4 (&w)[2], int j) { return __uint_as_float(w[j >> 2][j & 3]); }
 
 template <class T>
 __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
@@ -76,34 +88,61 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
     __shared__ float part[8][3 * kBlock];
     __shared__ __align__(16) float gs[3 * kBlock], glo[3 * kBlock], ghi[3 * kBlock];      // the channels' groups
     __shared__ __align__(16) uint32_t codes[3][kBlock * kBlock / 4];
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, c8 = (t & 15) * 8, r4 = (t >> 4) * 4;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const uint32_t c8 = (t & 15) * 8, r4 = (t >> 4) * 4;
     const int64_t nb = I / kBlock, kb = blockIdx.x, mb = blockIdx.y;
     int64_t end = rows ? int64_t(rows[0]) : M;
     end = end < M ? end : M;
     if (mb * kBlock >= end) return;
-    const int64_t ch = kb * kBlock + c8, m0 = mb * kBlock + r4;
+    const bool full = (mb + 1) * kBlock <= end;    // uniform: every row of the tile exists
+    const int64_t m0 = mb * kBlock + r4;
+    // offsets within the tile fit 32 bits (I <= 2^23)
+    const uint8_t* qg = qc + mb * kBlock * 2 * I + kb * kBlock;
+    const uint8_t* pd = reinterpret_cast<const uint8_t*>(dh + mb * kBlock * I + kb * kBlock);
+    const float* sg_ = sc + kb * M + mb * kBlock;
+    const float* su_ = sc + (nb + kb) * M + mb * kBlock;
+    GateRow<T> in[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // a row past the end: the tile's first row, with zeros in the place of its codes and dh
+        const bool live = full || m0 + i < end;
+        const uint32_t r = live ? r4 : 0u;
+        const int64_t step = full ? i : 0;
+        const uint32_t ri = full ? r : (live ? r + i : 0u);
+        const uint32_t oc = ri * uint32_t(2 * I) + c8, od = (ri * uint32_t(I) + c8) * uint32_t(sizeof(T));
+        in[i].g = ld_once<u32x2_t>(qg + step * 2 * I + oc);
+        in[i].u = ld_once<u32x2_t>(qg + step * 2 * I + I + oc);
+#pragma unroll
+        for (int p = 0; p < int(sizeof(in[i].dh) / 16); ++p) in[i].dh[p] = ld_once<u32x4>(pd + step * I * sizeof(T) + od + 16 * p);
+        in[i].sg = sg_[step + ri];
+        in[i].su = su_[step + ri];
+    }
+    if (!full) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (m0 + i >= end) {
+                in[i].g = in[i].u = u32x2_t{0u, 0u};
+#pragma unroll
+                for (int p = 0; p < int(sizeof(in[i].dh) / 16); ++p) in[i].dh[p] = u32x4{0u, 0u, 0u, 0u};
+                in[i].sg = in[i].su = 0.0f;
+            }
+    }
     float d[3][4][8];              // dg, du, h
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const bool live = m0 + i < end;
-        const int64_t m = live ? m0 + i : end - 1;     // rows past the end: loaded, then zero
-        const u32x2_t wg = ld_once<u32x2_t>(qc + m * 2 * I + ch), wu = ld_once<u32x2_t>(qc + m * 2 * I + I + ch);
-        const float fg = live ? sc[kb * M + m] : 0.0f, fu = live ? sc[(nb + kb) * M + m] : 0.0f;
-        float e[8];
-        load_n<8, true>(dh + m * I + ch, e);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const v2f g2 = (p & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wg[p >> 1], 1.0f, true)
-                                   : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wg[p >> 1], 1.0f, false);
-            const v2f u2 = (p & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wu[p >> 1], 1.0f, true)
-                                   : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(wu[p >> 1], 1.0f, false);
+            const v2f g2 = (p & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(in[i].g[p >> 1], 1.0f, true)
+                                   : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(in[i].g[p >> 1], 1.0f, false);
+            const v2f u2 = (p & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(in[i].u[p >> 1], 1.0f, true)
+                                   : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(in[i].u[p >> 1], 1.0f, false);
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
                 const int j = 2 * p + o;
-                const float g = g2[o] * fg, u = u2[o] * fu;
+                const float g = g2[o] * in[i].sg, u = u2[o] * in[i].su, e = dh_of(in[i].dh, j);
                 const float sg = sigmoid_fast(g), si = g * sg;
-                d[0][i][j] = e[j] * u * (sg * __builtin_fmaf(g, 1.0f - sg, 1.0f));
-                d[1][i][j] = e[j] * si;
+                d[0][i][j] = e * u * __builtin_fmaf(si, 1.0f - sg, sg);      // sg (1 + g (1 - sg))
+                d[1][i][j] = e * si;
                 d[2][i][j] = si * u;
             }
         }
@@ -149,6 +188,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
     // along the channels
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
+        uint8_t* out = q + mb * kBlock * 2 * I + k * I + kb * kBlock;
         float a[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -159,7 +199,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
             a[i] = g.s;
             uint32_t w[2];
             g.encode<2>(d[k][i], w);
-            if (m0 + i < end) st<u32x2_t>(q + (m0 + i) * 2 * I + k * I + ch, u32x2_t{w[0], w[1]});
+            if (full || m0 + i < end) st<u32x2_t>(out + i * 2 * I + (r4 * uint32_t(2 * I) + c8), u32x2_t{w[0], w[1]});
             __builtin_amdgcn_sched_barrier(0);
         }
         if (c8 == 0) {
@@ -175,6 +215,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
     }
     __syncthreads();
     // along the rows
+    const uint32_t even = code_word(c8, r4 >> 2), odd = code_word(c8 + 1, r4 >> 2);    // channels c8 + 2 i are 64 words apart
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         float lo[8], hi[8];
@@ -182,24 +223,23 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
         load_n<8>(ghi + k * kBlock + c8, hi);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = c8 + j;
             const float x[4] = {d[k][0][j], d[k][1][j], d[k][2][j], d[k][3][j]};
             uint32_t w[1];
-            Bracket(gs[k * kBlock + c], lo[j], hi[j]).encode<1>(x, w);
-            codes[k][code_word(c, r4 >> 2)] = w[0];
+            Bracket(gs[k * kBlock + c8 + j], lo[j], hi[j]).encode<1>(x, w);
+            codes[k][((j & 1) ? odd : even) + (j >> 1) * 64] = w[0];
             if (j & 1) __builtin_amdgcn_sched_barrier(0);
         }
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        uint8_t* out = k < 2 ? qt + (k * I + kb * kBlock) * M : qh + kb * kBlock * M;
+        uint8_t* out = (k < 2 ? qt + (k * I + kb * kBlock) * M : qh + kb * kBlock * M) + mb * kBlock;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int piece = t + kTileThreads * i;          // 128 channels x 8 pieces of 16 rows
-            const int c = piece >> 3, off = (piece & 7) * 16;
-            if (mb * kBlock + off < M)                        // M % 16 == 0: whole pieces
-                st<u32x4>(out + c * M + mb * kBlock + off, ld<u32x4>(&codes[k][code_word(c, off >> 2)]));
+            const uint32_t piece = t + kTileThreads * i;          // 128 channels x 8 pieces of 16 rows
+            const uint32_t c = piece >> 3, off = (piece & 7) * 16;
+            if (full || mb * kBlock + off < M)                     // M % 16 == 0: whole pieces
+                st<u32x4>(out + (c * uint32_t(M) + off), ld<u32x4>(&codes[k][code_word(c, off >> 2)]));
         }
     }
 }

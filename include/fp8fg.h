@@ -537,7 +537,7 @@ int fp8_moe_combine_backward(const void* dout, int dout_bf16, int64_t T, int64_t
  * rows: int32 [G] (4-byte aligned), or NULL for all rows: only rows
  * r < rows[g] of buffer g are read and written.  The contiguous layout is G = 1 with
  * rows = &group_offsets[G]; the masked one rows = masked_m.
- * Requires I % 128 == 0, I <= 2^25, G <= 65535; h must be finite.
+ * Requires I % 128 == 0, I <= 2^23, G <= 65535; h must be finite.
  */
 int fp8_swiglu(const void* gu, int gu_bf16, int64_t G, int64_t M, int64_t I, const int32_t* rows, uint8_t* q, float* s,
                uint8_t* qc, float* sc, void* stream);
@@ -555,7 +555,7 @@ int fp8_swiglu(const void* gu, int gu_bf16, int64_t G, int64_t M, int64_t I, con
  * the gate+up and down products' weight gradients.
  * rows: int32 [1], or NULL: rows from rows[0] on count as zero; their rows of
  * q and s, and the 128-row groups of qt and qh that lie wholly past them, are
- * not written.  Requires I % 128 == 0, I <= 2^25, M % 16 == 0,
+ * not written.  Requires I % 128 == 0, I <= 2^23, M % 16 == 0,
  * M <= 128 * 65535.
  */
 int fp8_swiglu_backward(const uint8_t* qc, const float* sc, const void* dh, int dh_bf16, int64_t M, int64_t I,

@@ -114,7 +114,7 @@ def test_swiglu_refusals():
     assert f(rows=ctypes.c_void_p(0x10002)) == EALIGN and f(rows=MIS) == OK
     for bad in (dict(I=64), dict(I=200), dict(M=-1), dict(G=-1)):
         assert f(**bad) == ESHAPE, bad
-    for bad in (dict(bf16=2), dict(G=65536), dict(M=BIG), dict(I=(1 << 25) + 128)):
+    for bad in (dict(bf16=2), dict(G=65536), dict(M=BIG), dict(I=(1 << 23) + 128)):
         assert f(**bad) == EUNSUP, bad
 
     def b(**k):
@@ -125,7 +125,7 @@ def test_swiglu_refusals():
         assert b(M=16, **{k: NUL}) == ENULL and b(**{k: MIS}) == EALIGN
     for bad in (dict(I=64), dict(M=8), dict(M=-16)):
         assert b(**bad) == ESHAPE, bad
-    for bad in (dict(bf16=2), dict(M=128 * 65536), dict(I=(1 << 25) + 128)):
+    for bad in (dict(bf16=2), dict(M=128 * 65536), dict(I=(1 << 23) + 128)):
         assert b(**bad) == EUNSUP, bad
 
 
