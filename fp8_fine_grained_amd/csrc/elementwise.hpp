@@ -227,8 +227,47 @@ struct Ratio {
     }
 };
 
+// Values formed in FP32 here (a gate, a gradient): the same two-part quotient,
+// within half a last place and 2^-40 of x / s, which differs from RN32(x / s) far less
+// than the value's own roundings do.  For a far scale r and rl are those of s k, rl
+// with its sign set, and the operands are scaled; a subnormal scale can be a
+// third below amax / 448, so there the quotient saturates.
+struct Derived {
+    float s, r, rl;
+    __device__ __forceinline__ explicit Derived(float amax) : s(scale_near(amax)) {
+        if (far_scale(s)) {
+            s = amax / 448.0f;
+            const float t = s * far_factor(s);
+            r = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(t) * (1.0f - 0x1p-22f);
+            rl = s == 0.0f ? 0.0f : -r * __builtin_fmaf(-t, r, 1.0f);
+        } else {
+            r = __builtin_amdgcn_rcpf(s);
+            r = __builtin_fmaf(r, -0x1p-22f, r);
+            rl = r * __builtin_fmaf(-s, r, 1.0f);
+        }
+    }
+    __device__ __forceinline__ Derived(float s_, float r_, float rl_) : s(s_), r(r_), rl(rl_) {}
+    template <int N>
+    __device__ __forceinline__ void encode(const float (&x)[4 * N], uint32_t (&code)[N]) const {
+        float y[4 * N];
+        if (rl >= 0.0f) {
+#pragma unroll
+            for (int i = 0; i < 4 * N; ++i) y[i] = __builtin_fmaf(x[i], r, x[i] * rl);
+        } else {
+            const float k = far_factor(s);
+#pragma unroll
+            for (int i = 0; i < 4 * N; ++i) {
+                const float xs = x[i] * k;
+                y[i] = __builtin_amdgcn_fmed3f(__builtin_fmaf(xs, r, xs * -rl), -448.0f, 448.0f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) code[i] = codes4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+    }
+};
+
 // 16 consecutive values of a lane, eight lanes to a 128-group: the group's
-// scale and the lane's codes (G: Bracket, or Ratio for values that are BF16)
+// scale and the lane's codes (G: Bracket, Ratio for values that are BF16, or Derived)
 template <class G>
 __device__ __forceinline__ u32x4 encode16(const float (&v)[16], float& sc) {
     float amax = 0.0f;

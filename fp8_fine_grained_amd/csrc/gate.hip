@@ -33,7 +33,7 @@ __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t 
 #pragma unroll
         for (int i = 0; i < 16; ++i) h[i] = g[i] * sigmoid_fast(g[i]) * u[i];
         float a;
-        const u32x4 codes = encode16<Bracket>(h, a);
+        const u32x4 codes = encode16<Derived>(h, a);
         st<u32x4>(q + (b * M + m0) * I + kb * kBlock + in, codes);
         if (c16 == 0) s[(b * nb + kb) * M + m0 + r] = a;
         if (qc) {
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
     const int32_t* __restrict__ rows, uint8_t* __restrict__ q, float* __restrict__ s, uint8_t* __restrict__ qt,
     float* __restrict__ st_, uint8_t* __restrict__ qh, float* __restrict__ sh) {
     __shared__ float part[8][3 * kBlock];
-    __shared__ __align__(16) float gs[3 * kBlock], glo[3 * kBlock], ghi[3 * kBlock];      // the channels' groups
+    __shared__ __align__(16) float gs[3 * kBlock], gr[3 * kBlock], grl[3 * kBlock];      // the channels' groups
     __shared__ __align__(16) uint32_t codes[3][kBlock * kBlock / 4];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const uint32_t c8 = (t & 15) * 8, r4 = (t >> 4) * 4;
@@ -176,10 +176,10 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
         float a = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) a = fmaxf(a, part[i][t]);
-        const Bracket g(a);
+        const Derived g(a);
         gs[t] = a = g.s;
-        glo[t] = g.lo;
-        ghi[t] = g.hi;
+        gr[t] = g.r;
+        grl[t] = g.rl;
         if (t < 2 * kBlock)
             st_[mb * 2 * I + (t >> 7) * I + kb * kBlock + (t & 127)] = a;
         else
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
             a[i] = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) a[i] = fmaxf(a[i], fabsf(d[k][i][j]));
-            const Bracket g(lanes_max<16>(a[i]));
+            const Derived g(lanes_max<16>(a[i]));
             a[i] = g.s;
             uint32_t w[2];
             g.encode<2>(d[k][i], w);
@@ -218,14 +218,14 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
     const uint32_t even = code_word(c8, r4 >> 2), odd = code_word(c8 + 1, r4 >> 2);    // channels c8 + 2 i are 64 words apart
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        float lo[8], hi[8];
-        load_n<8>(glo + k * kBlock + c8, lo);
-        load_n<8>(ghi + k * kBlock + c8, hi);
+        float r[8], rl[8];
+        load_n<8>(gr + k * kBlock + c8, r);
+        load_n<8>(grl + k * kBlock + c8, rl);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float x[4] = {d[k][0][j], d[k][1][j], d[k][2][j], d[k][3][j]};
             uint32_t w[1];
-            Bracket(gs[k * kBlock + c8 + j], lo[j], hi[j]).encode<1>(x, w);
+            Derived(gs[k * kBlock + c8 + j], r[j], rl[j]).encode<1>(x, w);
             codes[k][((j & 1) ? odd : even) + (j >> 1) * 64] = w[0];
             if (j & 1) __builtin_amdgcn_sched_barrier(0);
         }
