@@ -15,7 +15,7 @@ namespace gate_detail {
 // A workgroup takes 32 rows of one 128-channel group: eight lanes per row.
 // Row r of buffer blockIdx.z exists when r < rows[blockIdx.z] (rows may be
 // null: all of them).  Offsets within the 32 rows fit 32 bits.
-template <class T>
+template <class T, bool STREAM>
 __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t M, int64_t I,
                                               const int32_t* __restrict__ rows, uint8_t* __restrict__ q,
                                               float* __restrict__ s, uint8_t* __restrict__ qc, float* __restrict__ sc) {
@@ -34,14 +34,14 @@ __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t 
         for (int i = 0; i < 16; ++i) h[i] = g[i] * sigmoid_fast(g[i]) * u[i];
         float a;
         const u32x4 codes = encode16<Derived>(h, a);
-        st<u32x4>(q + (b * M + m0) * I + kb * kBlock + in, codes);
+        st_out<STREAM>(q + (b * M + m0) * I + kb * kBlock + in, codes);
         if (c16 == 0) s[(b * nb + kb) * M + m0 + r] = a;
         if (qc) {
             float sg, su;
             const u32x4 cg = encode16<Enc>(g, sg), cu = encode16<Enc>(u, su);
             uint8_t* c = qc + (b * M + m0) * 2 * I + kb * kBlock;
-            st<u32x4>(c + (in + r * uint32_t(I)), cg);
-            st<u32x4>(c + I + (in + r * uint32_t(I)), cu);
+            st_out<STREAM>(c + (in + r * uint32_t(I)), cg);
+            st_out<STREAM>(c + I + (in + r * uint32_t(I)), cu);
             if (c16 == 0) {
                 sc[(b * 2 * nb + kb) * M + m0 + r] = sg;
                 sc[(b * 2 * nb + nb + kb) * M + m0 + r] = su;
@@ -80,7 +80,7 @@ __device__ __forceinline__ float dh_of(const u32x4 (&w)[1], int j) {
 }
 __device__ __forceinline__ float dh_of(const u32x4 (&w)[2], int j) { return __uint_as_float(w[j >> 2][j & 3]); }
 
-template <class T>
+template <class T, bool STREAM>
 __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
     const uint8_t* __restrict__ qc, const float* __restrict__ sc, const T* __restrict__ dh, int64_t M, int64_t I,
     const int32_t* __restrict__ rows, uint8_t* __restrict__ q, float* __restrict__ s, uint8_t* __restrict__ qt,
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
             a[i] = g.s;
             uint32_t w[2];
             g.encode<2>(d[k][i], w);
-            if (full || m0 + i < end) st<u32x2_t>(out + i * 2 * I + (r4 * uint32_t(2 * I) + c8), u32x2_t{w[0], w[1]});
+            if (full || m0 + i < end) st_out<STREAM>(out + i * 2 * I + (r4 * uint32_t(2 * I) + c8), u32x2_t{w[0], w[1]});
             __builtin_amdgcn_sched_barrier(0);
         }
         if (c8 == 0) {
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
             const uint32_t piece = t + kTileThreads * i;          // 128 channels x 8 pieces of 16 rows
             const uint32_t c = piece >> 3, off = (piece & 7) * 16;
             if (full || mb * kBlock + off < M)                     // M % 16 == 0: whole pieces
-                st<u32x4>(out + (c * uint32_t(M) + off), ld<u32x4>(&codes[k][code_word(c, off >> 2)]));
+                st_out<STREAM>(out + (c * uint32_t(M) + off), ld<u32x4>(&codes[k][code_word(c, off >> 2)]));
         }
     }
 }
@@ -253,21 +253,33 @@ hipError_t launch_swiglu(const void* gu, int bf16, int64_t G, int64_t M, int64_t
     int64_t groups = (M + 31) / 32;
     if (groups > 65535) groups = 65535;      // the kernel strides over the rest
     const dim3 grid(unsigned(I / kBlock), unsigned(groups), unsigned(G));
-    if (bf16)
-        return launch_kernel(swiglu<uint16_t>, grid, dim3(256), stream, static_cast<const uint16_t*>(gu), M, I, rows, q,
-                             s, qc, sc);
-    return launch_kernel(swiglu<float>, grid, dim3(256), stream, static_cast<const float*>(gu), M, I, rows, q, s, qc, sc);
+    const bool stream_out = G * M * I * (qc ? 3 : 1) >= kStreamBytes;
+#define FP8FG_GATE(T, S) \
+    return launch_kernel(swiglu<T, S>, grid, dim3(256), stream, static_cast<const T*>(gu), M, I, rows, q, s, qc, sc)
+    if (bf16) {
+        if (stream_out) FP8FG_GATE(uint16_t, true);
+        FP8FG_GATE(uint16_t, false);
+    }
+    if (stream_out) FP8FG_GATE(float, true);
+    FP8FG_GATE(float, false);
+#undef FP8FG_GATE
 }
 
 hipError_t launch_swiglu_backward(const uint8_t* qc, const float* sc, const void* dh, int bf16, int64_t M, int64_t I,
                                   const int32_t* rows, uint8_t* q, float* s, uint8_t* qt, float* st, uint8_t* qh,
                                   float* sh, hipStream_t stream) {
     const dim3 grid(unsigned(I / kBlock), unsigned((M + kBlock - 1) / kBlock));
-    if (bf16)
-        return launch_kernel(swiglu_backward<uint16_t>, grid, dim3(kTileThreads), stream, qc, sc,
-                             static_cast<const uint16_t*>(dh), M, I, rows, q, s, qt, st, qh, sh);
-    return launch_kernel(swiglu_backward<float>, grid, dim3(kTileThreads), stream, qc, sc,
-                         static_cast<const float*>(dh), M, I, rows, q, s, qt, st, qh, sh);
+    const bool stream_out = 5 * M * I >= kStreamBytes;
+#define FP8FG_GATE(T, S)                                                                                              \
+    return launch_kernel(swiglu_backward<T, S>, grid, dim3(kTileThreads), stream, qc, sc, static_cast<const T*>(dh), M, \
+                         I, rows, q, s, qt, st, qh, sh)
+    if (bf16) {
+        if (stream_out) FP8FG_GATE(uint16_t, true);
+        FP8FG_GATE(uint16_t, false);
+    }
+    if (stream_out) FP8FG_GATE(float, true);
+    FP8FG_GATE(float, false);
+#undef FP8FG_GATE
 }
 
 }  // namespace fp8fg

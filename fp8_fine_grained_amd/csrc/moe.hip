@@ -248,10 +248,10 @@ __global__ __launch_bounds__(256) void route_backward(const T* __restrict__ x, c
 //
 // One workgroup per `chunk` entries.  It counts every expert's entries before
 // its chunk and in all (32 counters per expert, one per lane pair, so that
-// the lanes of a wave never meet on an address), then ranks its own chunk
-// 1024 entries at a time: the lanes of a wave with the same expert find each
-// other with one ballot per bit of the index, the waves' counts are summed in
-// order.  No workgroup waits for another.
+// the lanes of a wave never meet on an address; 16 entries per thread in
+// flight), then ranks its own chunk 1024 entries at a time: the lanes of a wave
+// with the same expert find each other with one ballot per bit of the index,
+// the waves' counts are summed in order.  No workgroup waits for another.
 constexpr int kMaxLocal = 256;
 
 __global__ __launch_bounds__(1024) void rows_layout(const int32_t* __restrict__ idx, int64_t n, int first, int G,
@@ -265,41 +265,69 @@ __global__ __launch_bounds__(1024) void rows_layout(const int32_t* __restrict__ 
     const int64_t lo = int64_t(blockIdx.x) * chunk, hi = lo + chunk < n ? lo + chunk : n;
     for (int i = t; i < G * 32; i += 1024) hist[i] = 0;
     __syncthreads();
+    auto add = [&](int32_t id) {
+        const uint32_t e = uint32_t(id) - uint32_t(first);
+        if (e < uint32_t(G)) atomicAdd(&hist[e * 32 + (lane & 31)], 1u);
+    };
+    // entries [from, to), from a multiple of 1024
     auto count = [&](int64_t from, int64_t to) {
-        for (int64_t i = from + t; i < to; i += 1024) {
-            const uint32_t e = uint32_t(idx[i]) - uint32_t(first);
-            if (e < uint32_t(G)) atomicAdd(&hist[e * 32 + (lane & 31)], 1u);
+        int64_t i = from + 4 * t;
+        typedef int i32x4 __attribute__((ext_vector_type(4)));
+        for (; i + 3 * 4096 + 4 <= to; i += 4 * 4096) {
+            i32x4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = ld<i32x4>(idx + i + 4096 * k);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) add(v[k][j]);
         }
+        for (; i + 4 <= to; i += 4096) {
+            const i32x4 v = ld<i32x4>(idx + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) add(v[j]);
+        }
+        for (int64_t j = i; j < to && j < i + 4; ++j) add(idx[j]);
         __syncthreads();
     };
     auto total = [&](int e) {
         uint32_t c = 0;
+#pragma unroll 8
         for (int i = 0; i < 32; ++i) c += hist[e * 32 + ((i + e) & 31)];
         return c;
     };
-    count(0, lo);
-    if (t < G) base[t] = total(t);
+    if (lo > 0) count(0, lo);
+    if (t < G) base[t] = lo > 0 ? total(t) : 0u;
     __syncthreads();
     count(lo, n);
-    if (t < G) {
-        const uint32_t c = total(t);
-        start[t + 1] = m_max ? 0u : (c + 127u) / 128u * 128u;
-        if (blockIdx.x == 0) counts[t] = int32_t(m_max && c > uint64_t(m_max) ? uint32_t(m_max) : c);
+    if (t < kMaxLocal) {
+        const uint32_t c = t < G ? total(t) : 0u;
+        if (blockIdx.x == 0 && t < G) counts[t] = int32_t(m_max && c > uint64_t(m_max) ? uint32_t(m_max) : c);
+        // first rows: an inclusive scan over the wave's 64 experts, the four waves' sums below
+        uint32_t sum = m_max ? uint32_t(m_max) : (c + 127u) / 128u * 128u;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t below = __shfl_up(sum, o, 64);
+            sum += lane >= o ? below : 0u;
+        }
+        start[t + 1] = sum;
     }
     if (t == 0) start[0] = 0;
     __syncthreads();
-    if (t == 0)
-        for (int e = 0; e < G; ++e) start[e + 1] = m_max ? uint32_t((e + 1) * m_max) : start[e] + start[e + 1];
+    uint32_t below = 0;
+    if (t < kMaxLocal)
+        for (int w = 0; w < wave; ++w) below += start[64 * w + 64];
     __syncthreads();
-    if (blockIdx.x == 0 && offsets)
-        for (int i = t; i <= G; i += 1024) offsets[i] = int32_t(start[i]);
+    if (t < kMaxLocal) start[t + 1] += below;
+    __syncthreads();
+    if (blockIdx.x == 0 && offsets && t <= G) offsets[t] = int32_t(start[t]);
     for (int64_t at = lo; at < hi; at += 1024) {
         for (int i = t; i < 16 * kMaxLocal; i += 1024) wave_count[i / kMaxLocal][i % kMaxLocal] = 0;
-        __syncthreads();
         const int64_t i = at + t;
         const uint32_t e0 = i < hi ? uint32_t(idx[i]) - uint32_t(first) : uint32_t(G);
         const bool mine = e0 < uint32_t(G);
         const uint32_t e = mine ? e0 : uint32_t(G);
+        __syncthreads();
         uint64_t same = ~uint64_t(0);
         for (int b = 0; (1 << b) <= G; ++b) {
             const uint64_t set = __builtin_amdgcn_ballot_w64((e >> b) & 1);
@@ -310,6 +338,7 @@ __global__ __launch_bounds__(1024) void rows_layout(const int32_t* __restrict__ 
         __syncthreads();
         if (t < G) {
             uint32_t run = base[t];
+#pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const uint32_t c = wave_count[k][t];
                 wave_count[k][t] = run;
@@ -340,50 +369,67 @@ struct RowsOut {
     uint8_t* q;
     float* s;
     int64_t H, kbs, rows_per;      // rows_per: rows of one scale array (M_total, or M_max of an expert)
-    __device__ __forceinline__ float* scale(int64_t row, int64_t kb) const {
-        const int64_t b = row / rows_per;
-        return s + (b * kbs + kb) * rows_per + (row - b * rows_per);
+    template <bool MASKED>
+    __device__ __forceinline__ float* scale(uint32_t row, uint32_t kb) const {
+        if (!MASKED) return s + kb * rows_per + row;
+        const uint32_t b = row / uint32_t(rows_per);
+        return s + (b * kbs + kb) * rows_per + (row - b * uint32_t(rows_per));
     }
 };
 
-// zero rows [counts[g], padded count) of every expert: wave p = (expert, row)
-__device__ __forceinline__ void zero_padding(int64_t p, const int32_t* offsets, const int32_t* counts, int64_t R,
-                                             const RowsOut& o, int lane) {
-    const int64_t g = p / 127, row = int64_t(offsets[g]) + counts[g] + p % 127;
-    if (row < 0 || row >= offsets[g + 1] || row >= R) return;
-    for (int64_t c = lane * 16; c < o.H; c += 1024) st<u32x4>(o.q + row * o.H + c, u32x4{0u, 0u, 0u, 0u});
-    for (int64_t kb = lane; kb < o.kbs; kb += 64) *o.scale(row, kb) = 0.0f;
+// Workgroup b of n runs on XCD b mod 8; it takes item x (n / 8) + b / 8, so
+// that an XCD works through consecutive tokens: their rows' scales, four bytes
+// at a time beside those of the expert's previous rows, fill whole lines of
+// one L2.  A bijection on [0, n).
+constexpr uint32_t kXcds = 8;
+__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
+    const uint32_t per = n / kXcds;
+    return b < per * kXcds ? (b % kXcds) * per + b / kXcds : b;
 }
 
-template <class T>
+// zero rows [counts[g], padded count) of every expert: wave p = (expert, row)
+__device__ __forceinline__ void zero_padding(uint32_t p, const int32_t* offsets, const int32_t* counts, int64_t R,
+                                             const RowsOut& o, int lane) {
+    const uint32_t g = p / 127;
+    const int64_t row = int64_t(offsets[g]) + counts[g] + p % 127;
+    if (row < 0 || row >= offsets[g + 1] || row >= R) return;
+    for (int64_t c = lane * 16; c < o.H; c += 1024) st<u32x4>(o.q + row * o.H + c, u32x4{0u, 0u, 0u, 0u});
+    for (int64_t kb = lane; kb < o.kbs; kb += 64) *o.scale<false>(uint32_t(row), uint32_t(kb)) = 0.0f;
+}
+
+template <class T, bool MASKED, bool STREAM>
 __global__ __launch_bounds__(256) void dispatch_rows(const T* __restrict__ x, const int32_t* __restrict__ row_of,
-                                                     int64_t T_, int topk, int64_t chunks, RowsOut o,
-                                                     const int32_t* __restrict__ offsets,
-                                                     const int32_t* __restrict__ counts, int64_t G, int64_t R) {
+                                                     uint32_t waves, int topk, uint32_t chunks, uint32_t blocks,
+                                                     RowsOut o, const int32_t* __restrict__ offsets,
+                                                     const int32_t* __restrict__ counts, uint32_t G, int64_t R) {
     const int lane = threadIdx.x & 63;
-    const int64_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + int64_t(blockIdx.x) * 4;
-    if (w >= T_ * chunks) {
-        if (offsets && w - T_ * chunks < 127 * G) zero_padding(w - T_ * chunks, offsets, counts, R, o, lane);
+    const uint32_t b = blockIdx.x < blocks ? xcd_run(blockIdx.x, blocks) : blockIdx.x;
+    const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + b * 4;
+    if (b >= blocks) {
+        const uint32_t p = w - blocks * 4;
+        if (!MASKED && p < 127 * G) zero_padding(p, offsets, counts, R, o, lane);
         return;
     }
-    const int64_t token = w / chunks, c = w - token * chunks;
-    const int64_t ch = c * kWaveChan + lane * kChan;
+    if (w >= waves) return;
+    const uint32_t token = w / chunks, c = w - token * chunks;
+    const uint32_t ch = c * kWaveChan + lane * kChan;
     float v[kChan];
 #pragma unroll
     for (int i = 0; i < kChan; ++i) v[i] = 0.0f;
-    if (ch < o.H) load_n<kChan>(x + token * o.H + ch, v);
+    if (ch < o.H) load_n<kChan, true>(x + int64_t(token) * o.H + ch, v);
+    const int32_t* rows = row_of + int64_t(token) * topk;
     float sc;
     const u32x4 code = encode16<typename encoder_of<T>::type>(v, sc);
-    const int32_t* rows = row_of + token * topk;
-    for (int j = 0; j < topk; ++j) {
-        const int64_t r = rows[j];
-        if (r >= 0 && ch < o.H) st<u32x4>(o.q + r * o.H + ch, code);
-    }
-    const int64_t kb = c * 8 + (lane >> 3);
+    if (ch < o.H)
+        for (int j = 0; j < topk; ++j) {
+            const int64_t r = rows[j];
+            if (r >= 0) st_out<STREAM>(o.q + r * o.H + ch, code);
+        }
+    const uint32_t kb = c * 8 + (lane >> 3);
     if (kb < o.kbs)
         for (int j = lane & 7; j < topk; j += 8) {
-            const int64_t r = rows[j];
-            if (r >= 0) *o.scale(r, kb) = sc;
+            const int32_t r = rows[j];
+            if (r >= 0) *o.scale<MASKED>(uint32_t(r), kb) = sc;
         }
 }
 
@@ -407,7 +453,7 @@ __global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t
         if (r < 0 || r >= R) continue;
         const float wt = wts ? wts[token * topk + j] : 1.0f;
         float v[8];
-        load_n<8>(y + r * H + ch, v);
+        load_n<8, true>(y + r * H + ch, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = fmaf(wt, v[i], acc[i]);
     }
@@ -419,7 +465,7 @@ __global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t
 // rows dy = w_tj Q(dout_t), where Q is the 1x128 quantization of dout_t: every
 // row of a token shares its codes, and its scales are |w| times the token's
 // (the sign of w goes into the codes).  A workgroup per token.
-template <class TD, class TY>
+template <class TD, class TY, bool STREAM>
 __global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ dout, const TY* __restrict__ y,
                                                         const int32_t* __restrict__ row_of,
                                                         const float* __restrict__ wts, int64_t T_, int topk, RowsOut o,
@@ -428,10 +474,10 @@ __global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ d
                                                         float* __restrict__ dw) {
     __shared__ float part[4][16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t token = blockIdx.x;
+    const int64_t token = blockIdx.x < T_ ? int64_t(xcd_run(blockIdx.x, uint32_t(T_))) : int64_t(blockIdx.x);
     if (token >= T_) {
         const int64_t p = (token - T_) * 4 + wave;
-        if (p < 127 * G) zero_padding(p, offsets, counts, R, o, lane);
+        if (p < 127 * G) zero_padding(uint32_t(p), offsets, counts, R, o, lane);
         return;
     }
     const int32_t* rows = row_of + token * topk;
@@ -460,9 +506,9 @@ __global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ d
 #pragma unroll
                 for (int i = 0; i < kChan; ++i) dot[j] = fmaf(v[i], u[i], dot[j]);
                 const uint32_t flip = wt < 0.0f ? 0x80808080u : 0u;
-                st<u32x4>(o.q + r * o.H + ch, u32x4{code[0] ^ flip, code[1] ^ flip, code[2] ^ flip, code[3] ^ flip});
+                st_out<STREAM>(o.q + r * o.H + ch, u32x4{code[0] ^ flip, code[1] ^ flip, code[2] ^ flip, code[3] ^ flip});
             }
-            if ((lane & 7) == 0 && kb < o.kbs) *o.scale(r, kb) = sc * fabsf(wt);
+            if ((lane & 7) == 0 && kb < o.kbs) *o.scale<false>(uint32_t(r), uint32_t(kb)) = sc * fabsf(wt);
         }
     }
 #pragma unroll
@@ -484,7 +530,6 @@ inline int pow2_at_least(int64_t n) {
     while (p < n) p *= 2;
     return p;
 }
-constexpr int64_t kGridMax = 0x7FFFFFFF;
 
 template <class T, int LPT, int V>
 hipError_t run_route(const void* x, const float* bias, const RouteArgs& a, int32_t* idx, float* w, hipStream_t stream) {
@@ -558,17 +603,28 @@ hipError_t launch_rows_layout(const int32_t* idx, int64_t n, int64_t first, int6
                          row_of, offsets, counts);
 }
 
+template <class T, bool MASKED>
+static hipError_t run_dispatch_rows(const void* x, int64_t T_, const int32_t* row_of, int64_t topk, const RowsOut& o,
+                                    const int32_t* offsets, const int32_t* counts, int64_t G, int64_t R,
+                                    hipStream_t stream) {
+    const int64_t chunks = (o.H + kWaveChan - 1) / kWaveChan, waves = T_ * chunks, blocks = (waves + 3) / 4;
+    const int64_t grid = blocks + (MASKED ? 0 : (127 * G + 3) / 4);
+    // (R rows bound what is written: the routing is known on the device only)
+    const bool stream_out = (R < T_ * topk ? R : T_ * topk) * o.H >= kStreamBytes;
+    return launch_kernel(stream_out ? dispatch_rows<T, MASKED, true> : dispatch_rows<T, MASKED, false>,
+                         dim3(unsigned(grid)), dim3(256), stream, static_cast<const T*>(x), row_of, uint32_t(waves),
+                         int(topk), uint32_t(chunks), uint32_t(blocks), o, offsets, counts, uint32_t(G), R);
+}
+
 hipError_t launch_dispatch_rows(const void* x, int bf16, int64_t T, int64_t H, const int32_t* row_of, int64_t topk,
                                 int64_t R, int64_t rows_per, const int32_t* offsets, const int32_t* counts, int64_t G,
                                 uint8_t* q, float* s, hipStream_t stream) {
     const RowsOut o{q, s, H, (H + kBlock - 1) / kBlock, rows_per};
-    const int64_t chunks = (H + kWaveChan - 1) / kWaveChan;
-    const int64_t waves = T * chunks + (offsets ? 127 * G : 0), blocks = (waves + 3) / 4;
-    if (bf16)
-        return launch_kernel(dispatch_rows<uint16_t>, dim3(unsigned(blocks)), dim3(256), stream,
-                             static_cast<const uint16_t*>(x), row_of, T, int(topk), chunks, o, offsets, counts, G, R);
-    return launch_kernel(dispatch_rows<float>, dim3(unsigned(blocks)), dim3(256), stream, static_cast<const float*>(x),
-                         row_of, T, int(topk), chunks, o, offsets, counts, G, R);
+    if (offsets)
+        return bf16 ? run_dispatch_rows<uint16_t, false>(x, T, row_of, topk, o, offsets, counts, G, R, stream)
+                    : run_dispatch_rows<float, false>(x, T, row_of, topk, o, offsets, counts, G, R, stream);
+    return bf16 ? run_dispatch_rows<uint16_t, true>(x, T, row_of, topk, o, offsets, counts, G, R, stream)
+                : run_dispatch_rows<float, true>(x, T, row_of, topk, o, offsets, counts, G, R, stream);
 }
 
 template <class TY, class TO>
@@ -595,7 +651,8 @@ static hipError_t run_combine_backward(const void* dout, int64_t T, int64_t H, c
                                        hipStream_t stream) {
     const RowsOut o{q, s, H, (H + kBlock - 1) / kBlock, R};
     const int64_t blocks = T + (127 * G + 3) / 4;
-    return launch_kernel(combine_backward<TD, TY>, dim3(unsigned(blocks)), dim3(256), stream,
+    const bool stream_out = (R < T * topk ? R : T * topk) * H >= kStreamBytes;
+    return launch_kernel(stream_out ? combine_backward<TD, TY, true> : combine_backward<TD, TY, false>, dim3(unsigned(blocks)), dim3(256), stream,
                          static_cast<const TD*>(dout), static_cast<const TY*>(y), row_of, w, T, int(topk), o, offsets,
                          counts, G, R, dw);
 }
