@@ -444,11 +444,8 @@ int fp8_moe_dispatch_contiguous(const void* x, int x_bf16, int64_t T, int64_t H,
         return FP8FG_ERR_ALIGN;
     if (!flag(x_bf16)) return FP8FG_ERR_UNSUPPORTED;
     if (G == 0) return FP8FG_OK;
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    if (const hipError_t e = fp8fg::launch_rows_layout(idx, n, first, G, 0, row_of, group_offsets, counts, st)) return hip_status(e);
-    if (T == 0 || H == 0) return FP8FG_OK;
-    return hip_status(fp8fg::launch_dispatch_rows(x, x_bf16, T, H, row_of, topk, M_total, M_total, group_offsets, counts,
-                                                  G, q, s, st));
+    return hip_status(fp8fg::launch_dispatch(x, x_bf16, T, H, idx, topk, first, G, M_total, 0, q, s, row_of,
+                                             group_offsets, counts, static_cast<hipStream_t>(stream)));
 }
 
 int fp8_moe_dispatch_masked(const void* x, int x_bf16, int64_t T, int64_t H, const int32_t* idx, int64_t topk,
@@ -464,12 +461,8 @@ int fp8_moe_dispatch_masked(const void* x, int x_bf16, int64_t T, int64_t H, con
         return FP8FG_ERR_ALIGN;
     if (!flag(x_bf16)) return FP8FG_ERR_UNSUPPORTED;
     if (G == 0) return FP8FG_OK;
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    if (const hipError_t e = fp8fg::launch_rows_layout(idx, T * topk, first, G, M_max, row_of, nullptr, masked_m, st))
-        return hip_status(e);
-    if (T == 0 || H == 0) return FP8FG_OK;
-    return hip_status(fp8fg::launch_dispatch_rows(x, x_bf16, T, H, row_of, topk, G * M_max, M_max, nullptr, nullptr, G, q,
-                                                  s, st));
+    return hip_status(fp8fg::launch_dispatch(x, x_bf16, T, H, idx, topk, first, G, G * M_max, M_max, q, s, row_of,
+                                             nullptr, masked_m, static_cast<hipStream_t>(stream)));
 }
 
 int moe_combine(const void* y, int y_bf16, int64_t R, int64_t H, const int32_t* row_of, const float* w, int64_t T,

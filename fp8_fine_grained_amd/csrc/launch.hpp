@@ -80,13 +80,11 @@ struct RouteCall {
 hipError_t launch_route(const RouteCall& call, hipStream_t stream);
 // dx: [T][E] in the logits' type; call.idx is read, call.w and call.bias are not used
 hipError_t launch_route_backward(const RouteCall& call, const float* dw, void* dx, hipStream_t stream);
-// m_max 0: contiguous layout (offsets [G + 1] written); else masked (offsets null)
-hipError_t launch_rows_layout(const int32_t* idx, int64_t n, int64_t first, int64_t G, int64_t m_max, int32_t* row_of,
-                              int32_t* offsets, int32_t* counts, hipStream_t stream);
-// rows_per: rows of one scale array; offsets null: no padding rows to clear
-hipError_t launch_dispatch_rows(const void* x, int bf16, int64_t T, int64_t H, const int32_t* row_of, int64_t topk,
-                                int64_t R, int64_t rows_per, const int32_t* offsets, const int32_t* counts, int64_t G,
-                                uint8_t* q, float* s, hipStream_t stream);
+// m_max 0: contiguous layout (R rows; offsets [G + 1] and padding rows written), else masked
+// (R = G * m_max rows, offsets unused)
+hipError_t launch_dispatch(const void* x, int bf16, int64_t T, int64_t H, const int32_t* idx, int64_t topk,
+                           int64_t first, int64_t G, int64_t R, int64_t m_max, uint8_t* q, float* s, int32_t* row_of,
+                           int32_t* offsets, int32_t* counts, hipStream_t stream);
 hipError_t launch_combine(const void* y, int y_bf16, int64_t R, int64_t H, const int32_t* row_of, const float* w,
                           int64_t T, int64_t topk, void* out, int out_fp32, hipStream_t stream);
 hipError_t launch_combine_backward(const void* dout, int dout_bf16, int64_t T, int64_t H, const void* y, int y_bf16,

@@ -41,6 +41,8 @@ __device__ __forceinline__ float sigmoidf(float x) { return 1.0f / (1.0f + expf(
 // FP32's smallest normal, sigmoid(x) is exp(x) to FP32's accuracy.
 __device__ __forceinline__ float chosen_sigmoid(float x, float ms) { return ms < -80.0f ? expf(x - ms) : sigmoidf(x); }
 
+constexpr int kMaxTopk = 16;
+
 struct RouteArgs {
     int64_t T, ld;
     int E, topk, groups, gs, lpg, topk_groups, group_top, sigmoid, renorm, vec;
@@ -61,34 +63,43 @@ __device__ __forceinline__ void load_logits(const T* row, int at, int n, int vec
 template <class T, int LPT, int V>
 __global__ __launch_bounds__(256) void route(const T* __restrict__ x, const float* __restrict__ bias, RouteArgs a,
                                              int32_t* __restrict__ idx, float* __restrict__ w) {
-    const int lane = threadIdx.x & 63, sl = lane & (LPT - 1), seg0 = lane & ~(LPT - 1);
+    __shared__ int chosen[256 / LPT][kMaxTopk];
+    const int lane = threadIdx.x & 63, sl = lane & (LPT - 1), seg0 = lane & ~(LPT - 1), seg = threadIdx.x / LPT;
     const int64_t token = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LPT;
     const bool there = token < a.T;
     const int g = sl / a.lpg, p = sl - g * a.lpg;
     const int left = a.gs - p * V, n = !there || g >= a.groups || left < 0 ? 0 : (left < V ? left : V);
     const int e0 = g * a.gs + p * V;
     const T* row = x + (there ? token : 0) * a.ld;
-    float v[V];
+    float v[V], b[V];
     load_logits<V>(row, e0, n, a.vec, v);
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = bias && j < n ? bias[e0 + j] : 0.0f;
+    if (sl < kMaxTopk) chosen[seg][sl] = -1;
     float m = 0.0f, inv = 0.0f;
-    if (!a.sigmoid) {
+    uint32_t key[V];
+    if (a.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float c = sigmoid_fast(v[j]) + b[j];
+            key[j] = (v[j] == kNegInf || c == kNegInf) ? 0u : ordered(c);
+        }
+    } else {
         m = kNegInf;
 #pragma unroll
         for (int j = 0; j < V; ++j) m = fmaxf(m, v[j]);
         m = lanes_max<LPT>(m);
         if (m == kNegInf) m = 0.0f;
-        float sum = 0.0f;
+        float s[V], sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum += expf(v[j] - m);
+        for (int j = 0; j < V; ++j) sum += s[j] = expf(v[j] - m);
         sum = lanes_sum<LPT>(sum);
         inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    }
-    uint32_t key[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float c = a.sigmoid ? sigmoidf(v[j]) : expf(v[j] - m) * inv;
-        if (bias) c += j < n ? bias[e0 + j] : 0.0f;
-        key[j] = (v[j] == kNegInf || c == kNegInf) ? 0u : ordered(c);
+        for (int j = 0; j < V; ++j) {
+            const float c = s[j] * inv + b[j];
+            key[j] = (v[j] == kNegInf || c == kNegInf) ? 0u : ordered(c);
+        }
     }
     if (a.topk_groups < a.groups) {
         uint32_t k1 = 0, k2 = 0;       // the two largest keys of the lane, then of its group
@@ -119,7 +130,8 @@ __global__ __launch_bounds__(256) void route(const T* __restrict__ x, const floa
             for (int j = 0; j < V; ++j) key[j] = 0u;
         }
     }
-    int mine = -1;                     // lane i < topk keeps the i-th choice
+    // the chosen, one after the other: the segment's largest key belongs to its
+    // lowest lane that holds it, there to the first element that equals it
     for (int i = 0; i < a.topk; ++i) {
         uint32_t best = 0;
 #pragma unroll
@@ -127,17 +139,20 @@ __global__ __launch_bounds__(256) void route(const T* __restrict__ x, const floa
         const uint32_t top = lanes_max<LPT>(best);
         uint64_t who = __builtin_amdgcn_ballot_w64(best == top && top != 0u);
         if (LPT < 64) who = (who >> seg0) & ((uint64_t(1) << (LPT & 63)) - 1);
-        const int owner = who ? int(__builtin_ctzll(who)) : -1;
+        bool open = who != 0 && sl == int(__builtin_ctzll(who));
         int at = 0;
+        const bool mine = open;
 #pragma unroll
-        for (int j = V - 1; j >= 0; --j) at = key[j] == best ? j : at;
-        const int e = __shfl(e0 + at, seg0 + (owner < 0 ? 0 : owner), 64);
-        if (sl == owner) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) key[j] = j == at ? 0u : key[j];
+        for (int j = 0; j < V; ++j) {
+            const bool hit = open && key[j] == best;
+            key[j] = hit ? 0u : key[j];
+            at = hit ? j : at;
+            open = open && !hit;
         }
-        if (sl == i && owner >= 0) mine = e;
+        if (mine) chosen[seg][i] = e0 + at;
     }
+    __syncthreads();
+    const int mine = there && sl < a.topk ? chosen[seg][sl] : -1;      // lane i < topk takes the i-th
     const float xs = mine >= 0 ? f32_of(row[mine]) : kNegInf;
     float wt;
     if (a.sigmoid) {
@@ -434,6 +449,85 @@ __global__ __launch_bounds__(256) void dispatch_rows(const T* __restrict__ x, co
 }
 
 // ---------------------------------------------------------------------------
+// The row layout and the rows themselves in one launch, for few entries: every
+// workgroup counts all entries for itself, so none waits for another.  A
+// workgroup takes four 1024-channel chunks of one token; in the contiguous layout G more
+// clear one expert's padding rows each.
+constexpr int64_t kSmallEntries = 2048;
+
+template <class T, bool MASKED>
+__global__ __launch_bounds__(256) void dispatch_small(const T* __restrict__ x, const int32_t* __restrict__ idx,
+                                                      uint32_t tokens, int topk, uint32_t per_token, int first,
+                                                      uint32_t G, RowsOut o, int32_t* __restrict__ row_of,
+                                                      int32_t* __restrict__ offsets, int32_t* __restrict__ counts) {
+    __shared__ uint32_t all[kMaxLocal], before[kMaxLocal], start[kMaxLocal + 1];
+    const uint32_t t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const uint32_t token = blockIdx.x / per_token, part = blockIdx.x - token * per_token;
+    const bool padding = token >= tokens;               // (uniform) expert blockIdx.x - tokens * per_token
+    const uint32_t n = tokens * uint32_t(topk), mine = padding ? 0u : token * uint32_t(topk);
+    const uint32_t c = part * 4 + wave, ch = c * kWaveChan + lane * kChan;
+    float v[kChan];
+#pragma unroll
+    for (int i = 0; i < kChan; ++i) v[i] = 0.0f;
+    if (!padding && ch < o.H) load_n<kChan, true>(x + int64_t(token) * o.H + ch, v);
+    all[t] = before[t] = 0;                             // kMaxLocal threads
+    __syncthreads();
+    for (uint32_t i = t; i < n; i += 256) {
+        const uint32_t e = uint32_t(idx[i]) - uint32_t(first);
+        if (e < G) {
+            atomicAdd(&all[e], 1u);
+            if (i < mine) atomicAdd(&before[e], 1u);
+        }
+    }
+    __syncthreads();
+    if (!MASKED) {
+        uint32_t sum = (all[t] + 127u) / 128u * 128u;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) {
+            const uint32_t below = __shfl_up(sum, k, 64);
+            sum += int(lane) >= k ? below : 0u;
+        }
+        start[t + 1] = sum;
+        if (t == 0) start[0] = 0;
+        __syncthreads();
+        uint32_t below = 0;
+        for (uint32_t w = 0; w < wave; ++w) below += start[64 * w + 64];
+        __syncthreads();
+        start[t + 1] += below;
+        __syncthreads();
+        if (blockIdx.x == 0)
+            for (uint32_t i = t; i <= G; i += 256) offsets[i] = int32_t(start[i]);
+    }
+    if (blockIdx.x == 0 && t < G) counts[t] = int32_t(MASKED && all[t] > uint64_t(o.rows_per) ? uint32_t(o.rows_per) : all[t]);
+    if (padding) {
+        const uint32_t g = blockIdx.x - tokens * per_token;
+        for (uint32_t row = start[g] + all[g] + wave; row < start[g + 1]; row += 4) {
+            for (int64_t i = lane * 16; i < o.H; i += 1024) st<u32x4>(o.q + int64_t(row) * o.H + i, u32x4{0u, 0u, 0u, 0u});
+            for (uint32_t kb = lane; kb < o.kbs; kb += 64) *o.scale<false>(row, kb) = 0.0f;
+        }
+        return;
+    }
+    // lane j < topk: the row of the token's j-th entry
+    int32_t row = -1;
+    const uint32_t e = lane < uint32_t(topk) ? uint32_t(idx[mine + lane]) - uint32_t(first) : G;
+    uint32_t rank = e < G ? before[e] : 0u;
+    for (int j = 0; j < topk; ++j) rank += uint32_t(j) < lane && uint32_t(__builtin_amdgcn_readlane(int(e), j)) == e ? 1u : 0u;
+    if (e < G && (!MASKED || rank < uint64_t(o.rows_per))) row = int32_t(MASKED ? e * uint32_t(o.rows_per) + rank : start[e] + rank);
+    if (part == 0 && wave == 0 && lane < uint32_t(topk)) row_of[mine + lane] = row;
+    float sc;
+    const u32x4 code = encode16<typename encoder_of<T>::type>(v, sc);
+    for (int j = 0; j < topk; ++j) {
+        const int64_t r = __builtin_amdgcn_readlane(row, j);
+        if (r >= 0 && ch < o.H) st<u32x4>(o.q + r * o.H + ch, code);
+    }
+    const uint32_t kb = c * 8 + (lane >> 3);
+    for (int j0 = 0; j0 < topk; j0 += 8) {
+        const int32_t r = __shfl(row, j0 + int(lane & 7), 64);      // lanes from topk on hold -1
+        if (r >= 0 && kb < o.kbs) *o.scale<MASKED>(uint32_t(r), kb) = sc;
+    }
+}
+
+// ---------------------------------------------------------------------------
 // out_t = sum_j w_tj y[row_tj], in the order of the choices, in FP32.  A wave
 // takes 512 channels of one token, eight per lane.
 template <class TY, class TO>
@@ -481,39 +575,49 @@ __global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ d
         return;
     }
     const int32_t* rows = row_of + token * topk;
-    float dot[16];
+    const float* wt = wts + token * topk;
+    float dot[kMaxTopk];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) dot[j] = 0.0f;
-    const int64_t chunks = (o.H + kWaveChan - 1) / kWaveChan;
-    for (int64_t c = wave; c < chunks; c += 4) {
-        const int64_t ch = c * kWaveChan + lane * kChan;
+    for (int j = 0; j < kMaxTopk; ++j) dot[j] = 0.0f;
+    const uint32_t chunks = uint32_t((o.H + kWaveChan - 1) / kWaveChan);
+    for (uint32_t c = wave; c < chunks; c += 4) {
+        const uint32_t ch = c * kWaveChan + lane * kChan;
+        const bool in = ch < o.H;
         float v[kChan];
 #pragma unroll
         for (int i = 0; i < kChan; ++i) v[i] = 0.0f;
-        if (ch < o.H) load_n<kChan>(dout + token * o.H + ch, v);
+        if (in) load_n<kChan>(dout + token * o.H + ch, v);
         float sc;
         const u32x4 code = encode16<typename encoder_of<TD>::type>(v, sc);
-        const int64_t kb = c * 8 + (lane >> 3);
+        const uint32_t kb = c * 8 + (lane >> 3);
+        // four entries at a time, their loads in flight together (an entry
+        // without a row reads row 0 and is left out)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            if (j >= topk) break;
-            const int64_t r = rows[j];
-            if (r < 0 || r >= R) continue;
-            const float wt = wts[token * topk + j];
-            if (ch < o.H) {
-                float u[kChan];
-                load_n<kChan>(y + r * o.H + ch, u);
+        for (int j0 = 0; j0 < kMaxTopk; j0 += 4) {
+            if (j0 < topk) {
+                int64_t r[4];
+                float u[4][kChan];
 #pragma unroll
-                for (int i = 0; i < kChan; ++i) dot[j] = fmaf(v[i], u[i], dot[j]);
-                const uint32_t flip = wt < 0.0f ? 0x80808080u : 0u;
-                st_out<STREAM>(o.q + r * o.H + ch, u32x4{code[0] ^ flip, code[1] ^ flip, code[2] ^ flip, code[3] ^ flip});
+                for (int j = 0; j < 4; ++j) {
+                    r[j] = j0 + j < topk ? rows[j0 + j] : -1;
+                    if (r[j] >= R) r[j] = -1;
+                    if (in && R > 0) load_n<kChan>(y + (r[j] < 0 ? 0 : r[j]) * o.H + ch, u[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (r[j] >= 0 && in) {
+                        const uint32_t flip = wt[j0 + j] < 0.0f ? 0x80808080u : 0u;
+                        st_out<STREAM>(o.q + r[j] * o.H + ch, u32x4{code[0] ^ flip, code[1] ^ flip, code[2] ^ flip, code[3] ^ flip});
+                        if ((lane & 7) == 0) *o.scale<false>(uint32_t(r[j]), kb) = sc * fabsf(wt[j0 + j]);
+#pragma unroll
+                        for (int i = 0; i < kChan; ++i) dot[j0 + j] = fmaf(v[i], u[j][i], dot[j0 + j]);
+                    }
+                }
             }
-            if ((lane & 7) == 0 && kb < o.kbs) *o.scale<false>(uint32_t(r), uint32_t(kb)) = sc * fabsf(wt);
         }
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        if (j >= topk) break;
+    for (int j = 0; j < kMaxTopk; ++j) {
         dot[j] = lanes_sum<64>(dot[j]);
         if (lane == 0) part[wave][j] = dot[j];
     }
@@ -553,9 +657,13 @@ hipError_t launch_route(const RouteCall& c, hipStream_t stream) {
                 c.sigmoid, c.renorm, 0, c.scale};
     const int ng = pow2_at_least(c.n_groups);
     const int el = c.bf16 ? 2 : 4;
-    // 16 lanes per token (four tokens per wave) where a lane's share is at
-    // most 16 experts, else the whole wave
-    const int lpt = (a.gs + 16 / ng - 1) / (16 / ng) <= 16 ? 16 : 64;
+    // 16 lanes per token (four tokens per wave) or the whole wave.  The wave's
+    // chain is shorter (fewer experts per lane), the 16 lanes' instructions per
+    // token fewer.  Measured (us, 16 lanes / 64): 256 experts 7.8 / 4.9 at 64 tokens, 8.3 / 6.7 at
+    // 4096, 10.7 / 9.8 at 8192, 15.2 / 16.3 at 16384; 128 experts 6.4 / 8.0 at 8192;
+    // 64 experts 3.7 / 4.1 at 64, 4.5 / 8.1 at 8192.
+    const int share = (a.gs + 16 / ng - 1) / (16 / ng);      // experts per lane of 16
+    const int lpt = share > 16 || (share > 8 && c.T <= 8192) || (share > 4 && c.T <= 4096) ? 64 : 16;
     a.lpg = lpt / ng;
     const int need = (a.gs + a.lpg - 1) / a.lpg, v = need <= 4 ? 4 : need <= 8 ? 8 : 16;
     const int unit = v * el < 16 ? v * el : 16;
@@ -591,7 +699,7 @@ hipError_t launch_route_backward(const RouteCall& c, const float* dw, void* dx, 
     return hipErrorInvalidValue;
 }
 
-hipError_t launch_rows_layout(const int32_t* idx, int64_t n, int64_t first, int64_t G, int64_t m_max, int32_t* row_of,
+static hipError_t launch_rows_layout(const int32_t* idx, int64_t n, int64_t first, int64_t G, int64_t m_max, int32_t* row_of,
                               int32_t* offsets, int32_t* counts, hipStream_t stream) {
     int64_t chunk = 1024, blocks = (n + chunk - 1) / chunk;
     if (blocks > 256) {
@@ -604,27 +712,35 @@ hipError_t launch_rows_layout(const int32_t* idx, int64_t n, int64_t first, int6
 }
 
 template <class T, bool MASKED>
-static hipError_t run_dispatch_rows(const void* x, int64_t T_, const int32_t* row_of, int64_t topk, const RowsOut& o,
-                                    const int32_t* offsets, const int32_t* counts, int64_t G, int64_t R,
-                                    hipStream_t stream) {
-    const int64_t chunks = (o.H + kWaveChan - 1) / kWaveChan, waves = T_ * chunks, blocks = (waves + 3) / 4;
-    const int64_t grid = blocks + (MASKED ? 0 : (127 * G + 3) / 4);
+static hipError_t run_dispatch(const void* x, int64_t T_, const int32_t* idx, int64_t topk, int64_t first, int64_t G,
+                               int64_t R, const RowsOut& o, int32_t* row_of, int32_t* offsets, int32_t* counts,
+                               hipStream_t stream) {
+    const int64_t n = T_ * topk, chunks = (o.H + kWaveChan - 1) / kWaveChan, waves = T_ * chunks;
+    if (n <= kSmallEntries && waves > 0) {
+        const int64_t per_token = (chunks + 3) / 4, grid = T_ * per_token + (MASKED ? 0 : G);
+        return launch_kernel(dispatch_small<T, MASKED>, dim3(unsigned(grid)), dim3(256), stream, static_cast<const T*>(x),
+                             idx, uint32_t(T_), int(topk), uint32_t(per_token), int(first), uint32_t(G), o, row_of,
+                             offsets, counts);
+    }
+    const hipError_t e = launch_rows_layout(idx, n, first, G, MASKED ? o.rows_per : 0, row_of, offsets, counts, stream);
+    if (e != hipSuccess || waves == 0) return e;
+    const int64_t blocks = (waves + 3) / 4, grid = blocks + (MASKED ? 0 : (127 * G + 3) / 4);
     // (R rows bound what is written: the routing is known on the device only)
-    const bool stream_out = (R < T_ * topk ? R : T_ * topk) * o.H >= kStreamBytes;
+    const bool stream_out = (R < n ? R : n) * o.H >= kStreamBytes;
     return launch_kernel(stream_out ? dispatch_rows<T, MASKED, true> : dispatch_rows<T, MASKED, false>,
                          dim3(unsigned(grid)), dim3(256), stream, static_cast<const T*>(x), row_of, uint32_t(waves),
                          int(topk), uint32_t(chunks), uint32_t(blocks), o, offsets, counts, uint32_t(G), R);
 }
 
-hipError_t launch_dispatch_rows(const void* x, int bf16, int64_t T, int64_t H, const int32_t* row_of, int64_t topk,
-                                int64_t R, int64_t rows_per, const int32_t* offsets, const int32_t* counts, int64_t G,
-                                uint8_t* q, float* s, hipStream_t stream) {
-    const RowsOut o{q, s, H, (H + kBlock - 1) / kBlock, rows_per};
-    if (offsets)
-        return bf16 ? run_dispatch_rows<uint16_t, false>(x, T, row_of, topk, o, offsets, counts, G, R, stream)
-                    : run_dispatch_rows<float, false>(x, T, row_of, topk, o, offsets, counts, G, R, stream);
-    return bf16 ? run_dispatch_rows<uint16_t, true>(x, T, row_of, topk, o, offsets, counts, G, R, stream)
-                : run_dispatch_rows<float, true>(x, T, row_of, topk, o, offsets, counts, G, R, stream);
+hipError_t launch_dispatch(const void* x, int bf16, int64_t T, int64_t H, const int32_t* idx, int64_t topk,
+                           int64_t first, int64_t G, int64_t R, int64_t m_max, uint8_t* q, float* s, int32_t* row_of,
+                           int32_t* offsets, int32_t* counts, hipStream_t stream) {
+    const RowsOut o{q, s, H, (H + kBlock - 1) / kBlock, m_max ? m_max : R};
+    if (m_max)
+        return bf16 ? run_dispatch<uint16_t, true>(x, T, idx, topk, first, G, R, o, row_of, nullptr, counts, stream)
+                    : run_dispatch<float, true>(x, T, idx, topk, first, G, R, o, row_of, nullptr, counts, stream);
+    return bf16 ? run_dispatch<uint16_t, false>(x, T, idx, topk, first, G, R, o, row_of, offsets, counts, stream)
+                : run_dispatch<float, false>(x, T, idx, topk, first, G, R, o, row_of, offsets, counts, stream);
 }
 
 template <class TY, class TO>
