@@ -2463,7 +2463,8 @@ __global__ __launch_bounds__(MxTile::THREADS) void gemm_mxbs_o1_dense(GemmArgs a
     X(big_e1_b0_o1_dense, 0, 4, 2, 2, 2, 3, 1, 0, 1, 0)                    \
     X(big_e1_b1_o0_dense, 0, 4, 2, 2, 2, 3, 1, 1, 0, 0)                    \
     X(big_e1_b1_o1_dense, 0, 4, 2, 2, 2, 3, 1, 1, 1, 0)                    \
-    X(big_e0_b1_o1_wgrad, 0, 4, 2, 2, 2, 3, 0, 1, 1, 3)
+    X(big_e0_b1_o1_wgrad, 0, 4, 2, 2, 2, 3, 0, 1, 1, 3)                    \
+    X(dec_e0_b1_o1_wgrad, 1, 2, 4, 1, 1, 3, 0, 1, 1, 3)
 
 #define FP8FG_DEFINE_KERNEL(NAME, TILE, WM, WN, FM, FN, ST, E, BS, OF, MODE)                  \
     __global__ __launch_bounds__(kThreads) void gemm_##NAME(GemmArgs args) {                  \
@@ -3146,6 +3147,14 @@ bool wide_wgrad_fits(const GemmArgs& args) {
            WGRAD_BLOCKS * rows * 4 <= int64_t(0xFFFFFFFF);
 }
 
+// Weight gradients whose 256 x 256 tiles do not fill the chip's 256 CUs once
+// run 64 x 128 fold tiles: eight times as many workgroups, each with a shorter
+// prologue and epilogue.  Measured (us, 256-wide / 64 x 128), experts x rows x
+// M x N: 1 x 1024 x 512 x 512 34.4 / 11.4; 5 x 1111 x 512 x 768 24.4 / 8.8;
+// 8 x 4096 x 1024 x 1024 (128 tiles) 38.1 / 22.5; 8 x 8192 x 2048 x 1024 (256 tiles)
+// 62.2 / 56.9; 8 x 2048 x 2048 x 2048 (512 tiles) 44.1 / 57.3.
+constexpr int64_t kCus = 256;
+
 // gfx950 (MI350 series): eight XCDs, each with its own L2
 constexpr int kXcds = 8;
 // the masked layout's XCD grouping for tiles of bm rows: on when 8 divides the
@@ -3239,6 +3248,8 @@ hipError_t dispatch(int engine, GemmMode mode, int bscale_1x128, int out_fp32, c
     int tile = 0;
     if (mode == GemmMode::Masked && args.M <= 128)
         tile = wide ? 3 : 1;
+    else if (mode == GemmMode::Wgrad && tile_count<WideTile>(mode, args) <= kCus)
+        tile = 1;
     else if (wide)
         tile = 2;
     const int64_t tiles = tile == 0   ? tile_count<BigTile>(mode, args)

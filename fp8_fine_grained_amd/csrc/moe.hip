@@ -263,7 +263,7 @@ __global__ __launch_bounds__(256) void route_backward(const T* __restrict__ x, c
 //
 // One workgroup per `chunk` entries.  It counts every expert's entries before
 // its chunk and in all (32 counters per expert, one per lane pair, so that
-// the lanes of a wave never meet on an address; 16 entries per thread in
+// the lanes of a wave never meet on an address; 32 entries per thread in
 // flight), then ranks its own chunk 1024 entries at a time: the lanes of a wave
 // with the same expert find each other with one ballot per bit of the index,
 // the waves' counts are summed in order.  No workgroup waits for another.
@@ -288,15 +288,16 @@ __global__ __launch_bounds__(1024) void rows_layout(const int32_t* __restrict__ 
     auto count = [&](int64_t from, int64_t to) {
         int64_t i = from + 4 * t;
         typedef int i32x4 __attribute__((ext_vector_type(4)));
-        for (; i + 3 * 4096 + 4 <= to; i += 4 * 4096) {
-            i32x4 v[4];
+        for (; i + 7 * 4096 + 4 <= to; i += 8 * 4096) {
+            i32x4 v[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = ld<i32x4>(idx + i + 4096 * k);
+            for (int k = 0; k < 8; ++k) v[k] = ld<i32x4>(idx + i + 4096 * k);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 8; ++k)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) add(v[k][j]);
         }
+#pragma unroll 4
         for (; i + 4 <= to; i += 4096) {
             const i32x4 v = ld<i32x4>(idx + i);
 #pragma unroll

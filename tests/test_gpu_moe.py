@@ -504,18 +504,57 @@ def test_wgrad(M, N):
         held(more[g] - (ref + start[g]), gemm.U * mag + 2 * EPS * (np.abs(ref) + np.abs(start[g])), f"expert {g} accumulated")
 
 
-def test_wgrad_is_the_dense_call_per_expert():
-    rng = np.random.default_rng(4)
-    M, N, R = 320, 512, 1024
-    off = np.array([0, 640, 1024], np.int32)
+def check_experts(c, qa, sa, qb, sb, off, rng, start=None):
+    """Every expert's result on some of its rows, whole where it has no rows."""
+    M = qa.shape[0]
+    for g in range(len(off) - 1):
+        lo, hi = off[g], off[g + 1]
+        if lo == hi:
+            assert np.all(c[g] == (0 if start is None else start[g]))
+            continue
+        rows = np.unique(np.concatenate([np.arange(min(M, 3)), rng.integers(0, M, 24), np.arange(max(M - 3, 0), M)]))
+        ref, mag = gemm.gemm_blockscaled_ref(qa[:, lo:hi], sa[lo // 128:hi // 128], qb[:, lo:hi], sb[lo // 128:hi // 128], "1x128", rows=rows)
+        lim = gemm.U * mag
+        if start is not None:
+            ref = ref + start[g][rows]
+            lim = lim + 4 * EPS * (np.abs(ref) + np.abs(start[g][rows]))
+        held(c[g][rows] - ref, lim, f"expert {g}")
+
+
+@pytest.mark.parametrize("M,N", [(1000, 1024), (1024, 1024), (1024, 1040)])
+def test_wgrad_large_tiles(M, N):
+    """Over 256 tiles of 256 x 256: one expert longer than an accumulator takes, several short ones, some empty."""
+    rng = np.random.default_rng(M + N)
+    blocks = np.array([1, 0, 2, 70, 1, 3, 0, 1, 2, 1, 1, 4, 1, 0, 1, 2, 1, 1, 64, 1])
+    off = np.concatenate([[0], np.cumsum(blocks)]).astype(np.int32) * 128
+    R = int(off[-1]) + 256
     qa, sa = operand(rng, M, R, 1e-3)
     qb, sb = operand(rng, N, R, 1.0)
-    c = fp8.fp8_grouped_gemm_wgrad(dev(qa), dev(sa), dev(qb), dev(sb), dev(off))
-    for g in range(2):
-        lo, hi = off[g], off[g + 1]
-        d = fp8.fp8_gemm_blockscaled(dev(qa[:, lo:hi]), dev(sa[lo // 128:hi // 128]), dev(qb[:, lo:hi]), dev(sb[lo // 128:hi // 128]),
-                                     fp8.BSCALE_1x128, torch.float32)
-        assert torch.equal(c[g], d)
+    qa[:, off[-1]:], qb[:, off[-1]:] = 0x7F, 0x7F
+    args = (dev(qa), dev(sa), dev(qb), dev(sb), dev(off))
+    G = len(blocks)
+    c = fp8.fp8_grouped_gemm_wgrad(*args, out=torch.full((G, M, N), float("nan"), device=DEV))
+    check_experts(host(c), qa, sa, qb, sb, off, rng)
+    start = rng.standard_normal((G, M, N)).astype(np.float32)
+    more = fp8.fp8_grouped_gemm_wgrad(*args, out=dev(start), accumulate=True)
+    check_experts(host(more), qa, sa, qb, sb, off, rng, start)
+    if N % 256 == 0:                                       # the dense call's bits, up to 64 K-blocks
+        for g in (2, 11, 18):
+            k, kb = slice(off[g], off[g + 1]), slice(off[g] // 128, off[g + 1] // 128)
+            d = fp8.fp8_gemm_blockscaled(dev(qa[:, k]), dev(sa[kb]), dev(qb[:, k]), dev(sb[kb]), fp8.BSCALE_1x128, torch.float32)
+            assert torch.equal(c[g], d)
+
+
+def test_wgrad_many_experts_large_tiles():
+    """Over 64 experts and over 256 tiles: the natural order of the experts."""
+    rng = np.random.default_rng(16)
+    G, M, N = 80, 512, 512
+    blocks = rng.integers(0, 3, G)
+    off = np.concatenate([[0], np.cumsum(blocks)]).astype(np.int32) * 128
+    qa, sa = operand(rng, M, int(off[-1]), 1e-3)
+    qb, sb = operand(rng, N, int(off[-1]), 1.0)
+    c = host(fp8.fp8_grouped_gemm_wgrad(dev(qa), dev(sa), dev(qb), dev(sb), dev(off)))
+    check_experts(c, qa, sa, qb, sb, off, rng)
 
 
 @pytest.mark.parametrize("N", [256, 128])
