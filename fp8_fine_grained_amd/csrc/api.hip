@@ -534,7 +534,8 @@ int fp8_grouped_gemm_wgrad(const uint8_t* a, const float* sa, const uint8_t* b, 
     if (G == 0 || M == 0 || N == 0) return FP8FG_OK;
     const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
     if (G > kMaxDim / tiles) return FP8FG_ERR_UNSUPPORTED;
-    fp8fg::GemmArgs args{a, sa, b, sb, c, group_offsets, M, N, R, G, nullptr, accumulate};
+    fp8fg::GemmArgs args{a, sa, b, sb, c, group_offsets, M, N, R, G, nullptr};
+    args.accumulate = accumulate;
     return hip_status(fp8fg::launch_gemm(0, fp8fg::GemmMode::Wgrad, 1, 1, args, static_cast<hipStream_t>(stream)));
 }
 

@@ -117,19 +117,41 @@ __device__ __forceinline__ T lanes_max(T v) { return lanes_reduce<L>(v, MaxOp())
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) { return lanes_reduce<L>(v, SumOp()); }
 
-// 1 / (1 + exp(-x)), within about two roundings.  exp is 2^(-x log2 e) with the
-// product's low part put back; the reciprocal's one Newton step takes the
-// place of an IEEE division.  x is clamped where the result is 1 to FP32's last bit,
-// or below FP32's smallest normal.
-__device__ __forceinline__ float sigmoid_fast(float x) {
+// exp(-x) as 2^(-x log2 e) with the product's low part put back.  x is clamped
+// where 1 / (1 + exp(-x)) is 1 to FP32's last bit, or below FP32's smallest normal.
+__device__ __forceinline__ float exp_minus(float x) {
     constexpr float kHi = -0x1.715476p+0f, kLo = -0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;      // -log2 e, ln 2
     x = __builtin_amdgcn_fmed3f(x, -88.0f, 100.0f);
     const float t = x * kHi;
     const float lo = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -t));
     const float e = __builtin_amdgcn_exp2f(t);
-    const float d = 1.0f + __builtin_fmaf(e, lo * kLn2, e);
+    return __builtin_fmaf(e, lo * kLn2, e);
+}
+
+// sigmoid(x) = 1 / (1 + exp(-x)), within about two roundings: the reciprocal's
+// one Newton step takes the place of an IEEE division.  `rest` takes
+// 1 - sigmoid(x) = exp(-x) sigmoid(x) with a small relative error of its own (the
+// difference would lose it for large x).
+__device__ __forceinline__ float sigmoid_fast(float x, float& rest) {
+    const float e = exp_minus(x), d = 1.0f + e;
     const float r = __builtin_amdgcn_rcpf(d);
-    return __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);
+    const float sg = __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);
+    rest = e * sg;
+    return sg;
+}
+__device__ __forceinline__ float sigmoid_fast(float x) {
+    float rest;
+    return sigmoid_fast(x, rest);
+}
+
+// g sigmoid(g) u = g u / (1 + exp(-g)): the quotient of the product and the sum,
+// corrected once by its remainder with what either lost in rounding, so that
+// only the exponential's error and the last rounding remain
+__device__ __forceinline__ float gate_of(float g, float u) {
+    const float e = exp_minus(g), d = 1.0f + e, n = g * u;
+    const float r = __builtin_amdgcn_rcpf(d), q = n * r;
+    const float d_lost = e < 1.0f ? e - (d - 1.0f) : 1.0f - (d - e), n_lost = __builtin_fmaf(g, u, -n);
+    return __builtin_fmaf(__builtin_fmaf(-q, d_lost, __builtin_fmaf(-q, d, n) + n_lost), r, q);
 }
 
 // cvt4 without clearing its result first: the conversion of a pair keeps the

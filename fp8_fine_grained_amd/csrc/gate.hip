@@ -31,7 +31,7 @@ __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t 
         load_n<16, true>(row + (in + r * uint32_t(I)), g);
         load_n<16, true>(row + I + (in + r * uint32_t(I)), u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) h[i] = g[i] * sigmoid_fast(g[i]) * u[i];
+        for (int i = 0; i < 16; ++i) h[i] = gate_of(g[i], u[i]);
         float a;
         const u32x4 codes = encode16<Derived>(h, a);
         st_out<STREAM>(q + (b * M + m0) * I + kb * kBlock + in, codes);
@@ -140,8 +140,9 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
             for (int o = 0; o < 2; ++o) {
                 const int j = 2 * p + o;
                 const float g = g2[o] * in[i].sg, u = u2[o] * in[i].su, e = dh_of(in[i].dh, j);
-                const float sg = sigmoid_fast(g), si = g * sg;
-                d[0][i][j] = e * u * __builtin_fmaf(si, 1.0f - sg, sg);      // sg (1 + g (1 - sg))
+                float rest;
+                const float sg = sigmoid_fast(g, rest), si = g * sg;
+                d[0][i][j] = e * u * __builtin_fmaf(si, rest, sg);      // sg (1 + g (1 - sg))
                 d[1][i][j] = e * si;
                 d[2][i][j] = si * u;
             }

@@ -1325,19 +1325,21 @@ struct IlCopier {
     }
 };
 
-template <class W, int CW, bool BS1 = false>
+// WHOLE: the contraction is the whole row (pitch == K)
+template <class W, int CW, bool BS1 = false, bool WHOLE = true>
 __device__ __forceinline__ IlCopier<W, CW> make_il_copier(const Tile& t, int wave, int lane, int64_t K, int64_t N,
-                                                          int64_t n0, int64_t pitch) {
+                                                          int64_t n0, int64_t row_pitch) {
     typedef WStage<W> S;
     typedef IlCopier<W, CW> C;
     C c;
     c.K = K;
+    const int64_t pitch = WHOLE ? K : row_pitch;
     c.copier = wave < CW;
     const int cw = c.copier ? wave : 0;     // non-copying waves set up (unused) offsets of wave 0
     const int sub = lane >> 2, slot = lane & 3;
     const int64_t tile_rows = t.rows_valid - t.m0 < W::BM ? t.rows_valid - t.m0 : W::BM;   // >= 1
-    c.ra = make_rsrc(t.A + t.m0 * pitch, uint32_t((tile_rows - 1) * pitch + K));
-    c.rb = make_rsrc(t.B + n0 * pitch, uint32_t((W::BN - 1) * pitch + K));
+    c.ra = make_rsrc(t.A + t.m0 * pitch, uint32_t(WHOLE ? tile_rows * K : (tile_rows - 1) * pitch + K));
+    c.rb = make_rsrc(t.B + n0 * pitch, uint32_t(WHOLE ? W::BN * K : (W::BN - 1) * pitch + K));
     // row r = r0 + sub of a piece holds the lane's chunk at slot ^ ((r >> 2) & 3),
     // and with r0 % 16 == 0 (sub < 16) that is slot ^ ((sub >> 2) & 3) in every piece
     static_assert(W::ROWS_PER_PIECE % 16 == 0, "one swizzle phase per piece");
@@ -1916,9 +1918,9 @@ __device__ __forceinline__ void il_kloop(uint8_t* lds_raw, WStage<W>* ring, cons
 
 // BS1: B is 1x128-scaled (one scale per column and K-block, [K/128][N]: the
 // Wgrad operand); dense layout, BF16 / FP32 out.
-// K: the contraction's length from t.A and t.B on, whose rows are `pitch`
-// bytes apart; add: the FP32 result is added to C.
-template <class W, int OUT, bool BS1 = false, bool ADD = false>
+// PART: the contraction is a part of the rows, K bytes from t.A and t.B on, the
+// rows `pitch` bytes apart, and add: the FP32 result is added to C.
+template <class W, int OUT, bool BS1 = false, bool PART = false>
 __device__ __forceinline__ void wide_il_tile(const GemmArgs& args, uint8_t* lds_raw, const Tile& t, int64_t K,
                                              int64_t pitch, bool add) {
     static_assert(!BS1 || OUT != 2, "1x128 B: BF16 / FP32 out");
@@ -1933,7 +1935,7 @@ __device__ __forceinline__ void wide_il_tile(const GemmArgs& args, uint8_t* lds_
     const int64_t N = args.N;
     const int halves = int(2 * ((K + BK - 1) / BK));
     const int64_t n0 = int64_t(t.bn) * W::BN;
-    const IlCopier<W, IL_COPY_WAVES> cp = make_il_copier<W, IL_COPY_WAVES, BS1>(t, wave, lane, K, N, n0, pitch);
+    const IlCopier<W, IL_COPY_WAVES> cp = make_il_copier<W, IL_COPY_WAVES, BS1, !PART>(t, wave, lane, K, N, n0, pitch);
     const int64_t wrow0 = t.m0 + wm * FM * 32;
     const bool live = wrow0 < t.rows_valid;   // uniform
     const int r = lane & 31, h = lane >> 5;
@@ -2078,7 +2080,7 @@ __device__ __forceinline__ void wide_il_tile(const GemmArgs& args, uint8_t* lds_
                         v[j] = v[j] * ld<v4f>(lds_raw + cl + 1024u + uint32_t((ni * 32 + 8 * j + 4 * h) * 4));
                 }
                 float* c = static_cast<float*>(args.c) + t.c_base + m0 * N + n0 + wn * FN * 32 + ni * 32;
-                if (ADD && add)
+                if (PART && add)
                     store_f32_rows64<true>(c, N, lane, t.rows_valid - m0, v);
                 else
                     store_f32_rows64(c, N, lane, t.rows_valid - m0, v);
