@@ -484,6 +484,14 @@ def fp8_grouped_gemm_masked_tiled(a, sa, b_tiled, sb, masked_m, out_dtype=torch.
 
 # The operators around the grouped GEMMs of a mixture-of-experts layer.
 
+def _out(t, shape, dtype, like, name):
+    """An output: the caller's tensor once checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _need(t, dtype, shape, name)
+    return t
+
+
 def _f32_or_bf16(t, name):
     if t.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
@@ -509,10 +517,8 @@ def moe_route(logits, topk, bias=None, n_groups=1, topk_groups=1, group_top=1, s
     T, E = logits.shape
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
-    idx = _empty((T, topk), torch.int32, logits) if idx is None else idx
-    w = _empty((T, topk), torch.float32, logits) if w is None else w
-    _need(idx, torch.int32, (T, topk), "idx")
-    _need(w, torch.float32, (T, topk), "w")
+    idx = _out(idx, (T, topk), torch.int32, logits, "idx")
+    w = _out(w, (T, topk), torch.float32, logits, "w")
     _check("moe_route", load_library().moe_route(
         _ptr(logits), bf16, ld, _ptr(bias), T, E, topk, n_groups, topk_groups, group_top, score, int(bool(renormalize)),
         scale, _ptr(idx), _ptr(w), _stream(logits)))
@@ -527,8 +533,7 @@ def moe_route_backward(logits, idx, dw, score=SCORE_SIGMOID, renormalize=True, s
     topk = idx.shape[1]
     _need(idx, torch.int32, (T, topk), "idx")
     _need(dw, torch.float32, (T, topk), "dw")
-    out = _empty((T, E), logits.dtype, logits) if out is None else out
-    _need(out, logits.dtype, (T, E), "out")
+    out = _out(out, (T, E), logits.dtype, logits, "out")
     _check("moe_route_backward", load_library().moe_route_backward(
         _ptr(logits), bf16, ld, _ptr(idx), _ptr(dw), T, E, topk, score, int(bool(renormalize)), scale, _ptr(out),
         _stream(logits)))
@@ -554,10 +559,8 @@ def fp8_moe_dispatch_contiguous(x, idx, n_experts, first=0, M_total=None, q=None
     _need(idx, torch.int32, (T, topk), "idx")
     if M_total is None:
         M_total = moe_rows_bound(T, topk, n_experts) if q is None else q.shape[0]
-    q = _empty((M_total, H), torch.uint8, x) if q is None else q
-    s = _empty((_nb(H), M_total), torch.float32, x) if s is None else s
-    _need(q, torch.uint8, (M_total, H), "q")
-    _need(s, torch.float32, (_nb(H), M_total), "s")
+    q = _out(q, (M_total, H), torch.uint8, x, "q")
+    s = _out(s, (_nb(H), M_total), torch.float32, x, "s")
     row_of = _empty((T, topk), torch.int32, x)
     offsets = _empty((n_experts + 1,), torch.int32, x)
     counts = _empty((n_experts,), torch.int32, x)
@@ -575,10 +578,8 @@ def fp8_moe_dispatch_masked(x, idx, n_experts, M_max, first=0, q=None, s=None):
     topk = idx.shape[1]
     _need(x, x.dtype, (T, H), "x")
     _need(idx, torch.int32, (T, topk), "idx")
-    q = _empty((n_experts, M_max, H), torch.uint8, x) if q is None else q
-    s = _empty((n_experts, _nb(H), M_max), torch.float32, x) if s is None else s
-    _need(q, torch.uint8, (n_experts, M_max, H), "q")
-    _need(s, torch.float32, (n_experts, _nb(H), M_max), "s")
+    q = _out(q, (n_experts, M_max, H), torch.uint8, x, "q")
+    s = _out(s, (n_experts, _nb(H), M_max), torch.float32, x, "s")
     row_of = _empty((T, topk), torch.int32, x)
     masked_m = _empty((n_experts,), torch.int32, x)
     _check("fp8_moe_dispatch_masked", load_library().fp8_moe_dispatch_masked(
@@ -598,8 +599,7 @@ def moe_combine(y, row_of, w=None, out_dtype=torch.bfloat16, out=None):
     _need(row_of, torch.int32, (T, topk), "row_of")
     if w is not None:
         _need(w, torch.float32, (T, topk), "w")
-    out = _empty((T, H), out_dtype, y) if out is None else out
-    _need(out, out_dtype, (T, H), "out")
+    out = _out(out, (T, H), out_dtype, y, "out")
     _check("moe_combine", load_library().moe_combine(
         _ptr(y), _f32_or_bf16(y, "y"), R, H, _ptr(row_of), _ptr(w), T, topk, _ptr(out), _out_dtype(out_dtype), _stream(y)))
     return out
@@ -619,12 +619,9 @@ def fp8_moe_combine_backward(dout, y, row_of, w, group_offsets, counts, q=None, 
     _need(w, torch.float32, (T, topk), "w")
     _need(group_offsets, torch.int32, (G + 1,), "group_offsets")
     _need(counts, torch.int32, (G,), "counts")
-    q = _empty((R, H), torch.uint8, y) if q is None else q
-    s = _empty((_nb(H), R), torch.float32, y) if s is None else s
-    dw = _empty((T, topk), torch.float32, y) if dw is None else dw
-    _need(q, torch.uint8, (R, H), "q")
-    _need(s, torch.float32, (_nb(H), R), "s")
-    _need(dw, torch.float32, (T, topk), "dw")
+    q = _out(q, (R, H), torch.uint8, y, "q")
+    s = _out(s, (_nb(H), R), torch.float32, y, "s")
+    dw = _out(dw, (T, topk), torch.float32, y, "dw")
     _check("fp8_moe_combine_backward", load_library().fp8_moe_combine_backward(
         _ptr(dout), _f32_or_bf16(dout, "dout"), T, H, _ptr(y), _f32_or_bf16(y, "y"), R, _ptr(row_of), _ptr(w), topk,
         _ptr(group_offsets), _ptr(counts), G, _ptr(q), _ptr(s), _ptr(dw), _stream(y)))
@@ -650,16 +647,12 @@ def fp8_swiglu(gu, rows=None, checkpoint=False, q=None, s=None, qc=None, sc=None
     _need(gu, gu.dtype, gu.shape, "gu")
     _need_rows(rows, G)
     ss = lead[:-1] + (_nb(I), M)
-    q = _empty(lead + (I,), torch.uint8, gu) if q is None else q
-    s = _empty(ss, torch.float32, gu) if s is None else s
-    _need(q, torch.uint8, lead + (I,), "q")
-    _need(s, torch.float32, ss, "s")
+    q = _out(q, lead + (I,), torch.uint8, gu, "q")
+    s = _out(s, ss, torch.float32, gu, "s")
     if checkpoint:
         cs = lead[:-1] + (2 * _nb(I), M)
-        qc = _empty(gu.shape, torch.uint8, gu) if qc is None else qc
-        sc = _empty(cs, torch.float32, gu) if sc is None else sc
-        _need(qc, torch.uint8, gu.shape, "qc")
-        _need(sc, torch.float32, cs, "sc")
+        qc = _out(qc, gu.shape, torch.uint8, gu, "qc")
+        sc = _out(sc, cs, torch.float32, gu, "sc")
     elif qc is not None or sc is not None:
         raise ValueError("qc and sc are written with checkpoint=True only")
     _check("fp8_swiglu", load_library().fp8_swiglu(
@@ -680,11 +673,10 @@ def fp8_swiglu_backward(qc, sc, dh, rows=None, out=None):
     _need_rows(rows, 1)
     shapes = ((torch.uint8, (M, 2 * I), "q"), (torch.float32, (2 * _nb(I), M), "s"), (torch.uint8, (2 * I, M), "qt"),
               (torch.float32, (_nb(M), 2 * I), "st"), (torch.uint8, (I, M), "qh"), (torch.float32, (_nb(M), I), "sh"))
-    out = tuple(_empty(shape, dtype, dh) for dtype, shape, _ in shapes) if out is None else tuple(out)
+    out = (None,) * 6 if out is None else tuple(out)
     if len(out) != 6:
         raise ValueError("out must hold six tensors")
-    for t, (dtype, shape, name) in zip(out, shapes):
-        _need(t, dtype, shape, name)
+    out = tuple(_out(t, shape, dtype, dh, name) for t, (dtype, shape, name) in zip(out, shapes))
     _check("fp8_swiglu_backward", load_library().fp8_swiglu_backward(
         _ptr(qc), _ptr(sc), _ptr(dh), _f32_or_bf16(dh, "dh"), M, I, _ptr(rows), *(_ptr(t) for t in out), _stream(dh)))
     return out
@@ -705,8 +697,7 @@ def fp8_grouped_gemm_wgrad(a, sa, b, sb, group_offsets, out=None, accumulate=Fal
     _need(group_offsets, torch.int32, (G + 1,), "group_offsets")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    out = _empty((G, M, N), torch.float32, a) if out is None else out
-    _need(out, torch.float32, (G, M, N), "out")
+    out = _out(out, (G, M, N), torch.float32, a, "out")
     _check("fp8_grouped_gemm_wgrad", load_library().fp8_grouped_gemm_wgrad(
         _ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(group_offsets), G, M, N, R, _ptr(out), int(bool(accumulate)),
         _stream(a)))

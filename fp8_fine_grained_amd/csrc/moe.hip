@@ -534,25 +534,28 @@ __global__ __launch_bounds__(256) void dispatch_small(const T* __restrict__ x, c
 template <class TY, class TO>
 __global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t R, int64_t H,
                                                const int32_t* __restrict__ row_of, const float* __restrict__ wts,
-                                               int64_t T_, int topk, int64_t chunks, TO* __restrict__ out) {
+                                               uint32_t waves, int topk, uint32_t chunks, TO* __restrict__ out) {
     const int lane = threadIdx.x & 63;
-    const int64_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + int64_t(blockIdx.x) * 4;
-    if (w >= T_ * chunks) return;
-    const int64_t token = w / chunks, ch = (w - token * chunks) * 512 + lane * 8;
+    const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + blockIdx.x * 4;
+    if (w >= waves) return;
+    const uint32_t token = w / chunks, ch = (w - token * chunks) * 512 + lane * 8;
     if (ch >= H) return;
+    const int32_t* rows = row_of + int64_t(token) * topk;
+    const float* wt = wts ? wts + int64_t(token) * topk : nullptr;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+#pragma unroll 4
     for (int j = 0; j < topk; ++j) {
-        const int64_t r = row_of[token * topk + j];
+        const int64_t r = rows[j];
         if (r < 0 || r >= R) continue;
-        const float wt = wts ? wts[token * topk + j] : 1.0f;
+        const float f = wt ? wt[j] : 1.0f;
         float v[8];
         load_n<8, true>(y + r * H + ch, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(wt, v[i], acc[i]);
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(f, v[i], acc[i]);
     }
-    store_n<8>(out + token * H + ch, acc);
+    store_n<8>(out + int64_t(token) * H + ch, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -749,7 +752,7 @@ static hipError_t run_combine(const void* y, int64_t R, int64_t H, const int32_t
                               int64_t topk, void* out, hipStream_t stream) {
     const int64_t chunks = (H + 511) / 512, blocks = (T * chunks + 3) / 4;
     return launch_kernel(combine<TY, TO>, dim3(unsigned(blocks)), dim3(256), stream, static_cast<const TY*>(y), R, H,
-                         row_of, w, T, int(topk), chunks, static_cast<TO*>(out));
+                         row_of, w, uint32_t(T * chunks), int(topk), uint32_t(chunks), static_cast<TO*>(out));
 }
 
 hipError_t launch_combine(const void* y, int y_bf16, int64_t R, int64_t H, const int32_t* row_of, const float* w,

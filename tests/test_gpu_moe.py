@@ -596,3 +596,35 @@ def test_wgrad_many_experts_and_offsets_out_of_range():
         ref, mag = gemm.gemm_blockscaled_ref(qa[:, lo:hi], sa[lo // 128:hi // 128], qb[:, lo:hi], sb[lo // 128:hi // 128], "1x128")
         held(c[g] - ref, gemm.U * mag, f"expert {g}")
     assert np.all(c[2] == 0)
+
+
+# ---------------------------------------------------------------------------
+# capture
+
+def test_decode_path_in_a_graph():
+    """Route, dispatch, gate and combine captured once and replayed with new inputs, eager work in between."""
+    T, E, H, I, M = 24, 16, 256, 128, 32
+    g = torch.Generator(device=DEV).manual_seed(1)
+    logits = torch.randn(T, E, generator=g, device=DEV)
+    x = torch.randn(T, H, generator=g, device=DEV).bfloat16()
+    gu = torch.randn(E, M, 2 * I, generator=g, device=DEV).bfloat16()
+
+    def step():
+        idx, w = fp8.moe_route(logits, 4, score=fp8.SCORE_SOFTMAX, n_groups=4, topk_groups=2)
+        q, s, row, mm = fp8.fp8_moe_dispatch_masked(x, idx, E, M)
+        h, hs = fp8.fp8_swiglu(gu, mm)
+        return idx, w, row, mm, fp8.moe_combine(gu, row, w)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for k in range(4):
+        logits.copy_(torch.randn(T, E, generator=g, device=DEV))
+        gu.copy_(torch.randn(E, M, 2 * I, generator=g, device=DEV))
+        graph.replay()
+        got = [t.clone() for t in out]
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), k
