@@ -39,6 +39,24 @@ __device__ __forceinline__ void load_n(const uint16_t* p, float (&v)[N]) {
         }
     }
 }
+// N consecutive elements as loaded, widened when they are used: a load under a
+// branch then stays in flight past it
+template <class T, int N>
+struct Raw {
+    static constexpr int W = N * int(sizeof(T)) / 16;
+    u32x4 w[W];
+    template <bool ONCE = false>
+    __device__ __forceinline__ void load(const T* p) {
+        const uint8_t* b = reinterpret_cast<const uint8_t*>(p);
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = ONCE ? ld_once<u32x4>(b + 16 * i) : ld<u32x4>(b + 16 * i);
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i >> 2][i & 3]);
+        const uint32_t two = w[i >> 3][(i >> 1) & 3];
+        return __uint_as_float((i & 1) ? two & 0xFFFF0000u : two << 16);
+    }
+};
 template <int N>
 __device__ __forceinline__ void store_n(float* p, const float (&v)[N]) {
 #pragma unroll

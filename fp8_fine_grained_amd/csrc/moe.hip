@@ -545,15 +545,26 @@ __global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-    for (int j = 0; j < topk; ++j) {
-        const int64_t r = rows[j];
-        if (r < 0 || r >= R) continue;
-        const float f = wt ? wt[j] : 1.0f;
-        float v[8];
-        load_n<8, true>(y + r * H + ch, v);
+    // four entries at a time, their loads in flight together.  Measured (us, one
+    // at a time / four): 64 tokens of 7168 channels x 8 rows 4.9 / 4.4, 512 11.6 /
+    // 11.3, 8192 182.2 / 183.0.
+    for (int j0 = 0; j0 < topk; j0 += 4) {
+        bool has[4];
+        Raw<TY, 8> v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(f, v[i], acc[i]);
+        for (int j = 0; j < 4; ++j) {
+            const int64_t r = j0 + j < topk ? rows[j0 + j] : -1;
+            has[j] = r >= 0 && r < R;
+            if (has[j]) v[j].template load<true>(y + r * H + ch);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (has[j]) {
+                const float f = wt ? wt[j0 + j] : 1.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = fmaf(f, v[j].get(i), acc[i]);
+            }
+        }
     }
     store_n<8>(out + int64_t(token) * H + ch, acc);
 }
@@ -594,28 +605,20 @@ __global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ d
         float sc;
         const u32x4 code = encode16<typename encoder_of<TD>::type>(v, sc);
         const uint32_t kb = c * 8 + (lane >> 3);
-        // four entries at a time, their loads in flight together (an entry
-        // without a row reads row 0 and is left out)
+        // (two or four entries' loads together measured no faster: 121.9 and
+        // 125.6 us against 121.6 at 3001 tokens x 8 rows of 7168)
 #pragma unroll
-        for (int j0 = 0; j0 < kMaxTopk; j0 += 4) {
-            if (j0 < topk) {
-                int64_t r[4];
-                float u[4][kChan];
+        for (int j = 0; j < kMaxTopk; ++j) {
+            if (j < topk) {
+                const int64_t r = rows[j];
+                if (r >= 0 && r < R && in) {
+                    Raw<TY, kChan> u;
+                    u.load(y + r * o.H + ch);
+                    const uint32_t flip = wt[j] < 0.0f ? 0x80808080u : 0u;
+                    st_out<STREAM>(o.q + r * o.H + ch, u32x4{code[0] ^ flip, code[1] ^ flip, code[2] ^ flip, code[3] ^ flip});
+                    if ((lane & 7) == 0) *o.scale<false>(uint32_t(r), kb) = sc * fabsf(wt[j]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    r[j] = j0 + j < topk ? rows[j0 + j] : -1;
-                    if (r[j] >= R) r[j] = -1;
-                    if (in && R > 0) load_n<kChan>(y + (r[j] < 0 ? 0 : r[j]) * o.H + ch, u[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (r[j] >= 0 && in) {
-                        const uint32_t flip = wt[j0 + j] < 0.0f ? 0x80808080u : 0u;
-                        st_out<STREAM>(o.q + r[j] * o.H + ch, u32x4{code[0] ^ flip, code[1] ^ flip, code[2] ^ flip, code[3] ^ flip});
-                        if ((lane & 7) == 0) *o.scale<false>(uint32_t(r[j]), kb) = sc * fabsf(wt[j0 + j]);
-#pragma unroll
-                        for (int i = 0; i < kChan; ++i) dot[j0 + j] = fmaf(v[i], u[j][i], dot[j0 + j]);
-                    }
+                    for (int i = 0; i < kChan; ++i) dot[j] = fmaf(v[i], u.get(i), dot[j]);
                 }
             }
         }
