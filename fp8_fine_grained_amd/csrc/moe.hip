@@ -20,6 +20,10 @@ namespace moe_detail {
 // is -1 and the weight 0.  Weights are scale * s, divided by their sum when
 // renormalised.
 //
+// Bound by instruction issue and by the chain of dependent reductions, not by
+// memory: 8192 x 256 logits (8.9 MB, 1.7 us at this card's copy rate) take 9.8 us,
+// 64 x 256 take 4.9 us, launch included.
+//
 // LPT lanes hold a token's row; a lane owns V consecutive experts of one
 // group (groups rounded up to a power of two of lane runs), so ascending
 // lanes are ascending experts and ties fall to the lowest lane.  Scores are
@@ -266,7 +270,8 @@ __global__ __launch_bounds__(256) void route_backward(const T* __restrict__ x, c
 // the lanes of a wave never meet on an address; 32 entries per thread in
 // flight), then ranks its own chunk 1024 entries at a time: the lanes of a wave
 // with the same expert find each other with one ballot per bit of the index,
-// the waves' counts are summed in order.  No workgroup waits for another.
+// the waves' counts are summed in order.  No workgroup waits for another, at the
+// price of each reading every entry: 65536 entries take 9.8 us (64 workgroups).
 constexpr int kMaxLocal = 256;
 
 __global__ __launch_bounds__(1024) void rows_layout(const int32_t* __restrict__ idx, int64_t n, int first, int G,
@@ -378,7 +383,11 @@ __global__ __launch_bounds__(1024) void rows_layout(const int32_t* __restrict__ 
 // ---------------------------------------------------------------------------
 // A token's row quantized 1x128 and written to its rows.  A wave takes 1024
 // channels of one token: 16 per lane, eight lanes to a 128-group, so one
-// store instruction writes 1 KB of a row.
+// store instruction writes 1 KB of a row.  Reading each token once and writing its
+// codes k times moves 602 MB for 8192 tokens x 7168 channels x 8 rows; a row by row gather
+// would read (and quantize) each token eight times.  Bound by the writes: 131 us,
+// 4.6 TB/s against 5.2 for a plain copy; without the scales' scattered 4-byte
+// writes it takes 121 us.
 constexpr int kChan = 16, kWaveChan = 64 * kChan;
 
 struct RowsOut {
@@ -432,8 +441,11 @@ __global__ __launch_bounds__(256) void dispatch_rows(const T* __restrict__ x, co
     float v[kChan];
 #pragma unroll
     for (int i = 0; i < kChan; ++i) v[i] = 0.0f;
-    if (ch < o.H) load_n<kChan, true>(x + int64_t(token) * o.H + ch, v);
     const int32_t* rows = row_of + int64_t(token) * topk;
+    int32_t none = -1;
+    for (int j = 0; j < topk; ++j) none &= rows[j];
+    if (none < 0) return;                                // every entry elsewhere (-1): the token is not read
+    if (ch < o.H) load_n<kChan, true>(x + int64_t(token) * o.H + ch, v);
     float sc;
     const u32x4 code = encode16<typename encoder_of<T>::type>(v, sc);
     if (ch < o.H)
@@ -453,7 +465,8 @@ __global__ __launch_bounds__(256) void dispatch_rows(const T* __restrict__ x, co
 // The row layout and the rows themselves in one launch, for few entries: every
 // workgroup counts all entries for itself, so none waits for another.  A
 // workgroup takes four 1024-channel chunks of one token; in the contiguous layout G more
-// clear one expert's padding rows each.
+// clear one expert's padding rows each.  Bound by latency: 128 tokens x 8 entries,
+// 7168 channels, 4.9 us against 3.9 + 3.7 us for the two launches it replaces.
 constexpr int64_t kSmallEntries = 2048;
 
 template <class T, bool MASKED>
@@ -530,7 +543,9 @@ __global__ __launch_bounds__(256) void dispatch_small(const T* __restrict__ x, c
 
 // ---------------------------------------------------------------------------
 // out_t = sum_j w_tj y[row_tj], in the order of the choices, in FP32.  A wave
-// takes 512 channels of one token, eight per lane.
+// takes 512 channels of one token, eight per lane.  Bound by the reads: 8192
+// tokens x 8 rows of 7168 BF16 channels, 1.06 GB, 178 us, 5.9 TB/s (the rows are read once: with the
+// non-temporal hint, without it 204 us).
 template <class TY, class TO>
 __global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t R, int64_t H,
                                                const int32_t* __restrict__ row_of, const float* __restrict__ wts,
@@ -573,7 +588,8 @@ __global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t
 // The backward pass of combine: dw_tj = <dout_t, y[row_tj]> in FP32, and the
 // rows dy = w_tj Q(dout_t), where Q is the 1x128 quantization of dout_t: every
 // row of a token shares its codes, and its scales are |w| times the token's
-// (the sign of w goes into the codes).  A workgroup per token.
+// (the sign of w goes into the codes).  A workgroup per token.  Bound by memory:
+// 3001 tokens x 8 rows of 7168 BF16 channels, 565 MB, 122 us, 4.6 TB/s.
 template <class TD, class TY, bool STREAM>
 __global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ dout, const TY* __restrict__ y,
                                                         const int32_t* __restrict__ row_of,
