@@ -63,8 +63,8 @@ __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t 
 // register each time, over the eight waves in LDS.  The transposed codes pass through
 // LDS so that whole 128-byte row segments are written.  Everything is formed
 // from one read of the checkpoint and dh: 67456 x 2048, 1.27 GB, 254 us, 5.0 TB/s.  The
-// vector units are about as busy as the memory (53 instructions per value of dg, du
-// and h): the first form, with divisions and LDS shuffles, took 710 us.
+// vector units are about as busy as the memory (about 50 instructions for each
+// triple dg, du, h): the first form, with divisions and LDS shuffles, took 710 us.
 constexpr int kTileThreads = 512;
 
 // The transposed codes of a tile in LDS: word row4 of channel ch (rows 4 row4
