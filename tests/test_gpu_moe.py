@@ -159,6 +159,29 @@ def test_route_softmax_of_small_chosen_scores():
     assert np.allclose(host(w)[0], 0.5)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,ng,tg", [(8200, 256, 8, 4), (4100, 128, 4, 2), (8200, 240, 1, 1), (9000, 64, 1, 1)])
+def test_route_many_tokens(T, E, ng, tg, dtype):
+    """Batches that take other lane counts choose as small batches of the same tokens do."""
+    g = torch.Generator(device=DEV).manual_seed(T + E)
+    x = torch.randn(T, E, generator=g, device=DEV).to(dtype)
+    x[T // 2] = -np.inf
+    bias = torch.randn(E, generator=g, device=DEV) * 0.05
+    for score in (fp8.SCORE_SIGMOID, fp8.SCORE_SOFTMAX):
+        idx, w = fp8.moe_route(x, 8, bias, ng, tg, 2, score)
+        parts = [fp8.moe_route(x[i:i + 1000], 8, bias, ng, tg, 2, score) for i in range(0, T, 1000)]
+        idx2, w2 = torch.cat([p[0] for p in parts]), torch.cat([p[1] for p in parts])
+        if score == fp8.SCORE_SIGMOID:
+            assert torch.equal(idx, idx2) and torch.equal(w, w2)
+        else:                                              # the row's sum is taken in another order
+            same = (idx == idx2).all(1)
+            assert same.float().mean() > 0.999 and torch.allclose(w[same], w2[same], rtol=1e-5)
+        dw = torch.randn(T, 8, generator=g, device=DEV)
+        full = fp8.moe_route_backward(x, idx, dw, score)
+        part = torch.cat([fp8.moe_route_backward(x[i:i + 1000], idx[i:i + 1000], dw[i:i + 1000], score) for i in range(0, T, 1000)])
+        assert torch.equal(full, part)
+
+
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("score", [fp8.SCORE_SOFTMAX, fp8.SCORE_SIGMOID])
 @pytest.mark.parametrize("T,E,topk", [(1, 1, 1), (6, 8, 3), (65, 64, 6), (33, 100, 4), (40, 256, 8), (9, 300, 16), (5, 1024, 8)])
@@ -204,7 +227,8 @@ def entries(rng, T, E, topk, missing=0.1):
 
 DISPATCH = [  # T, H, E, topk, first, G
     (1, 16, 4, 1, 0, 4), (5, 128, 8, 2, 0, 8), (40, 272, 16, 8, 4, 8), (129, 1040, 8, 3, 0, 8), (300, 1024, 256, 8, 0, 256),
-    (700, 144, 60, 16, 30, 30), (2500, 128, 8, 2, 0, 8), (3, 7168, 32, 8, 0, 32), (1100, 32, 1, 1, 0, 1)]
+    (700, 144, 60, 16, 30, 30), (2500, 128, 8, 2, 0, 8), (3, 7168, 32, 8, 0, 32), (1100, 32, 1, 1, 0, 1),
+    (4200, 1024, 32, 8, 0, 32)]     # the last one's rows pass 32 MB: streaming stores
 
 
 @pytest.mark.parametrize("T,H,E,topk,first,G", DISPATCH)
@@ -359,7 +383,7 @@ def test_combine_ignores_rows_without_an_entry():
 
 
 @pytest.mark.parametrize("T,H,E,topk,first,G", [(1, 16, 4, 1, 0, 4), (40, 272, 16, 8, 4, 8), (129, 1040, 8, 3, 0, 8), (333, 2048, 24, 16, 0, 6),
-                                                (5, 7168, 32, 8, 0, 32)])
+                                                (5, 7168, 32, 8, 0, 32), (4200, 1024, 32, 8, 0, 32)])
 def test_combine_backward(T, H, E, topk, first, G):
     rng = np.random.default_rng(T * H)
     idx = entries(rng, T, E, topk)
@@ -469,6 +493,27 @@ def test_swiglu_backward(M, I, bf16):
         moe.check_quantized(qh[:, :done], sh[: -(-n // 128)], h.T[:, :done], gate_error(g, u).T[:, :done], "h")
         assert np.all(qt[:, done:] == 0x55) and np.all(qh[:, done:] == 0x55)
         assert np.all(st[-(-n // 128):] == 7.0) and np.all(sh[-(-n // 128):] == 7.0)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_gate_large(bf16):
+    """Outputs past 32 MB (streaming stores): the bits of small calls on the same rows."""
+    M, I = 6144, 2048
+    g = torch.Generator(device=DEV).manual_seed(3)
+    dtype = torch.bfloat16 if bf16 else torch.float32
+    gu = (torch.randn(M, 2 * I, generator=g, device=DEV) * 2).to(dtype)
+    dh = torch.randn(M, I, generator=g, device=DEV).to(dtype)
+    q, s, qc, sc = fp8.fp8_swiglu(gu, checkpoint=True)
+    big = fp8.fp8_swiglu_backward(qc, sc, dh)
+    for lo in (0, 2048, M - 256):
+        k = slice(lo, lo + 256)
+        a = fp8.fp8_swiglu(gu[k].contiguous(), checkpoint=True)
+        for t, u in zip((q[k], s[:, k], qc[k], sc[:, k]), a):
+            assert torch.equal(t, u)
+        b = fp8.fp8_swiglu_backward(qc[k].contiguous(), sc[:, k].contiguous(), dh[k].contiguous())
+        kb = slice(lo // 128, lo // 128 + 2)
+        for t, u in zip((big[0][k], big[1][:, k], big[2][:, k], big[3][kb], big[4][:, k], big[5][kb]), b):
+            assert torch.equal(t, u)
 
 
 # ---------------------------------------------------------------------------
