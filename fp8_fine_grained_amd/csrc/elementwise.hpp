@@ -321,18 +321,29 @@ struct Derived {
     }
 };
 
-// 16 consecutive values of a lane, eight lanes to a 128-group: the group's
+// N = 16 or 8 consecutive values of a lane, 128 / N lanes to a group: the group's
 // scale and the lane's codes (G: Bracket, Ratio for values that are BF16, or Derived)
-template <class G>
-__device__ __forceinline__ u32x4 encode16(const float (&v)[16], float& sc) {
+template <int N>
+struct code_words {
+    typedef u32x4 type;
+};
+template <>
+struct code_words<8> {
+    typedef u32x2_t type;
+};
+template <class G, int N>
+__device__ __forceinline__ typename code_words<N>::type encode_lane(const float (&v)[N], float& sc) {
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
-    const G g(lanes_max<8>(amax));
+    for (int i = 0; i < N; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    const G g(lanes_max<128 / N>(amax));
     sc = g.s;
-    uint32_t c[4];
-    g.template encode<4>(v, c);
-    return u32x4{c[0], c[1], c[2], c[3]};
+    uint32_t c[N / 4];
+    g.template encode<N / 4>(v, c);
+    typename code_words<N>::type w;
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = c[i];
+    return w;
 }
 // the encoding of values read as T
 template <class T>

@@ -12,12 +12,18 @@ namespace fp8fg {
 
 namespace gate_detail {
 
-// A workgroup takes 32 rows of one 128-channel group: eight lanes per row.
-// Row r of buffer blockIdx.z exists when r < rows[blockIdx.z] (rows may be
-// null: all of them).  Offsets within the 32 rows fit 32 bits.  Bound by memory
-// once the encoding is cheap: 66900 x 2048 with the checkpoint, 972 MB, 182 us, 5.3
-// TB/s (a plain copy 5.2); with an IEEE division and library exponential per element and
-// per-element checks in the encoding it took 248 us.
+// A workgroup takes 16 rows of one 128-channel group: 16 lanes per row, eight
+// channels per lane (one 16-byte load of BF16).  Row r of buffer blockIdx.z exists when r <
+// rows[blockIdx.z] (rows may be null: all of them).  Offsets within the 16
+// rows fit 32 bits.  Bound by memory once the encoding is cheap: 66900 x 2048 with
+// the checkpoint, 972 MB, 181 us, 5.4 TB/s (a plain copy 5.2); with an IEEE division and
+// library exponential per element and per-element checks in the encoding it took 248 us.
+// Few rows are bound by latency and a wave's instructions.  With 16 channels per
+// lane (us, 16 / 8): FP32 with the checkpoint 351 / 258, FP32 without 308 / 211 (a lane's
+// 64 bytes pass through the cache in four loads), BF16 182 / 181 and 130 / 122; masked,
+// 32 x 128 rows of which 1 to 64 are used, 6.4 / 5.1.
+constexpr int V = 8, kLanes = kBlock / V, kRows = 256 / kLanes;
+
 template <class T, bool STREAM>
 __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t M, int64_t I,
                                               const int32_t* __restrict__ rows, uint8_t* __restrict__ q,
@@ -26,26 +32,26 @@ __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t 
     const int64_t b = blockIdx.z, kb = blockIdx.x, nb = I / kBlock;
     int64_t end = rows ? int64_t(rows[b]) : M;
     end = end < M ? end : M;
-    const uint32_t r = threadIdx.x >> 3, c16 = (threadIdx.x & 7) * 16, in = r * uint32_t(I) + c16;
-    for (int64_t m0 = int64_t(blockIdx.y) * 32; m0 < end; m0 += int64_t(gridDim.y) * 32) {
+    const uint32_t r = threadIdx.x / kLanes, c = (threadIdx.x % kLanes) * V, in = r * uint32_t(I) + c;
+    for (int64_t m0 = int64_t(blockIdx.y) * kRows; m0 < end; m0 += int64_t(gridDim.y) * kRows) {
         if (m0 + r >= end) return;
         const T* row = gu + (b * M + m0) * 2 * I + kb * kBlock;
-        float g[16], u[16], h[16];
-        load_n<16, true>(row + (in + r * uint32_t(I)), g);
-        load_n<16, true>(row + I + (in + r * uint32_t(I)), u);
+        float g[V], u[V], h[V];
+        load_n<V, true>(row + (in + r * uint32_t(I)), g);
+        load_n<V, true>(row + I + (in + r * uint32_t(I)), u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) h[i] = gate_of(g[i], u[i]);
+        for (int i = 0; i < V; ++i) h[i] = gate_of(g[i], u[i]);
         float a;
-        const u32x4 codes = encode16<Derived>(h, a);
+        const auto codes = encode_lane<Derived>(h, a);
         st_out<STREAM>(q + (b * M + m0) * I + kb * kBlock + in, codes);
-        if (c16 == 0) s[(b * nb + kb) * M + m0 + r] = a;
+        if (c == 0) s[(b * nb + kb) * M + m0 + r] = a;
         if (qc) {
             float sg, su;
-            const u32x4 cg = encode16<Enc>(g, sg), cu = encode16<Enc>(u, su);
-            uint8_t* c = qc + (b * M + m0) * 2 * I + kb * kBlock;
-            st_out<STREAM>(c + (in + r * uint32_t(I)), cg);
-            st_out<STREAM>(c + I + (in + r * uint32_t(I)), cu);
-            if (c16 == 0) {
+            const auto cg = encode_lane<Enc>(g, sg), cu = encode_lane<Enc>(u, su);
+            uint8_t* out = qc + (b * M + m0) * 2 * I + kb * kBlock;
+            st_out<STREAM>(out + (in + r * uint32_t(I)), cg);
+            st_out<STREAM>(out + I + (in + r * uint32_t(I)), cu);
+            if (c == 0) {
                 sc[(b * 2 * nb + kb) * M + m0 + r] = sg;
                 sc[(b * 2 * nb + nb + kb) * M + m0 + r] = su;
             }
@@ -257,7 +263,7 @@ using namespace gate_detail;
 
 hipError_t launch_swiglu(const void* gu, int bf16, int64_t G, int64_t M, int64_t I, const int32_t* rows, uint8_t* q,
                          float* s, uint8_t* qc, float* sc, hipStream_t stream) {
-    int64_t groups = (M + 31) / 32;
+    int64_t groups = (M + kRows - 1) / kRows;
     if (groups > 65535) groups = 65535;      // the kernel strides over the rest
     const dim3 grid(unsigned(I / kBlock), unsigned(groups), unsigned(G));
     const bool stream_out = G * M * I * (qc ? 3 : 1) >= kStreamBytes;

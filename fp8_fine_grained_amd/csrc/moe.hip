@@ -381,14 +381,16 @@ __global__ __launch_bounds__(1024) void rows_layout(const int32_t* __restrict__ 
 }
 
 // ---------------------------------------------------------------------------
-// A token's row quantized 1x128 and written to its rows.  A wave takes 1024
-// channels of one token: 16 per lane, eight lanes to a 128-group, so one
-// store instruction writes 1 KB of a row.  Reading each token once and writing its
+// A token's row quantized 1x128 and written to its rows.  A wave takes 512
+// channels of one token: eight per lane, 16 lanes to a 128-group, so one store
+// instruction writes 512 bytes of a row.  Reading each token once and writing its
 // codes k times moves 602 MB for 8192 tokens x 7168 channels x 8 rows; a row by row gather
-// would read (and quantize) each token eight times.  Bound by the writes: 131 us,
+// would read (and quantize) each token eight times.  Bound by the writes: 130 us,
 // 4.6 TB/s against 5.2 for a plain copy; the scales' scattered 4-byte writes
-// are the difference (with plain stores, 146 us with them and 121 without).
-constexpr int kChan = 16, kWaveChan = 64 * kChan;
+// are the difference (with plain stores, 146 us with them and 121 without).  With
+// 16 channels per lane the whole call takes (us, 16 / 8) 143 / 141 there, 180 / 170 from
+// FP32 tokens, 25.4 / 27.4 for 1024 tokens, 34.5 / 32.6 for 20000 tokens x 512 channels x 6.
+constexpr int kChan = 8, kWaveChan = 64 * kChan, kLanes = kBlock / kChan;      // kLanes: lanes of a 128-group
 
 struct RowsOut {
     uint8_t* q;
@@ -447,15 +449,15 @@ __global__ __launch_bounds__(256) void dispatch_rows(const T* __restrict__ x, co
     if (none < 0) return;                                // every entry elsewhere (-1): the token is not read
     if (ch < o.H) load_n<kChan, true>(x + int64_t(token) * o.H + ch, v);
     float sc;
-    const u32x4 code = encode16<typename encoder_of<T>::type>(v, sc);
+    const auto code = encode_lane<typename encoder_of<T>::type>(v, sc);
     if (ch < o.H)
         for (int j = 0; j < topk; ++j) {
             const int64_t r = rows[j];
             if (r >= 0) st_out<STREAM>(o.q + r * o.H + ch, code);
         }
-    const uint32_t kb = c * 8 + (lane >> 3);
+    const uint32_t kb = c * (64 / kLanes) + lane / kLanes;
     if (kb < o.kbs)
-        for (int j = lane & 7; j < topk; j += 8) {
+        for (int j = lane % kLanes; j < topk; j += kLanes) {
             const int32_t r = rows[j];
             if (r >= 0) *o.scale<MASKED>(uint32_t(r), kb) = sc;
         }
@@ -464,10 +466,13 @@ __global__ __launch_bounds__(256) void dispatch_rows(const T* __restrict__ x, co
 // ---------------------------------------------------------------------------
 // The row layout and the rows themselves in one launch, for few entries: every
 // workgroup counts all entries for itself, so none waits for another.  A
-// workgroup takes four 1024-channel chunks of one token; in the contiguous layout G more
-// clear one expert's padding rows each.  Bound by latency: 128 tokens x 8 entries,
-// 7168 channels, 4.9 us against 3.9 + 3.7 us for the two launches it replaces.
+// workgroup takes four 512-channel chunks of one token; in the contiguous layout
+// kPadParts more per expert clear its padding rows.  Bound by latency: 128 tokens x 8 entries,
+// 7168 channels, 4.9 us against 3.9 + 3.7 us for the two launches it replaces.  The
+// padding is most of a small contiguous call: with 1 / 8 / 16 parts, 1 token x 2 rows of 7168
+// channels in 8 experts 13.7 / 4.5 / 4.0 us, 64 tokens x 8 in 32 experts 16.0 / 9.3 / 9.1.
 constexpr int64_t kSmallEntries = 2048;
+constexpr uint32_t kPadParts = 8;
 
 template <class T, bool MASKED>
 __global__ __launch_bounds__(256) void dispatch_small(const T* __restrict__ x, const int32_t* __restrict__ idx,
@@ -477,7 +482,7 @@ __global__ __launch_bounds__(256) void dispatch_small(const T* __restrict__ x, c
     __shared__ uint32_t all[kMaxLocal], before[kMaxLocal], start[kMaxLocal + 1];
     const uint32_t t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const uint32_t token = blockIdx.x / per_token, part = blockIdx.x - token * per_token;
-    const bool padding = token >= tokens;               // (uniform) expert blockIdx.x - tokens * per_token
+    const bool padding = token >= tokens;               // (uniform) the p-th of the padding's workgroups
     const uint32_t n = tokens * uint32_t(topk), mine = padding ? 0u : token * uint32_t(topk);
     const uint32_t c = part * 4 + wave, ch = c * kWaveChan + lane * kChan;
     float v[kChan];
@@ -514,8 +519,8 @@ __global__ __launch_bounds__(256) void dispatch_small(const T* __restrict__ x, c
     }
     if (blockIdx.x == 0 && t < G) counts[t] = int32_t(MASKED && all[t] > uint64_t(o.rows_per) ? uint32_t(o.rows_per) : all[t]);
     if (padding) {
-        const uint32_t g = blockIdx.x - tokens * per_token;
-        for (uint32_t row = start[g] + all[g] + wave; row < start[g + 1]; row += 4) {
+        const uint32_t p = blockIdx.x - tokens * per_token, g = p / kPadParts;
+        for (uint32_t row = start[g] + all[g] + p % kPadParts * 4 + wave; row < start[g + 1]; row += kPadParts * 4) {
             for (int64_t i = lane * 16; i < o.H; i += 1024) st<u32x4>(o.q + int64_t(row) * o.H + i, u32x4{0u, 0u, 0u, 0u});
             for (uint32_t kb = lane; kb < o.kbs; kb += 64) *o.scale<false>(row, kb) = 0.0f;
         }
@@ -529,14 +534,14 @@ __global__ __launch_bounds__(256) void dispatch_small(const T* __restrict__ x, c
     if (e < G && (!MASKED || rank < uint64_t(o.rows_per))) row = int32_t(MASKED ? e * uint32_t(o.rows_per) + rank : start[e] + rank);
     if (part == 0 && wave == 0 && lane < uint32_t(topk)) row_of[mine + lane] = row;
     float sc;
-    const u32x4 code = encode16<typename encoder_of<T>::type>(v, sc);
+    const auto code = encode_lane<typename encoder_of<T>::type>(v, sc);
     for (int j = 0; j < topk; ++j) {
         const int64_t r = __builtin_amdgcn_readlane(row, j);
-        if (r >= 0 && ch < o.H) st<u32x4>(o.q + r * o.H + ch, code);
+        if (r >= 0 && ch < o.H) st_out<false>(o.q + r * o.H + ch, code);
     }
-    const uint32_t kb = c * 8 + (lane >> 3);
-    for (int j0 = 0; j0 < topk; j0 += 8) {
-        const int32_t r = __shfl(row, j0 + int(lane & 7), 64);      // lanes from topk on hold -1
+    const uint32_t kb = c * (64 / kLanes) + lane / kLanes;
+    for (int j0 = 0; j0 < topk; j0 += kLanes) {
+        const int32_t r = __shfl(row, j0 + int(lane % kLanes), 64);      // lanes from topk on hold -1
         if (r >= 0 && kb < o.kbs) *o.scale<MASKED>(uint32_t(r), kb) = sc;
     }
 }
@@ -588,30 +593,41 @@ __global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t
 // The backward pass of combine: dw_tj = <dout_t, y[row_tj]> in FP32, and the
 // rows dy = w_tj Q(dout_t), where Q is the 1x128 quantization of dout_t: every
 // row of a token shares its codes, and its scales are |w| times the token's
-// (the sign of w goes into the codes).  A workgroup per token.  Bound by memory:
-// 3001 tokens x 8 rows of 7168 BF16 channels, 565 MB, 122 us, 4.6 TB/s.
-template <class TD, class TY, bool STREAM>
-__global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ dout, const TY* __restrict__ y,
-                                                        const int32_t* __restrict__ row_of,
-                                                        const float* __restrict__ wts, int64_t T_, int topk, RowsOut o,
-                                                        const int32_t* __restrict__ offsets,
-                                                        const int32_t* __restrict__ counts, int64_t G, int64_t R,
-                                                        float* __restrict__ dw) {
-    __shared__ float part[4][16];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t token = blockIdx.x < T_ ? int64_t(xcd_run(blockIdx.x, uint32_t(T_))) : int64_t(blockIdx.x);
-    if (token >= T_) {
-        const int64_t p = (token - T_) * 4 + wave;
+// (the sign of w goes into the codes).  A workgroup per token; a wave takes 512
+// channels at a time, eight per lane, and F entries' rows in flight.  Bound by memory:
+// 3001 tokens x 8 rows of 7168 BF16 channels, 565 MB, 112 us, 5.0 TB/s (16
+// channels per lane: 118 us).
+//
+// Waves of a workgroup: at most 4 for streaming outputs, 8 otherwise, 16 with four
+// entries in flight for few tokens, whose time is that of one workgroup; evenly loaded.
+// Measured (us, 4 / 8 / 16, 7168 channels x 8 rows in BF16 unless noted): 64 tokens 21.9 /
+// 15.6 / 11.0, 256 tokens 32.5 / 22.3 / 16.7; 512 tokens of 4096 channels 20.6 / 14.5 / 16.0, 512
+// tokens x 2 rows 11.5 / 9.0 / 11.9; 1024 tokens (streaming) 43.9 / 48.2 / 51.7, 3001 tokens
+// 112.4 / 115.2 / 140.5.
+constexpr int64_t kFewTokens = 256;
+
+template <class TD, class TY, bool STREAM, int F>
+__global__ __launch_bounds__(1024) void combine_backward(const TD* __restrict__ dout, const TY* __restrict__ y,
+                                                           const int32_t* __restrict__ row_of,
+                                                           const float* __restrict__ wts, int64_t T_, int topk, RowsOut o,
+                                                           const int32_t* __restrict__ offsets,
+                                                           const int32_t* __restrict__ counts, int64_t G, int64_t R,
+                                                           float* __restrict__ dw) {
+    __shared__ float part[16][kMaxTopk];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    if (blockIdx.x >= T_) {
+        const int64_t p = (int64_t(blockIdx.x) - T_) * waves + wave;
         if (p < 127 * G) zero_padding(uint32_t(p), offsets, counts, R, o, lane);
         return;
     }
+    const int64_t token = xcd_run(blockIdx.x, uint32_t(T_));
     const int32_t* rows = row_of + token * topk;
     const float* wt = wts + token * topk;
     float dot[kMaxTopk];
 #pragma unroll
     for (int j = 0; j < kMaxTopk; ++j) dot[j] = 0.0f;
     const uint32_t chunks = uint32_t((o.H + kWaveChan - 1) / kWaveChan);
-    for (uint32_t c = wave; c < chunks; c += 4) {
+    for (uint32_t c = wave; c < chunks; c += waves) {
         const uint32_t ch = c * kWaveChan + lane * kChan;
         const bool in = ch < o.H;
         float v[kChan];
@@ -619,22 +635,29 @@ __global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ d
         for (int i = 0; i < kChan; ++i) v[i] = 0.0f;
         if (in) load_n<kChan>(dout + token * o.H + ch, v);
         float sc;
-        const u32x4 code = encode16<typename encoder_of<TD>::type>(v, sc);
-        const uint32_t kb = c * 8 + (lane >> 3);
-        // (two or four entries' loads together measured no faster: 121.9 and
-        // 125.6 us against 121.6 at 3001 tokens x 8 rows of 7168)
+        const auto code = encode_lane<typename encoder_of<TD>::type>(v, sc);
+        const uint32_t kb = c * (64 / kLanes) + lane / kLanes;
 #pragma unroll
-        for (int j = 0; j < kMaxTopk; ++j) {
-            if (j < topk) {
-                const int64_t r = rows[j];
-                if (r >= 0 && r < R && in) {
-                    Raw<TY, kChan> u;
-                    u.load(y + r * o.H + ch);
-                    const uint32_t flip = wt[j] < 0.0f ? 0x80808080u : 0u;
-                    st_out<STREAM>(o.q + r * o.H + ch, u32x4{code[0] ^ flip, code[1] ^ flip, code[2] ^ flip, code[3] ^ flip});
-                    if ((lane & 7) == 0) *o.scale<false>(uint32_t(r), kb) = sc * fabsf(wt[j]);
+        for (int j0 = 0; j0 < kMaxTopk; j0 += F) {
+            if (j0 < topk) {
+                int64_t r[F];
+                Raw<TY, kChan> u[F];
 #pragma unroll
-                    for (int i = 0; i < kChan; ++i) dot[j] = fmaf(v[i], u.get(i), dot[j]);
+                for (int j = 0; j < F; ++j) {
+                    r[j] = j0 + j < topk && in ? rows[j0 + j] : -1;
+                    if (r[j] >= R) r[j] = -1;
+                    if (r[j] >= 0) u[j].template load<STREAM>(y + r[j] * o.H + ch);
+                }
+#pragma unroll
+                for (int j = 0; j < F; ++j) {
+                    if (r[j] >= 0) {
+                        const float wj = wt[j0 + j];
+                        const uint32_t flip = wj < 0.0f ? 0x80808080u : 0u;
+                        st_out<STREAM>(o.q + r[j] * o.H + ch, u32x2_t{code[0] ^ flip, code[1] ^ flip});
+                        if (lane % kLanes == 0) *o.scale<false>(uint32_t(r[j]), kb) = sc * fabsf(wj);
+#pragma unroll
+                        for (int i = 0; i < kChan; ++i) dot[j0 + j] = fmaf(v[i], u[j].get(i), dot[j0 + j]);
+                    }
                 }
             }
         }
@@ -646,7 +669,11 @@ __global__ __launch_bounds__(256) void combine_backward(const TD* __restrict__ d
     }
     __syncthreads();
     const int j = threadIdx.x;
-    if (j < topk) dw[token * topk + j] = part[0][j] + part[1][j] + part[2][j] + part[3][j];
+    if (j < topk) {
+        float sum = 0.0f;
+        for (int k = 0; k < waves; ++k) sum += part[k][j];
+        dw[token * topk + j] = sum;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -740,7 +767,7 @@ static hipError_t run_dispatch(const void* x, int64_t T_, const int32_t* idx, in
                                hipStream_t stream) {
     const int64_t n = T_ * topk, chunks = (o.H + kWaveChan - 1) / kWaveChan, waves = T_ * chunks;
     if (n <= kSmallEntries && waves > 0) {
-        const int64_t per_token = (chunks + 3) / 4, grid = T_ * per_token + (MASKED ? 0 : G);
+        const int64_t per_token = (chunks + 3) / 4, grid = T_ * per_token + (MASKED ? 0 : G * kPadParts);
         return launch_kernel(dispatch_small<T, MASKED>, dim3(unsigned(grid)), dim3(256), stream, static_cast<const T*>(x),
                              idx, uint32_t(T_), int(topk), uint32_t(per_token), int(first), uint32_t(G), o, row_of,
                              offsets, counts);
@@ -789,9 +816,14 @@ static hipError_t run_combine_backward(const void* dout, int64_t T, int64_t H, c
                                        const int32_t* counts, int64_t G, uint8_t* q, float* s, float* dw,
                                        hipStream_t stream) {
     const RowsOut o{q, s, H, (H + kBlock - 1) / kBlock, R};
-    const int64_t blocks = T + (127 * G + 3) / 4;
-    const bool stream_out = (R < T * topk ? R : T * topk) * H >= kStreamBytes;
-    return launch_kernel(stream_out ? combine_backward<TD, TY, true> : combine_backward<TD, TY, false>, dim3(unsigned(blocks)), dim3(256), stream,
+    const int64_t chunks = (H + kWaveChan - 1) / kWaveChan;
+    const bool stream_out = (R < T * topk ? R : T * topk) * H >= kStreamBytes, few = T <= kFewTokens && !stream_out;
+    const int64_t most = few ? 16 : stream_out ? 4 : 8, each = (chunks + most - 1) / most;
+    const int64_t waves = chunks ? (chunks + each - 1) / each : 1;
+    auto* kernel = few          ? combine_backward<TD, TY, false, 4>
+                   : stream_out ? combine_backward<TD, TY, true, 1>
+                                : combine_backward<TD, TY, false, 1>;
+    return launch_kernel(kernel, dim3(unsigned(T + (127 * G + waves - 1) / waves)), dim3(unsigned(64 * waves)), stream,
                          static_cast<const TD*>(dout), static_cast<const TY*>(y), row_of, w, T, int(topk), o, offsets,
                          counts, G, R, dw);
 }
