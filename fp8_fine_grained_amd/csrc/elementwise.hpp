@@ -321,15 +321,16 @@ struct Derived {
     }
 };
 
-// N = 16 or 8 consecutive values of a lane, 128 / N lanes to a group: the group's
+// N = 8 or 4 consecutive values of a lane, 128 / N lanes to a group: the group's
 // scale and the lane's codes (G: Bracket, Ratio for values that are BF16, or Derived)
+typedef uint32_t u32x1_t __attribute__((ext_vector_type(1)));
 template <int N>
 struct code_words {
-    typedef u32x4 type;
+    typedef u32x2_t type;
 };
 template <>
-struct code_words<8> {
-    typedef u32x2_t type;
+struct code_words<4> {
+    typedef u32x1_t type;
 };
 template <class G, int N>
 __device__ __forceinline__ typename code_words<N>::type encode_lane(const float (&v)[N], float& sc) {

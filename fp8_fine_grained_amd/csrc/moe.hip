@@ -548,29 +548,30 @@ __global__ __launch_bounds__(256) void dispatch_small(const T* __restrict__ x, c
 
 // ---------------------------------------------------------------------------
 // out_t = sum_j w_tj y[row_tj], in the order of the choices, in FP32.  A wave
-// takes 512 channels of one token, eight per lane.  Bound by the reads: 8192
+// takes 512 channels of one token, eight per lane (many FP32 rows:
+// four, one 16-byte load).  Bound by the reads: 8192
 // tokens x 8 rows of 7168 BF16 channels, 1.06 GB, 178 us, 5.9 TB/s (the rows are read once: with the
 // non-temporal hint, without it 204 us).
-template <class TY, class TO>
+template <class TY, class TO, int V>
 __global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t R, int64_t H,
                                                const int32_t* __restrict__ row_of, const float* __restrict__ wts,
                                                uint32_t waves, int topk, uint32_t chunks, TO* __restrict__ out) {
     const int lane = threadIdx.x & 63;
     const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + blockIdx.x * 4;
     if (w >= waves) return;
-    const uint32_t token = w / chunks, ch = (w - token * chunks) * 512 + lane * 8;
+    const uint32_t token = w / chunks, ch = (w - token * chunks) * (64 * V) + lane * V;
     if (ch >= H) return;
     const int32_t* rows = row_of + int64_t(token) * topk;
     const float* wt = wts ? wts + int64_t(token) * topk : nullptr;
-    float acc[8];
+    float acc[V];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
     // four entries at a time, their loads in flight together.  Measured (us, one
     // at a time / four): 64 tokens of 7168 channels x 8 rows 4.9 / 4.4, 512 11.6 /
     // 11.3, 8192 182.2 / 183.0.
     for (int j0 = 0; j0 < topk; j0 += 4) {
         bool has[4];
-        Raw<TY, 8> v[4];
+        Raw<TY, V> v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int64_t r = j0 + j < topk ? rows[j0 + j] : -1;
@@ -582,11 +583,11 @@ __global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t
             if (has[j]) {
                 const float f = wt ? wt[j0 + j] : 1.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = fmaf(f, v[j].get(i), acc[i]);
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(f, v[j].get(i), acc[i]);
             }
         }
     }
-    store_n<8>(out + int64_t(token) * H + ch, acc);
+    store_n<V>(out + int64_t(token) * H + ch, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -594,7 +595,7 @@ __global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t
 // rows dy = w_tj Q(dout_t), where Q is the 1x128 quantization of dout_t: every
 // row of a token shares its codes, and its scales are |w| times the token's
 // (the sign of w goes into the codes).  A workgroup per token; a wave takes 512
-// channels at a time, eight per lane, and F entries' rows in flight.  Bound by memory:
+// channels at a time, eight per lane (V), and F entries' rows in flight.  Bound by memory:
 // 3001 tokens x 8 rows of 7168 BF16 channels, 565 MB, 112 us, 5.0 TB/s (16
 // channels per lane: 118 us).
 //
@@ -606,6 +607,13 @@ __global__ __launch_bounds__(256) void combine(const TY* __restrict__ y, int64_t
 // 112.4 / 115.2 / 140.5.
 constexpr int64_t kFewTokens = 256;
 
+// Channels of a lane.  Many FP32 rows: four, one 16-byte load (us, eight / four: 1024 tokens x 8
+// rows of 7168 channels 69.2 / 66.8, 3001 199 / 178, 8192 568 / 516; 512 tokens, not
+// streaming, 12.8 / 14.4).
+template <class TY, bool STREAM>
+constexpr int back_run() {
+    return STREAM && sizeof(TY) == 4 ? 4 : 8;
+}
 template <class TD, class TY, bool STREAM, int F>
 __global__ __launch_bounds__(1024) void combine_backward(const TD* __restrict__ dout, const TY* __restrict__ y,
                                                            const int32_t* __restrict__ row_of,
@@ -613,6 +621,7 @@ __global__ __launch_bounds__(1024) void combine_backward(const TD* __restrict__ 
                                                            const int32_t* __restrict__ offsets,
                                                            const int32_t* __restrict__ counts, int64_t G, int64_t R,
                                                            float* __restrict__ dw) {
+    constexpr int V = back_run<TY, STREAM>(), kGroup = kBlock / V;            // channels of a lane, lanes of a 128-group
     __shared__ float part[16][kMaxTopk];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     if (blockIdx.x >= T_) {
@@ -626,22 +635,22 @@ __global__ __launch_bounds__(1024) void combine_backward(const TD* __restrict__ 
     float dot[kMaxTopk];
 #pragma unroll
     for (int j = 0; j < kMaxTopk; ++j) dot[j] = 0.0f;
-    const uint32_t chunks = uint32_t((o.H + kWaveChan - 1) / kWaveChan);
+    const uint32_t chunks = uint32_t((o.H + 64 * V - 1) / (64 * V));
     for (uint32_t c = wave; c < chunks; c += waves) {
-        const uint32_t ch = c * kWaveChan + lane * kChan;
+        const uint32_t ch = c * (64 * V) + lane * V;
         const bool in = ch < o.H;
-        float v[kChan];
+        float v[V];
 #pragma unroll
-        for (int i = 0; i < kChan; ++i) v[i] = 0.0f;
-        if (in) load_n<kChan>(dout + token * o.H + ch, v);
+        for (int i = 0; i < V; ++i) v[i] = 0.0f;
+        if (in) load_n<V>(dout + token * o.H + ch, v);
         float sc;
         const auto code = encode_lane<typename encoder_of<TD>::type>(v, sc);
-        const uint32_t kb = c * (64 / kLanes) + lane / kLanes;
+        const uint32_t kb = c * (64 / kGroup) + lane / kGroup;
 #pragma unroll
         for (int j0 = 0; j0 < kMaxTopk; j0 += F) {
             if (j0 < topk) {
                 int64_t r[F];
-                Raw<TY, kChan> u[F];
+                Raw<TY, V> u[F];
 #pragma unroll
                 for (int j = 0; j < F; ++j) {
                     r[j] = j0 + j < topk && in ? rows[j0 + j] : -1;
@@ -653,10 +662,13 @@ __global__ __launch_bounds__(1024) void combine_backward(const TD* __restrict__ 
                     if (r[j] >= 0) {
                         const float wj = wt[j0 + j];
                         const uint32_t flip = wj < 0.0f ? 0x80808080u : 0u;
-                        st_out<STREAM>(o.q + r[j] * o.H + ch, u32x2_t{code[0] ^ flip, code[1] ^ flip});
-                        if (lane % kLanes == 0) *o.scale<false>(uint32_t(r[j]), kb) = sc * fabsf(wj);
+                        auto signed_code = code;
 #pragma unroll
-                        for (int i = 0; i < kChan; ++i) dot[j0 + j] = fmaf(v[i], u[j].get(i), dot[j0 + j]);
+                        for (int i = 0; i < V / 4; ++i) signed_code[i] ^= flip;
+                        st_out<STREAM>(o.q + r[j] * o.H + ch, signed_code);
+                        if (lane % kGroup == 0) *o.scale<false>(uint32_t(r[j]), kb) = sc * fabsf(wj);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) dot[j0 + j] = fmaf(v[i], u[j].get(i), dot[j0 + j]);
                     }
                 }
             }
@@ -796,9 +808,16 @@ hipError_t launch_dispatch(const void* x, int bf16, int64_t T, int64_t H, const 
 template <class TY, class TO>
 static hipError_t run_combine(const void* y, int64_t R, int64_t H, const int32_t* row_of, const float* w, int64_t T,
                               int64_t topk, void* out, hipStream_t stream) {
-    const int64_t chunks = (H + 511) / 512, blocks = (T * chunks + 3) / 4;
-    return launch_kernel(combine<TY, TO>, dim3(unsigned(blocks)), dim3(256), stream, static_cast<const TY*>(y), R, H,
-                         row_of, w, uint32_t(T * chunks), int(topk), uint32_t(chunks), static_cast<TO*>(out));
+    // FP32 rows of 32 MB and more: four channels per lane.  Measured (us, eight / four): 64
+    // tokens x 8 rows of 7168 channels 5.7 / 6.9, 500 x 8 x 2048 (32 MB) 8.7 / 8.8, 1024 x 8 x
+    // 7168 50.3 / 44.8, 8192 x 8 x 7168 395 / 341.
+    const bool four = sizeof(TY) == 4 && T * topk * H * 4 >= kStreamBytes;
+    const int64_t per = 64 * (four ? 4 : 8), chunks = (H + per - 1) / per, blocks = (T * chunks + 3) / 4;
+    auto* kernel = combine<TY, TO, 8>;
+    if constexpr (sizeof(TY) == 4)
+        if (four) kernel = combine<TY, TO, 4>;
+    return launch_kernel(kernel, dim3(unsigned(blocks)), dim3(256), stream, static_cast<const TY*>(y), R, H, row_of, w,
+                         uint32_t(T * chunks), int(topk), uint32_t(chunks), static_cast<TO*>(out));
 }
 
 hipError_t launch_combine(const void* y, int y_bf16, int64_t R, int64_t H, const int32_t* row_of, const float* w,
@@ -816,8 +835,8 @@ static hipError_t run_combine_backward(const void* dout, int64_t T, int64_t H, c
                                        const int32_t* counts, int64_t G, uint8_t* q, float* s, float* dw,
                                        hipStream_t stream) {
     const RowsOut o{q, s, H, (H + kBlock - 1) / kBlock, R};
-    const int64_t chunks = (H + kWaveChan - 1) / kWaveChan;
     const bool stream_out = (R < T * topk ? R : T * topk) * H >= kStreamBytes, few = T <= kFewTokens && !stream_out;
+    const int64_t per = 64 * (stream_out ? back_run<TY, true>() : back_run<TY, false>()), chunks = (H + per - 1) / per;
     const int64_t most = few ? 16 : stream_out ? 4 : 8, each = (chunks + most - 1) / most;
     const int64_t waves = chunks ? (chunks + each - 1) / each : 1;
     auto* kernel = few          ? combine_backward<TD, TY, false, 4>

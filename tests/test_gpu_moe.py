@@ -354,7 +354,8 @@ def test_dispatch_scales_of_every_kind():
 
 
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("T,H,topk,R", [(1, 8, 1, 1), (7, 264, 3, 20), (65, 1040, 8, 512), (300, 512, 16, 700), (4, 7168, 8, 40)])
+@pytest.mark.parametrize("T,H,topk,R", [(1, 8, 1, 1), (7, 264, 3, 20), (65, 1040, 8, 512), (300, 512, 16, 700), (4, 7168, 8, 40),
+                                        (1100, 1032, 8, 500)])     # the last one: four channels per lane for FP32 rows
 def test_combine(T, H, topk, R, out):
     rng = np.random.default_rng(T + H)
     row = rng.integers(-1, R, (T, topk)).astype(np.int32)
@@ -383,7 +384,8 @@ def test_combine_ignores_rows_without_an_entry():
 
 
 @pytest.mark.parametrize("T,H,E,topk,first,G", [(1, 16, 4, 1, 0, 4), (40, 272, 16, 8, 4, 8), (129, 1040, 8, 3, 0, 8), (333, 2048, 24, 16, 0, 6),
-                                                (5, 7168, 32, 8, 0, 32), (4200, 1024, 32, 8, 0, 32)])
+                                                (5, 7168, 32, 8, 0, 32), (4200, 1024, 32, 8, 0, 32), (4150, 1040, 16, 8, 4, 8),
+                                                (260, 1552, 8, 5, 0, 8)])
 def test_combine_backward(T, H, E, topk, first, G):
     rng = np.random.default_rng(T * H)
     idx = entries(rng, T, E, topk)
