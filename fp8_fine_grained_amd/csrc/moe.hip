@@ -187,7 +187,13 @@ __global__ __launch_bounds__(256) void route(const T* __restrict__ x, const floa
 // (1 - s_i) and softmax dx_e = s_e (scale g_e [e chosen] - scale sum_j g_j s_j)
 // for every expert.  The differences g_i - g_j keep a single renormalised
 // weight's gradient exactly 0.
-template <class T, int LPT, int V>
+//
+// LPT lanes hold a token's row, V experts each, in 16-byte pieces (U experts) that
+// alternate over the lanes; where rows do not consist of such pieces, one by one (U
+// = 1), neighbouring lanes on neighbouring experts.  Bound by instruction issue above
+// launch: FP32 logits, sigmoid, us: 64 x 256 4.8, 8192 x 256 7.3, 14890 x 330 14.8 (with
+// V consecutive experts per lane 5.1, 8.3, 19.8).
+template <class T, int LPT, int V, int U>
 __global__ __launch_bounds__(256) void route_backward(const T* __restrict__ x, const int32_t* __restrict__ idx,
                                                       const float* __restrict__ dw, RouteArgs a, T* __restrict__ dx) {
     const int lane = threadIdx.x & 63, sl = lane & (LPT - 1), seg0 = lane & ~(LPT - 1);
@@ -195,16 +201,27 @@ __global__ __launch_bounds__(256) void route_backward(const T* __restrict__ x, c
     const bool there = token < a.T;
     const int64_t tk = there ? token : 0;
     const T* row = x + tk * a.ld;
-    const int e0 = sl * V, left = a.E - e0, n = !there || left < 0 ? 0 : (left < V ? left : V);
+    const auto expert = [&](int j) { return (j / U * LPT + sl) * U + j % U; };
     const bool dense = !a.sigmoid && !a.renorm;
     float v[V], m = 0.0f, inv = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = 0.0f;
     if (dense) {
-        load_logits<V>(row, e0, n, a.vec, v);
         m = kNegInf;
 #pragma unroll
-        for (int j = 0; j < V; ++j) m = fmaxf(m, v[j]);
+        for (int j = 0; j < V; j += U) {
+            float p[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) p[u] = kNegInf;
+            if (there && expert(j) < a.E) {
+                if constexpr (U > 1)
+                    load_n<U>(row + expert(j), p);
+                else
+                    p[0] = f32_of(row[expert(j)]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) m = fmaxf(m, v[j + u] = p[u]);
+        }
         m = lanes_max<LPT>(m);
         if (m == kNegInf) m = 0.0f;
         float sum = 0.0f;
@@ -246,15 +263,20 @@ __global__ __launch_bounds__(256) void route_backward(const T* __restrict__ x, c
         const int e = __shfl(mine, seg0 + i, 64);
         const float ci = __shfl(c, seg0 + i, 64);
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] += e0 + j == e ? ci : 0.0f;
+        for (int j = 0; j < V; ++j) v[j] += expert(j) == e ? ci : 0.0f;
     }
-    T* out = dx + tk * a.E + e0;
-    if (n == V && a.E % V == 0) {
-        store_n<V>(out, v);
-    } else {
+    T* out = dx + tk * a.E;
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (j < n) store1(out + j, v[j]);
+    for (int j = 0; j < V; j += U) {
+        if (!there || expert(j) >= a.E) continue;
+        if constexpr (U > 1) {
+            float p[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) p[u] = v[j + u];
+            store_n<U>(out + expert(j), p);
+        } else {
+            store1(out + expert(j), v[j]);
+        }
     }
 }
 
@@ -706,8 +728,9 @@ template <class T, int LPT, int V>
 hipError_t run_route_backward(const void* x, const int32_t* idx, const float* dw, const RouteArgs& a, void* dx,
                               hipStream_t stream) {
     const int64_t blocks = (a.T + 256 / LPT - 1) / (256 / LPT);
-    return launch_kernel(route_backward<T, LPT, V>, dim3(unsigned(blocks)), dim3(256), stream,
-                         static_cast<const T*>(x), idx, dw, a, static_cast<T*>(dx));
+    constexpr int U = 16 / int(sizeof(T)) < V ? 16 / int(sizeof(T)) : V;
+    const bool pieces = a.ld % U == 0 && a.E % U == 0;
+    return launch_kernel(pieces ? route_backward<T, LPT, V, U> : route_backward<T, LPT, V, 1>, dim3(unsigned(blocks)), dim3(256), stream, static_cast<const T*>(x), idx, dw, a, static_cast<T*>(dx));
 }
 
 }  // namespace moe_detail
@@ -744,11 +767,10 @@ hipError_t launch_route(const RouteCall& c, hipStream_t stream) {
 
 hipError_t launch_route_backward(const RouteCall& c, const float* dw, void* dx, hipStream_t stream) {
     RouteArgs a{c.T, c.ld, int(c.E), int(c.topk), 1, int(c.E), 0, 1, 1, c.sigmoid, c.renorm, 0, c.scale};
-    const int el = c.bf16 ? 2 : 4;
+    // 16 lanes of 32 experts each for up to 512 are slower (us, 64 x 8 / 16 x 32): 1000 x 330 4.1 /
+    // 5.6, 16384 x 512 softmax 19.7 / 21.5
     const int lpt = c.E <= 256 ? 16 : 64;
     const int need = (a.E + lpt - 1) / lpt, v = need <= 4 ? 4 : need <= 8 ? 8 : 16;
-    const int unit = v * el < 16 ? v * el : 16;
-    a.vec = (c.ld * el) % unit == 0;
 #define FP8FG_ROUTE_B(T, L, V) \
     if (lpt == L && v == V) return run_route_backward<T, L, V>(c.x, c.idx, dw, a, dx, stream);
 #define FP8FG_ROUTES_B(T) \

@@ -184,7 +184,8 @@ def test_route_many_tokens(T, E, ng, tg, dtype):
 
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("score", [fp8.SCORE_SOFTMAX, fp8.SCORE_SIGMOID])
-@pytest.mark.parametrize("T,E,topk", [(1, 1, 1), (6, 8, 3), (65, 64, 6), (33, 100, 4), (40, 256, 8), (9, 300, 16), (5, 1024, 8)])
+@pytest.mark.parametrize("T,E,topk", [(1, 1, 1), (6, 8, 3), (65, 64, 6), (33, 100, 4), (40, 256, 8), (9, 300, 16), (5, 1024, 8),
+                                      (70, 37, 3), (50, 330, 7), (20, 1001, 16)])
 def test_route_backward(T, E, topk, score, renorm):
     rng = np.random.default_rng(T + E)
     for bf16 in (False, True):
