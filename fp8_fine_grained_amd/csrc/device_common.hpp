@@ -99,8 +99,8 @@ __device__ __forceinline__ float abs_max4(v4f v) {
 // Four E4M3 codes (RNE, saturating) of four floats, packed little-endian, by
 // the hardware conversion.  v_cvt_pk_fp8_f32 was compared with e4m3_from_f32
 // above on every 32-bit pattern whose value is finite with |y| <= 464 and
-// agreed on all of them (signed zeros, subnormals, ties, saturation); the
-// quantizers only ever convert |y| <= 448 * (1 + 2^-23).
+// agreed on all of them (signed zeros, subnormals, ties, saturation); beyond 464
+// it gives NaN codes.  The quantizers only ever convert |y| <= 448 * (1 + 2^-20).
 __device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) {
     const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
@@ -116,7 +116,9 @@ __device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) {
 // than an ulp of the 4 ulps of margin).  Rounding to E4M3 is monotone, so when
 // both ends of the bracket give the same code every value inside -- RN32(x/s)
 // included -- has that code.  Otherwise (the bracket straddles a rounding
-// boundary: about 2^-16 of elements) the IEEE quotient is computed.
+// boundary: about 2^-16 of elements) the IEEE quotient is computed, and clamped to
+// +-448: a scale below 2^-128 (r = +inf) has so few bits that it can be a third
+// below amax / 448.
 __device__ __forceinline__ uint32_t encode4(v4f x, float s, float r) {
     if (s == 0.0f) return cvt4(x[0], x[1], x[2], x[3]);       // signed zeros
     if (r < __builtin_inff()) {
@@ -128,7 +130,9 @@ __device__ __forceinline__ uint32_t encode4(v4f x, float s, float r) {
                                  __builtin_fmaf(__builtin_fabsf(y[2]), e, y[2]), __builtin_fmaf(__builtin_fabsf(y[3]), e, y[3]));
         if (lo == hi) return lo;
     }
-    return cvt4(x[0] / s, x[1] / s, x[2] / s, x[3] / s);
+    constexpr float top = 448.0f;
+    return cvt4(__builtin_amdgcn_fmed3f(x[0] / s, -top, top), __builtin_amdgcn_fmed3f(x[1] / s, -top, top),
+                __builtin_amdgcn_fmed3f(x[2] / s, -top, top), __builtin_amdgcn_fmed3f(x[3] / s, -top, top));
 }
 
 }  // namespace fp8fg
