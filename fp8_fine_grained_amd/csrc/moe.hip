@@ -41,9 +41,11 @@ constexpr float kNegInf = -__builtin_inff();
 __device__ __forceinline__ float sigmoidf(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // A chosen expert's score up to a factor that all the chosen share, for
-// renormalised weights: where the largest of them (at logit ms) comes near
-// FP32's smallest normal, sigmoid(x) is exp(x) to FP32's accuracy.
-__device__ __forceinline__ float chosen_sigmoid(float x, float ms) { return ms < -80.0f ? expf(x - ms) : sigmoidf(x); }
+// renormalised weights: exp(x) sigmoid(-x) = sigmoid(x) over exp(ms), ms < 0 the largest
+// of their logits, so that the ratios of scores below FP32's range are kept.
+__device__ __forceinline__ float chosen_sigmoid(float x, float ms) {
+    return ms < 0.0f ? expf(x - ms) * sigmoidf(-x) : sigmoidf(x);
+}
 
 constexpr int kMaxTopk = 16;
 

@@ -1,0 +1,53 @@
+"""The mixture-of-experts operators where FP32's range ends: against the 64-bit oracle."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_fine_grained_amd as fp8
+from oracle import moe
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+EPS = 2.0 ** -24
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+# logits of the chosen in decreasing order, the largest from -0.5 to -250: the others' own
+# scores lie below FP32's normals, below all of FP32, or within it
+FADING = [[-79.9, -88.8], [-50.0, -89.0], [-40.0, -88.0, -92.0, -100.0], [-0.5, -1.0, -87.0, -95.0], [-79.0, -79.5, -88.5, -103.0],
+          [-86.0, -88.0, -90.0, -92.0], [-120.0, -121.0, -150.0], [-250.0, -250.5, -251.0, -340.0], [3.0, -20.0, -60.0, -80.0]]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("row", FADING, ids=str)
+def test_renormalised_sigmoid_weights_keep_their_ratios(row, bf16):
+    """Weights and logits' gradients of chosen experts whose scores are far below the largest one's."""
+    k = len(row)
+    x = np.full((3, 16), -np.inf, np.float32)
+    x[:, 2:2 + k] = row
+    t = dev(x).to(torch.bfloat16) if bf16 else dev(x)
+    vals = t.float().cpu().numpy()
+    idx, w = fp8.moe_route(t, k, scale=2.5)
+    ridx, rw, _ = moe.route(vals, k, scale=2.5)
+    idx, w = idx.cpu().numpy(), w.cpu().numpy()
+    assert np.array_equal(idx, ridx)
+    # FP32 arguments (x - ms, x) of two exponentials and a few roundings; weights below FP32's normals
+    rel = 4 * (moe.exp_error(2 * np.abs(np.array(vals[0, 2:2 + k])).max()) + 32 * EPS)
+    assert np.all(np.abs(w - rw) <= rel * np.abs(rw) + 2.0 ** -126), (w[0], rw[0])
+    dw = np.zeros((3, k), np.float32)
+    dw[0, 0], dw[1, k - 1], dw[2] = 1.0, 1.0, np.linspace(-1, 1, k)
+    g = fp8.moe_route_backward(t, dev(idx), dev(dw), scale=2.5).float().cpu().numpy()
+    # dx_i = scale p_i (1 - s_i) d_i with d_i a sum over the chosen: each term p_i p_j carries the errors of both weights
+    # (the differences keep what 1 / v - s / v^2 would lose in 64 bits where one weight is nearly 1)
+    p = rw / 2.5
+    ref, size = np.zeros(x.shape), np.zeros(x.shape)
+    for r in range(3):
+        for i in range(k):
+            rest = 1.0 / (1.0 + np.exp(np.float64(vals[r, idx[r, i]])))
+            terms = [2.5 * p[r, i] * rest * (float(dw[r, i]) - float(dw[r, j])) * p[r, j] for j in range(k)]
+            ref[r, idx[r, i]], size[r, idx[r, i]] = sum(terms), sum(abs(v) for v in terms)
+    lim = 2 * rel * size + 2.0 ** -120 + (2.0 ** -8 * np.abs(ref) if bf16 else 0)
+    assert np.all(np.abs(g - ref) <= lim), (g, ref)
