@@ -47,6 +47,9 @@ __device__ __forceinline__ float chosen_sigmoid(float x, float ms) {
     return ms < 0.0f ? expf(x - ms) * sigmoidf(-x) : sigmoidf(x);
 }
 
+// bits of the finite floats below -80: kLowLogits of them from kLowFirst on
+constexpr uint32_t kLowFirst = 0xC2A00001u, kLowLogits = 0xFF800000u - kLowFirst;
+
 constexpr int kMaxTopk = 16;
 
 struct RouteArgs {
@@ -85,9 +88,21 @@ __global__ __launch_bounds__(256) void route(const T* __restrict__ x, const floa
     float m = 0.0f, inv = 0.0f;
     uint32_t key[V];
     if (a.sigmoid) {
+        float s[V];
+        uint32_t low = ~0u;            // below kLowLogits where a finite logit is below -80
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float c = sigmoid_fast(v[j]) + b[j];
+            s[j] = sigmoid_fast(v[j]);
+            const uint32_t u = __float_as_uint(v[j]) - kLowFirst;
+            low = u < low ? u : low;
+        }
+        if (low < kLowLogits) {        // exp(x) down to FP32's smallest subnormal, where the reciprocal gives 0
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] = v[j] < -80.0f ? expf(v[j]) : s[j];
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float c = s[j] + b[j];
             key[j] = (v[j] == kNegInf || c == kNegInf) ? 0u : ordered(c);
         }
     } else {

@@ -428,8 +428,8 @@ int fp8_grouped_gemm_masked_tiled_fp8out(const uint8_t* a, const float* sa, cons
  * groups stay in (all of them when topk_groups = n_groups), and the topk
  * largest c among their experts are chosen, in decreasing order.  Equal
  * scores go to the lowest index, for groups and experts alike; scores are
- * compared in FP32.  An expert whose logit, or c, is -inf is never chosen and
- * adds nothing to its group's score; where fewer than topk experts can be
+ * compared in FP32, subnormals included.  An expert whose logit, or c, is -inf is
+ * never chosen and adds nothing to its group's score; where fewer than topk experts can be
  * chosen the index is -1 and the weight 0 (a row of -inf, a padding token,
  * chooses nothing).  A NaN or +inf logit gives unspecified weights and an
  * unspecified choice, with every index still in [-1, E).

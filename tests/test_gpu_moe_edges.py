@@ -51,3 +51,28 @@ def test_renormalised_sigmoid_weights_keep_their_ratios(row, bf16):
             ref[r, idx[r, i]], size[r, idx[r, i]] = sum(terms), sum(abs(v) for v in terms)
     lim = 2 * rel * size + 2.0 ** -120 + (2.0 ** -8 * np.abs(ref) if bf16 else 0)
     assert np.all(np.abs(g - ref) <= lim), (g, ref)
+
+
+@pytest.mark.parametrize("T", [5, 5000, 10000])            # both lane counts
+def test_choice_among_scores_below_normals(T):
+    """Sigmoid logits of -80 to -103 have scores that FP32 still tells apart: the largest are chosen, in order."""
+    rng = np.random.default_rng(T)
+    E, k = 128, 6
+    x = np.full((T, E), -np.inf, np.float32)
+    levels = np.arange(-102.0, -79.0, 0.75).astype(np.float32)        # neighbours differ by more than FP32's step at 2^-147
+    for t in range(T):
+        x[t, rng.permutation(E)[:levels.size]] = levels
+    idx, w = fp8.moe_route(dev(x), k)
+    order = np.argsort(-x, axis=1, kind="stable")[:, :k]
+    assert np.array_equal(idx.cpu().numpy(), order)
+    few = x.copy()
+    few[few > -95.0] = -np.inf                                        # scores of 5e-42 and less only
+    idx, w = fp8.moe_route(dev(few), k, n_groups=4, topk_groups=2, group_top=1)
+    best = few.reshape(T, 4, E // 4).max(axis=2)
+    keep = np.argsort(-best, axis=1, kind="stable")[:, :2]
+    live = np.zeros((T, 4), bool)
+    np.put_along_axis(live, keep, True, axis=1)
+    few[~np.repeat(live, E // 4, axis=1)] = -np.inf
+    order = np.argsort(-few, axis=1, kind="stable")[:, :k]
+    order = np.where(np.isneginf(np.take_along_axis(few, order, axis=1)), -1, order)
+    assert np.array_equal(idx.cpu().numpy(), order)
