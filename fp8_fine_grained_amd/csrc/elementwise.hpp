@@ -162,14 +162,15 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
     return sigmoid_fast(x, rest);
 }
 
-// g sigmoid(g) u = g u / (1 + exp(-g)): the quotient of the product and the sum,
-// corrected once by its remainder with what either lost in rounding, so that
-// only the exponential's error and the last rounding remain
+// g sigmoid(g) u: q = g / (1 + exp(-g)) and its remainder, with what the sum
+// lost in rounding, both times u in one rounding, so that only the exponential's error
+// and the last rounding remain (and no product passes FP32's range before the result does)
 __device__ __forceinline__ float gate_of(float g, float u) {
-    const float e = exp_minus(g), d = 1.0f + e, n = g * u;
-    const float r = __builtin_amdgcn_rcpf(d), q = n * r;
-    const float d_lost = e < 1.0f ? e - (d - 1.0f) : 1.0f - (d - e), n_lost = __builtin_fmaf(g, u, -n);
-    return __builtin_fmaf(__builtin_fmaf(-q, d_lost, __builtin_fmaf(-q, d, n) + n_lost), r, q);
+    const float e = exp_minus(g), d = 1.0f + e;
+    const float r = __builtin_amdgcn_rcpf(d), q = g * r;
+    const float d_lost = e < 1.0f ? e - (d - 1.0f) : 1.0f - (d - e);
+    const float rest = __builtin_fmaf(-q, d_lost, __builtin_fmaf(-q, d, g)) * r;
+    return __builtin_fmaf(q, u, rest * u);
 }
 
 // cvt4 without clearing its result first: the conversion of a pair keeps the

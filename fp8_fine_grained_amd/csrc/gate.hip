@@ -16,7 +16,7 @@ namespace gate_detail {
 // channels per lane (one 16-byte load of BF16).  Row r of buffer blockIdx.z exists when r <
 // rows[blockIdx.z] (rows may be null: all of them).  Offsets within the 16
 // rows fit 32 bits.  Bound by memory once the encoding is cheap: 66900 x 2048 with
-// the checkpoint, 972 MB, 181 us, 5.4 TB/s (a plain copy 5.2); with an IEEE division and
+// the checkpoint, 972 MB, 174 us, 5.6 TB/s (a plain copy 5.2); with an IEEE division and
 // library exponential per element and per-element checks in the encoding it took 248 us.
 // Few rows are bound by latency and a wave's instructions.  With 16 channels per
 // lane (us, 16 / 8): FP32 with the checkpoint 351 / 258, FP32 without 308 / 211 (a lane's
@@ -39,8 +39,14 @@ __global__ __launch_bounds__(256) void swiglu(const T* __restrict__ gu, int64_t 
         float g[V], u[V], h[V];
         load_n<V, true>(row + (in + r * uint32_t(I)), g);
         load_n<V, true>(row + I + (in + r * uint32_t(I)), u);
+        // BF16: two values at a time.  Interleaved over all eight, as the compiler would, the
+        // kernel is slower (us, with a checkpoint and without, in pairs / all): 170 / 179
+        // and 113 / 128; FP32 the other way, 156 / 152
 #pragma unroll
-        for (int i = 0; i < V; ++i) h[i] = gate_of(g[i], u[i]);
+        for (int i = 0; i < V; ++i) {
+            h[i] = gate_of(g[i], u[i]);
+            if (sizeof(T) == 2 && (i & 1)) __builtin_amdgcn_sched_barrier(0);
+        }
         float a;
         const auto codes = encode_lane<Derived>(h, a);
         st_out<STREAM>(q + (b * M + m0) * I + kb * kBlock + in, codes);
@@ -154,7 +160,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void swiglu_backward(
                 const float g = g2[o] * in[i].sg, u = u2[o] * in[i].su, e = dh_of(in[i].dh, j);
                 float rest;
                 const float sg = sigmoid_fast(g, rest), si = g * sg;
-                d[0][i][j] = e * u * __builtin_fmaf(si, rest, sg);      // sg (1 + g (1 - sg))
+                d[0][i][j] = e * __builtin_fmaf(si, rest, sg) * u;      // sg (1 + g (1 - sg)); e u alone might pass FP32's range
                 d[1][i][j] = e * si;
                 d[2][i][j] = si * u;
             }

@@ -537,7 +537,8 @@ int fp8_moe_combine_backward(const void* dout, int dout_bf16, int64_t T, int64_t
  * rows: int32 [G] (4-byte aligned), or NULL for all rows: only rows
  * r < rows[g] of buffer g are read and written.  The contiguous layout is G = 1 with
  * rows = &group_offsets[G]; the masked one rows = masked_m.
- * Requires I % 128 == 0, I <= 2^23, G <= 65535; h must be finite.
+ * A sigmoid(g) below FP32's smallest normal (g < -87.3) counts as 0.  Requires
+ * I % 128 == 0, I <= 2^23, G <= 65535; h must be finite.
  */
 int fp8_swiglu(const void* gu, int gu_bf16, int64_t G, int64_t M, int64_t I, const int32_t* rows, uint8_t* q, float* s,
                uint8_t* qc, float* sc, void* stream);
@@ -547,7 +548,8 @@ int fp8_swiglu(const void* gu, int gu_bf16, int64_t G, int64_t M, int64_t I, con
  * contiguous layout) and dh ([M][I], f32 or bf16).  With g, u the decoded
  * checkpoint and sg = sigmoid(g):
  *   du = dh * g * sg,  dg = dh * u * sg * (1 + g * (1 - sg)),  h = g * sg * u,
- * formed in FP32 and quantized 1x128 once in each layout that the products read:
+ * formed in FP32 (sg below FP32's smallest normal counts as 0) and quantized 1x128
+ * once in each layout that the products read:
  *   q:  u8 [M][2 I],  s:  f32 [2 I/128][M]   (dg, du) along the channels
  *   qt: u8 [2 I][M],  st: f32 [M/128][2 I]   (dg, du) along the rows, transposed
  *   qh: u8 [I][M],    sh: f32 [M/128][I]     h along the rows, transposed

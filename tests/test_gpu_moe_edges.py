@@ -76,3 +76,39 @@ def test_choice_among_scores_below_normals(T):
     order = np.argsort(-few, axis=1, kind="stable")[:, :k]
     order = np.where(np.isneginf(np.take_along_axis(few, order, axis=1)), -1, order)
     assert np.array_equal(idx.cpu().numpy(), order)
+
+
+# g, u, dh whose products g u or dh u pass FP32's range while h, dg and du do not, and small rows beside them
+HUGE = [(-50.0, 1e38, 1e-3), (-80.0, 3e38, 1e25), (-60.0, -2e38, 1e20), (-30.0, 1e38, 1e8), (5e19, 2e18, 1e-3), (-87.0, 1e38, -1e30)]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_gate_of_products_past_range(bf16):
+    """The gate and its gradients where a product on the way passes FP32's range and the result does not."""
+    M, I = 16, 128
+    g, u, dh = (np.zeros((M, I), np.float32) for _ in range(3))
+    for r, row in enumerate(HUGE):
+        g[r], u[r], dh[r] = row
+    rng = np.random.default_rng(5)
+    g[8:], u[8:], dh[8:] = rng.standard_normal((8, I)), rng.standard_normal((8, I)), rng.standard_normal((8, I))
+    x = dev(np.concatenate([g, u], axis=1))
+    x = x.to(torch.bfloat16) if bf16 else x
+    vals = x.float().cpu().numpy()
+    gv, uv = vals[:, :I], vals[:, I:]
+    q, s, qc, sc = fp8.fp8_swiglu(x, checkpoint=True)
+    h = moe.gate(gv, uv)
+    assert np.all(np.abs(h) < 3e38)
+    err = moe.exp_error(gv)
+    moe.check_quantized(q.cpu().numpy(), s.cpu().numpy(), h, err * np.abs(h), "h")
+    t = dev(dh).to(torch.bfloat16) if bf16 else dev(dh)
+    dv = t.float().cpu().numpy()
+    q, s, qt, st, qh, sh = (v.cpu().numpy() for v in fp8.fp8_swiglu_backward(qc, sc, t))
+    v = moe.decode_rows(qc.cpu().numpy(), sc.cpu().numpy())
+    (dg, ag), (du, au) = moe.gate_backward(v[:, :I], v[:, I:], dv)
+    hb = moe.gate(v[:, :I], v[:, I:])
+    err = moe.exp_error(v[:, :I])
+    d, a = np.concatenate([dg, du], 1), np.concatenate([ag * err * 2, au * err * 2], 1)
+    assert np.all(np.abs(d) < 3e38)
+    moe.check_quantized(q, s, d, a, "gradients along the channels")
+    moe.check_quantized(qt, st, d.T, a.T, "gradients along the rows")
+    moe.check_quantized(qh, sh, hb.T, (err * np.abs(hb)).T, "h along the rows")
