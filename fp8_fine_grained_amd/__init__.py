@@ -543,8 +543,13 @@ def moe_route_backward(logits, idx, dw, score=SCORE_SIGMOID, renormalize=True, s
 def moe_rows_bound(T, topk, n_experts):
     """Rows of the contiguous layout that hold any choice of topk experts for T
     tokens among n_experts local ones (every expert's rows padded to 128)."""
-    n = T * topk
+    n = T * topk if n_experts else 0
     return (n + 127 * min(n_experts, n)) // 128 * 128
+
+
+def _row_of(idx, n_experts):
+    """The entries' rows, for the call to write; all -1 where no expert is local, for which it writes nothing."""
+    return torch.empty_like(idx) if n_experts else torch.full_like(idx, -1)
 
 
 def fp8_moe_dispatch_contiguous(x, idx, n_experts, first=0, M_total=None, q=None, s=None):
@@ -561,8 +566,8 @@ def fp8_moe_dispatch_contiguous(x, idx, n_experts, first=0, M_total=None, q=None
         M_total = moe_rows_bound(T, topk, n_experts) if q is None else q.shape[0]
     q = _out(q, (M_total, H), torch.uint8, x, "q")
     s = _out(s, (_nb(H), M_total), torch.float32, x, "s")
-    row_of = _empty((T, topk), torch.int32, x)
-    offsets = _empty((n_experts + 1,), torch.int32, x)
+    row_of = _row_of(idx, n_experts)
+    offsets = _empty((n_experts + 1,), torch.int32, x) if n_experts else torch.zeros(1, dtype=torch.int32, device=x.device)
     counts = _empty((n_experts,), torch.int32, x)
     _check("fp8_moe_dispatch_contiguous", load_library().fp8_moe_dispatch_contiguous(
         _ptr(x), _f32_or_bf16(x, "x"), T, H, _ptr(idx), topk, first, n_experts, M_total, _ptr(q), _ptr(s), _ptr(row_of),
@@ -580,7 +585,7 @@ def fp8_moe_dispatch_masked(x, idx, n_experts, M_max, first=0, q=None, s=None):
     _need(idx, torch.int32, (T, topk), "idx")
     q = _out(q, (n_experts, M_max, H), torch.uint8, x, "q")
     s = _out(s, (n_experts, _nb(H), M_max), torch.float32, x, "s")
-    row_of = _empty((T, topk), torch.int32, x)
+    row_of = _row_of(idx, n_experts)
     masked_m = _empty((n_experts,), torch.int32, x)
     _check("fp8_moe_dispatch_masked", load_library().fp8_moe_dispatch_masked(
         _ptr(x), _f32_or_bf16(x, "x"), T, H, _ptr(idx), topk, first, n_experts, M_max, _ptr(q), _ptr(s), _ptr(row_of),

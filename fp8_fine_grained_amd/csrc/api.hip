@@ -437,7 +437,7 @@ int fp8_moe_dispatch_contiguous(const void* x, int x_bf16, int64_t T, int64_t H,
     if (H % 16 != 0 || M_total % 128 != 0) return FP8FG_ERR_SHAPE;
     if (const int e = rows_args(T, H, topk, G, M_total)) return e;
     const int64_t n = T * topk;
-    if (M_total < (n + 127 * (G < n ? G : n)) / 128 * 128) return FP8FG_ERR_SHAPE;
+    if (G > 0 && M_total < (n + 127 * (G < n ? G : n)) / 128 * 128) return FP8FG_ERR_SHAPE;
     if (!first_ok(first)) return FP8FG_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(idx) || !aligned16(q) || !aligned16(s) || !aligned16(row_of) ||
         !aligned16(group_offsets) || !aligned16(counts))

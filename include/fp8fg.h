@@ -475,7 +475,8 @@ int moe_route_backward(const void* logits, int logits_bf16, int64_t ld, const in
  *     is quantized once, whatever its number of rows).  Rows from an expert's
  *     count to the next offset are zero (codes and scales); rows from
  *     group_offsets[G] on are not written.
- * Requires H % 16 == 0, 1 <= topk <= 16, 1 <= G <= 256 (G = 0: a no-op),
+ * Requires H % 16 == 0, 1 <= topk <= 16, 1 <= G <= 256 (G = 0: a no-op, for any
+ * M_total),
  * M_total % 128 == 0 and M_total >= the bound that holds any choice:
  * (n + 127 * min(G, n)) / 128 * 128 with n = T * topk; M_total < 2^31.
  * T = 0 writes the (zero) counts and offsets.
@@ -491,7 +492,7 @@ int fp8_moe_dispatch_contiguous(const void* x, int x_bf16, int64_t T, int64_t H,
  * reads them).  row_of holds g * M_max + r, r the entry's place among the
  * expert's; entries beyond M_max have no row (-1).  Rows at or beyond
  * masked_m[g] are not written.  Requires H % 16 == 0, 1 <= topk <= 16,
- * G <= 256, M_max >= 1, G * M_max < 2^31.
+ * G <= 256 (G = 0: a no-op), M_max >= 1, G * M_max < 2^31.
  */
 int fp8_moe_dispatch_masked(const void* x, int x_bf16, int64_t T, int64_t H, const int32_t* idx, int64_t topk,
                             int64_t first, int64_t G, int64_t M_max, uint8_t* q, float* s, int32_t* row_of,

@@ -112,3 +112,23 @@ def test_gate_of_products_past_range(bf16):
     moe.check_quantized(q, s, d, a, "gradients along the channels")
     moe.check_quantized(qt, st, d.T, a.T, "gradients along the rows")
     moe.check_quantized(qh, sh, hb.T, (err * np.abs(hb)).T, "h along the rows")
+
+
+def test_dispatch_without_local_experts():
+    """A rank that holds no expert: no entry has a row, in whatever memory the outputs come to lie."""
+    x = torch.randn(40, 256, device=DEV)
+    idx = torch.randint(0, 8, (40, 4), dtype=torch.int32, device=DEV)
+    for _ in range(4):
+        spoiled = [torch.full(shape, 7, dtype=torch.int32, device=DEV) for shape in ((40, 4), (40, 4), (1,), (1,))]
+        torch.cuda.synchronize()
+        del spoiled
+        q, s, row_of, offsets, counts = fp8.fp8_moe_dispatch_contiguous(x, idx, 0)
+        assert q.shape == (0, 256) and s.shape == (2, 0) and counts.shape == (0,)
+        assert torch.all(row_of == -1) and offsets.tolist() == [0]
+        spoiled = torch.full((40, 4), 7, dtype=torch.int32, device=DEV)
+        torch.cuda.synchronize()
+        del spoiled
+        q, s, masked, mm = fp8.fp8_moe_dispatch_masked(x, idx, 0, 16)
+        assert q.shape == (0, 16, 256) and mm.shape == (0,) and torch.all(masked == -1)
+        y = torch.full((128, 256), float("nan"), device=DEV)
+        assert torch.all(fp8.moe_combine(y, row_of, torch.ones(40, 4, device=DEV)) == 0)
