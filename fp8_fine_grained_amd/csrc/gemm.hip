@@ -3158,12 +3158,19 @@ bool wide_wgrad_fits(const GemmArgs& args) {
            WGRAD_BLOCKS * rows * 4 <= int64_t(0xFFFFFFFF);
 }
 
-// Weight gradients whose 256 x 256 tiles do not fill the chip's 256 CUs once
-// run 64 x 128 fold tiles: eight times as many workgroups, each with a shorter
-// prologue and epilogue.  Measured (us, 256-wide / 64 x 128), experts x rows x
-// M x N: 1 x 1024 x 512 x 512 34.4 / 11.4; 5 x 1111 x 512 x 768 24.4 / 8.8;
-// 8 x 4096 x 1024 x 1024 (128 tiles) 38.1 / 22.5; 8 x 8192 x 2048 x 1024 (256 tiles)
-// 62.2 / 56.9; 8 x 2048 x 2048 x 2048 (512 tiles) 44.1 / 57.3.
+// Weight gradients whose 256 x 256 tiles do not fill the chip's 256 CUs once run
+// 64 x 128 fold tiles, eight times as many workgroups, unless one expert's wide tiles
+// alone fill half of it.  A 64 x 128 tile takes 1 us per K-block, a wide one 3, so the wide
+// ones lose by up to three times where one expert has most rows and few tiles, and which
+// expert has how many is known on the device only; the fold tiles' time hardly depends on it.
+// Measured (us, 64 x 128 / wide), experts x rows x M x N:
+//   one expert: 8192 x 2048 x 2048 (64 tiles) 113 / 198, x 4096 (128) 206 / 203, x 7168 (224)
+//     346 / 227; 2048 x 2048 x 7168 94 / 68; 16384 x 4096 x 4096 (256) 779 / 494; 512 x 4096 x
+//     4096 39 / 30; 1024 x 512 x 512 12 / 35;
+//   even experts: 2 x 8192 x 2048 x 4096 (128 each) 210 / 133, x 2560 (80 each) 144 / 123;
+//     4 x 8192 x 2048 x 2048 (64 each) 107 / 74; 8 x 8192 x 2048 x 1024 64 / 46; 8 x 4096 x
+//     1024 x 1024 24 / 28;
+//   the same with rows by Zipf's law, exponent 1.1: 203 / 158, 134 / 146, 105 / 119, 61 / 105, 25 / 63.
 constexpr int64_t kCus = 256;
 
 // gfx950 (MI350 series): eight XCDs, each with its own L2
@@ -3259,7 +3266,8 @@ hipError_t dispatch(int engine, GemmMode mode, int bscale_1x128, int out_fp32, c
     int tile = 0;
     if (mode == GemmMode::Masked && args.M <= 128)
         tile = wide ? 3 : 1;
-    else if (mode == GemmMode::Wgrad && tile_count<WideTile>(mode, args) <= kCus)
+    else if (mode == GemmMode::Wgrad && tile_count<WideTile>(mode, args) <= kCus &&
+             !(wide && 2 * tile_count<WideTile>(mode, args) >= kCus * args.G))
         tile = 1;
     else if (wide)
         tile = 2;
