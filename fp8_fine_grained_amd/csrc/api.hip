@@ -19,7 +19,10 @@ constexpr int64_t kWideMaxKBlocks = 92;
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-inline int hip_status(hipError_t e) { return e == hipSuccess ? FP8FG_OK : FP8FG_ERR_HIP; }
+// hipErrorInvalidConfiguration: a size whose grid is longer than a launch takes
+inline int hip_status(hipError_t e) {
+    return e == hipSuccess ? FP8FG_OK : e == hipErrorInvalidConfiguration ? FP8FG_ERR_UNSUPPORTED : FP8FG_ERR_HIP;
+}
 
 inline bool valid_out(int out_dtype) { return out_dtype == FP8FG_OUT_BF16 || out_dtype == FP8FG_OUT_FP32; }
 
@@ -373,8 +376,6 @@ constexpr int64_t kMaxTopk = 16, kMaxLocalExperts = 256, kMaxExperts = 1024;
 
 static inline bool flag(int f) { return f == 0 || f == 1; }
 static inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-// blocks of a launch that needs `n` of them
-static inline bool grid_fits(int64_t n) { return n <= kMaxDim; }
 
 // the checks that both routing calls share
 static int route_args(int64_t ld, int64_t T, int64_t E, int64_t topk, int logits_bf16, int score, int renormalize) {
@@ -421,8 +422,9 @@ static int rows_args(int64_t T, int64_t H, int64_t topk, int64_t G, int64_t R) {
     if (topk > kMaxTopk || G > kMaxLocalExperts) return FP8FG_ERR_UNSUPPORTED;
     if (T > kMaxDim / topk || H > kMaxDim || R > kMaxDim) return FP8FG_ERR_UNSUPPORTED;
     if (H > 0 && (T > kMaxElems / H || R > kMaxElems / H)) return FP8FG_ERR_UNSUPPORTED;
-    // one wave per token and 512 channels at the most
-    if (!grid_fits(T * ((H + 511) / 512) + 127 * G)) return FP8FG_ERR_UNSUPPORTED;
+    // waves are counted in 32 bits, one per token and 512 channels at the most (whether a launch takes them is
+    // checked with its grid)
+    if (T * ((H + 511) / 512) + 127 * G > kMaxDim) return FP8FG_ERR_UNSUPPORTED;
     return FP8FG_OK;
 }
 

@@ -12,10 +12,13 @@ namespace fp8fg {
 // Launch `kernel` on `stream` and return the status of this launch itself.
 // (hipGetLastError() after a <<<>>> launch would also report an earlier,
 // unrelated error left in the runtime's last-error slot as this call's.)
-// The arguments are converted to the kernel's parameter types.
+// The arguments are converted to the kernel's parameter types.  HIP takes fewer than
+// 2^32 threads along the first axis; a longer grid is refused here, nothing enqueued.
+inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks * threads < (int64_t(1) << 32); }
 template <typename... P>
 hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t stream,
                          typename std::common_type<P>::type... args) {
+    if (!grid_fits(grid.x, block.x)) return hipErrorInvalidConfiguration;
     void* ptrs[] = {static_cast<void*>(&args)...};
     return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, ptrs, 0, stream);
 }

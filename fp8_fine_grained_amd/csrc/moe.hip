@@ -823,9 +823,10 @@ static hipError_t run_dispatch(const void* x, int64_t T_, const int32_t* idx, in
                              idx, uint32_t(T_), int(topk), uint32_t(per_token), int(first), uint32_t(G), o, row_of,
                              offsets, counts);
     }
+    const int64_t blocks = (waves + 3) / 4, grid = blocks + (MASKED ? 0 : (127 * G + 3) / 4);
+    if (!grid_fits(grid, 256)) return hipErrorInvalidConfiguration;      // before the first of the two launches
     const hipError_t e = launch_rows_layout(idx, n, first, G, MASKED ? o.rows_per : 0, row_of, offsets, counts, stream);
     if (e != hipSuccess || waves == 0) return e;
-    const int64_t blocks = (waves + 3) / 4, grid = blocks + (MASKED ? 0 : (127 * G + 3) / 4);
     // (R rows bound what is written: the routing is known on the device only)
     const bool stream_out = (R < n ? R : n) * o.H >= kStreamBytes;
     return launch_kernel(stream_out ? dispatch_rows<T, MASKED, true> : dispatch_rows<T, MASKED, false>,
