@@ -111,9 +111,15 @@ def _ptr(t):
 
 
 # The current stream's handle on t's device.  torch.cuda.current_stream builds a
-# Stream object around the same handle, 2 us of host time per call.
+# Stream object around the same handle, 2 us of host time per call; it serves where
+# torch has no entry for the handle alone.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t):
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    if _raw_stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream(t.get_device())
 
 
 def _check(fn, status):
