@@ -507,7 +507,7 @@ def _f32_or_bf16(t, name):
 def _logits(x):
     if not x.is_cuda:
         raise ValueError("logits must be a GPU tensor")
-    if x.dim() != 2 or x.stride(1) != 1 or (x.shape[0] > 1 and x.stride(0) < x.shape[1]):
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < x.shape[1]):
         raise ValueError("logits must have shape [T][E] with contiguous rows")
     return _f32_or_bf16(x, "logits"), (x.stride(0) if x.shape[0] > 1 else x.shape[1])
 

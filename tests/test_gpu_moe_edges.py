@@ -132,3 +132,16 @@ def test_dispatch_without_local_experts():
         assert q.shape == (0, 16, 256) and mm.shape == (0,) and torch.all(masked == -1)
         y = torch.full((128, 256), float("nan"), device=DEV)
         assert torch.all(fp8.moe_combine(y, row_of, torch.ones(40, 4, device=DEV)) == 0)
+
+
+def test_one_expert_from_a_column():
+    """One expert's logits, a column whose second stride means nothing: contiguous, strided and transposed."""
+    base = torch.randn(1, 40, device=DEV)
+    for x in (base.t(), base.t().contiguous(), torch.randn(40, 8, device=DEV)[:, :1]):
+        idx, w = fp8.moe_route(x, 1, renormalize=False)
+        assert torch.all(idx == 0) and torch.allclose(w, torch.sigmoid(x), rtol=1e-5)
+        g = fp8.moe_route_backward(x, idx, torch.ones(40, 1, device=DEV), renormalize=False)
+        s = torch.sigmoid(x.double())
+        assert torch.allclose(g.double(), s * (1 - s), rtol=1e-5)
+    with pytest.raises(ValueError):
+        fp8.moe_route(torch.zeros(2, 8, device=DEV).t(), 1)
