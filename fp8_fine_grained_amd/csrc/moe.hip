@@ -510,7 +510,19 @@ __global__ __launch_bounds__(256) void dispatch_rows(const T* __restrict__ x, co
 // 7168 channels, 4.9 us against 3.9 + 3.7 us for the two launches it replaces.  The
 // padding is most of a small contiguous call: with 1 / 8 / 16 parts, 1 token x 2 rows of 7168
 // channels in 8 experts 13.7 / 4.5 / 4.0 us, 64 tokens x 8 in 32 experts 16.0 / 9.3 / 9.1.
+//
+// Up to 2048 entries, and up to about as many workgroups as the chip holds at once (256
+// CUs x 8): each counts all entries, so more of them cost more than the second launch
+// (us, one launch / two; tokens x channels x choices in 8 to 32 experts).  Contiguous: 256 x 7168 x 8
+// (1024 workgroups) 11.7 / 14.2, 1024 x 512 x 2 6.8 / 7.6, 400 x 7168 x 4 (1600) 9.5 / 11.3, 2000 x
+// 1024 x 1 10.1 / 8.0, 512 x 7168 x 2 (2048) 11.1 / 9.5, 1024 x 7168 x 2 (4096) 19.6 / 13.3, 2048 x
+// 7168 x 1 (8192) 32.8 / 17.6; 512 x 7168 x 8 (4096 entries) 19.2 / 17.5.  Masked: 512 x 7168 x 2
+// 7.1 / 9.1, 1024 x 4096 x 1 6.7 / 8.5, 2000 x 1024 x 1 8.6 / 8.2, 1500 x 7168 x 1 (6000) 17.9 / 14.0.
 constexpr int64_t kSmallEntries = 2048;
+template <bool MASKED>
+constexpr int64_t small_grid() {
+    return MASKED ? 2048 : 1600;
+}
 constexpr uint32_t kPadParts = 8;
 
 template <class T, bool MASKED>
@@ -817,8 +829,9 @@ static hipError_t run_dispatch(const void* x, int64_t T_, const int32_t* idx, in
                                int64_t R, const RowsOut& o, int32_t* row_of, int32_t* offsets, int32_t* counts,
                                hipStream_t stream) {
     const int64_t n = T_ * topk, chunks = (o.H + kWaveChan - 1) / kWaveChan, waves = T_ * chunks;
-    if (n <= kSmallEntries && waves > 0) {
-        const int64_t per_token = (chunks + 3) / 4, grid = T_ * per_token + (MASKED ? 0 : G * kPadParts);
+    const int64_t per_token = (chunks + 3) / 4;
+    if (n <= kSmallEntries && waves > 0 && T_ * per_token <= small_grid<MASKED>()) {
+        const int64_t grid = T_ * per_token + (MASKED ? 0 : G * kPadParts);
         return launch_kernel(dispatch_small<T, MASKED>, dim3(unsigned(grid)), dim3(256), stream, static_cast<const T*>(x),
                              idx, uint32_t(T_), int(topk), uint32_t(per_token), int(first), uint32_t(G), o, row_of,
                              offsets, counts);
