@@ -238,7 +238,6 @@ struct Bracket {
             hi = -1.0f;
         }
     }
-    __device__ __forceinline__ Bracket(float s_, float lo_, float hi_) : s(s_), lo(lo_), hi(hi_) {}
     template <int N>
     __device__ __forceinline__ void encode(const float (&x)[4 * N], uint32_t (&code)[N]) const {
         uint32_t differ = 0;

@@ -2109,7 +2109,7 @@ __device__ __forceinline__ void gemm_wide_il_body(const GemmArgs& args, uint8_t*
 // gets zeros.  Bound by the loop's vector instructions (two multiplies per
 // element and K-block) and, with 16 K-blocks to a tile, by the bursts of FP32 C
 // stores: 32 experts, 65536 rows, 7168 x 2048, 1.92 TFLOP in 2.08-2.17 ms, 0.89-0.92
-// PFLOP/s; with the stores left out 1.91 ms.  Tiles of one expert run together: with the
+// PFLOP/s; with the stores left out 1.91 ms, adding to C 2.42-2.49 ms.  Tiles of one expert run together: with the
 // tiles of 2, 4 or 8 experts interleaved (to spread the bursts) the operand
 // panels leave the L2s, 2.84, 4.33 and 3.88 ms.
 constexpr int64_t WGRAD_BLOCKS = 64;
@@ -3151,7 +3151,9 @@ bool wide_b1_fits(const GemmArgs& args) {
 
 // The experts' weight gradients on the wide kernel: 256-wide n-tiles, and the
 // byte ranges of a 256-row slice of an operand (rows K apart) and of the scales
-// of one piece of the contraction below 4 GiB.
+// of one piece of the contraction below 4 GiB.  The others run 256 x 128 fold tiles: 32
+// experts, 65536 rows, 2048 x 1408 529 us with even experts and with Zipf-distributed ones, against
+// 461 and 620 us of 2048 x 1536 on the wide kernel.
 bool wide_wgrad_fits(const GemmArgs& args) {
     const int64_t rows = args.M > args.N ? args.M : args.N;
     return args.N % WideTile::BN == 0 && 256 * args.K <= int64_t(0xFFFFFFFF) &&

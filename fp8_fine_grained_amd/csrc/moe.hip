@@ -305,9 +305,8 @@ __global__ __launch_bounds__(256) void route_backward(const T* __restrict__ x, c
 // past m_max have no row.
 //
 // One workgroup per `chunk` entries.  It counts every expert's entries before
-// its chunk and in all (32 counters per expert, one per lane pair, so that
-// the lanes of a wave never meet on an address; 32 entries per thread in
-// flight), then ranks its own chunk 1024 entries at a time: the lanes of a wave
+// its chunk and in all (32 counters per expert, so that at most two lanes of a
+// wave, l and l + 32, meet on an address; 32 entries per thread in flight), then ranks its own chunk 1024 entries at a time: the lanes of a wave
 // with the same expert find each other with one ballot per bit of the index,
 // the waves' counts are summed in order.  No workgroup waits for another, at the
 // price of each reading every entry: 65536 entries take 9.8 us (64 workgroups).

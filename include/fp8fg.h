@@ -577,7 +577,9 @@ int fp8_swiglu_backward(const uint8_t* qc, const float* sc, const void* dh, int 
  * are clamped to [0, R] and rounded down to multiples of 128).  An expert
  * without rows gets zeros.  c: FP32 [G][M][N]; accumulate = 1 adds to it
  * (gradient accumulation) instead of writing it.  The accuracy contract and
- * engine are fp8_gemm_blockscaled's (2^-14 * S), for any number of rows.
+ * engine are fp8_gemm_blockscaled's (2^-14 * S; in the worst case for experts of up
+ * to 114688 rows, as for K there); each addition to c, one per 8192 rows at the most,
+ * rounds once more, by up to 2^-24 of the sum there.
  * Requires R % 128 == 0, N % 16 == 0; M, N, R < 2^31.
  */
 int fp8_grouped_gemm_wgrad(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb,
