@@ -24,7 +24,7 @@ OUT_FP32 = 1
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
 
-ABI_VERSION = 15
+ABI_VERSION = 16
 EXPORTS = ("fp8_quant_act_1x128", "fp8_quant_weight_128x128", "fp8_gemm_blockscaled",
            "fp8_grouped_gemm_contiguous", "fp8_grouped_gemm_masked",
            "fp8_quant_act_1x128_bf16", "fp8_quant_weight_128x128_bf16", "fp8_requant_act_tokenwise",
@@ -34,7 +34,8 @@ EXPORTS = ("fp8_quant_act_1x128", "fp8_quant_weight_128x128", "fp8_gemm_blocksca
            "fp8_quant_mx_1x32_transposed", "fp8_grouped_gemm_masked_tiled_fp8out",
            "fp8_grouped_gemm_masked_tiled_mx", "moe_route", "moe_route_backward", "fp8_moe_dispatch_contiguous",
            "fp8_moe_dispatch_masked", "moe_combine", "fp8_moe_combine_backward", "fp8_swiglu", "fp8_swiglu_backward",
-           "fp8_grouped_gemm_wgrad", "fp8fg_status_string", "fp8fg_abi_version")
+           "fp8_grouped_gemm_wgrad", "kv_assign_pages", "kv_release_pages", "rope", "fp8_kv_append",
+           "fp8_kv_attention_workspace", "fp8_kv_attention", "fp8fg_status_string", "fp8fg_abi_version")
 _COMPUTE = EXPORTS[:-2]
 
 
@@ -88,6 +89,12 @@ def load_library(path=LIB_PATH):
     lib.fp8_swiglu.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp]
     lib.fp8_swiglu_backward.argtypes = [vp, vp, vp, i32, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.fp8_grouped_gemm_wgrad.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp]
+    lib.kv_assign_pages.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp]
+    lib.kv_release_pages.argtypes = [vp, vp, vp, i64, i64, i64, vp, i64, vp, vp, vp, vp]
+    lib.rope.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, i64, i64, i32, vp, vp, i64, i64, i64, i32, f32, i32, vp]
+    lib.fp8_kv_append.argtypes = [vp, i64, vp, i64, i32, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp]
+    lib.fp8_kv_attention_workspace.argtypes = [i64, i64, i64, i64, i64, i64, i64, ctypes.POINTER(i64)]
+    lib.fp8_kv_attention.argtypes = [vp, i64, vp, vp, vp, vp, i64, i64, vp, i64, vp, vp, i64, i64, i64, i64, i64, f32, vp, vp, vp, i64, vp]
     for name in _COMPUTE:
         getattr(lib, name).restype = ctypes.c_int
     lib.fp8fg_status_string.argtypes = [ctypes.c_int]
@@ -713,3 +720,174 @@ def fp8_grouped_gemm_wgrad(a, sa, b, sb, group_offsets, out=None, accumulate=Fal
         _ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(group_offsets), G, M, N, R, _ptr(out), int(bool(accumulate)),
         _stream(a)))
     return out
+
+
+# Attention over a key/value cache held in 8 bits, in pages.
+
+def kv_cache(n_pages, heads, page, dim, device="cuda"):
+    """An empty cache of one layer: (k_cache u8 [n_pages][heads][page][dim], k_scale f32
+    [n_pages][heads], v_cache u8 [n_pages][heads][dim][page], v_scale f32 [n_pages][heads])."""
+    def zeros(*shape, dtype=torch.uint8):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+    return (zeros(n_pages, heads, page, dim), zeros(n_pages, heads, dtype=torch.float32),
+            zeros(n_pages, heads, dim, page), zeros(n_pages, heads, dtype=torch.float32))
+
+
+def kv_assign_pages(have, add, table, free_pages, n_free, page, T, out=None):
+    """A step's pages, slots and positions.  have, add int32 [B]: tokens that the
+    cache holds of each request, and new ones; table int32 [B][width], to which the new pages are
+    added; free_pages int32 [F], of which the first n_free (int32 [1]) are free; T rows
+    -> (lens int32 [B], cu int32 [B+1], positions int32 [T], slots int32 [T], left int32
+    [2]: pages left free, pages missing).  out: the five buffers to write."""
+    B, width = table.shape
+    F = free_pages.shape[0]
+    _need(table, torch.int32, (B, width), "table")
+    _need(have, torch.int32, (B,), "have")
+    _need(add, torch.int32, (B,), "add")
+    _need(free_pages, torch.int32, (F,), "free_pages")
+    _need(n_free, torch.int32, (1,), "n_free")
+    lens, cu, positions, slots, left = (None,) * 5 if out is None else out
+    lens = _out(lens, (B,), torch.int32, table, "lens")
+    cu = _out(cu, (B + 1,), torch.int32, table, "cu")
+    positions = _out(positions, (T,), torch.int32, table, "positions")
+    slots = _out(slots, (T,), torch.int32, table, "slots")
+    left = _out(left, (2,), torch.int32, table, "left")
+    _check("kv_assign_pages", load_library().kv_assign_pages(
+        _ptr(have), _ptr(add), B, _ptr(free_pages), _ptr(n_free), F, page, _ptr(table), width, T, _ptr(lens), _ptr(cu),
+        _ptr(positions), _ptr(slots), _ptr(left), _stream(table)))
+    return lens, cu, positions, slots, left
+
+
+def kv_release_pages(done, lens, table, free_pages, n_free, page, out=None):
+    """The pages of the requests that are done (int32 [B], 0 or not) back to the free
+    list, which is extended in place -> (lens int32 [B], 0 where done; left int32 [1],
+    the pages that are free now).  out: the two buffers to write."""
+    B, width = table.shape
+    F = free_pages.shape[0]
+    _need(table, torch.int32, (B, width), "table")
+    _need(done, torch.int32, (B,), "done")
+    _need(lens, torch.int32, (B,), "lens")
+    _need(free_pages, torch.int32, (F,), "free_pages")
+    _need(n_free, torch.int32, (1,), "n_free")
+    lens_out, left = (None, None) if out is None else out
+    lens_out = _out(lens_out, (B,), torch.int32, table, "lens")
+    left = _out(left, (1,), torch.int32, table, "left")
+    _check("kv_release_pages", load_library().kv_release_pages(
+        _ptr(done), _ptr(lens), _ptr(table), B, width, page, _ptr(free_pages), F, _ptr(n_free), _ptr(lens_out), _ptr(left),
+        _stream(table)))
+    return lens_out, left
+
+
+def _heads(t, dtype, shape, name):
+    """The distance of the rows of t [T][H][D], whose heads are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    T, H, D = shape
+    ld, step, one = t.stride()
+    if (D > 1 and one != 1) or (H > 1 and step != D) or (T > 1 and ld < H * D):
+        raise ValueError(f"{name} must have contiguous heads")
+    return ld if T > 1 else H * D
+
+
+def rope_frequencies(rot, base=10000.0, factor=1.0, original=4096, fast=32.0, slow=1.0, device="cuda"):
+    """Frequencies f32 [rot/2] for rope, base^(-2 i / rot), and the scale that goes
+    with them.  factor > 1 stretches a context of `original` tokens: frequencies that turn
+    fewer than `slow` times in it are divided by factor, those that turn more than `fast`
+    times are kept, with a linear ramp between, and the scale is 0.1 ln(factor) + 1."""
+    f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    if factor > 1.0:
+        turns = f * (original / 6.283185307179586)
+        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+    scale = 0.1 * float(torch.log(torch.tensor(factor, dtype=torch.float64))) + 1.0 if factor > 1.0 else 1.0
+    return f.float().to(device), scale
+
+
+def rope(q, k, positions, freqs, interleaved=False, scale=1.0, inverse=False, q_out=None, k_out=None):
+    """Rotary positions: q [T][Hq][D] and k [T][Hkv][D] (or None), f32 or bf16, rows may
+    be strided, turned by positions int32 [T] * freqs f32 [rot/2] and times scale ->
+    (q_out, k_out).  Pairs (i, i + rot/2), or (2 i, 2 i + 1) when interleaved; channels from
+    rot on are copied; rows with a negative position are not written.  inverse=True: the
+    gradient of q and k from that of the outputs.  q_out=q, k_out=k turns in place."""
+    T, Hq, D = q.shape
+    ldq = _heads(q, q.dtype, (T, Hq, D), "q")
+    bf16 = _f32_or_bf16(q, "q")
+    _need(positions, torch.int32, (T,), "positions")
+    _need(freqs, torch.float32, (freqs.shape[0],), "freqs")
+    q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    ldqo = _heads(q_out, q.dtype, (T, Hq, D), "q_out")
+    Hkv = ldk = ldko = 0
+    if k is not None:
+        Hkv = k.shape[1]
+        ldk = _heads(k, q.dtype, (T, Hkv, D), "k")
+        k_out = torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device) if k_out is None else k_out
+        ldko = _heads(k_out, q.dtype, (T, Hkv, D), "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    _check("rope", load_library().rope(
+        _ptr(q), ldq, _ptr(q_out), ldqo, Hq, _ptr(k), ldk, _ptr(k_out), ldko, Hkv, bf16, _ptr(positions), _ptr(freqs), T, D,
+        2 * freqs.shape[0], int(bool(interleaved)), scale, int(bool(inverse)), _stream(q)))
+    return q_out, k_out
+
+
+def _need_cache(k_cache, k_scale, v_cache, v_scale):
+    n, H, page, D = k_cache.shape
+    _need(k_cache, torch.uint8, (n, H, page, D), "k_cache")
+    _need(v_cache, torch.uint8, (n, H, D, page), "v_cache")
+    _need(k_scale, torch.float32, (n, H), "k_scale")
+    _need(v_scale, torch.float32, (n, H), "v_scale")
+    return n, H, page, D
+
+
+def fp8_kv_append(k, v, slots, k_cache, k_scale, v_cache, v_scale):
+    """New keys and values k, v f32 or bf16 [T][H][D] (rows may be strided) into their
+    slots int32 [T] of the cache (see kv_cache), in place: E4M3 codes under one power of
+    two per page and head.  Rows with a slot outside the cache are skipped; the rows of
+    a page are consecutive, with consecutive slots."""
+    n, H, page, D = _need_cache(k_cache, k_scale, v_cache, v_scale)
+    T = k.shape[0]
+    ldk, ldv = _heads(k, k.dtype, (T, H, D), "k"), _heads(v, k.dtype, (T, H, D), "v")
+    _need(slots, torch.int32, (T,), "slots")
+    _check("fp8_kv_append", load_library().fp8_kv_append(
+        _ptr(k), ldk, _ptr(v), ldv, _f32_or_bf16(k, "k"), _ptr(slots), T, H, D, page, n, _ptr(k_cache), _ptr(k_scale),
+        _ptr(v_cache), _ptr(v_scale), _stream(k)))
+
+
+def fp8_kv_attention_workspace(T, B, Hq, Hkv, D, page, width):
+    """Bytes of workspace of a call of fp8_kv_attention with these sizes."""
+    got = ctypes.c_int64(0)
+    _check("fp8_kv_attention_workspace", load_library().fp8_kv_attention_workspace(T, B, Hq, Hkv, D, page, width, ctypes.byref(got)))
+    return got.value
+
+
+def fp8_kv_attention(q, k_cache, k_scale, v_cache, v_scale, table, cu, lens, scale=None, out=None, lse=None, workspace=None):
+    """Causal attention of the new tokens q bf16 [T][Hq][D] (rows may be strided) over
+    the cache, which holds them already: request b's rows cu[b] .. cu[b+1] - 1 (int32
+    [B+1]), its lens[b] tokens (int32 [B]) in the pages table[b] (int32 [B][width]).
+    scale defaults to D^-0.5.  Returns out bf16 [T][Hq][D], or (out, lse) where lse f32 [T][Hq] is given to be
+    written.  Rows from cu[B] on are not written.  workspace: a uint8 tensor of at least
+    fp8_kv_attention_workspace bytes, used by one call at a time."""
+    n, Hkv, page, D = _need_cache(k_cache, k_scale, v_cache, v_scale)
+    T, Hq, _ = q.shape
+    B, width = table.shape
+    ldq = _heads(q, torch.bfloat16, (T, Hq, D), "q")
+    _need(table, torch.int32, (B, width), "table")
+    _need(cu, torch.int32, (B + 1,), "cu")
+    _need(lens, torch.int32, (B,), "lens")
+    out = _out(out, (T, Hq, D), torch.bfloat16, q, "out")
+    if lse is not None:
+        _need(lse, torch.float32, (T, Hq), "lse")
+    if workspace is None:
+        workspace = _empty((fp8_kv_attention_workspace(T, B, Hq, Hkv, D, page, width),), torch.uint8, q)
+    else:
+        _need(workspace, torch.uint8, (workspace.numel(),), "workspace")
+    _check("fp8_kv_attention", load_library().fp8_kv_attention(
+        _ptr(q), ldq, _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), n, page, _ptr(table), width, _ptr(cu),
+        _ptr(lens), B, T, Hq, Hkv, D, D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel(), _stream(q)))
+    return out if lse is None else (out, lse)

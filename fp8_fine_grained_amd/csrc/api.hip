@@ -541,4 +541,157 @@ int fp8_grouped_gemm_wgrad(const uint8_t* a, const float* sa, const uint8_t* b, 
     return hip_status(fp8fg::launch_gemm(0, fp8fg::GemmMode::Wgrad, 1, 1, args, static_cast<hipStream_t>(stream)));
 }
 
+// ---- the key/value cache ----
+
+// log2 of a page's tokens, -1 where they are no power of two in [16, 256]
+static int page_log(int64_t page) {
+    for (int l = 4; l <= 8; ++l)
+        if (page == int64_t(1) << l) return l;
+    return -1;
+}
+
+// B requests with a block table of `width` entries each
+static int table_args(int64_t B, int64_t width, int64_t page) {
+    if (B < 0 || width < 0) return FP8FG_ERR_SHAPE;
+    if (page_log(page) < 0 || B > 65536 || (width > 0 && (B > kMaxDim / width || page > kMaxDim / width))) return FP8FG_ERR_UNSUPPORTED;
+    return FP8FG_OK;
+}
+
+int kv_assign_pages(const int32_t* have, const int32_t* add, int64_t B, const int32_t* free_pages, const int32_t* n_free,
+                    int64_t F, int64_t page, int32_t* table, int64_t width, int64_t T, int32_t* lens, int32_t* cu,
+                    int32_t* positions, int32_t* slots, int32_t* left, void* stream) {
+    if (!n_free || !cu || !left || (F > 0 && !free_pages) || (T > 0 && (!positions || !slots))) return FP8FG_ERR_NULL;
+    if (B > 0 && (!have || !add || !lens || (width > 0 && !table))) return FP8FG_ERR_NULL;
+    if (F < 0 || T < 0) return FP8FG_ERR_SHAPE;
+    if (const int e = table_args(B, width, page)) return e;
+    if (!aligned16(have) || !aligned16(add) || !aligned16(free_pages) || !aligned4(n_free) || !aligned16(table) || !aligned16(lens) ||
+        !aligned16(cu) || !aligned16(positions) || !aligned16(slots) || !aligned16(left))
+        return FP8FG_ERR_ALIGN;
+    if (F > kMaxDim || T > kMaxDim) return FP8FG_ERR_UNSUPPORTED;
+    return hip_status(fp8fg::launch_kv_assign(have, add, B, free_pages, n_free, F, page_log(page), table, width, T, lens, cu, positions,
+                                              slots, left, static_cast<hipStream_t>(stream)));
+}
+
+int kv_release_pages(const int32_t* done, const int32_t* lens, const int32_t* table, int64_t B, int64_t width, int64_t page,
+                     int32_t* free_pages, int64_t F, const int32_t* n_free, int32_t* lens_out, int32_t* left, void* stream) {
+    if (!n_free || !left || (F > 0 && !free_pages)) return FP8FG_ERR_NULL;
+    if (B > 0 && (!done || !lens || !lens_out || (width > 0 && !table))) return FP8FG_ERR_NULL;
+    if (F < 0) return FP8FG_ERR_SHAPE;
+    if (const int e = table_args(B, width, page)) return e;
+    if (!aligned16(done) || !aligned16(lens) || !aligned16(table) || !aligned16(free_pages) || !aligned4(n_free) || !aligned16(lens_out) ||
+        !aligned16(left))
+        return FP8FG_ERR_ALIGN;
+    if (F > kMaxDim) return FP8FG_ERR_UNSUPPORTED;
+    return hip_status(fp8fg::launch_kv_release(done, lens, table, B, width, page_log(page), free_pages, F, n_free, lens_out, left,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+// [T][H][D] with rows ld elements of `size` bytes apart
+static int rows_of_heads(int64_t T, int64_t H, int64_t D, int64_t ld, int size) {
+    if (H > 0 && (ld < H * D || ld * size % 16 != 0)) return FP8FG_ERR_SHAPE;
+    return ld > kMaxElems || (T > 0 && ld > kMaxElems / T) ? FP8FG_ERR_UNSUPPORTED : FP8FG_OK;
+}
+
+int rope(const void* q, int64_t ldq, void* q_out, int64_t ldqo, int64_t Hq, const void* k, int64_t ldk, void* k_out, int64_t ldko,
+         int64_t Hkv, int x_bf16, const int32_t* positions, const float* freqs, int64_t T, int64_t D, int64_t rot, int interleaved,
+         float scale, int inverse, void* stream) {
+    if (T > 0 && ((Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out)) || !positions || !freqs)) return FP8FG_ERR_NULL;
+    if (T < 0 || Hq < 0 || Hkv < 0 || D <= 0 || D % 8 != 0 || rot <= 0 || rot % 16 != 0 || rot > D) return FP8FG_ERR_SHAPE;
+    if (!flag(x_bf16) || !flag(interleaved) || !flag(inverse) || rot > 256 || D > 1024 || Hq > 65535 || Hkv > 65535 || T > kMaxDim)
+        return FP8FG_ERR_UNSUPPORTED;
+    const int size = x_bf16 ? 2 : 4;
+    for (const int e : {rows_of_heads(T, Hq, D, ldq, size), rows_of_heads(T, Hq, D, ldqo, size), rows_of_heads(T, Hkv, D, ldk, size),
+                        rows_of_heads(T, Hkv, D, ldko, size)})
+        if (e) return e;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out) || !aligned16(positions) || !aligned16(freqs))
+        return FP8FG_ERR_ALIGN;
+    if (T == 0 || Hq + Hkv == 0) return FP8FG_OK;
+    return hip_status(fp8fg::launch_rope({q, k, q_out, k_out, ldq, ldk, ldqo, ldko, T, Hq, Hkv, D, rot, x_bf16, interleaved, inverse, scale,
+                                          positions, freqs}, static_cast<hipStream_t>(stream)));
+}
+
+// the cache's own sizes
+static int cache_args(int64_t n_pages, int64_t H, int64_t page, int64_t D) {
+    if (n_pages < 0 || H < 0) return FP8FG_ERR_SHAPE;
+    if (page_log(page) < 0 || (D != 64 && D != 128 && D != 192 && D != 256) || H > 65535) return FP8FG_ERR_UNSUPPORTED;
+    return n_pages > kMaxDim / page || (n_pages > 0 && H > kMaxElems / (n_pages * page * D)) ? FP8FG_ERR_UNSUPPORTED : FP8FG_OK;
+}
+
+int fp8_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int x_bf16, const int32_t* slots, int64_t T, int64_t H,
+                  int64_t D, int64_t page, int64_t n_pages, uint8_t* k_cache, float* k_scale, uint8_t* v_cache, float* v_scale,
+                  void* stream) {
+    if (T > 0 && H > 0 && (!k || !v || !slots || (n_pages > 0 && (!k_cache || !k_scale || !v_cache || !v_scale)))) return FP8FG_ERR_NULL;
+    if (T < 0) return FP8FG_ERR_SHAPE;
+    if (const int e = cache_args(n_pages, H, page, D)) return e;
+    if (!flag(x_bf16) || T > kMaxDim) return FP8FG_ERR_UNSUPPORTED;
+    for (const int e : {rows_of_heads(T, H, D, ldk, x_bf16 ? 2 : 4), rows_of_heads(T, H, D, ldv, x_bf16 ? 2 : 4)})
+        if (e) return e;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(slots) || !aligned16(k_cache) || !aligned16(k_scale) || !aligned16(v_cache) ||
+        !aligned16(v_scale))
+        return FP8FG_ERR_ALIGN;
+    if (T == 0 || H == 0 || n_pages == 0) return FP8FG_OK;
+    return hip_status(fp8fg::launch_kv_append({k, v, ldk, ldv, T, H, D, n_pages, x_bf16, page_log(page), slots, k_cache, v_cache, k_scale,
+                                               v_scale}, static_cast<hipStream_t>(stream)));
+}
+
+// the sizes of an attention call, and what they are together
+static int attend_args(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t width, fp8fg::AttendCall& c) {
+    if (T < 0 || Hq < 0 || Hkv < 0 || (Hkv == 0 ? Hq != 0 : Hq % Hkv != 0)) return FP8FG_ERR_SHAPE;
+    if (const int e = table_args(B, width, page)) return e;
+    if (const int e = cache_args(0, Hkv, page, D)) return e;
+    if (Hq > 65535 || T > kMaxDim || (Hq > 0 && T > kMaxElems / (Hq * D))) return FP8FG_ERR_UNSUPPORTED;
+    c.T = T;
+    c.B = B;
+    c.Hq = Hq;
+    c.Hkv = Hkv;
+    c.D = D;
+    c.page_log = page_log(page);
+    c.width = width;
+    return FP8FG_OK;
+}
+
+int fp8_kv_attention_workspace(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t width, int64_t* bytes) {
+    if (!bytes) return FP8FG_ERR_NULL;
+    fp8fg::AttendCall c{};
+    if (const int e = attend_args(T, B, Hq, Hkv, D, page, width, c)) return e;
+    *bytes = T == 0 || B == 0 || Hq == 0 ? 0 : fp8fg::attend_workspace(c);
+    return FP8FG_OK;
+}
+
+int fp8_kv_attention(const uint16_t* q, int64_t ldq, const uint8_t* k_cache, const float* k_scale, const uint8_t* v_cache,
+                     const float* v_scale, int64_t n_pages, int64_t page, const int32_t* table, int64_t width, const int32_t* cu,
+                     const int32_t* lens, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, float scale, uint16_t* out,
+                     float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+    const bool work = T > 0 && B > 0 && Hq > 0;
+    if (work && (!q || !k_cache || !k_scale || !v_cache || !v_scale || !cu || !lens || !out || (width > 0 && !table))) return FP8FG_ERR_NULL;
+    fp8fg::AttendCall c{};
+    if (const int e = attend_args(T, B, Hq, Hkv, D, page, width, c)) return e;
+    if (const int e = cache_args(n_pages, Hkv, page, D)) return e;
+    if (work && n_pages == 0) return FP8FG_ERR_SHAPE;
+    if (const int e = rows_of_heads(T, Hq, D, ldq, 2)) return e;
+    if (!(scale >= 0.0f) || scale > 0x1p64f) return FP8FG_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(k_scale) || !aligned16(v_cache) || !aligned16(v_scale) || !aligned16(table) ||
+        !aligned16(cu) || !aligned16(lens) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace))
+        return FP8FG_ERR_ALIGN;
+    if (!work) return FP8FG_OK;
+    const int64_t need = fp8fg::attend_workspace(c);
+    if (need > 0 && !workspace) return FP8FG_ERR_NULL;
+    if (workspace_bytes < need) return FP8FG_ERR_SHAPE;
+    c.q = q;
+    c.ldq = ldq;
+    c.kc = k_cache;
+    c.ks = k_scale;
+    c.vc = v_cache;
+    c.vs = v_scale;
+    c.table = table;
+    c.cu = cu;
+    c.lens = lens;
+    c.n_pages = n_pages;
+    c.scale = scale;
+    c.out = out;
+    c.lse = lse;
+    c.workspace = workspace;
+    return hip_status(fp8fg::launch_attend(c, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -1,0 +1,422 @@
+// Attention of new tokens over the 8-bit cache (gfx950).
+//
+//   out_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale q_i . k_j - m_i)
+//
+// over the keys j that token i sees, in one pass with a running maximum m.
+// Keys and values are E4M3 codes times one scale per page and head.  K's codes
+// are widened exactly to BF16 and multiplied with the BF16 queries, V's exactly
+// to FP16 and multiplied with FP16 probabilities, sums in FP32.
+//
+// A tile is 64 tokens of one head, S^T = K Q^T of it four 16-token products.
+// The 16 x 16 result of the matrix instruction leaves row 4 g + i of a 16-lane
+// group g in register i, so with row n of product j holding token
+// 16 (n / 4) + 4 j + n % 4, group g ends up with tokens 16 g .. 16 g + 15 of one
+// query row: exactly the operand P^T of O^T = V^T P^T, in which group g's
+// lanes supply 16 consecutive tokens.  No probability moves between lanes, a
+// lane's V operand is 16 consecutive bytes of the value page ([channel][token]),
+// and its 16 tokens lie in one page, whose scales are two registers.
+#include "elementwise.hpp"
+#include "launch.hpp"
+
+namespace fp8fg {
+
+namespace attend_detail {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kTile = 64;                 // tokens of a tile
+constexpr int kMinTiles = kWaves;         // tiles that a split holds at the least: one per wave
+constexpr int kTarget = 1024;             // workgroups that the whole call is split into, about
+constexpr float kPBias = 15.0f;           // probabilities are held times 2^15: FP16 keeps them normal down to 2^-29
+
+struct Args {
+    const uint16_t* q;
+    const uint8_t *kc, *vc;
+    const float *ks, *vs;
+    const int32_t *table, *cu, *lens;
+    int64_t ldq, n_pages, width, B, T;
+    int Hq, Hkv, G, page_log;             // G: query heads of a key/value head
+    float scale2;                         // softmax scale * log2(e)
+    uint16_t* out;
+    float* lse;
+    int32_t* head;                        // workspace: [0] number of row tiles
+    int32_t* desc;                        // row tile -> its rows and parts
+    float* parts;                         // unjoined results
+    int64_t most_tiles, most_parts;       // room for them
+    int target;                           // workgroups wanted for each key/value head
+};
+
+// What a workgroup does: rows tile * ROWS .. of request b (n tokens from row cu of q on), the
+// split-th of `splits` parts of its keys
+struct Item {
+    int32_t b, cu, n, len, tile, tile_id, split, splits, part;
+};
+
+constexpr int kDescInts = 8;
+
+__device__ __forceinline__ int scan_add(int v, int* part, int& all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int by = 1; by < 64; by *= 2) {
+        const int a = __shfl_up(v, by, 64);
+        if (lane >= by) v += a;
+    }
+    __syncthreads();
+    if (lane == 63) part[wave] = v;
+    __syncthreads();
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) v += part[w];
+        all += part[w];
+    }
+    return v;
+}
+
+// The requests' row tiles and their splits, numbered in order; every workgroup
+// finds its own from the lengths.  Splits are of equal numbers of tiles, as long as
+// it takes for about `target` workgroups to do all the work.
+template <int ROWS>
+__device__ __forceinline__ bool find_item(const Args& p, Item& it) {
+    __shared__ int part[kWaves];
+    __shared__ float fpart[kWaves];
+    __shared__ Item found;
+    const int64_t room = p.width << p.page_log;
+    const auto shape = [&](int64_t b, int& cu, int& n, int& len, int& tiles, int& kt) {
+        cu = p.cu[b];
+        n = p.cu[b + 1] - cu;
+        len = p.lens[b];
+        cu = cu < 0 ? 0 : cu;
+        n = cu >= p.T ? 0 : n > p.T - cu ? int(p.T - cu) : n;
+        n = n < 0 ? 0 : n;
+        len = len < 0 ? 0 : len > room ? int(room) : len;
+        tiles = int((int64_t(n) * p.G + ROWS - 1) / ROWS);
+        kt = (len + kTile - 1) / kTile;
+    };
+    float work = 0.0f;
+    int cu = 0, n = 0, len = 0, tiles = 0, kt = 0;
+    for (int64_t b = threadIdx.x; b < p.B; b += kThreads) {
+        shape(b, cu, n, len, tiles, kt);
+        work += float(tiles) * float(kt);
+    }
+    work = lanes_sum<64>(work);
+    if ((threadIdx.x & 63) == 0) fpart[threadIdx.x >> 6] = work;
+    if (threadIdx.x == 0) found.b = -1;
+    __syncthreads();
+    work = fpart[0] + fpart[1] + fpart[2] + fpart[3];
+    const float want = ceilf(work / float(p.target));
+    const int per = want < float(kMinTiles) ? kMinTiles : want > 0x1p30f ? 1 << 30 : int(want);
+    const bool whole = p.B <= kThreads;
+    const int me = blockIdx.x;
+    int items0 = 0, parts0 = 0, tiles0 = 0;
+    for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int64_t b = b0 + threadIdx.x;
+        if (!whole || b >= p.B) tiles = 0;
+        if (!whole && b < p.B) shape(b, cu, n, len, tiles, kt);
+        const int splits = kt > per ? (kt + per - 1) / per : 1;
+        const int items = tiles * splits, parts = splits > 1 ? items : 0;
+        int all_items, all_parts, all_tiles;
+        const int i1 = items0 + scan_add(items, part, all_items);
+        const int p1 = parts0 + scan_add(parts, part, all_parts);
+        const int t1 = tiles0 + scan_add(tiles, part, all_tiles);
+        if (me >= i1 - items && me < i1) {
+            const int at = me - (i1 - items), tile = at / splits;
+            found = Item{int32_t(b), cu, n, len, tile, t1 - tiles + tile, at - tile * splits, splits, p1 - parts + tile * splits};
+        }
+        items0 += all_items;
+        parts0 += all_parts;
+        tiles0 += all_tiles;
+    }
+    __syncthreads();
+    if (me == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.head) p.head[0] = tiles0;
+    it = found;
+    return it.b >= 0 && (it.splits == 1 || it.part + it.splits <= p.most_parts);
+}
+
+template <bool HI>
+__device__ __forceinline__ uint32_t to_bf16(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(int(w), 1.0f, HI));
+}
+template <bool HI>
+__device__ __forceinline__ uint32_t to_f16(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(w), 1.0f, HI));
+}
+__device__ __forceinline__ v8bf wide_bf16(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(v8bf, u32x4{to_bf16<false>(a), to_bf16<true>(a), to_bf16<false>(b), to_bf16<true>(b)});
+}
+__device__ __forceinline__ v8h wide_f16(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(v8h, u32x4{to_f16<false>(a), to_f16<true>(a), to_f16<false>(b), to_f16<true>(b)});
+}
+
+// max over the four 16-lane groups
+__device__ __forceinline__ float groups_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float groups_sum(float v) {
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+
+// the bytes of w (tokens first .. first + 3) that lie before `end`
+__device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int first, int end) {
+    const int n = end - first;
+    return n >= 4 ? w : n <= 0 ? 0u : w & (0xFFFFFFFFu >> (32 - 8 * n));
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
+    constexpr int ROWS = 16, KC = D / 64, DT = D / 16;
+    __shared__ __align__(16) float joined[kWaves][ROWS * D];
+    __shared__ float stat[kWaves][2][ROWS];
+    Item it;
+    if (!find_item<ROWS>(p, it)) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4, kvh = blockIdx.y;
+    // this lane's query row, and the last key that it sees
+    const int row = it.tile * ROWS + col, tq = row / p.G, hq = kvh * p.G + (row - tq * p.G);
+    const bool live = tq < it.n;
+    const int before = it.len - it.n;
+    const auto sees = [&](int t) { return t < it.n ? (before + t < it.len ? before + t : it.len - 1) : -1; };
+    const int last = sees(tq);
+    const int first_tq = it.tile * ROWS / p.G, end_tq = (it.tile * ROWS + ROWS - 1) / p.G;
+    const int least = sees(first_tq), most = sees(end_tq < it.n ? end_tq : it.n - 1);
+    const int kt = most < 0 ? 0 : most / kTile + 1;
+    const int per = (kt + it.splits - 1) / it.splits, kt0 = it.split * per, kt1 = kt0 + per < kt ? kt0 + per : kt;
+    const int32_t* table = p.table + int64_t(it.b) * p.width;
+    const int64_t page_bytes = int64_t(D) << p.page_log;
+
+    v8bf qf[KC][2];
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            u32x4 w{0u, 0u, 0u, 0u};
+            if (live) w = ld<u32x4>(p.q + int64_t(it.cu + tq) * p.ldq + hq * D + 64 * c + 16 * g + 8 * h);
+            qf[c][h] = __builtin_bit_cast(v8bf, w);
+        }
+    v4f o[DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    float m = -__builtin_inff(), l = 0.0f, ref = 0.0f, largest = 0.0f;
+
+    for (int tile = kt0 + wave; tile < kt1; tile += kWaves) {
+        const int t0 = tile * kTile;
+        // the page of this group's tokens, and the page of the group whose keys this lane loads
+        const auto page_of = [&](int group, bool& good) {
+            const int token = t0 + 16 * group;
+            const int64_t entry = token >> p.page_log;
+            int32_t id = token < it.len ? table[entry] : -1;
+            good = id >= 0 && id < p.n_pages;
+            return good ? id : 0;
+        };
+        bool good, kgood;
+        const int64_t vid = page_of(g, good), kid = page_of(col >> 2, kgood);
+        const float ksc = good ? p.ks[vid * p.Hkv + kvh] * p.scale2 : 0.0f, vsc = good ? p.vs[vid * p.Hkv + kvh] : 0.0f;
+        const int mask = (1 << p.page_log) - 1;
+        const uint8_t* kp = p.kc + (kid * p.Hkv + kvh) * page_bytes + ((t0 + 16 * (col >> 2)) & mask) * D + (col & 3) * D + 16 * g;
+        const uint8_t* vp = p.vc + (vid * p.Hkv + kvh) * page_bytes + ((t0 + 16 * g) & mask) + (int64_t(col) << p.page_log);
+        v4f s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const u32x4 w = ld<u32x4>(kp + 4 * j * D + 64 * c);
+                s[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide_bf16(w[0], w[1]), qf[c][0], s[j], 0, 0, 0);
+                s[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide_bf16(w[2], w[3]), qf[c][1], s[j], 0, 0, 0);
+            }
+        }
+        // scores in units of log2; keys out of sight at -inf
+        const bool all_good = __all(good);
+        const bool masked = t0 + kTile - 1 > least || !all_good;
+        const int seen = good ? last - (t0 + 16 * g) : -1;           // the last of the lane's tokens in sight
+        float mt = -__builtin_inff();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[j][i] *= ksc;
+                if (masked && 4 * j + i > seen) s[j][i] = -__builtin_inff();
+                mt = fmaxf(mt, s[j][i]);
+            }
+        const float m_new = fmaxf(m, groups_max(mt)), m_use = m_new == -__builtin_inff() ? 0.0f : m_new;
+        const float alpha = __builtin_amdgcn_exp2f(m - m_use);
+        m = m_new;
+        // O is held in units of `ref`, the largest of the four pages' value scales, but no
+        // less than 2^-40 of the largest so far: FP32 holds the sums in such units
+        const float top = groups_max(vsc);
+        largest = fmaxf(largest, top);
+        const float unit = fmaxf(top, largest * 0x1p-40f);
+        float factor = alpha;
+        if (unit != ref) {
+            factor *= ref / unit;
+            ref = unit;
+        }
+        const float ratio = ref > 0.0f ? vsc / ref : 0.0f;
+        float sum = 0.0f;
+        v8h pf[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = __builtin_amdgcn_exp2f(s[j][i] - (m_use - kPBias));
+                sum += e;
+                pf[j >> 1][(j & 1) * 4 + i] = _Float16(e * ratio);
+            }
+        l = __builtin_fmaf(l, alpha, sum);
+        const int end = !good ? 0 : it.len - (t0 + 16 * g);          // codes past the last token are not numbers
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            o[d] *= factor;
+            u32x4 w = ld<u32x4>(vp + (int64_t(16 * d) << p.page_log));
+            if (masked) w = u32x4{keep_bytes(w[0], 0, end), keep_bytes(w[1], 4, end), keep_bytes(w[2], 8, end), keep_bytes(w[3], 12, end)};
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wide_f16(w[0], w[1]), pf[0], o[d], 0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wide_f16(w[2], w[3]), pf[1], o[d], 0, 0, 0);
+        }
+    }
+
+    // the four waves' results joined
+    l = groups_sum(l);
+    if (g == 0) {
+        stat[wave][0][col] = m;
+        stat[wave][1][col] = l;
+    }
+    __syncthreads();
+    float M = stat[0][0][col];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) M = fmaxf(M, stat[w][0][col]);
+    const float M_use = M == -__builtin_inff() ? 0.0f : M;
+    float L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) L = __builtin_fmaf(stat[w][1][col], __builtin_amdgcn_exp2f(stat[w][0][col] - M_use), L);
+    const float mine = __builtin_amdgcn_exp2f(m - M_use) * ref;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)      // [row][channel], the 16-byte pieces of a row swapped by row
+        st<v4f>(&joined[wave][col * D + (((4 * d + g) ^ col) * 4)], o[d] * mine);
+    __syncthreads();
+    const bool split = it.splits > 1;
+    float* part = p.parts + (int64_t(it.part + it.split) * p.Hkv + kvh) * (ROWS * (D + 2));
+    for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
+        const int r = i / (D / 4), c = i - r * (D / 4);
+        v4f v = ld<v4f>(&joined[0][r * D + ((c ^ r) * 4)]);
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += ld<v4f>(&joined[w][r * D + ((c ^ r) * 4)]);
+        if (split) {
+            st<v4f>(part + 2 * ROWS + r * D + 4 * c, v);
+            continue;
+        }
+        const int rr = it.tile * ROWS + r, t = rr / p.G;
+        float sum = 0.0f, top = stat[0][0][r];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, stat[w][0][r]);
+        top = top == -__builtin_inff() ? 0.0f : top;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) sum = __builtin_fmaf(stat[w][1][r], __builtin_amdgcn_exp2f(stat[w][0][r] - top), sum);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        if (t < it.n) {
+            const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+            store_n<4>(p.out + (int64_t(it.cu + t) * p.Hq + kvh * p.G + (rr - t * p.G)) * D + 4 * c, out);
+        }
+    }
+    if (wave == 0 && g == 0) {
+        if (split) {
+            part[col] = M;
+            part[ROWS + col] = L;
+        } else if (live && p.lse) {
+            p.lse[int64_t(it.cu + tq) * p.Hq + hq] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
+        }
+    }
+    if (p.head && it.split == 0 && kvh == 0 && threadIdx.x == 0 && it.tile_id < p.most_tiles) {
+        int32_t* d = p.desc + int64_t(it.tile_id) * kDescInts;
+        d[0] = it.splits;
+        d[1] = it.part;
+        d[2] = it.cu;
+        d[3] = it.n;
+        d[4] = it.tile;
+    }
+}
+
+// The splits of a row tile joined, in their order
+template <int D, int ROWS>
+__global__ __launch_bounds__(kThreads) void join(const Args p) {
+    const int id = blockIdx.x, kvh = blockIdx.y;
+    if (id >= p.head[0]) return;
+    const int32_t* d = p.desc + int64_t(id) * kDescInts;
+    const int splits = d[0], first = d[1], cu = d[2], n = d[3], tile = d[4];
+    if (splits <= 1) return;
+    const float* part = p.parts + (int64_t(first) * p.Hkv + kvh) * (ROWS * (D + 2));
+    const int64_t step = int64_t(p.Hkv) * (ROWS * (D + 2));
+    for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
+        const int r = i / (D / 4), c = i - r * (D / 4), rr = tile * ROWS + r, t = rr / p.G;
+        if (t >= n) continue;
+        float M = -__builtin_inff();
+        for (int s = 0; s < splits; ++s) M = fmaxf(M, part[s * step + r]);
+        const float M_use = M == -__builtin_inff() ? 0.0f : M;
+        float L = 0.0f;
+        v4f v{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < splits; ++s) {
+            const float f = __builtin_amdgcn_exp2f(part[s * step + r] - M_use);
+            L = __builtin_fmaf(part[s * step + ROWS + r], f, L);
+            v += ld<v4f>(part + s * step + 2 * ROWS + r * D + 4 * c) * f;
+        }
+        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        const int64_t at = int64_t(cu + t) * p.Hq + kvh * p.G + (rr - t * p.G);
+        const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+        store_n<4>(p.out + at * D + 4 * c, out);
+        if (c == 0 && p.lse) p.lse[at] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
+    }
+}
+
+struct Plan {
+    int64_t tiles, items, parts;          // bounds: row tiles, workgroups, unjoined results, per key/value head
+    int target;
+    int64_t bytes;
+};
+inline Plan plan_of(const AttendCall& c, int rows) {
+    Plan r;
+    const int64_t G = c.Hq / c.Hkv, seqs = c.B < c.T ? c.B : c.T, kt = ((c.width << c.page_log) + kTile - 1) / kTile;
+    r.target = int((kTarget + c.Hkv - 1) / c.Hkv);
+    r.tiles = c.T * G / rows + seqs;
+    const bool split = kt > kMinTiles;
+    // a tile has one item more than the work's share at the most, a split one twice as many
+    // (the work is summed in FP32)
+    r.items = r.tiles + (split ? r.target + 1 : 0);
+    r.parts = split ? 2 * int64_t(r.target) + 2 : 0;
+    r.bytes = split ? 256 + (r.tiles * kDescInts * 4 + 255) / 256 * 256 + r.parts * c.Hkv * rows * (c.D + 2) * 4 : 0;
+    return r;
+}
+
+template <int D>
+hipError_t run(const AttendCall& c, Args p, const Plan& plan, hipStream_t stream) {
+    if (const hipError_t e = launch_kernel(attend<D>, dim3(unsigned(plan.items), unsigned(c.Hkv)), dim3(kThreads), stream, p)) return e;
+    if (plan.bytes == 0) return hipSuccess;
+    return launch_kernel(join<D, 16>, dim3(unsigned(plan.tiles), unsigned(c.Hkv)), dim3(kThreads), stream, p);
+}
+
+}  // namespace attend_detail
+
+int64_t attend_workspace(const AttendCall& c) { return attend_detail::plan_of(c, 16).bytes; }
+
+hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
+    using namespace attend_detail;
+    const Plan plan = plan_of(c, 16);
+    Args p{c.q, c.kc, c.vc, c.ks, c.vs, c.table, c.cu, c.lens, c.ldq, c.n_pages, c.width, c.B, c.T, int(c.Hq), int(c.Hkv), int(c.Hq / c.Hkv),
+           c.page_log, c.scale * 1.4426950408889634f, c.out, c.lse, nullptr, nullptr, nullptr, plan.tiles, plan.parts, plan.target};
+    if (plan.bytes) {
+        uint8_t* w = static_cast<uint8_t*>(c.workspace);
+        p.head = reinterpret_cast<int32_t*>(w);
+        p.desc = reinterpret_cast<int32_t*>(w + 256);
+        p.parts = reinterpret_cast<float*>(w + 256 + (plan.tiles * kDescInts * 4 + 255) / 256 * 256);
+    }
+    switch (c.D) {
+        case 64: return run<64>(c, p, plan, stream);
+        case 128: return run<128>(c, p, plan, stream);
+        case 192: return run<192>(c, p, plan, stream);
+        default: return run<256>(c, p, plan, stream);
+    }
+}
+
+}  // namespace fp8fg

@@ -1,0 +1,417 @@
+// The key/value cache's bookkeeping and its writes (gfx950): a step's pages,
+// slots and positions from the requests' lengths, rotary positions, and new keys
+// and values quantized into the cache's pages.
+#include "elementwise.hpp"
+#include "launch.hpp"
+
+namespace fp8fg {
+
+namespace kv_detail {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+
+__device__ __forceinline__ int64_t shfl_up64(int64_t v, int by) {
+    const int lo = __shfl_up(int(uint32_t(v)), by, 64), hi = __shfl_up(int(v >> 32), by, 64);
+    return int64_t(uint64_t(uint32_t(hi)) << 32 | uint32_t(lo));
+}
+
+// Inclusive sums over the workgroup's threads of two values at once; `all`: the
+// workgroup's totals
+struct Two {
+    int64_t a, b;
+};
+__device__ __forceinline__ Two block_scan(Two v, Two* part, Two& all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int by = 1; by < 64; by *= 2) {
+        const int64_t a = shfl_up64(v.a, by), b = shfl_up64(v.b, by);
+        if (lane >= by) {
+            v.a += a;
+            v.b += b;
+        }
+    }
+    __syncthreads();                      // the last use of part is over
+    if (lane == 63) part[wave] = v;
+    __syncthreads();
+    all = Two{0, 0};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) {
+            v.a += part[w].a;
+            v.b += part[w].b;
+        }
+        all.a += part[w].a;
+        all.b += part[w].b;
+    }
+    return v;
+}
+
+// The last index i in [0, n) with start[i] <= x (start non-decreasing, start[0] <= x)
+__device__ __forceinline__ int last_not_past(const int32_t* start, int n, int32_t x) {
+    int lo = 0;
+    while (n > 1) {
+        const int half = n / 2;
+        if (start[lo + half] <= x) lo += half;
+        n -= half;
+    }
+    return lo;
+}
+
+// A step's tables.  Request b holds have[b] tokens in ceil(have / page) pages and
+// brings add[b] more; the rows of the step are the new tokens in the order of the
+// requests.  Each workgroup forms the sums over all requests, 256 at a time, and
+// writes the rows and requests that are its own: no workgroup waits for another.  Its row
+// of a page's first token writes the page into the table.
+struct AssignArgs {
+    const int32_t *have, *add, *free_pages, *n_free;
+    int64_t B, F, width, T;
+    int page_log;
+    int32_t *table, *lens, *cu, *positions, *slots, *left;
+};
+constexpr int kRows = 1024;               // rows of a workgroup
+
+__global__ __launch_bounds__(kThreads) void assign(const AssignArgs p) {
+    __shared__ Two part[kWaves];
+    __shared__ int32_t start[kThreads], held[kThreads], first_new[kThreads];    // rows; tokens; place of its first new page, -1: refused
+    const int64_t row0 = int64_t(blockIdx.x) * kRows, row1 = row0 + kRows < p.T ? row0 + kRows : p.T;
+    const int page = 1 << p.page_log;
+    int64_t n = p.n_free[0];
+    n = n < 0 ? 0 : n > p.F ? p.F : n;
+    int64_t rows = 0, wanted = 0, used = 0;
+    for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int64_t b = b0 + threadIdx.x;
+        const bool real = b < p.B;
+        int64_t have = real ? p.have[b] : 0, add = real ? p.add[b] : 0;
+        have = have < 0 ? 0 : have;
+        add = add < 0 ? 0 : add;
+        // rows are counted before the pages: a request past the last row brings fewer tokens
+        Two all;
+        const int64_t end = rows + block_scan(Two{add, 0}, part, all).a;
+        const int64_t at = end - add < p.T ? end - add : p.T, to = end < p.T ? end : p.T;
+        add = to - at;
+        const int64_t pages = (have + page - 1) >> p.page_log;
+        int64_t need = ((have + add + page - 1) >> p.page_log) - pages;
+        const bool fits = pages + need <= p.width;
+        if (!fits) need = 0;
+        rows += all.a;
+        const int64_t upto = wanted + block_scan(Two{need, 0}, part, all).a;
+        const bool given = fits && (need == 0 || upto <= n);
+        wanted += all.a;
+        // the pages given away: the largest sum that was still covered
+        if (need > 0 && given) used = upto;
+        start[threadIdx.x] = real ? int32_t(at) : 0x7FFFFFFF;
+        held[threadIdx.x] = int32_t(have);
+        first_new[threadIdx.x] = !given ? -1 : need > 0 ? int32_t(upto - need) : 0;
+        if (real && (b0 / kThreads) % gridDim.x == blockIdx.x) {
+            p.cu[b + 1] = int32_t(to);
+            p.lens[b] = int32_t(given ? have + add : have);
+        }
+        __syncthreads();
+        const int64_t chunk0 = start[0], chunk1 = rows < p.T ? rows : p.T;
+        const int64_t from = row0 > chunk0 ? row0 : chunk0, until = row1 < chunk1 ? row1 : chunk1;
+        const int there = int(p.B - b0 < kThreads ? p.B - b0 : kThreads);
+        for (int64_t t = from + threadIdx.x; t < until; t += kThreads) {
+            const int i = last_not_past(start, there, int32_t(t));
+            const int64_t pos = int64_t(held[i]) + (t - start[i]);
+            int64_t slot = -1;
+            if (first_new[i] >= 0) {
+                const int64_t entry = pos >> p.page_log, k = entry - ((int64_t(held[i]) + page - 1) >> p.page_log);
+                int32_t* where = p.table + (b0 + i) * p.width + entry;
+                int32_t id;
+                if (k >= 0) {
+                    id = p.free_pages[n - 1 - first_new[i] - k];
+                    if ((pos & (page - 1)) == 0) *where = id;
+                } else {
+                    id = *where;
+                }
+                if (id >= 0) slot = (int64_t(id) << p.page_log) + (pos & (page - 1));
+                if (slot > 0x7FFFFFFF) slot = -1;
+            }
+            p.positions[t] = int32_t(pos < 0x7FFFFFFF ? pos : 0x7FFFFFFF);
+            p.slots[t] = int32_t(slot);
+        }
+        __syncthreads();
+    }
+    for (int64_t t = (row0 > rows ? row0 : rows) + threadIdx.x; t < row1; t += kThreads) p.positions[t] = p.slots[t] = -1;
+    if (blockIdx.x == 0) {
+        __shared__ int32_t top;
+        if (threadIdx.x == 0) top = 0;
+        __syncthreads();
+        atomicMax(&top, int32_t(used));
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            p.cu[0] = 0;
+            p.left[0] = int32_t(n - top);
+            p.left[1] = int32_t(wanted > n ? wanted - n : 0);
+        }
+    }
+}
+
+// The pages of the requests that are done, back on the free list in the order of
+// the requests and of their entries
+struct ReleaseArgs {
+    const int32_t *done, *lens, *table, *n_free;
+    int64_t B, F, width;
+    int page_log;
+    int32_t *free_pages, *lens_out, *left;
+};
+
+__global__ __launch_bounds__(kThreads) void release(const ReleaseArgs p) {
+    __shared__ Two part[kWaves];
+    __shared__ int32_t start[kThreads];
+    const int64_t row0 = int64_t(blockIdx.x) * kRows, row1 = row0 + kRows;
+    const int page = 1 << p.page_log;
+    int64_t n = p.n_free[0];
+    n = n < 0 ? 0 : n > p.F ? p.F : n;
+    int64_t rows = 0;
+    for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int64_t b = b0 + threadIdx.x;
+        const bool real = b < p.B, done = real && p.done[b] != 0;
+        int64_t len = real ? p.lens[b] : 0;
+        len = len < 0 ? 0 : len;
+        int64_t count = done ? (len + page - 1) >> p.page_log : 0;
+        count = count < p.width ? count : p.width;
+        Two all;
+        const int64_t end = rows + block_scan(Two{count, 0}, part, all).a;
+        start[threadIdx.x] = real ? int32_t(end - count) : 0x7FFFFFFF;
+        if (real && (b0 / kThreads) % gridDim.x == blockIdx.x) p.lens_out[b] = int32_t(done ? 0 : len);
+        __syncthreads();
+        const int64_t chunk0 = rows;
+        rows += all.a;
+        const int64_t from = row0 > chunk0 ? row0 : chunk0, until = row1 < rows ? row1 : rows;
+        const int there = int(p.B - b0 < kThreads ? p.B - b0 : kThreads);
+        for (int64_t t = from + threadIdx.x; t < until; t += kThreads) {
+            const int i = last_not_past(start, there, int32_t(t));
+            if (n + t < p.F) p.free_pages[n + t] = p.table[(b0 + i) * p.width + (t - start[i])];
+        }
+        __syncthreads();
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.left[0] = int32_t(n + rows < p.F ? n + rows : p.F);
+}
+
+// Rotary positions.  A wave takes one token: its lanes form the angles' sines and
+// cosines, one pair each, and pass them through LDS; then a lane turns eight
+// pairs of one head after another.  Angles are position * frequency in
+// revolutions in 64 bits (FP32 would lose them from positions of some
+// thousands on), their fraction in FP32.
+struct RopeArgs {
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t ldq, ldk, ldqo, ldko, T;
+    int Hq, H, D, rot, inverse;            // H: heads of both
+    float scale;
+    const int32_t* positions;
+    const float* freqs;
+};
+constexpr int kMaxPairs = 128;
+
+template <class T, bool NEXT>
+__global__ __launch_bounds__(kThreads) void rope(const RopeArgs p) {
+    __shared__ __align__(16) float cs[kWaves][2][kMaxPairs];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t t = int64_t(blockIdx.x) * kWaves + wave;
+    const int32_t pos = t < p.T ? p.positions[t] : -1;
+    const int pairs = p.rot / 2, units = pairs / 8;
+    for (int i = lane; i < pairs; i += 64) {
+        const double turns = double(pos) * double(p.freqs[i]) * 0.15915494309189535;
+        const float r = float(turns - __builtin_rint(turns));
+        float s, c;
+        sincospif(2.0f * r, &s, &c);
+        cs[wave][0][i] = c * p.scale;
+        cs[wave][1][i] = (p.inverse ? -s : s) * p.scale;
+    }
+    __syncthreads();
+    if (pos < 0) return;
+    const int per = 64 / units, u = lane % units, first = blockIdx.y * per + lane / units;
+    if (lane < per * units) {
+        float c[8], s[8];
+        load_n<8>(&cs[wave][0][u * 8], c);
+        load_n<8>(&cs[wave][1][u * 8], s);
+        for (int h = first; h < p.H; h += per * gridDim.y) {
+            const T* x = h < p.Hq ? static_cast<const T*>(p.q) + t * p.ldq + h * p.D : static_cast<const T*>(p.k) + t * p.ldk + (h - p.Hq) * p.D;
+            T* y = h < p.Hq ? static_cast<T*>(p.q_out) + t * p.ldqo + h * p.D : static_cast<T*>(p.k_out) + t * p.ldko + (h - p.Hq) * p.D;
+            float a[8], b[8], ya[8], yb[8];
+            if constexpr (NEXT) {
+                float w[16], z[16];
+                load_n<16>(x + u * 16, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    z[2 * i] = __builtin_fmaf(w[2 * i], c[i], -w[2 * i + 1] * s[i]);
+                    z[2 * i + 1] = __builtin_fmaf(w[2 * i + 1], c[i], w[2 * i] * s[i]);
+                }
+                store_n<16>(y + u * 16, z);
+            } else {
+                load_n<8>(x + u * 8, a);
+                load_n<8>(x + pairs + u * 8, b);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    ya[i] = __builtin_fmaf(a[i], c[i], -b[i] * s[i]);
+                    yb[i] = __builtin_fmaf(b[i], c[i], a[i] * s[i]);
+                }
+                store_n<8>(y + u * 8, ya);
+                store_n<8>(y + pairs + u * 8, yb);
+            }
+        }
+    }
+    // channels that are not turned, where they have to move
+    const int rest = (p.D - p.rot) / 8;
+    if (rest > 0)
+        for (int i = blockIdx.y * 64 + lane; i < rest * p.H; i += 64 * gridDim.y) {
+            const int h = i / rest, d = p.rot + (i - h * rest) * 8;
+            const T* x = h < p.Hq ? static_cast<const T*>(p.q) + t * p.ldq + h * p.D : static_cast<const T*>(p.k) + t * p.ldk + (h - p.Hq) * p.D;
+            T* y = h < p.Hq ? static_cast<T*>(p.q_out) + t * p.ldqo + h * p.D : static_cast<T*>(p.k_out) + t * p.ldko + (h - p.Hq) * p.D;
+            if (x != y) {
+                Raw<T, 8> w;
+                w.load(x + d);
+#pragma unroll
+                for (int j = 0; j < Raw<T, 8>::W; ++j) st<u32x4>(reinterpret_cast<uint8_t*>(y + d) + 16 * j, w.w[j]);
+            }
+        }
+}
+
+// New keys and values into their pages.  The tokens of a page are a run of
+// consecutive rows with consecutive slots; the workgroup of the run's first
+// token takes one head's run.  The scale is the least power of two s with
+// amax <= 448 s (2^-126 at the least), over the run and the page's older tokens; when it
+// grows, older codes are re-encoded by the exact factor.
+struct AppendArgs {
+    const void *k, *v;
+    int64_t ldk, ldv, T, n_slots;
+    int H, D, page_log;
+    const int32_t* slots;
+    uint8_t *kc, *vc;
+    float *ks, *vs;
+};
+
+// 2^e with amax <= 448 * 2^e = 1.75 * 2^(e + 8), e >= -126; 0 for 0
+__device__ __forceinline__ float pow2_scale(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    if (u == 0) return 0.0f;
+    int e = int(u >> 23) - 8 + ((u & 0x7FFFFF) > 0x600000);       // biased
+    e = e < 1 ? 1 : e;
+    return __uint_as_float(uint32_t(e) << 23);
+}
+// the power of two that takes values to codes: 1 / s, exact for s in [2^-126, 2^119]
+__device__ __forceinline__ float inverse_of(float s) { return s == 0.0f ? 1.0f : 1.0f / s; }
+
+__device__ __forceinline__ float block_max(float v, float* part) {
+    v = wave_max(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+}
+__device__ __forceinline__ uint32_t shift_codes(uint32_t w, float f) {
+    const v2f lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, 1.0f, false), hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, 1.0f, true);
+    return cvt4(lo[0] * f, lo[1] * f, hi[0] * f, hi[1] * f);
+}
+
+template <class T, bool V>
+__device__ __forceinline__ void append_run(const T* x, int64_t ld, int run, int off, int page, int D, uint8_t* codes, float* scale,
+                                           float* part) {
+    float amax = 0.0f;
+    const int per = D / 8;
+    for (int i = threadIdx.x; i < run * per; i += kThreads) {
+        float v[8];
+        load_n<8>(x + int64_t(i / per) * ld + i % per * 8, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    }
+    amax = block_max(amax, part);
+    const float was = off > 0 ? *scale : 0.0f;
+    const float need = pow2_scale(amax), s = fmaxf(was, need), r = inverse_of(s);
+    __syncthreads();
+    if (threadIdx.x == 0) *scale = s;
+    if (off > 0 && s > was) {
+        const float f = was / s;
+        if constexpr (V) {
+            for (int i = threadIdx.x; i < D * off; i += kThreads) {
+                uint8_t* c = codes + (i / off) * page + i % off;
+                *c = uint8_t(shift_codes(*c, f));
+            }
+        } else {
+            for (int i = threadIdx.x; i < off * D / 4; i += kThreads) {
+                uint32_t* c = reinterpret_cast<uint32_t*>(codes) + i;
+                *c = shift_codes(*c, f);
+            }
+        }
+    }
+    if constexpr (V) {
+        for (int i = threadIdx.x; i < run * D; i += kThreads) {
+            const int t = i / D, d = i % D;
+            codes[d * page + off + t] = uint8_t(cvt4(f32_of(x[int64_t(t) * ld + d]) * r, 0.0f, 0.0f, 0.0f));
+        }
+    } else {
+        for (int i = threadIdx.x; i < run * per; i += kThreads) {
+            const int t = i / per, d = i % per * 8;
+            float v[8];
+            load_n<8>(x + int64_t(t) * ld + d, v);
+            st<u32x2_t>(codes + (off + t) * D + d,
+                        u32x2_t{cvt4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), cvt4(v[4] * r, v[5] * r, v[6] * r, v[7] * r)});
+        }
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void append(const AppendArgs p) {
+    __shared__ float part[kWaves];
+    __shared__ int first_off;
+    const int64_t t = blockIdx.x;
+    const int h = blockIdx.y, page = 1 << p.page_log;
+    const int64_t slot = p.slots[t];
+    if (slot < 0 || slot >= p.n_slots) return;
+    const int off = int(slot & (page - 1));
+    if (off > 0 && t > 0 && p.slots[t - 1] == slot - 1) return;         // not its page's first new token
+    if (threadIdx.x == 0) first_off = page - off;
+    __syncthreads();
+    if (int(threadIdx.x) < page - off && (t + threadIdx.x >= p.T || p.slots[t + threadIdx.x] != slot + threadIdx.x))
+        atomicMin(&first_off, int(threadIdx.x));
+    __syncthreads();
+    const int run = first_off;
+    const int64_t id = slot >> p.page_log, at = id * p.H + h, tile = int64_t(page) * p.D;
+    if (blockIdx.z == 0)
+        append_run<T, false>(static_cast<const T*>(p.k) + t * p.ldk + h * p.D, p.ldk, run, off, page, p.D, p.kc + at * tile, p.ks + at, part);
+    else
+        append_run<T, true>(static_cast<const T*>(p.v) + t * p.ldv + h * p.D, p.ldv, run, off, page, p.D, p.vc + at * tile, p.vs + at, part);
+}
+
+}  // namespace kv_detail
+
+hipError_t launch_kv_assign(const int32_t* have, const int32_t* add, int64_t B, const int32_t* free_pages, const int32_t* n_free,
+                            int64_t F, int page_log, int32_t* table, int64_t width, int64_t T, int32_t* lens, int32_t* cu,
+                            int32_t* positions, int32_t* slots, int32_t* left, hipStream_t stream) {
+    using namespace kv_detail;
+    const int64_t blocks = T > 0 ? (T + kRows - 1) / kRows : 1;
+    return launch_kernel(assign, dim3(unsigned(blocks)), dim3(kThreads), stream,
+                         AssignArgs{have, add, free_pages, n_free, B, F, width, T, page_log, table, lens, cu, positions, slots, left});
+}
+
+hipError_t launch_kv_release(const int32_t* done, const int32_t* lens, const int32_t* table, int64_t B, int64_t width, int page_log,
+                             int32_t* free_pages, int64_t F, const int32_t* n_free, int32_t* lens_out, int32_t* left,
+                             hipStream_t stream) {
+    using namespace kv_detail;
+    // no more pages than the free list can take come back
+    const int64_t most = B * width < F ? B * width : F, blocks = most > 0 ? (most + kRows - 1) / kRows : 1;
+    return launch_kernel(release, dim3(unsigned(blocks)), dim3(kThreads), stream,
+                         ReleaseArgs{done, lens, table, n_free, B, F, width, page_log, free_pages, lens_out, left});
+}
+
+hipError_t launch_rope(const RopeCall& c, hipStream_t stream) {
+    using namespace kv_detail;
+    const RopeArgs p{c.q, c.k, c.q_out, c.k_out, c.ldq, c.ldk, c.ldqo, c.ldko, c.T, int(c.Hq), int(c.Hq + c.Hkv), int(c.D), int(c.rot),
+                     c.inverse, c.scale, c.positions, c.freqs};
+    const int units = p.rot / 16, per = 64 / units, passes = (p.H + per - 1) / per;
+    const dim3 grid(unsigned((c.T + kWaves - 1) / kWaves), unsigned(c.T < 1024 ? passes : 1));
+    if (c.bf16)
+        return launch_kernel(c.interleaved ? rope<uint16_t, true> : rope<uint16_t, false>, grid, dim3(kThreads), stream, p);
+    return launch_kernel(c.interleaved ? rope<float, true> : rope<float, false>, grid, dim3(kThreads), stream, p);
+}
+
+hipError_t launch_kv_append(const KvAppendCall& c, hipStream_t stream) {
+    using namespace kv_detail;
+    const AppendArgs p{c.k, c.v, c.ldk, c.ldv, c.T, c.n_pages << c.page_log, int(c.H), int(c.D), c.page_log, c.slots, c.kc, c.vc, c.ks, c.vs};
+    const dim3 grid(unsigned(c.T), unsigned(c.H), 2);
+    return launch_kernel(c.bf16 ? append<uint16_t> : append<float>, grid, dim3(kThreads), stream, p);
+}
+
+}  // namespace fp8fg

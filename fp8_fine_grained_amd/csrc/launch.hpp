@@ -102,4 +102,47 @@ hipError_t launch_swiglu_backward(const uint8_t* qc, const float* sc, const void
                                   const int32_t* rows, uint8_t* q, float* s, uint8_t* qt, float* st, uint8_t* qh,
                                   float* sh, hipStream_t stream);
 
+// ---- kv.hip ----  (pages of 2^page_log tokens)
+hipError_t launch_kv_assign(const int32_t* have, const int32_t* add, int64_t B, const int32_t* free_pages, const int32_t* n_free,
+                            int64_t F, int page_log, int32_t* table, int64_t width, int64_t T, int32_t* lens, int32_t* cu,
+                            int32_t* positions, int32_t* slots, int32_t* left, hipStream_t stream);
+hipError_t launch_kv_release(const int32_t* done, const int32_t* lens, const int32_t* table, int64_t B, int64_t width, int page_log,
+                             int32_t* free_pages, int64_t F, const int32_t* n_free, int32_t* lens_out, int32_t* left,
+                             hipStream_t stream);
+struct RopeCall {
+    const void *q, *k;                        // [T][Hq][D], [T][Hkv][D], rows ld elements apart
+    void *q_out, *k_out;
+    int64_t ldq, ldk, ldqo, ldko, T, Hq, Hkv, D, rot;
+    int bf16, interleaved, inverse;
+    float scale;
+    const int32_t* positions;
+    const float* freqs;
+};
+hipError_t launch_rope(const RopeCall& call, hipStream_t stream);
+struct KvAppendCall {
+    const void *k, *v;                        // [T][H][D], rows ld elements apart
+    int64_t ldk, ldv, T, H, D, n_pages;
+    int bf16, page_log;
+    const int32_t* slots;
+    uint8_t *kc, *vc;
+    float *ks, *vs;
+};
+hipError_t launch_kv_append(const KvAppendCall& call, hipStream_t stream);
+
+// ---- attend.hip ----
+struct AttendCall {
+    const uint16_t* q;                        // [T][Hq][D], rows ldq elements apart
+    const uint8_t *kc, *vc;                   // [n_pages][Hkv][page][D], [n_pages][Hkv][D][page]
+    const float *ks, *vs;                     // [n_pages][Hkv]
+    const int32_t *table, *cu, *lens;         // [B][width], [B + 1], [B]
+    int64_t ldq, n_pages, width, B, T, Hq, Hkv, D;
+    int page_log;
+    float scale;
+    uint16_t* out;                            // [T][Hq][D]
+    float* lse;                               // [T][Hq], may be null
+    void* workspace;
+};
+int64_t attend_workspace(const AttendCall& call);        // bytes; sizes only are read
+hipError_t launch_attend(const AttendCall& call, hipStream_t stream);
+
 }  // namespace fp8fg

@@ -71,7 +71,7 @@
 extern "C" {
 #endif
 
-#define FP8FG_ABI_VERSION 15
+#define FP8FG_ABI_VERSION 16
 
 enum fp8fg_status {
     FP8FG_OK = 0,
@@ -585,6 +585,134 @@ int fp8_swiglu_backward(const uint8_t* qc, const float* sc, const void* dh, int 
 int fp8_grouped_gemm_wgrad(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb,
                            const int32_t* group_offsets, int64_t G, int64_t M, int64_t N, int64_t R, float* c,
                            int accumulate, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over a key/value cache held in 8 bits, in pages.
+ *   a step:  kv_assign_pages -> rope -> fp8_kv_append -> fp8_kv_attention
+ *            (the first once, the others in every layer);  kv_release_pages
+ *            when requests end.
+ * The cache of a layer is a pool of n_pages pages of `page` tokens:
+ *   k_cache u8 [n_pages][Hkv][page][D]     v_cache u8 [n_pages][Hkv][D][page]
+ *   k_scale f32 [n_pages][Hkv]             v_scale f32 [n_pages][Hkv]
+ * (a value page holds its tokens along the rows, so that sixteen tokens of a
+ * channel, the operand of the second product, are 16 consecutive bytes).
+ * value = decode(code) * scale of its page and head.  `page` is a power of two
+ * from 16 to 256, D is 64, 128, 192 or 256.  Request b's tokens page * e ..
+ * page * e + page - 1 lie in page table[b][e] (int32 [B][width]); slot
+ * table[b][e] * page + offset names a token's place.
+ * A step brings new tokens of the requests, concatenated: request b owns rows
+ * cu[b] .. cu[b+1] - 1 (int32 [B+1], non-decreasing from 0).  Rows from cu[B] on
+ * (a batch padded to a fixed size T) are left as they were by every call.
+ * All of them are deterministic: no sum depends on the order of execution.
+ * Sizes common to them: B <= 65536 requests, B * width < 2^31, page * width <
+ * 2^31, n_pages * page < 2^31, at most 65535 heads.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A step's pages, slots and positions from the requests' lengths.
+ * have, add: int32 [B], the tokens that the cache holds of each request and the
+ * ones that the step brings (negative counts as 0).  Where more rows are brought
+ * than T, the last requests bring fewer.  free_pages: int32 [F], of which the
+ * first n_free[0] (DEVICE int32 [1], 4-byte aligned, clamped to [0, F]) are free page numbers.
+ *   A request needs ceil((have + add) / page) - ceil(have / page) new pages.  They
+ *   are taken from the end of the list in the order of the requests; a request
+ *   whose pages no longer suffice, or whose tokens its row of the table does
+ *   not hold, is refused: it gets no page, and needs more than `width` count as none.
+ *   table: int32 [B][width]: the new pages are written behind the ceil(have / page)
+ *     that are there, nothing else is.
+ *   lens: int32 [B] = have + add, or have where refused;
+ *   cu: int32 [B+1], the first rows;
+ *   positions: int32 [T], have[b] + i for row cu[b] + i, -1 from cu[B] on;
+ *   slots: int32 [T], the rows' places, -1 from cu[B] on and where refused;
+ *   left: int32 [2], the pages that are left free (the first left[0] of free_pages) and
+ *     the number that was missing (0 where every request got its pages).
+ * `left` and `lens` may not overlap n_free and have.  B = 0 or T = 0 writes the outputs
+ * that exist.
+ */
+int kv_assign_pages(const int32_t* have, const int32_t* add, int64_t B, const int32_t* free_pages, const int32_t* n_free,
+                    int64_t F, int64_t page, int32_t* table, int64_t width, int64_t T, int32_t* lens, int32_t* cu,
+                    int32_t* positions, int32_t* slots, int32_t* left, void* stream);
+
+/*
+ * The pages of ended requests back to the free list.
+ * done: int32 [B] (0 or not); lens: int32 [B]; table, free_pages, n_free, F as for
+ * kv_assign_pages.  The first min(ceil(lens[b] / page), width) entries of each done
+ * request's row go to free_pages[n_free[0]] onwards, in the order of the requests
+ * and entries, as far as the list is long.
+ *   lens_out: int32 [B] = 0 where done, lens (at least 0) elsewhere;
+ *   left: int32 [1], the pages that are free now.
+ * The table is not written (entries past a request's length mean nothing).
+ * `left` and lens_out may not overlap n_free and lens.
+ */
+int kv_release_pages(const int32_t* done, const int32_t* lens, const int32_t* table, int64_t B, int64_t width, int64_t page,
+                     int32_t* free_pages, int64_t F, const int32_t* n_free, int32_t* lens_out, int32_t* left, void* stream);
+
+/*
+ * Rotary positions of queries and keys, and their gradient.
+ * q: [T][Hq][D] with rows ldq elements apart, k: [T][Hkv][D] with rows ldk apart, both
+ * f32 or bf16 (x_bf16); either may have no heads.  Of each head the first `rot`
+ * channels are turned, the others copied:
+ *   angle = positions[t] * freqs[i],  i < rot / 2   (freqs: f32 [rot / 2])
+ *   (a, b) -> scale * (a cos - b sin, b cos + a sin)
+ * of the channel pairs (i, i + rot / 2), or (2 i, 2 i + 1) when interleaved = 1.
+ * inverse = 1 turns the other way: with the same scale, the gradient of the
+ * inputs from that of the outputs.  The angle is formed in 64 bits, its sine and cosine
+ * and the products in FP32 (an absolute error below 2^-21 of scale * (|a| + |b|)), and
+ * rounded once to the outputs' type.  Rows with a negative position are not written.
+ * q_out, k_out: as q and k, rows ldqo and ldko apart, or q and k themselves (with
+ * the same distance).
+ * Requires D % 8 == 0, D <= 1024, rot % 16 == 0, 0 < rot <= min(D, 256), rows at
+ * least H * D elements and a multiple of 16 bytes apart.
+ */
+int rope(const void* q, int64_t ldq, void* q_out, int64_t ldqo, int64_t Hq, const void* k, int64_t ldk, void* k_out, int64_t ldko,
+         int64_t Hkv, int x_bf16, const int32_t* positions, const float* freqs, int64_t T, int64_t D, int64_t rot, int interleaved,
+         float scale, int inverse, void* stream);
+
+/*
+ * New keys and values into the cache.
+ * k, v: [T][H][D], f32 or bf16 (x_bf16), rows ldk and ldv elements apart; slots: int32
+ * [T], each row's place; rows whose slot is outside [0, n_pages * page) are skipped.
+ * The rows of one page have to be consecutive, with consecutive slots.  Where a
+ * page's first new row has offset o > 0, its tokens 0 .. o - 1 are in the cache
+ * already; with o = 0 the page starts anew.
+ *   scale = the least power of two s >= 2^-126 with max |x| <= 448 s, over the page's new
+ *   tokens (0 if all of them are 0), and at least the scale it has where o > 0;
+ *   code = E4M3 round-to-nearest-even of x / s.  Where the scale grows, the page's older
+ *   codes are re-encoded under it (exactly, but for codes that become subnormal):
+ *   powers of two, so that no value drifts as a page fills up.
+ * Nothing but the pages' codes up to the last new token and their scales is written.  A
+ * page named by two separate runs of rows in one call gets unspecified codes.
+ * Requires rows as in rope.
+ */
+int fp8_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int x_bf16, const int32_t* slots, int64_t T, int64_t H,
+                  int64_t D, int64_t page, int64_t n_pages, uint8_t* k_cache, float* k_scale, uint8_t* v_cache, float* v_scale,
+                  void* stream);
+
+/*
+ * Causal attention of the new tokens over the cache, which holds them already.
+ * q: bf16 [T][Hq][D], rows ldq elements apart; query head h reads key/value head
+ * h / (Hq / Hkv).  lens: int32 [B], all tokens of each request.  Token i of the
+ * n = cu[b+1] - cu[b] new ones of request b sees the keys j <= lens[b] - n + i (j < lens[b]):
+ *   x_j = scale * <q, k_j>,  p = softmax(x),  out = sum_j p_j v_j.
+ *   out: bf16 [T][Hq][D];  lse: f32 [T][Hq] = log sum_j exp(x_j), or NULL.
+ * Tokens in pages outside [0, n_pages) (and past the table's last entry) are not
+ * seen.  A token that sees nothing gets 0, and -inf for lse.
+ * What lies in the cache past a request's last token has no influence.
+ * Scales may be any finite non-negative FP32 values.
+ * Accuracy: codes are multiplied exactly and summed in FP32, probabilities are
+ * rounded to FP16's 11 bits:  |out - out*| <= 2^-10 * sum_j p_j |v_j| + 2^-50 max |v| before the one
+ * rounding to BF16, where the scores are below 2^6 (larger scores: their FP32
+ * rounding, 2^-22 |x|, is the relative error of p).
+ * workspace: fp8_kv_attention_workspace bytes (may be 0, then NULL), contents unspecified before
+ * and after; calls that may run at the same time need one each.
+ * Requires Hq % Hkv == 0, 0 <= scale <= 2^64, rows of q at least Hq * D elements and
+ * a multiple of 16 bytes apart, n_pages >= 1 where there is work.
+ */
+int fp8_kv_attention_workspace(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t width, int64_t* bytes);
+int fp8_kv_attention(const uint16_t* q, int64_t ldq, const uint8_t* k_cache, const float* k_scale, const uint8_t* v_cache,
+                     const float* v_scale, int64_t n_pages, int64_t page, const int32_t* table, int64_t width, const int32_t* cu,
+                     const int32_t* lens, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, float scale, uint16_t* out,
+                     float* lse, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fp8fg_status_string(int status);
