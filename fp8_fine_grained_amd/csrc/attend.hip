@@ -170,6 +170,7 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int first, int end) {
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
     constexpr int ROWS = 16, KC = D / 64, DT = D / 16;
+    constexpr bool kAhead = D <= 192;     // registers for it
     __shared__ __align__(16) float joined[kWaves][ROWS * D];
     __shared__ float stat[kWaves][2][ROWS];
     Item it;
@@ -202,36 +203,71 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
     for (int i = 0; i < DT; ++i) o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     float m = -__builtin_inff(), l = 0.0f, ref = 0.0f, largest = 0.0f;
 
-    for (int tile = kt0 + wave; tile < kt1; tile += kWaves) {
+    // The pages of a tile's tokens: of the group whose keys this lane loads and of
+    // the lane's own group, -1 where there is none
+    const int mask = (1 << p.page_log) - 1;
+    const auto page_of = [&](int tile, int group) {
+        const int token = tile * kTile + 16 * group;
+        return token < it.len ? table[token >> p.page_log] : -1;
+    };
+    const auto exists = [&](int32_t id) { return id >= 0 && id < p.n_pages; };
+    // Keys of the next tile are loaded while this one's values are multiplied, values
+    // of this tile while its keys are
+    int tile = kt0 + wave;
+    int32_t kid = -1, vid = -1, kid2 = -1, vid2 = -1;
+    u32x4 kraw[4][KC], vraw[DT];
+    const auto load_keys = [&](int tile, int32_t id) {
+        const uint8_t* kp = p.kc + (int64_t(exists(id) ? id : 0) * p.Hkv + kvh) * page_bytes +
+                            ((tile * kTile + 16 * (col >> 2)) & mask) * D + (col & 3) * D + 16 * g;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) kraw[j][c] = ld<u32x4>(kp + 4 * j * D + 64 * c);
+    };
+    if (tile < kt1) {
+        kid = page_of(tile, col >> 2);
+        vid = page_of(tile, g);
+        if (tile + kWaves < kt1) {
+            kid2 = page_of(tile + kWaves, col >> 2);
+            vid2 = page_of(tile + kWaves, g);
+        }
+        if (kAhead) load_keys(tile, kid);
+    }
+    for (; tile < kt1; tile += kWaves) {
         const int t0 = tile * kTile;
-        // the page of this group's tokens, and the page of the group whose keys this lane loads
-        const auto page_of = [&](int group, bool& good) {
-            const int token = t0 + 16 * group;
-            const int64_t entry = token >> p.page_log;
-            int32_t id = token < it.len ? table[entry] : -1;
-            good = id >= 0 && id < p.n_pages;
-            return good ? id : 0;
+        const bool good = exists(vid);
+        const int64_t at = int64_t(good ? vid : 0) * p.Hkv + kvh;
+        const float ksc = good ? p.ks[at] * p.scale2 : 0.0f, vsc = good ? p.vs[at] : 0.0f;
+        const uint8_t* vp = p.vc + at * page_bytes + ((t0 + 16 * g) & mask) + (int64_t(col) << p.page_log);
+        const auto load_values = [&] {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) vraw[d] = ld<u32x4>(vp + (int64_t(16 * d) << p.page_log));
         };
-        bool good, kgood;
-        const int64_t vid = page_of(g, good), kid = page_of(col >> 2, kgood);
-        const float ksc = good ? p.ks[vid * p.Hkv + kvh] * p.scale2 : 0.0f, vsc = good ? p.vs[vid * p.Hkv + kvh] : 0.0f;
-        const int mask = (1 << p.page_log) - 1;
-        const uint8_t* kp = p.kc + (kid * p.Hkv + kvh) * page_bytes + ((t0 + 16 * (col >> 2)) & mask) * D + (col & 3) * D + 16 * g;
-        const uint8_t* vp = p.vc + (vid * p.Hkv + kvh) * page_bytes + ((t0 + 16 * g) & mask) + (int64_t(col) << p.page_log);
+        if (kAhead) load_values();
+        else load_keys(tile, kid);
         v4f s[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             s[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
-                const u32x4 w = ld<u32x4>(kp + 4 * j * D + 64 * c);
+                const u32x4 w = kraw[j][c];
                 s[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide_bf16(w[0], w[1]), qf[c][0], s[j], 0, 0, 0);
                 s[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide_bf16(w[2], w[3]), qf[c][1], s[j], 0, 0, 0);
             }
         }
+        kid = kid2;
+        vid = vid2;
+        if (tile + kWaves < kt1) {
+            if (kAhead) load_keys(tile + kWaves, kid);
+            if (tile + 2 * kWaves < kt1) {
+                kid2 = page_of(tile + 2 * kWaves, col >> 2);
+                vid2 = page_of(tile + 2 * kWaves, g);
+            }
+        }
+        if (!kAhead) load_values();
         // scores in units of log2; keys out of sight at -inf
-        const bool all_good = __all(good);
-        const bool masked = t0 + kTile - 1 > least || !all_good;
+        const bool masked = t0 + kTile - 1 > least || !__all(good);
         const int seen = good ? last - (t0 + 16 * g) : -1;           // the last of the lane's tokens in sight
         float mt = -__builtin_inff();
 #pragma unroll
@@ -267,12 +303,20 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
                 pf[j >> 1][(j & 1) * 4 + i] = _Float16(e * ratio);
             }
         l = __builtin_fmaf(l, alpha, sum);
-        const int end = !good ? 0 : it.len - (t0 + 16 * g);          // codes past the last token are not numbers
+        if (masked) {                     // codes past the last token are not numbers
+            const int end = !good ? 0 : it.len - (t0 + 16 * g);
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vraw[d][i] = keep_bytes(vraw[d][i], 4 * i, end);
+        }
+        if (__any(factor != 1.0f)) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] *= factor;
+        }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-            o[d] *= factor;
-            u32x4 w = ld<u32x4>(vp + (int64_t(16 * d) << p.page_log));
-            if (masked) w = u32x4{keep_bytes(w[0], 0, end), keep_bytes(w[1], 4, end), keep_bytes(w[2], 8, end), keep_bytes(w[3], 12, end)};
+            const u32x4 w = vraw[d];
             o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wide_f16(w[0], w[1]), pf[0], o[d], 0, 0, 0);
             o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wide_f16(w[2], w[3]), pf[1], o[d], 0, 0, 0);
         }
@@ -339,35 +383,54 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
     }
 }
 
-// The splits of a row tile joined, in their order
+// The splits of a row tile joined.  A workgroup takes one row: D / 4 threads of
+// four channels side by side, eight splits (for D = 128) at a time, whose sums meet in
+// LDS in a fixed order.
 template <int D, int ROWS>
 __global__ __launch_bounds__(kThreads) void join(const Args p) {
-    const int id = blockIdx.x, kvh = blockIdx.y;
+    constexpr int PER = D / 4, SIDE = kThreads / PER;
+    __shared__ __align__(16) float sums[SIDE][D];
+    __shared__ float tops[SIDE], total[SIDE];
+    const int id = blockIdx.x / ROWS, r = blockIdx.x % ROWS, kvh = blockIdx.y;
     if (id >= p.head[0]) return;
     const int32_t* d = p.desc + int64_t(id) * kDescInts;
-    const int splits = d[0], first = d[1], cu = d[2], n = d[3], tile = d[4];
-    if (splits <= 1) return;
-    const float* part = p.parts + (int64_t(first) * p.Hkv + kvh) * (ROWS * (D + 2));
+    const int splits = d[0], first = d[1], cu = d[2], n = d[3], rr = d[4] * ROWS + r, t = rr / p.G;
+    if (splits <= 1 || t >= n) return;
+    const float* part = p.parts + (int64_t(first) * p.Hkv + kvh) * (ROWS * (D + 2)) + r;
     const int64_t step = int64_t(p.Hkv) * (ROWS * (D + 2));
-    for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
-        const int r = i / (D / 4), c = i - r * (D / 4), rr = tile * ROWS + r, t = rr / p.G;
-        if (t >= n) continue;
-        float M = -__builtin_inff();
-        for (int s = 0; s < splits; ++s) M = fmaxf(M, part[s * step + r]);
-        const float M_use = M == -__builtin_inff() ? 0.0f : M;
-        float L = 0.0f;
-        v4f v{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < splits; ++s) {
-            const float f = __builtin_amdgcn_exp2f(part[s * step + r] - M_use);
-            L = __builtin_fmaf(part[s * step + ROWS + r], f, L);
-            v += ld<v4f>(part + s * step + 2 * ROWS + r * D + 4 * c) * f;
+    const int side = threadIdx.x / PER, c = threadIdx.x % PER;
+    float M = -__builtin_inff();
+    for (int s = threadIdx.x; s < splits; s += kThreads) M = fmaxf(M, part[s * step]);
+    M = wave_max(M);
+    if ((threadIdx.x & 63) == 0) total[threadIdx.x >> 6] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(total[0], total[1]), fmaxf(total[2], total[3]));
+    const float M_use = M == -__builtin_inff() ? 0.0f : M;
+    float L = 0.0f;
+    v4f v{0.0f, 0.0f, 0.0f, 0.0f};
+    if (side < SIDE) {
+#pragma unroll 4
+        for (int s = side; s < splits; s += SIDE) {
+            const float f = __builtin_amdgcn_exp2f(part[s * step] - M_use);
+            L = __builtin_fmaf(part[s * step + ROWS], f, L);
+            v += ld<v4f>(part - r + s * step + 2 * ROWS + r * D + 4 * c) * f;
         }
-        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-        const int64_t at = int64_t(cu + t) * p.Hq + kvh * p.G + (rr - t * p.G);
-        const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-        store_n<4>(p.out + at * D + 4 * c, out);
-        if (c == 0 && p.lse) p.lse[at] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
+        st<v4f>(&sums[side][4 * c], v);
+        if (c == 0) tops[side] = L;
     }
+    __syncthreads();
+    if (side != 0) return;
+    L = tops[0];
+#pragma unroll
+    for (int i = 1; i < SIDE; ++i) {
+        L += tops[i];
+        v += ld<v4f>(&sums[i][4 * c]);
+    }
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const int64_t at = int64_t(cu + t) * p.Hq + kvh * p.G + (rr - t * p.G);
+    const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+    store_n<4>(p.out + at * D + 4 * c, out);
+    if (c == 0 && p.lse) p.lse[at] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
 }
 
 struct Plan {
@@ -393,7 +456,7 @@ template <int D>
 hipError_t run(const AttendCall& c, Args p, const Plan& plan, hipStream_t stream) {
     if (const hipError_t e = launch_kernel(attend<D>, dim3(unsigned(plan.items), unsigned(c.Hkv)), dim3(kThreads), stream, p)) return e;
     if (plan.bytes == 0) return hipSuccess;
-    return launch_kernel(join<D, 16>, dim3(unsigned(plan.tiles), unsigned(c.Hkv)), dim3(kThreads), stream, p);
+    return launch_kernel(join<D, 16>, dim3(unsigned(plan.tiles * 16), unsigned(c.Hkv)), dim3(kThreads), stream, p);
 }
 
 }  // namespace attend_detail
