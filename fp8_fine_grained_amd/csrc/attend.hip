@@ -42,98 +42,107 @@ struct Args {
     float scale2;                         // softmax scale * log2(e)
     uint16_t* out;
     float* lse;
-    int32_t* head;                        // workspace: [0] number of row tiles
-    int32_t* desc;                        // row tile -> its rows and parts
+    int32_t* desc;                        // workspace: [T][G] x (splits, first part, row of it)
     float* parts;                         // unjoined results
-    int64_t most_tiles, most_parts;       // room for them
+    int64_t most_parts;                   // room for them
     int target;                           // workgroups wanted for each key/value head
 };
 
 // What a workgroup does: rows tile * ROWS .. of request b (n tokens from row cu of q on), the
 // split-th of `splits` parts of its keys
 struct Item {
-    int32_t b, cu, n, len, tile, tile_id, split, splits, part;
+    int32_t b, cu, n, len, tile, split, splits, part;
 };
 
-constexpr int kDescInts = 8;
-
-__device__ __forceinline__ int scan_add(int v, int* part, int& all) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int by = 1; by < 64; by *= 2) {
-        const int a = __shfl_up(v, by, 64);
-        if (lane >= by) v += a;
-    }
-    __syncthreads();
-    if (lane == 63) part[wave] = v;
-    __syncthreads();
-    all = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) v += part[w];
-        all += part[w];
-    }
-    return v;
+// Inclusive sums over the wave's lanes, by shifts within the 16-lane rows and
+// broadcasts of a row's last lane to the rows behind it
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_dpp(int v) { return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false); }
+__device__ __forceinline__ int wave_scan(int v) {
+    v = add_dpp<0x111, 0xF>(v);           // row_shr 1, 2, 4, 8
+    v = add_dpp<0x112, 0xF>(v);
+    v = add_dpp<0x114, 0xF>(v);
+    v = add_dpp<0x118, 0xF>(v);
+    v = add_dpp<0x142, 0xA>(v);           // row_bcast 15, 31
+    return add_dpp<0x143, 0xC>(v);
 }
+__device__ __forceinline__ int lane63(int v) { return __builtin_amdgcn_readlane(v, 63); }
 
-// The requests' row tiles and their splits, numbered in order; every workgroup
-// finds its own from the lengths.  Splits are of equal numbers of tiles, as long as
+// The requests' row tiles and their splits, numbered in order; every wave
+// finds its workgroup's own from the lengths, four consecutive requests to a
+// lane, without LDS or a barrier.  Splits are of equal numbers of tiles, as long as
 // it takes for about `target` workgroups to do all the work.
 template <int ROWS>
 __device__ __forceinline__ bool find_item(const Args& p, Item& it) {
-    __shared__ int part[kWaves];
-    __shared__ float fpart[kWaves];
-    __shared__ Item found;
-    const int64_t room = p.width << p.page_log;
-    const auto shape = [&](int64_t b, int& cu, int& n, int& len, int& tiles, int& kt) {
-        cu = p.cu[b];
-        n = p.cu[b + 1] - cu;
-        len = p.lens[b];
-        cu = cu < 0 ? 0 : cu;
-        n = cu >= p.T ? 0 : n > p.T - cu ? int(p.T - cu) : n;
-        n = n < 0 ? 0 : n;
-        len = len < 0 ? 0 : len > room ? int(room) : len;
-        tiles = int((int64_t(n) * p.G + ROWS - 1) / ROWS);
-        kt = (len + kTile - 1) / kTile;
+    constexpr int R = 4, CHUNK = 64 * R;
+    const int lane = threadIdx.x & 63;
+    const int room = int(p.width << p.page_log);
+    int cu[R + 1], n[R], len[R], tiles[R], kt[R];
+    const auto read = [&](int64_t b0) {
+#pragma unroll
+        for (int i = 0; i <= R; ++i) {
+            const int64_t b = b0 + lane * R + i;
+            cu[i] = p.cu[b < p.B ? b : p.B];
+            if (i < R) len[i] = b < p.B ? p.lens[b] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int end = cu[i + 1];
+            cu[i] = cu[i] < 0 ? 0 : cu[i];
+            n[i] = cu[i] >= p.T ? 0 : end > p.T ? int(p.T) - cu[i] : end - cu[i];
+            n[i] = n[i] < 0 ? 0 : n[i];
+            len[i] = len[i] < 0 ? 0 : len[i] > room ? room : len[i];
+            tiles[i] = int((int64_t(n[i]) * p.G + ROWS - 1) / ROWS);
+            kt[i] = (len[i] + kTile - 1) / kTile;
+        }
     };
     float work = 0.0f;
-    int cu = 0, n = 0, len = 0, tiles = 0, kt = 0;
-    for (int64_t b = threadIdx.x; b < p.B; b += kThreads) {
-        shape(b, cu, n, len, tiles, kt);
-        work += float(tiles) * float(kt);
+    for (int64_t b0 = 0; b0 < p.B; b0 += CHUNK) {
+        read(b0);
+#pragma unroll
+        for (int i = 0; i < R; ++i) work += float(tiles[i]) * float(kt[i]);
     }
-    work = lanes_sum<64>(work);
-    if ((threadIdx.x & 63) == 0) fpart[threadIdx.x >> 6] = work;
-    if (threadIdx.x == 0) found.b = -1;
-    __syncthreads();
-    work = fpart[0] + fpart[1] + fpart[2] + fpart[3];
-    const float want = ceilf(work / float(p.target));
+    const float want = ceilf(lanes_sum<64>(work) / float(p.target));
     const int per = want < float(kMinTiles) ? kMinTiles : want > 0x1p30f ? 1 << 30 : int(want);
-    const bool whole = p.B <= kThreads;
     const int me = blockIdx.x;
-    int items0 = 0, parts0 = 0, tiles0 = 0;
-    for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
-        const int64_t b = b0 + threadIdx.x;
-        if (!whole || b >= p.B) tiles = 0;
-        if (!whole && b < p.B) shape(b, cu, n, len, tiles, kt);
-        const int splits = kt > per ? (kt + per - 1) / per : 1;
-        const int items = tiles * splits, parts = splits > 1 ? items : 0;
-        int all_items, all_parts, all_tiles;
-        const int i1 = items0 + scan_add(items, part, all_items);
-        const int p1 = parts0 + scan_add(parts, part, all_parts);
-        const int t1 = tiles0 + scan_add(tiles, part, all_tiles);
-        if (me >= i1 - items && me < i1) {
-            const int at = me - (i1 - items), tile = at / splits;
-            found = Item{int32_t(b), cu, n, len, tile, t1 - tiles + tile, at - tile * splits, splits, p1 - parts + tile * splits};
+    int items0 = 0, parts0 = 0;
+    for (int64_t b0 = 0; b0 < p.B; b0 += CHUNK) {
+        if (p.B > CHUNK) read(b0);        // else as they were read above
+        int items = 0, parts = 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int splits = kt[i] > per ? (kt[i] + per - 1) / per : 1;
+            items += tiles[i] * splits;
+            parts += splits > 1 ? tiles[i] * splits : 0;
         }
-        items0 += all_items;
-        parts0 += all_parts;
-        tiles0 += all_tiles;
+        const int i1 = wave_scan(items), p1 = wave_scan(parts);
+        int at = me - items0 - (i1 - items);
+        const uint64_t who = __ballot(at >= 0 && at < items);
+        if (who) {
+            int part = parts0 + p1 - parts;
+            Item mine{};
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int splits = kt[i] > per ? (kt[i] + per - 1) / per : 1, here = tiles[i] * splits;
+                if (at >= 0 && at < here) {
+                    const int tile = at / splits;
+                    mine = Item{int32_t(b0) + lane * R + i, cu[i], n[i], len[i], tile, at - tile * splits, splits,
+                                splits > 1 ? part + tile * splits : 0};
+                }
+                at -= here;
+                part += splits > 1 ? here : 0;
+            }
+            const int src = __builtin_ctzll(who);
+            it = Item{__builtin_amdgcn_readlane(mine.b, src), __builtin_amdgcn_readlane(mine.cu, src), __builtin_amdgcn_readlane(mine.n, src),
+                      __builtin_amdgcn_readlane(mine.len, src), __builtin_amdgcn_readlane(mine.tile, src),
+                      __builtin_amdgcn_readlane(mine.split, src), __builtin_amdgcn_readlane(mine.splits, src),
+                      __builtin_amdgcn_readlane(mine.part, src)};
+            return it.splits == 1 || it.part + it.splits <= p.most_parts;
+        }
+        items0 += lane63(i1);
+        parts0 += lane63(p1);
     }
-    __syncthreads();
-    if (me == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.head) p.head[0] = tiles0;
-    it = found;
-    return it.b >= 0 && (it.splits == 1 || it.part + it.splits <= p.most_parts);
+    return false;
 }
 
 template <bool HI>
@@ -167,13 +176,13 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int first, int end) {
     return n >= 4 ? w : n <= 0 ? 0u : w & (0xFFFFFFFFu >> (32 - 8 * n));
 }
 
-template <int D>
+template <int D, bool ONCE>
 __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
     constexpr int ROWS = 16, KC = D / 64, DT = D / 16;
     constexpr bool kAhead = D <= 192;     // registers for it
     __shared__ __align__(16) float joined[kWaves][ROWS * D];
     __shared__ float stat[kWaves][2][ROWS];
-    Item it;
+    Item it{};
     if (!find_item<ROWS>(p, it)) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4, kvh = blockIdx.y;
     // this lane's query row, and the last key that it sees
@@ -241,7 +250,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
         const uint8_t* vp = p.vc + at * page_bytes + ((t0 + 16 * g) & mask) + (int64_t(col) << p.page_log);
         const auto load_values = [&] {
 #pragma unroll
-            for (int d = 0; d < DT; ++d) vraw[d] = ld<u32x4>(vp + (int64_t(16 * d) << p.page_log));
+            for (int d = 0; d < DT; ++d) vraw[d] = ONCE ? ld_once<u32x4>(vp + (int64_t(16 * d) << p.page_log)) : ld<u32x4>(vp + (int64_t(16 * d) << p.page_log));
         };
         if (kAhead) load_values();
         else load_keys(tile, kid);
@@ -373,61 +382,60 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
             p.lse[int64_t(it.cu + tq) * p.Hq + hq] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
         }
     }
-    if (p.head && it.split == 0 && kvh == 0 && threadIdx.x == 0 && it.tile_id < p.most_tiles) {
-        int32_t* d = p.desc + int64_t(it.tile_id) * kDescInts;
-        d[0] = it.splits;
-        d[1] = it.part;
-        d[2] = it.cu;
-        d[3] = it.n;
-        d[4] = it.tile;
-    }
+    if (p.desc && it.split == 0 && kvh == 0 && wave == 0 && g == 0 && live)
+        st<int4>(p.desc + 4 * (int64_t(it.cu + tq) * p.G + (hq - kvh * p.G)), int4{it.splits, it.part, col, 0});
 }
 
-// The splits of a row tile joined.  A workgroup takes one row: D / 4 threads of
-// four channels side by side, eight splits (for D = 128) at a time, whose sums meet in
-// LDS in a fixed order.
+// The splits of a query row joined, a workgroup for each: D / 4 threads of four
+// channels side by side, 1024 / D splits at a time, each with a running maximum of its
+// own; they meet in LDS in a fixed order.
 template <int D, int ROWS>
 __global__ __launch_bounds__(kThreads) void join(const Args p) {
     constexpr int PER = D / 4, SIDE = kThreads / PER;
     __shared__ __align__(16) float sums[SIDE][D];
-    __shared__ float tops[SIDE], total[SIDE];
-    const int id = blockIdx.x / ROWS, r = blockIdx.x % ROWS, kvh = blockIdx.y;
-    if (id >= p.head[0]) return;
-    const int32_t* d = p.desc + int64_t(id) * kDescInts;
-    const int splits = d[0], first = d[1], cu = d[2], n = d[3], rr = d[4] * ROWS + r, t = rr / p.G;
-    if (splits <= 1 || t >= n) return;
+    __shared__ float tops[SIDE], totals[SIDE];
+    const int64_t row = blockIdx.x;
+    const int kvh = blockIdx.y, used = p.cu[p.B];
+    const int4 d = ld<int4>(p.desc + 4 * row);
+    const int splits = d.x, first = d.y, r = d.z;
+    if (row >= int64_t(used) * p.G || splits <= 1 || first < 0 || splits > p.most_parts - first || r < 0 || r >= ROWS) return;
     const float* part = p.parts + (int64_t(first) * p.Hkv + kvh) * (ROWS * (D + 2)) + r;
     const int64_t step = int64_t(p.Hkv) * (ROWS * (D + 2));
     const int side = threadIdx.x / PER, c = threadIdx.x % PER;
-    float M = -__builtin_inff();
-    for (int s = threadIdx.x; s < splits; s += kThreads) M = fmaxf(M, part[s * step]);
-    M = wave_max(M);
-    if ((threadIdx.x & 63) == 0) total[threadIdx.x >> 6] = M;
-    __syncthreads();
-    M = fmaxf(fmaxf(total[0], total[1]), fmaxf(total[2], total[3]));
-    const float M_use = M == -__builtin_inff() ? 0.0f : M;
-    float L = 0.0f;
+    float M = -__builtin_inff(), L = 0.0f;
     v4f v{0.0f, 0.0f, 0.0f, 0.0f};
     if (side < SIDE) {
 #pragma unroll 4
         for (int s = side; s < splits; s += SIDE) {
-            const float f = __builtin_amdgcn_exp2f(part[s * step] - M_use);
-            L = __builtin_fmaf(part[s * step + ROWS], f, L);
-            v += ld<v4f>(part - r + s * step + 2 * ROWS + r * D + 4 * c) * f;
+            const float m = part[s * step], l = part[s * step + ROWS];
+            const v4f o = ld<v4f>(part - r + s * step + 2 * ROWS + r * D + 4 * c);
+            const float top = fmaxf(M, m), use = top == -__builtin_inff() ? 0.0f : top;
+            const float f = __builtin_amdgcn_exp2f(M - use), h = __builtin_amdgcn_exp2f(m - use);
+            M = top;
+            L = L * f + l * h;
+            v = v * f + o * h;
         }
         st<v4f>(&sums[side][4 * c], v);
-        if (c == 0) tops[side] = L;
+        if (c == 0) {
+            tops[side] = M;
+            totals[side] = L;
+        }
     }
     __syncthreads();
     if (side != 0) return;
-    L = tops[0];
+#pragma unroll
+    for (int i = 1; i < SIDE; ++i) M = fmaxf(M, tops[i]);
+    const float use = M == -__builtin_inff() ? 0.0f : M, f0 = __builtin_amdgcn_exp2f(tops[0] - use);
+    L *= f0;
+    v *= f0;
 #pragma unroll
     for (int i = 1; i < SIDE; ++i) {
-        L += tops[i];
-        v += ld<v4f>(&sums[i][4 * c]);
+        const float f = __builtin_amdgcn_exp2f(tops[i] - use);
+        L = __builtin_fmaf(totals[i], f, L);
+        v += ld<v4f>(&sums[i][4 * c]) * f;
     }
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    const int64_t at = int64_t(cu + t) * p.Hq + kvh * p.G + (rr - t * p.G);
+    const int64_t t = row / p.G, at = t * p.Hq + kvh * p.G + (row - t * p.G);
     const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
     store_n<4>(p.out + at * D + 4 * c, out);
     if (c == 0 && p.lse) p.lse[at] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
@@ -445,18 +453,20 @@ inline Plan plan_of(const AttendCall& c, int rows) {
     r.tiles = c.T * G / rows + seqs;
     const bool split = kt > kMinTiles;
     // a tile has one item more than the work's share at the most, a split one twice as many
-    // (the work is summed in FP32)
-    r.items = r.tiles + (split ? r.target + 1 : 0);
+    // (the work is summed in FP32), and no more than its keys' whole splits
+    const int64_t share = r.target + 1, most = split ? r.tiles * ((kt + kMinTiles - 1) / kMinTiles - 1) : 0;
+    r.items = r.tiles + (share < most ? share : most);
     r.parts = split ? 2 * int64_t(r.target) + 2 : 0;
-    r.bytes = split ? 256 + (r.tiles * kDescInts * 4 + 255) / 256 * 256 + r.parts * c.Hkv * rows * (c.D + 2) * 4 : 0;
+    r.bytes = split ? c.T * G * 16 + r.parts * c.Hkv * rows * (c.D + 2) * 4 : 0;
     return r;
 }
 
 template <int D>
 hipError_t run(const AttendCall& c, Args p, const Plan& plan, hipStream_t stream) {
-    if (const hipError_t e = launch_kernel(attend<D>, dim3(unsigned(plan.items), unsigned(c.Hkv)), dim3(kThreads), stream, p)) return e;
+    const bool once = c.T * p.G <= 16 * (c.B < c.T ? c.B : c.T);
+    if (const hipError_t e = launch_kernel(once ? attend<D, true> : attend<D, false>, dim3(unsigned(plan.items), unsigned(c.Hkv)), dim3(kThreads), stream, p)) return e;
     if (plan.bytes == 0) return hipSuccess;
-    return launch_kernel(join<D, 16>, dim3(unsigned(plan.tiles * 16), unsigned(c.Hkv)), dim3(kThreads), stream, p);
+    return launch_kernel(join<D, 16>, dim3(unsigned(c.T * p.G), unsigned(c.Hkv)), dim3(kThreads), stream, p);
 }
 
 }  // namespace attend_detail
@@ -467,12 +477,10 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
     using namespace attend_detail;
     const Plan plan = plan_of(c, 16);
     Args p{c.q, c.kc, c.vc, c.ks, c.vs, c.table, c.cu, c.lens, c.ldq, c.n_pages, c.width, c.B, c.T, int(c.Hq), int(c.Hkv), int(c.Hq / c.Hkv),
-           c.page_log, c.scale * 1.4426950408889634f, c.out, c.lse, nullptr, nullptr, nullptr, plan.tiles, plan.parts, plan.target};
+           c.page_log, c.scale * 1.4426950408889634f, c.out, c.lse, nullptr, nullptr, plan.parts, plan.target};
     if (plan.bytes) {
-        uint8_t* w = static_cast<uint8_t*>(c.workspace);
-        p.head = reinterpret_cast<int32_t*>(w);
-        p.desc = reinterpret_cast<int32_t*>(w + 256);
-        p.parts = reinterpret_cast<float*>(w + 256 + (plan.tiles * kDescInts * 4 + 255) / 256 * 256);
+        p.desc = static_cast<int32_t*>(c.workspace);
+        p.parts = reinterpret_cast<float*>(p.desc + 4 * c.T * p.G);
     }
     switch (c.D) {
         case 64: return run<64>(c, p, plan, stream);
