@@ -29,7 +29,7 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kTile = 64;                 // tokens of a tile
 constexpr int kMinTiles = kWaves;         // tiles that a split holds at the least: one per wave
-constexpr int kTarget = 1024;             // workgroups that the whole call is split into, about
+constexpr int kSlots = 512;               // workgroups that run at a time: two on each of 256 CUs
 constexpr float kPBias = 15.0f;           // probabilities are held times 2^15: FP16 keeps them normal down to 2^-29
 
 struct Args {
@@ -176,21 +176,28 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int first, int end) {
     return n >= 4 ? w : n <= 0 ? 0u : w & (0xFFFFFFFFu >> (32 - 8 * n));
 }
 
-template <int D, bool ONCE>
+// 16 NR query rows of one key/value head and a part of their keys.  The four waves
+// take every fourth tile; a wave widens a tile's codes once for all its rows.
+template <int D, int NR, bool ONCE>
 __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
-    constexpr int ROWS = 16, KC = D / 64, DT = D / 16;
+    constexpr int ROWS = 16 * NR, KC = D / 64, DT = D / 16;
     constexpr bool kAhead = D <= 192;     // registers for it
     __shared__ __align__(16) float joined[kWaves][ROWS * D];
     __shared__ float stat[kWaves][2][ROWS];
     Item it{};
     if (!find_item<ROWS>(p, it)) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4, kvh = blockIdx.y;
-    // this lane's query row, and the last key that it sees
-    const int row = it.tile * ROWS + col, tq = row / p.G, hq = kvh * p.G + (row - tq * p.G);
-    const bool live = tq < it.n;
     const int before = it.len - it.n;
     const auto sees = [&](int t) { return t < it.n ? (before + t < it.len ? before + t : it.len - 1) : -1; };
-    const int last = sees(tq);
+    // this lane's query rows, and the last key that each sees
+    int tq[NR], hq[NR], last[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int row = it.tile * ROWS + 16 * r + col;
+        tq[r] = row / p.G;
+        hq[r] = kvh * p.G + (row - tq[r] * p.G);
+        last[r] = sees(tq[r]);
+    }
     const int first_tq = it.tile * ROWS / p.G, end_tq = (it.tile * ROWS + ROWS - 1) / p.G;
     const int least = sees(first_tq), most = sees(end_tq < it.n ? end_tq : it.n - 1);
     const int kt = most < 0 ? 0 : most / kTile + 1;
@@ -198,19 +205,26 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
     const int32_t* table = p.table + int64_t(it.b) * p.width;
     const int64_t page_bytes = int64_t(D) << p.page_log;
 
-    v8bf qf[KC][2];
+    v8bf qf[NR][KC][2];
 #pragma unroll
-    for (int c = 0; c < KC; ++c)
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            u32x4 w{0u, 0u, 0u, 0u};
-            if (live) w = ld<u32x4>(p.q + int64_t(it.cu + tq) * p.ldq + hq * D + 64 * c + 16 * g + 8 * h);
-            qf[c][h] = __builtin_bit_cast(v8bf, w);
-        }
-    v4f o[DT];
+        for (int c = 0; c < KC; ++c)
 #pragma unroll
-    for (int i = 0; i < DT; ++i) o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = -__builtin_inff(), l = 0.0f, ref = 0.0f, largest = 0.0f;
+            for (int h = 0; h < 2; ++h) {
+                u32x4 w{0u, 0u, 0u, 0u};
+                if (tq[r] < it.n) w = ld<u32x4>(p.q + int64_t(it.cu + tq[r]) * p.ldq + hq[r] * D + 64 * c + 16 * g + 8 * h);
+                qf[r][c][h] = __builtin_bit_cast(v8bf, w);
+            }
+    v4f o[NR][DT];
+    float m[NR], l[NR], ref = 0.0f, largest = 0.0f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        m[r] = -__builtin_inff();
+        l[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) o[r][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
 
     // The pages of a tile's tokens: of the group whose keys this lane loads and of
     // the lane's own group, -1 where there is none
@@ -254,15 +268,20 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
         };
         if (kAhead) load_values();
         else load_keys(tile, kid);
-        v4f s[4];
+        v4f s[NR][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            s[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int r = 0; r < NR; ++r) s[r][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
                 const u32x4 w = kraw[j][c];
-                s[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide_bf16(w[0], w[1]), qf[c][0], s[j], 0, 0, 0);
-                s[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide_bf16(w[2], w[3]), qf[c][1], s[j], 0, 0, 0);
+                const v8bf a = wide_bf16(w[0], w[1]), b = wide_bf16(w[2], w[3]);
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    s[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, qf[r][c][0], s[r][j], 0, 0, 0);
+                    s[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, qf[r][c][1], s[r][j], 0, 0, 0);
+                }
             }
         }
         kid = kid2;
@@ -275,43 +294,50 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
             }
         }
         if (!kAhead) load_values();
-        // scores in units of log2; keys out of sight at -inf
-        const bool masked = t0 + kTile - 1 > least || !__all(good);
-        const int seen = good ? last - (t0 + 16 * g) : -1;           // the last of the lane's tokens in sight
-        float mt = -__builtin_inff();
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[j][i] *= ksc;
-                if (masked && 4 * j + i > seen) s[j][i] = -__builtin_inff();
-                mt = fmaxf(mt, s[j][i]);
-            }
-        const float m_new = fmaxf(m, groups_max(mt)), m_use = m_new == -__builtin_inff() ? 0.0f : m_new;
-        const float alpha = __builtin_amdgcn_exp2f(m - m_use);
-        m = m_new;
         // O is held in units of `ref`, the largest of the four pages' value scales, but no
         // less than 2^-40 of the largest so far: FP32 holds the sums in such units
         const float top = groups_max(vsc);
         largest = fmaxf(largest, top);
         const float unit = fmaxf(top, largest * 0x1p-40f);
-        float factor = alpha;
+        float moved = 1.0f;
         if (unit != ref) {
-            factor *= ref / unit;
+            moved = ref / unit;
             ref = unit;
         }
         const float ratio = ref > 0.0f ? vsc / ref : 0.0f;
-        float sum = 0.0f;
-        v8h pf[2];
+        // scores in units of log2; keys out of sight at -inf
+        const bool masked = t0 + kTile - 1 > least || !__all(good);
+        v8h pf[NR][2];
+        float factor[NR];
+        bool same = true;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int r = 0; r < NR; ++r) {
+            const int seen = good ? last[r] - (t0 + 16 * g) : -1;     // the last of the lane's tokens in sight
+            float mt = -__builtin_inff();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e = __builtin_amdgcn_exp2f(s[j][i] - (m_use - kPBias));
-                sum += e;
-                pf[j >> 1][(j & 1) * 4 + i] = _Float16(e * ratio);
-            }
-        l = __builtin_fmaf(l, alpha, sum);
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[r][j][i] *= ksc;
+                    if (masked && 4 * j + i > seen) s[r][j][i] = -__builtin_inff();
+                    mt = fmaxf(mt, s[r][j][i]);
+                }
+            const float m_new = fmaxf(m[r], groups_max(mt)), m_use = m_new == -__builtin_inff() ? 0.0f : m_new;
+            const float alpha = __builtin_amdgcn_exp2f(m[r] - m_use);
+            m[r] = m_new;
+            factor[r] = alpha * moved;
+            same = same && factor[r] == 1.0f;
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(s[r][j][i] - (m_use - kPBias));
+                    sum += e;
+                    pf[r][j >> 1][(j & 1) * 4 + i] = _Float16(e * ratio);
+                }
+            l[r] = __builtin_fmaf(l[r], alpha, sum);
+        }
         if (masked) {                     // codes past the last token are not numbers
             const int end = !good ? 0 : it.len - (t0 + 16 * g);
 #pragma unroll
@@ -319,71 +345,85 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) vraw[d][i] = keep_bytes(vraw[d][i], 4 * i, end);
         }
-        if (__any(factor != 1.0f)) {
+        if (!__all(same)) {
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[d] *= factor;
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[r][d] *= factor[r];
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
             const u32x4 w = vraw[d];
-            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wide_f16(w[0], w[1]), pf[0], o[d], 0, 0, 0);
-            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wide_f16(w[2], w[3]), pf[1], o[d], 0, 0, 0);
+            const v8h a = wide_f16(w[0], w[1]), b = wide_f16(w[2], w[3]);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf[r][0], o[r][d], 0, 0, 0);
+                o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, pf[r][1], o[r][d], 0, 0, 0);
+            }
         }
     }
 
     // the four waves' results joined
-    l = groups_sum(l);
-    if (g == 0) {
-        stat[wave][0][col] = m;
-        stat[wave][1][col] = l;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        l[r] = groups_sum(l[r]);
+        if (g == 0) {
+            stat[wave][0][16 * r + col] = m[r];
+            stat[wave][1][16 * r + col] = l[r];
+        }
     }
     __syncthreads();
-    float M = stat[0][0][col];
+    const auto joint = [&](int row, float& M, float& L) {
+        M = stat[0][0][row];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) M = fmaxf(M, stat[w][0][col]);
-    const float M_use = M == -__builtin_inff() ? 0.0f : M;
-    float L = 0.0f;
+        for (int w = 1; w < kWaves; ++w) M = fmaxf(M, stat[w][0][row]);
+        const float use = M == -__builtin_inff() ? 0.0f : M;
+        L = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) L = __builtin_fmaf(stat[w][1][col], __builtin_amdgcn_exp2f(stat[w][0][col] - M_use), L);
-    const float mine = __builtin_amdgcn_exp2f(m - M_use) * ref;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)      // [row][channel], the 16-byte pieces of a row swapped by row
-        st<v4f>(&joined[wave][col * D + (((4 * d + g) ^ col) * 4)], o[d] * mine);
-    __syncthreads();
+        for (int w = 0; w < kWaves; ++w) L = __builtin_fmaf(stat[w][1][row], __builtin_amdgcn_exp2f(stat[w][0][row] - use), L);
+    };
     const bool split = it.splits > 1;
     float* part = p.parts + (int64_t(it.part + it.split) * p.Hkv + kvh) * (ROWS * (D + 2));
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int row = 16 * r + col;
+        float M, L;
+        joint(row, M, L);
+        const float mine = __builtin_amdgcn_exp2f(m[r] - (M == -__builtin_inff() ? 0.0f : M)) * ref;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)  // [row][channel], the 16-byte pieces of a row swapped by row
+            st<v4f>(&joined[wave][row * D + (((4 * d + g) ^ col) * 4)], o[r][d] * mine);
+        if (wave == 0 && g == 0) {
+            if (split) {
+                part[row] = M;
+                part[ROWS + row] = L;
+                if (p.desc && it.split == 0 && kvh == 0 && tq[r] < it.n)
+                    st<int4>(p.desc + 4 * (int64_t(it.cu + tq[r]) * p.G + (hq[r] - kvh * p.G)), int4{it.splits, it.part, row, 0});
+            } else if (tq[r] < it.n) {
+                if (p.lse)
+                    p.lse[int64_t(it.cu + tq[r]) * p.Hq + hq[r]] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
+                if (p.desc && kvh == 0) st<int4>(p.desc + 4 * (int64_t(it.cu + tq[r]) * p.G + (hq[r] - kvh * p.G)), int4{1, 0, 0, 0});
+            }
+        }
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
         const int r = i / (D / 4), c = i - r * (D / 4);
-        v4f v = ld<v4f>(&joined[0][r * D + ((c ^ r) * 4)]);
+        const int rr = it.tile * ROWS + r, t = rr / p.G;
+        if (t >= it.n) continue;
+        v4f v = ld<v4f>(&joined[0][r * D + ((c ^ (r & 15)) * 4)]);
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += ld<v4f>(&joined[w][r * D + ((c ^ r) * 4)]);
+        for (int w = 1; w < kWaves; ++w) v += ld<v4f>(&joined[w][r * D + ((c ^ (r & 15)) * 4)]);
         if (split) {
             st<v4f>(part + 2 * ROWS + r * D + 4 * c, v);
             continue;
         }
-        const int rr = it.tile * ROWS + r, t = rr / p.G;
-        float sum = 0.0f, top = stat[0][0][r];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, stat[w][0][r]);
-        top = top == -__builtin_inff() ? 0.0f : top;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) sum = __builtin_fmaf(stat[w][1][r], __builtin_amdgcn_exp2f(stat[w][0][r] - top), sum);
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        if (t < it.n) {
-            const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-            store_n<4>(p.out + (int64_t(it.cu + t) * p.Hq + kvh * p.G + (rr - t * p.G)) * D + 4 * c, out);
-        }
+        float M, L;
+        joint(r, M, L);
+        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+        store_n<4>(p.out + (int64_t(it.cu + t) * p.Hq + kvh * p.G + (rr - t * p.G)) * D + 4 * c, out);
     }
-    if (wave == 0 && g == 0) {
-        if (split) {
-            part[col] = M;
-            part[ROWS + col] = L;
-        } else if (live && p.lse) {
-            p.lse[int64_t(it.cu + tq) * p.Hq + hq] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
-        }
-    }
-    if (p.desc && it.split == 0 && kvh == 0 && wave == 0 && g == 0 && live)
-        st<int4>(p.desc + 4 * (int64_t(it.cu + tq) * p.G + (hq - kvh * p.G)), int4{it.splits, it.part, col, 0});
 }
 
 // The splits of a query row joined, a workgroup for each: D / 4 threads of four
@@ -449,8 +489,14 @@ struct Plan {
 inline Plan plan_of(const AttendCall& c, int rows) {
     Plan r;
     const int64_t G = c.Hq / c.Hkv, seqs = c.B < c.T ? c.B : c.T, kt = ((c.width << c.page_log) + kTile - 1) / kTile;
-    r.target = int((kTarget + c.Hkv - 1) / c.Hkv);
     r.tiles = c.T * G / rows + seqs;
+    // Parts of equal length, about as many as fill whole rounds of workgroups: every row
+    // tile adds half a part, its last one.  us with 512 / 768 / 1024 / 2048 parts: one
+    // request of 32,768 tokens, 8 heads, 22 / 27 / 27 / 28; two of 131,072, 4 heads, 44 / 56 / 52 / 69;
+    // 64 of 1024 to 8192, 8 heads, 132 / 119 / 126 / 139
+    const int64_t all = (c.T * G / rows > seqs ? c.T * G / rows : seqs) * c.Hkv;
+    const int64_t rounds = (3 * all / 2 + kSlots - 1) / kSlots;
+    r.target = int(((rounds > 1 ? rounds : 1) * kSlots - all / 2 + c.Hkv - 1) / c.Hkv);
     const bool split = kt > kMinTiles;
     // a tile has one item more than the work's share at the most, a split one twice as many
     // (the work is summed in FP32), and no more than its keys' whole splits
@@ -461,21 +507,32 @@ inline Plan plan_of(const AttendCall& c, int rows) {
     return r;
 }
 
-template <int D>
-hipError_t run(const AttendCall& c, Args p, const Plan& plan, hipStream_t stream) {
-    const bool once = c.T * p.G <= 16 * (c.B < c.T ? c.B : c.T);
-    if (const hipError_t e = launch_kernel(once ? attend<D, true> : attend<D, false>, dim3(unsigned(plan.items), unsigned(c.Hkv)), dim3(kThreads), stream, p)) return e;
+// Rows of a workgroup: 32 where the requests bring more than 16 each on average
+// (their keys would be read twice) and the registers hold two 16-row products
+inline int rows_of(const AttendCall& c) {
+    const int64_t seqs = c.B < c.T ? c.B : c.T;
+    return c.D <= 128 && c.T * (c.Hq / c.Hkv) > 16 * seqs ? 32 : 16;
+}
+
+template <int D, int NR>
+hipError_t run(const AttendCall& c, const Args& p, const Plan& plan, hipStream_t stream) {
+    // values that no other workgroup reads pass the caches by
+    const bool once = c.T * p.G <= 16 * NR * (c.B < c.T ? c.B : c.T);
+    if (const hipError_t e = launch_kernel(once ? attend<D, NR, true> : attend<D, NR, false>, dim3(unsigned(plan.items), unsigned(c.Hkv)),
+                                           dim3(kThreads), stream, p))
+        return e;
     if (plan.bytes == 0) return hipSuccess;
-    return launch_kernel(join<D, 16>, dim3(unsigned(c.T * p.G), unsigned(c.Hkv)), dim3(kThreads), stream, p);
+    return launch_kernel(join<D, 16 * NR>, dim3(unsigned(c.T * p.G), unsigned(c.Hkv)), dim3(kThreads), stream, p);
 }
 
 }  // namespace attend_detail
 
-int64_t attend_workspace(const AttendCall& c) { return attend_detail::plan_of(c, 16).bytes; }
+int64_t attend_workspace(const AttendCall& c) { return attend_detail::plan_of(c, attend_detail::rows_of(c)).bytes; }
 
 hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
     using namespace attend_detail;
-    const Plan plan = plan_of(c, 16);
+    const int rows = rows_of(c);
+    const Plan plan = plan_of(c, rows);
     Args p{c.q, c.kc, c.vc, c.ks, c.vs, c.table, c.cu, c.lens, c.ldq, c.n_pages, c.width, c.B, c.T, int(c.Hq), int(c.Hkv), int(c.Hq / c.Hkv),
            c.page_log, c.scale * 1.4426950408889634f, c.out, c.lse, nullptr, nullptr, plan.parts, plan.target};
     if (plan.bytes) {
@@ -483,10 +540,10 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
         p.parts = reinterpret_cast<float*>(p.desc + 4 * c.T * p.G);
     }
     switch (c.D) {
-        case 64: return run<64>(c, p, plan, stream);
-        case 128: return run<128>(c, p, plan, stream);
-        case 192: return run<192>(c, p, plan, stream);
-        default: return run<256>(c, p, plan, stream);
+        case 64: return rows == 32 ? run<64, 2>(c, p, plan, stream) : run<64, 1>(c, p, plan, stream);
+        case 128: return rows == 32 ? run<128, 2>(c, p, plan, stream) : run<128, 1>(c, p, plan, stream);
+        case 192: return run<192, 1>(c, p, plan, stream);
+        default: return run<256, 1>(c, p, plan, stream);
     }
 }
 
