@@ -30,7 +30,11 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kTile = 64;                 // tokens of a tile
 constexpr int kMinTiles = kWaves;         // tiles that a split holds at the least: one per wave
 constexpr int kSlots = 512;               // workgroups that run at a time: two on each of 256 CUs
-constexpr float kPBias = 15.0f;           // probabilities are held times 2^15: FP16 keeps them normal down to 2^-29
+// Probabilities are held times 2^11, relative to a maximum that is raised only when
+// a score passes it by a factor of 2^4: at most 2^15, and FP16 keeps them normal
+// down to 2^-25.  With every new maximum taken, the wide kernel multiplied its sums by
+// it in most tiles (some row of 32 has one).
+constexpr float kPBias = 11.0f, kSlack = 4.0f;
 
 struct Args {
     const uint16_t* q;
@@ -72,8 +76,8 @@ __device__ __forceinline__ int lane63(int v) { return __builtin_amdgcn_readlane(
 // finds its workgroup's own from the lengths, four consecutive requests to a
 // lane, without LDS or a barrier.  Splits are of equal numbers of tiles, as long as
 // it takes for about `target` workgroups to do all the work.
-template <int ROWS>
-__device__ __forceinline__ bool find_item(const Args& p, Item& it) {
+template <int ROWS, bool CLASSES>
+__device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
     constexpr int R = 4, CHUNK = 64 * R;
     const int lane = threadIdx.x & 63;
     const int room = int(p.width << p.page_log);
@@ -102,45 +106,66 @@ __device__ __forceinline__ bool find_item(const Args& p, Item& it) {
 #pragma unroll
         for (int i = 0; i < R; ++i) work += float(tiles[i]) * float(kt[i]);
     }
-    const float want = ceilf(lanes_sum<64>(work) / float(p.target));
+    const float want = ceilf(lanes_sum<64>(work) * (1.0f + 0x1p-20f) / float(p.target));    // no less for FP32's roundings
     const int per = want < float(kMinTiles) ? kMinTiles : want > 0x1p30f ? 1 << 30 : int(want);
-    const int me = blockIdx.x;
-    int items0 = 0, parts0 = 0;
-    for (int64_t b0 = 0; b0 < p.B; b0 += CHUNK) {
-        if (p.B > CHUNK) read(b0);        // else as they were read above
-        int items = 0, parts = 0;
+    // CLASSES: requests whose parts are long come first, in four classes by their share of the
+    // longest (where all requests fit one chunk), so that what starts last is short.  Three chunks
+    // of 2048 tokens on 1024 to 8192: 528 / 461 us without and with.  Parts of a decode step are
+    // alike; there the classes' scans cost 0.7 us and save nothing.
+    int splits[R], size[R], longest = 0;
+    const auto divide = [&] {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int splits = kt[i] > per ? (kt[i] + per - 1) / per : 1;
-            items += tiles[i] * splits;
-            parts += splits > 1 ? tiles[i] * splits : 0;
+            splits[i] = kt[i] > per ? (kt[i] + per - 1) / per : 1;
+            size[i] = splits[i] > 1 ? (kt[i] + splits[i] - 1) / splits[i] : kt[i];
+            longest = size[i] > longest && tiles[i] > 0 ? size[i] : longest;
         }
-        const int i1 = wave_scan(items), p1 = wave_scan(parts);
-        int at = me - items0 - (i1 - items);
-        const uint64_t who = __ballot(at >= 0 && at < items);
-        if (who) {
-            int part = parts0 + p1 - parts;
-            Item mine{};
+    };
+    const bool whole = p.B <= CHUNK;
+    if (whole) divide();
+    if (CLASSES) longest = __builtin_amdgcn_readfirstlane(int(lanes_max<64>(uint32_t(longest))));
+    int items0 = 0, parts0 = 0;
+    const bool classes = CLASSES && whole;
+    for (int cls = classes ? 3 : 0; cls >= 0; --cls) {
+        const int over = classes && cls > 0 ? int(int64_t(longest) * cls / 4) : -1, upto = classes && cls < 3 ? int(int64_t(longest) * (cls + 1) / 4) : 0x7FFFFFFF;
+        for (int64_t b0 = 0; b0 < p.B; b0 += CHUNK) {
+            if (!whole) {
+                read(b0);
+                divide();
+            }
+            int items = 0, parts = 0, here[R];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int splits = kt[i] > per ? (kt[i] + per - 1) / per : 1, here = tiles[i] * splits;
-                if (at >= 0 && at < here) {
-                    const int tile = at / splits;
-                    mine = Item{int32_t(b0) + lane * R + i, cu[i], n[i], len[i], tile, at - tile * splits, splits,
-                                splits > 1 ? part + tile * splits : 0};
-                }
-                at -= here;
-                part += splits > 1 ? here : 0;
+                here[i] = size[i] > over && size[i] <= upto ? tiles[i] * splits[i] : 0;
+                items += here[i];
+                parts += splits[i] > 1 ? here[i] : 0;
             }
-            const int src = __builtin_ctzll(who);
-            it = Item{__builtin_amdgcn_readlane(mine.b, src), __builtin_amdgcn_readlane(mine.cu, src), __builtin_amdgcn_readlane(mine.n, src),
-                      __builtin_amdgcn_readlane(mine.len, src), __builtin_amdgcn_readlane(mine.tile, src),
-                      __builtin_amdgcn_readlane(mine.split, src), __builtin_amdgcn_readlane(mine.splits, src),
-                      __builtin_amdgcn_readlane(mine.part, src)};
-            return it.splits == 1 || it.part + it.splits <= p.most_parts;
+            const int i1 = wave_scan(items), p1 = wave_scan(parts);
+            int at = me - items0 - (i1 - items);
+            const uint64_t who = __ballot(at >= 0 && at < items);
+            if (who) {
+                int part = parts0 + p1 - parts;
+                Item mine{};
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    if (at >= 0 && at < here[i]) {
+                        const int tile = at / splits[i];
+                        mine = Item{int32_t(b0) + lane * R + i, cu[i], n[i], len[i], tile, at - tile * splits[i], splits[i],
+                                    splits[i] > 1 ? part + tile * splits[i] : 0};
+                    }
+                    at -= here[i];
+                    part += splits[i] > 1 ? here[i] : 0;
+                }
+                const int src = __builtin_ctzll(who);
+                it = Item{__builtin_amdgcn_readlane(mine.b, src), __builtin_amdgcn_readlane(mine.cu, src), __builtin_amdgcn_readlane(mine.n, src),
+                          __builtin_amdgcn_readlane(mine.len, src), __builtin_amdgcn_readlane(mine.tile, src),
+                          __builtin_amdgcn_readlane(mine.split, src), __builtin_amdgcn_readlane(mine.splits, src),
+                          __builtin_amdgcn_readlane(mine.part, src)};
+                return it.splits == 1 || it.part + it.splits <= p.most_parts;
+            }
+            items0 += lane63(i1);
+            parts0 += lane63(p1);
         }
-        items0 += lane63(i1);
-        parts0 += lane63(p1);
     }
     return false;
 }
@@ -185,7 +210,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
     __shared__ __align__(16) float joined[kWaves][ROWS * D];
     __shared__ float stat[kWaves][2][ROWS];
     Item it{};
-    if (!find_item<ROWS>(p, it)) return;
+    if (!find_item<ROWS, false>(p, blockIdx.x, it)) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4, kvh = blockIdx.y;
     const int before = it.len - it.n;
     const auto sees = [&](int t) { return t < it.n ? (before + t < it.len ? before + t : it.len - 1) : -1; };
@@ -322,7 +347,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
                     if (masked && 4 * j + i > seen) s[r][j][i] = -__builtin_inff();
                     mt = fmaxf(mt, s[r][j][i]);
                 }
-            const float m_new = fmaxf(m[r], groups_max(mt)), m_use = m_new == -__builtin_inff() ? 0.0f : m_new;
+            mt = groups_max(mt);
+            const float m_new = mt > m[r] + kSlack ? mt : m[r], m_use = m_new == -__builtin_inff() ? 0.0f : m_new;
             const float alpha = __builtin_amdgcn_exp2f(m[r] - m_use);
             m[r] = m_new;
             factor[r] = alpha * moved;
@@ -426,6 +452,224 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
     }
 }
 
+// Many query rows: each of the four waves holds 32 rows, and all of them read a
+// tile's keys and values from LDS, where they lie widened (BF16 and FP16), in two
+// buffers: while a tile is multiplied the next one's codes are on their way in
+// registers.  The products are 32 x 32 x 16, again S^T = K Q^T and O^T = V^T P^T: row n =
+// 8 b + 4 h + i of a 32-token product holds token 16 h + 4 b + i, so that lane half h ends up with
+// tokens 16 h .. 16 h + 15 of a row, one page's, in order.  16-byte pieces of LDS rows are
+// swapped by row, so that eight lanes' pieces meet different banks.
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+template <int D>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const Args p) {
+    constexpr int ROWS = 32 * kWaves, KC = D / 64, DT = D / 32;
+    __shared__ __align__(16) uint16_t keys[2][kTile * D], values[2][kTile * D];
+    __shared__ float scales[2][2][4];     // [buffer][keys, values][group of 16 tokens]; values' -1: no page
+    Item it{};
+    const int kvh = blockIdx.x % p.Hkv;
+    if (!find_item<ROWS, true>(p, blockIdx.x / p.Hkv, it)) return;
+    it.tile = int((int64_t(it.n) * p.G + ROWS - 1) / ROWS) - 1 - it.tile;       // the last rows see the most keys: they start first
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, h = lane >> 5, quad = threadIdx.x & 3;
+    const int before = it.len - it.n;
+    const auto sees = [&](int t) { return t < it.n ? (before + t < it.len ? before + t : it.len - 1) : -1; };
+    const int row = it.tile * ROWS + 32 * wave + col, tq = row / p.G, hq = kvh * p.G + (row - tq * p.G), last = sees(tq);
+    const bool live = tq < it.n;
+    const int end_tq = (it.tile * ROWS + ROWS - 1) / p.G;
+    const int least = sees((it.tile * ROWS + 32 * wave) / p.G), most = sees(end_tq < it.n ? end_tq : it.n - 1);
+    const int kt = most < 0 ? 0 : most / kTile + 1;
+    const int per = (kt + it.splits - 1) / it.splits, kt0 = it.split * per, kt1 = kt0 + per < kt ? kt0 + per : kt;
+    const int32_t* table = p.table + int64_t(it.b) * p.width;
+    const int64_t page_bytes = int64_t(D) << p.page_log;
+    const int mask = (1 << p.page_log) - 1;
+
+    v8bf qf[D / 16];
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+        u32x4 w{0u, 0u, 0u, 0u};
+        if (live) w = ld<u32x4>(p.q + int64_t(it.cu + tq) * p.ldq + hq * D + 16 * c + 8 * h);
+        qf[c] = __builtin_bit_cast(v8bf, w);
+    }
+    v16f o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+    float m = -__builtin_inff(), l = 0.0f, ref = 0.0f, largest = 0.0f;
+
+    // The page of group `quad` of a tile.  A wave brings the keys of group `wave`; values
+    // come by quads of lanes, four groups of a channel side by side.
+    // (What is loaded here is looked at only when it is used: a comparison would wait for it.)
+    const auto page_of = [&](int tile) {
+        const int token = tile * kTile + 16 * quad;
+        return token < it.len ? table[token >> p.page_log] : -1;
+    };
+    const auto exists = [&](int32_t id) { return id >= 0 && id < p.n_pages; };
+    u32x4 kraw[KC], vraw[KC];
+    float kscale, vscale;
+    const auto fetch = [&](int tile, int32_t id) {
+        const int32_t kid = __builtin_amdgcn_readlane(id, wave);
+        const uint8_t* kp = p.kc + (int64_t(exists(kid) ? kid : 0) * p.Hkv + kvh) * page_bytes + ((tile * kTile + 16 * wave) & mask) * D;
+        const int64_t at = int64_t(exists(id) ? id : 0) * p.Hkv + kvh;
+        const uint8_t* vp = p.vc + at * page_bytes + ((tile * kTile + 16 * quad) & mask);
+#pragma unroll
+        for (int i = 0; i < KC; ++i) {
+            kraw[i] = ld<u32x4>(kp + (lane + 64 * i) * 16);
+            vraw[i] = ld<u32x4>(vp + (int64_t(threadIdx.x / 4 + 64 * i) << p.page_log));
+        }
+        kscale = p.ks[at];
+        vscale = p.vs[at];
+    };
+    // Places of 16-byte pieces: rows of 16 pieces (or a multiple) start in the same bank,
+    // rows of 8 (or an odd multiple) in two
+    const auto key_at = [&](int n, int c) { return n * D + ((c ^ (D % 128 == 0 ? n & 15 : (n >> 1) & 7)) * 8); };
+    const auto value_at = [&](int d, int c) { return d * kTile + ((c ^ ((d >> 1) & 7)) * 8); };
+    // the fetched tile, widened, into buffer `to`
+    const auto put = [&](int tile, int32_t id, int to) {
+        const bool there = exists(id);
+        const int end = !there ? 0 : it.len - (tile * kTile + 16 * quad);     // codes past the last token are not numbers
+        if ((tile + 1) * kTile > it.len || !__all(there)) {
+#pragma unroll
+            for (int i = 0; i < KC; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) vraw[i][j] = keep_bytes(vraw[i][j], 4 * j, end);
+        }
+#pragma unroll
+        for (int i = 0; i < KC; ++i) {
+            const int at = lane + 64 * i, r = at / (D / 16), c = 2 * (at % (D / 16));
+            // token 16 wave + r: row n of the 32-token product wave / 2
+            const int n = 32 * (wave >> 1) + 8 * (r >> 2) + 4 * (wave & 1) + (r & 3);
+            const u32x4 w = kraw[i];
+            st<v8bf>(&keys[to][key_at(n, c)], wide_bf16(w[0], w[1]));
+            st<v8bf>(&keys[to][key_at(n, c + 1)], wide_bf16(w[2], w[3]));
+            const u32x4 v = vraw[i];
+            const int d = threadIdx.x / 4 + 64 * i;
+            st<v8h>(reinterpret_cast<v8h*>(&values[to][value_at(d, 2 * quad)]), wide_f16(v[0], v[1]));
+            st<v8h>(reinterpret_cast<v8h*>(&values[to][value_at(d, 2 * quad + 1)]), wide_f16(v[2], v[3]));
+        }
+        if (threadIdx.x < 4) {
+            // never 0: a masked score times it stays -inf (2^-149 times any other one is 0 to the exponential)
+            scales[to][0][quad] = there ? fmaxf(kscale * p.scale2, 0x1p-149f) : 0x1p-149f;
+            scales[to][1][quad] = there ? vscale : -1.0f;
+        }
+    };
+    int32_t id = page_of(kt0), id2 = page_of(kt0 + 1);
+    if (kt0 < kt1) {
+        fetch(kt0, id);
+        put(kt0, id, 0);
+    }
+    __syncthreads();
+    for (int tile = kt0; tile < kt1; ++tile) {
+        const int buf = (tile - kt0) & 1, t0 = tile * kTile;
+        id = id2;
+        id2 = page_of(tile + 2);
+        if (tile + 1 < kt1) fetch(tile + 1, id);
+        v16f s[2];
+        float ksc[2], vsc[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            ksc[t] = scales[buf][0][2 * t + h];
+            vsc[t] = scales[buf][1][2 * t + h];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                const v8bf k = ld<v8bf>(&keys[buf][key_at(32 * t + col, 2 * c + h)]);
+                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[c], s[t], 0, 0, 0);
+            }
+        }
+        if (t0 + kTile - 1 > least || !__all(vsc[0] >= 0.0f && vsc[1] >= 0.0f)) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int seen = vsc[t] >= 0.0f ? last - (t0 + 32 * t + 16 * h) : -1;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i > seen) s[t][i] = -__builtin_inff();
+            }
+        }
+        float mt = -__builtin_inff();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            float top = s[t][0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) top = fmaxf(top, s[t][i]);
+            mt = fmaxf(mt, top * ksc[t]);
+        }
+        mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+        const float m_new = mt > m + kSlack ? mt : m, m_use = m_new == -__builtin_inff() ? 0.0f : m_new;
+        const float alpha = __builtin_amdgcn_exp2f(m - m_use);
+        m = m_new;
+        float top = fmaxf(vsc[0], vsc[1]);
+        top = fmaxf(0.0f, fmaxf(top, __shfl_xor(top, 32, 64)));
+        largest = fmaxf(largest, top);
+        const float unit = fmaxf(top, largest * 0x1p-40f);
+        float factor = alpha;
+        if (unit != ref) {
+            factor *= ref / unit;
+            ref = unit;
+        }
+        float sum = 0.0f;
+        v8h pf[2][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float ratio = ref > 0.0f ? fmaxf(vsc[t], 0.0f) / ref : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], ksc[t], kPBias - m_use));
+                sum += e;
+                pf[t][i >> 3][i & 7] = _Float16(e * ratio);
+            }
+        }
+        l = __builtin_fmaf(l, alpha, sum);
+        if (!__all(factor == 1.0f)) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] *= factor;
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const v8h v = ld<v8h>(&values[buf][value_at(32 * d + col, 4 * t + 2 * h + k)]);
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pf[t][k], o[d], 0, 0, 0);
+                }
+        if (tile + 1 < kt1) put(tile + 1, id, buf ^ 1);
+        __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    if (!live) return;
+    const bool split = it.splits > 1;
+    const int r = 32 * wave + col;
+    const int64_t at = int64_t(it.cu + tq) * p.Hq + hq;
+    if (split) {
+        float* part = p.parts + (int64_t(it.part + it.split) * p.Hkv + kvh) * (ROWS * (D + 2));
+        if (h == 0) {
+            part[r] = m;
+            part[ROWS + r] = l;
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                st<v4f>(part + 2 * ROWS + r * D + 32 * d + 8 * b + 4 * h,
+                        v4f{o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]} * ref);
+    } else {
+        const float inv = l > 0.0f ? ref / l : 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const float out[4] = {o[d][4 * b] * inv, o[d][4 * b + 1] * inv, o[d][4 * b + 2] * inv, o[d][4 * b + 3] * inv};
+                store_n<4>(p.out + at * D + 32 * d + 8 * b + 4 * h, out);
+            }
+        if (h == 0 && p.lse) p.lse[at] = l > 0.0f ? (m + __log2f(l) - kPBias) * 0.6931471805599453f : -__builtin_inff();
+    }
+    if (p.desc && it.split == 0 && kvh == 0 && h == 0)
+        st<int4>(p.desc + 4 * (int64_t(it.cu + tq) * p.G + (hq - kvh * p.G)), int4{it.splits, it.part, r, 0});
+}
+
 // The splits of a query row joined, a workgroup for each: D / 4 threads of four
 // channels side by side, 1024 / D splits at a time, each with a running maximum of its
 // own; they meet in LDS in a fixed order.
@@ -481,6 +725,7 @@ __global__ __launch_bounds__(kThreads) void join(const Args p) {
     if (c == 0 && p.lse) p.lse[at] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
 }
 
+constexpr int kWideRows = 32 * kWaves;
 struct Plan {
     int64_t tiles, items, parts;          // bounds: row tiles, workgroups, unjoined results, per key/value head
     int target;
@@ -497,7 +742,8 @@ inline Plan plan_of(const AttendCall& c, int rows) {
     const int64_t all = (c.T * G / rows > seqs ? c.T * G / rows : seqs) * c.Hkv;
     const int64_t rounds = (3 * all / 2 + kSlots - 1) / kSlots;
     r.target = int(((rounds > 1 ? rounds : 1) * kSlots - all / 2 + c.Hkv - 1) / c.Hkv);
-    const bool split = kt > kMinTiles;
+    if (rows == kWideRows && all > kSlots / 4) r.target = 1;      // enough row tiles, and many rows to join
+    const bool split = kt > kMinTiles && r.target > 1;
     // a tile has one item more than the work's share at the most, a split one twice as many
     // (the work is summed in FP32), and no more than its keys' whole splits
     const int64_t share = r.target + 1, most = split ? r.tiles * ((kt + kMinTiles - 1) / kMinTiles - 1) : 0;
@@ -507,11 +753,10 @@ inline Plan plan_of(const AttendCall& c, int rows) {
     return r;
 }
 
-// Rows of a workgroup: 32 where the requests bring more than 16 each on average
-// (their keys would be read twice) and the registers hold two 16-row products
+// Rows of a workgroup, by what the requests bring on average
 inline int rows_of(const AttendCall& c) {
-    const int64_t seqs = c.B < c.T ? c.B : c.T;
-    return c.D <= 128 && c.T * (c.Hq / c.Hkv) > 16 * seqs ? 32 : 16;
+    const int64_t seqs = c.B < c.T ? c.B : c.T, rows = c.T * (c.Hq / c.Hkv);
+    return rows > 64 * seqs ? kWideRows : c.D <= 128 && rows > 16 * seqs ? 32 : 16;
 }
 
 template <int D, int NR>
@@ -523,6 +768,23 @@ hipError_t run(const AttendCall& c, const Args& p, const Plan& plan, hipStream_t
         return e;
     if (plan.bytes == 0) return hipSuccess;
     return launch_kernel(join<D, 16 * NR>, dim3(unsigned(c.T * p.G), unsigned(c.Hkv)), dim3(kThreads), stream, p);
+}
+
+template <int D>
+hipError_t run_wide(const AttendCall& c, const Args& p, const Plan& plan, hipStream_t stream) {
+    // a head's workgroups side by side: with eight heads each XCD reads one head's keys and values
+    if (const hipError_t e = launch_kernel(attend_wide<D>, dim3(unsigned(plan.items * c.Hkv)), dim3(kThreads), stream, p)) return e;
+    if (plan.bytes == 0) return hipSuccess;
+    return launch_kernel(join<D, kWideRows>, dim3(unsigned(c.T * p.G), unsigned(c.Hkv)), dim3(kThreads), stream, p);
+}
+
+template <int D>
+hipError_t run_any(const AttendCall& c, const Args& p, const Plan& plan, int rows, hipStream_t stream) {
+    if (rows == kWideRows) return run_wide<D>(c, p, plan, stream);
+    if constexpr (D <= 128) {
+        if (rows == 32) return run<D, 2>(c, p, plan, stream);
+    }
+    return run<D, 1>(c, p, plan, stream);
 }
 
 }  // namespace attend_detail
@@ -540,10 +802,10 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
         p.parts = reinterpret_cast<float*>(p.desc + 4 * c.T * p.G);
     }
     switch (c.D) {
-        case 64: return rows == 32 ? run<64, 2>(c, p, plan, stream) : run<64, 1>(c, p, plan, stream);
-        case 128: return rows == 32 ? run<128, 2>(c, p, plan, stream) : run<128, 1>(c, p, plan, stream);
-        case 192: return run<192, 1>(c, p, plan, stream);
-        default: return run<256, 1>(c, p, plan, stream);
+        case 64: return run_any<64>(c, p, plan, rows, stream);
+        case 128: return run_any<128>(c, p, plan, rows, stream);
+        case 192: return run_any<192>(c, p, plan, rows, stream);
+        default: return run_any<256>(c, p, plan, rows, stream);
     }
 }
 
