@@ -270,10 +270,9 @@ __global__ __launch_bounds__(kThreads) void rope(const RopeArgs p) {
 }
 
 // New keys and values into their pages.  The tokens of a page are a run of
-// consecutive rows with consecutive slots; the workgroup of the run's first
-// token takes one head's run.  The scale is the least power of two s with
-// amax <= 448 s (2^-126 at the least), over the run and the page's older tokens; when it
-// grows, older codes are re-encoded by the exact factor.
+// consecutive rows with consecutive slots, and a wave or a workgroup takes one head's run of keys or
+// values.  The scale is the least power of two s with amax <= 448 s (2^-126 at the least), over
+// the run and the page's older tokens; when it grows, older codes are re-encoded by the exact factor.
 struct AppendArgs {
     const void *k, *v;
     int64_t ldk, ldv, T, n_slots;
@@ -294,85 +293,262 @@ __device__ __forceinline__ float pow2_scale(float amax) {
 // the power of two that takes values to codes: 1 / s, exact for s in [2^-126, 2^119]
 __device__ __forceinline__ float inverse_of(float s) { return s == 0.0f ? 1.0f : 1.0f / s; }
 
-__device__ __forceinline__ float block_max(float v, float* part) {
-    v = wave_max(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-}
 __device__ __forceinline__ uint32_t shift_codes(uint32_t w, float f) {
     const v2f lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, 1.0f, false), hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, 1.0f, true);
     return cvt4(lo[0] * f, lo[1] * f, hi[0] * f, hi[1] * f);
 }
 
-template <class T, bool V>
-__device__ __forceinline__ void append_run(const T* x, int64_t ld, int run, int off, int page, int D, uint8_t* codes, float* scale,
-                                           float* part) {
-    float amax = 0.0f;
-    const int per = D / 8;
-    for (int i = threadIdx.x; i < run * per; i += kThreads) {
-        float v[8];
-        load_n<8>(x + int64_t(i / per) * ld + i % per * 8, v);
+// Two channels of a row
+__device__ __forceinline__ v2f widen2(uint32_t w) { return v2f{__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)}; }
+__device__ __forceinline__ v2f widen2(v2f w) { return w; }
+template <class T>
+struct pair_of {
+    typedef v2f type;
+};
+template <>
+struct pair_of<uint16_t> {
+    typedef uint32_t type;
+};
+
+// A run's place: x its first token's channels, rows `step` elements apart; codes, scale its page's.
+// Its team is the wave (team 64) or the workgroup (256), `me` the thread's place in it.
+template <class T>
+struct Run {
+    const T* x;
+    int64_t step;
+    int count, off, page, D;
+    uint8_t* codes;
+    float* scale;
+    float was;                            // the page's scale so far, 0 for a new page
+    int me, team;
+    float* part;                          // LDS for the workgroup's waves
+};
+
+// The page's scale after a run whose largest magnitude is amax (in any lane), and its
+// inverse; older codes are moved to it, 16 bytes at a time.  VALUES: [channel][token],
+// where only the bytes of the older tokens are changed.
+template <bool VALUES, class T>
+__device__ __forceinline__ float new_scale(const Run<T>& r, float amax) {
+    float s = fmaxf(r.was, pow2_scale(lanes_max<64>(amax)));
+    if (r.team > 64) {                    // (every wave has read the page's scale by now, before one writes it)
+        __syncthreads();                  // the last use of part is over
+        if ((r.me & 63) == 0) r.part[r.me >> 6] = s;
+        __syncthreads();
+        s = fmaxf(fmaxf(r.part[0], r.part[1]), fmaxf(r.part[2], r.part[3]));
+    }
+    if (r.me == 0) *r.scale = s;
+    if (r.off > 0 && s > r.was) {
+        const float f = r.was / s;
+        const int across = VALUES ? (r.off + 15) / 16 : 0, pieces = VALUES ? r.D * across : r.off * r.D / 16;
+#pragma unroll 4
+        for (int i = r.me; i < pieces; i += r.team) {
+            const int row = VALUES ? i / across : 0, at = VALUES ? i - row * across : i;
+            uint8_t* c = r.codes + row * r.page + 16 * at;
+            u32x4 w = ld<u32x4>(c);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
-    }
-    amax = block_max(amax, part);
-    const float was = off > 0 ? *scale : 0.0f;
-    const float need = pow2_scale(amax), s = fmaxf(was, need), r = inverse_of(s);
-    __syncthreads();
-    if (threadIdx.x == 0) *scale = s;
-    if (off > 0 && s > was) {
-        const float f = was / s;
-        if constexpr (V) {
-            for (int i = threadIdx.x; i < D * off; i += kThreads) {
-                uint8_t* c = codes + (i / off) * page + i % off;
-                *c = uint8_t(shift_codes(*c, f));
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t moved = shift_codes(w[j], f);
+                const int n = VALUES ? r.off - 16 * at - 4 * j : 4;
+                const uint32_t mask = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : 0xFFFFFFFFu >> (32 - 8 * n);
+                w[j] = (moved & mask) | (w[j] & ~mask);
             }
-        } else {
-            for (int i = threadIdx.x; i < off * D / 4; i += kThreads) {
-                uint32_t* c = reinterpret_cast<uint32_t*>(codes) + i;
-                *c = shift_codes(*c, f);
-            }
+            st<u32x4>(c, w);
         }
+        if (VALUES && r.team > 64) __syncthreads();      // the new tokens' bytes lie in the same 16-byte pieces
     }
-    if constexpr (V) {
-        for (int i = threadIdx.x; i < run * D; i += kThreads) {
-            const int t = i / D, d = i % D;
-            codes[d * page + off + t] = uint8_t(cvt4(f32_of(x[int64_t(t) * ld + d]) * r, 0.0f, 0.0f, 0.0f));
-        }
-    } else {
-        for (int i = threadIdx.x; i < run * per; i += kThreads) {
-            const int t = i / per, d = i % per * 8;
-            float v[8];
-            load_n<8>(x + int64_t(t) * ld + d, v);
-            st<u32x2_t>(codes + (off + t) * D + d,
-                        u32x2_t{cvt4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), cvt4(v[4] * r, v[5] * r, v[6] * r, v[7] * r)});
-        }
-    }
+    return inverse_of(s);
 }
 
+// A run's data are read once: up to HOLD pieces of a thread stay in registers between
+// the maximum and the encoding; longer runs read again.
+template <int HOLD, class Load, class Look, class Put, class Scale>
+__device__ __forceinline__ void in_two_passes(int pieces, int me, int team, Load load, Look look, Put put, Scale scale) {
+    typedef decltype(load(0)) Piece;
+    if (pieces <= team * HOLD) {
+        Piece w[HOLD];
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i)
+            if (team * i < pieces) w[i] = load(me + team * i < pieces ? me + team * i : pieces - 1);
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i)
+            if (team * i < pieces) look(w[i]);
+        const float r = scale();
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i)
+            if (me + team * i < pieces) put(me + team * i, w[i], r);
+        return;
+    }
+#pragma unroll 2
+    for (int i = me; i < pieces; i += team) look(load(i));
+    const float r = scale();
+#pragma unroll 2
+    for (int i = me; i < pieces; i += team) put(i, load(i), r);
+}
+
+// Keys: eight channels of a token at a time
 template <class T>
-__global__ __launch_bounds__(kThreads) void append(const AppendArgs p) {
+__device__ __forceinline__ void append_keys(const Run<T>& r) {
+    const int per = r.D / 8;
+    float amax = 0.0f;
+    in_two_passes<sizeof(T) == 2 ? 8 : 4>(
+        r.count * per, r.me, r.team,
+        [&](int i) {
+            Raw<T, 8> w;
+            w.load(r.x + int64_t(i / per) * r.step + i % per * 8);
+            return w;
+        },
+        [&](const Raw<T, 8>& w) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(w.get(j)));
+        },
+        [&](int i, const Raw<T, 8>& w, float f) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = w.get(j) * f;
+            st<u32x2_t>(r.codes + r.off * r.D + i * 8, u32x2_t{cvt4(v[0], v[1], v[2], v[3]), cvt4(v[4], v[5], v[6], v[7])});
+        },
+        [&] { return new_scale<false>(r, amax); });
+}
+
+// Values, transposed: two channels of a 16-token group of the page at a time, which
+// become one 16-byte piece of each channel's row (single bytes where the run does not
+// cover the group, whose other tokens read as the run's nearest).
+template <class T>
+struct Group {
+    typename pair_of<T>::type w[16];
+};
+template <class T>
+__device__ __forceinline__ void append_values(const Run<T>& r) {
+    const int pairs = r.D / 2, g0 = r.off / 16, groups = (r.off + r.count - 1) / 16 - g0 + 1;
+    float amax = 0.0f;
+    in_two_passes<sizeof(T) == 2 ? 2 : 1>(
+        pairs * groups, r.me, r.team,
+        [&](int task) {
+            const int g = task / pairs, first = (g0 + g) * 16 - r.off;      // the group's first token, counted from the run's
+            Group<T> a;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                int t = first + i;
+                t = t < 0 ? 0 : t < r.count ? t : r.count - 1;
+                a.w[i] = ld<typename pair_of<T>::type>(r.x + int64_t(t) * r.step + 2 * (task - g * pairs));
+            }
+            return a;
+        },
+        [&](const Group<T>& a) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const v2f v = widen2(a.w[i]);
+                amax = fmaxf(amax, fmaxf(fabsf(v[0]), fabsf(v[1])));
+            }
+        },
+        [&](int task, const Group<T>& a, float f) {
+            const int g = task / pairs, first = (g0 + g) * 16 - r.off;
+            uint8_t* c = r.codes + 2 * (task - g * pairs) * r.page + (g0 + g) * 16;
+            u32x4 x, y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const v2f v0 = widen2(a.w[4 * i]) * f, v1 = widen2(a.w[4 * i + 1]) * f, v2 = widen2(a.w[4 * i + 2]) * f,
+                          v3 = widen2(a.w[4 * i + 3]) * f;
+                x[i] = cvt4(v0[0], v1[0], v2[0], v3[0]);
+                y[i] = cvt4(v0[1], v1[1], v2[1], v3[1]);
+            }
+            if (first >= 0 && first + 16 <= r.count) {
+                st<u32x4>(c, x);
+                st<u32x4>(c + r.page, y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (first + i >= 0 && first + i < r.count) {
+                        c[i] = uint8_t(x[i / 4] >> (8 * (i % 4)));
+                        c[r.page + i] = uint8_t(y[i / 4] >> (8 * (i % 4)));
+                    }
+            }
+        },
+        [&] { return new_scale<true>(r, amax); });
+}
+
+// One token, as in a decode step, by a wave: two channels a lane
+template <bool VALUES, class T>
+__device__ __forceinline__ void append_one(const Run<T>& r) {
+    const int lane = threadIdx.x & 63, pairs = r.D / 2;
+    typename pair_of<T>::type w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) w[i] = ld<typename pair_of<T>::type>(r.x + 2 * (lane + 64 * i < pairs ? lane + 64 * i : 0));
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(widen2(w[i])[0]), fabsf(widen2(w[i])[1])));
+    const float f = new_scale<VALUES>(r, amax);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (lane + 64 * i < pairs) {
+            const v2f v = widen2(w[i]) * f;
+            const uint32_t two = cvt4(v[0], v[1], 0.0f, 0.0f);
+            if constexpr (VALUES) {
+                uint8_t* c = r.codes + 2 * (lane + 64 * i) * r.page + r.off;
+                c[0] = uint8_t(two);
+                c[r.page] = uint8_t(two >> 8);
+            } else {
+                st<uint16_t>(r.codes + r.off * r.D + 2 * (lane + 64 * i), uint16_t(two));
+            }
+        }
+}
+
+// A workgroup looks at `window` (a divisor of 64) rows of one head, its keys or its values, and takes
+// the runs that begin in them: three and more a wave each, in turn, fewer the whole
+// workgroup one after another.  Bit j of a word says that the j-th row continues the run of the
+// row before it.
+template <class T>
+__global__ __launch_bounds__(kThreads, 4) void append(const AppendArgs p, int window) {
     __shared__ float part[kWaves];
-    __shared__ int first_off;
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y, page = 1 << p.page_log;
-    const int64_t slot = p.slots[t];
-    if (slot < 0 || slot >= p.n_slots) return;
-    const int off = int(slot & (page - 1));
-    if (off > 0 && t > 0 && p.slots[t - 1] == slot - 1) return;         // not its page's first new token
-    if (threadIdx.x == 0) first_off = page - off;
-    __syncthreads();
-    if (int(threadIdx.x) < page - off && (t + threadIdx.x >= p.T || p.slots[t + threadIdx.x] != slot + threadIdx.x))
-        atomicMin(&first_off, int(threadIdx.x));
-    __syncthreads();
-    const int run = first_off;
-    const int64_t id = slot >> p.page_log, at = id * p.H + h, tile = int64_t(page) * p.D;
-    if (blockIdx.z == 0)
-        append_run<T, false>(static_cast<const T*>(p.k) + t * p.ldk + h * p.D, p.ldk, run, off, page, p.D, p.kc + at * tile, p.ks + at, part);
-    else
-        append_run<T, true>(static_cast<const T*>(p.v) + t * p.ldv + h * p.D, p.ldv, run, off, page, p.D, p.vc + at * tile, p.vs + at, part);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = blockIdx.y, page = 1 << p.page_log;
+    const bool values = blockIdx.z != 0;
+    const int64_t row0 = int64_t(blockIdx.x) * window;
+    const auto slot_of = [&](int64_t t) { return t >= 0 && t < p.T ? p.slots[t] : -2; };
+    const int32_t mine = slot_of(row0 + lane), before = slot_of(row0 + lane - 1), next = slot_of(row0 + 64 + lane), last = slot_of(row0 + 63 + lane);
+    const auto continues = [&](int32_t a, int32_t b) { return b >= 0 && int64_t(a) + 1 == b && (b & (page - 1)) != 0; };
+    const uint64_t joins = __ballot(continues(before, mine)), joins2 = __ballot(continues(last, next));
+    uint64_t heads = __ballot(lane < window && mine >= 0 && mine < p.n_slots) & ~joins;
+    const bool together = __popcll(heads) < 3;
+    for (int turn = 0; heads; ++turn, heads &= heads - 1) {
+        if (!together && turn % kWaves != wave) continue;
+        const int first = __builtin_ctzll(heads), slot = __builtin_amdgcn_readlane(mine, first);
+        // the run ends before the first row that continues nothing
+        uint64_t stop = ~joins & (first < 63 ? ~uint64_t(0) << (first + 1) : 0);
+        int end = 64;
+        if (stop) {
+            end = __builtin_ctzll(stop);
+        } else if (joins2 != ~uint64_t(0)) {
+            end = 64 + __builtin_ctzll(~joins2);
+        } else {
+            for (end = 128;; end += 64) {            // a page holds 256 tokens at the most
+                stop = ~__ballot(continues(slot_of(row0 + end + lane - 1), slot_of(row0 + end + lane)));
+                if (stop) break;
+            }
+            end += __builtin_ctzll(stop);
+        }
+        const int64_t t = row0 + first, at = (int64_t(slot) >> p.page_log) * p.H + h, tile = int64_t(page) * p.D;
+        Run<T> r;
+        r.x = static_cast<const T*>(values ? p.v : p.k) + t * (values ? p.ldv : p.ldk) + h * p.D;
+        r.step = values ? p.ldv : p.ldk;
+        r.count = end - first;
+        r.off = slot & (page - 1);
+        r.page = page;
+        r.D = p.D;
+        r.codes = (values ? p.vc : p.kc) + at * tile;
+        r.scale = (values ? p.vs : p.ks) + at;
+        r.was = r.off > 0 ? *r.scale : 0.0f;
+        r.part = part;
+        r.team = together && r.count > 1 ? kThreads : 64;
+        r.me = together && r.count > 1 ? threadIdx.x : lane;
+        if (r.count == 1) {
+            if (together && turn % kWaves != wave) continue;
+            if (values) append_one<true>(r);
+            else append_one<false>(r);
+        } else {
+            if (values) append_values(r);
+            else append_keys(r);
+        }
+    }
 }
 
 }  // namespace kv_detail
@@ -410,8 +586,10 @@ hipError_t launch_rope(const RopeCall& c, hipStream_t stream) {
 hipError_t launch_kv_append(const KvAppendCall& c, hipStream_t stream) {
     using namespace kv_detail;
     const AppendArgs p{c.k, c.v, c.ldk, c.ldv, c.T, c.n_pages << c.page_log, int(c.H), int(c.D), c.page_log, c.slots, c.kc, c.vc, c.ks, c.vs};
-    const dim3 grid(unsigned(c.T), unsigned(c.H), 2);
-    return launch_kernel(c.bf16 ? append<uint16_t> : append<float>, grid, dim3(kThreads), stream, p);
+    // few rows: each may begin a run of its own; many: most continue one
+    const int window = c.T <= 2048 ? 4 : 64;
+    return launch_kernel(c.bf16 ? append<uint16_t> : append<float>, dim3(unsigned((c.T + window - 1) / window), unsigned(c.H), 2),
+                         dim3(kThreads), stream, p, window);
 }
 
 }  // namespace fp8fg
