@@ -10,6 +10,7 @@ implementation behind these names.  Outputs are allocated here with torch
 unless the caller passes them in (``out=``/``q=``/``s=``).
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -781,13 +782,15 @@ def kv_release_pages(done, lens, table, free_pages, n_free, page, out=None):
 
 def _heads(t, dtype, shape, name):
     """The distance of the rows of t [T][H][D], whose heads are contiguous."""
+    T, H, D = shape
+    if t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return H * D
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    T, H, D = shape
     ld, step, one = t.stride()
     if (D > 1 and one != 1) or (H > 1 and step != D) or (T > 1 and ld < H * D):
         raise ValueError(f"{name} must have contiguous heads")
@@ -819,14 +822,20 @@ def rope(q, k, positions, freqs, interleaved=False, scale=1.0, inverse=False, q_
     bf16 = _f32_or_bf16(q, "q")
     _need(positions, torch.int32, (T,), "positions")
     _need(freqs, torch.float32, (freqs.shape[0],), "freqs")
-    q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if q_out is None else q_out
-    ldqo = _heads(q_out, q.dtype, (T, Hq, D), "q_out")
+    ldqo = Hq * D
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        ldqo = _heads(q_out, q.dtype, (T, Hq, D), "q_out")
     Hkv = ldk = ldko = 0
     if k is not None:
         Hkv = k.shape[1]
         ldk = _heads(k, q.dtype, (T, Hkv, D), "k")
-        k_out = torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device) if k_out is None else k_out
-        ldko = _heads(k_out, q.dtype, (T, Hkv, D), "k_out")
+        ldko = Hkv * D
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        else:
+            ldko = _heads(k_out, q.dtype, (T, Hkv, D), "k_out")
     elif k_out is not None:
         raise ValueError("k_out needs k")
     _check("rope", load_library().rope(
@@ -858,6 +867,7 @@ def fp8_kv_append(k, v, slots, k_cache, k_scale, v_cache, v_scale):
         _ptr(v_cache), _ptr(v_scale), _stream(k)))
 
 
+@functools.lru_cache(maxsize=4096)
 def fp8_kv_attention_workspace(T, B, Hq, Hkv, D, page, width):
     """Bytes of workspace of a call of fp8_kv_attention with these sizes."""
     got = ctypes.c_int64(0)
@@ -879,15 +889,20 @@ def fp8_kv_attention(q, k_cache, k_scale, v_cache, v_scale, table, cu, lens, sca
     _need(table, torch.int32, (B, width), "table")
     _need(cu, torch.int32, (B + 1,), "cu")
     _need(lens, torch.int32, (B,), "lens")
-    out = _out(out, (T, Hq, D), torch.bfloat16, q, "out")
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _need(out, torch.bfloat16, (T, Hq, D), "out")
     if lse is not None:
         _need(lse, torch.float32, (T, Hq), "lse")
     if workspace is None:
-        workspace = _empty((fp8_kv_attention_workspace(T, B, Hq, Hkv, D, page, width),), torch.uint8, q)
+        need = fp8_kv_attention_workspace(T, B, Hq, Hkv, D, page, width)
+        workspace = q.new_empty(need, dtype=torch.uint8) if need else None
     else:
-        _need(workspace, torch.uint8, (workspace.numel(),), "workspace")
+        need = workspace.numel()
+        _need(workspace, torch.uint8, (need,), "workspace")
     _check("fp8_kv_attention", load_library().fp8_kv_attention(
         _ptr(q), ldq, _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), n, page, _ptr(table), width, _ptr(cu),
         _ptr(lens), B, T, Hq, Hkv, D, D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(workspace),
-        workspace.numel(), _stream(q)))
+        need, _stream(q)))
     return out if lse is None else (out, lse)

@@ -567,7 +567,7 @@ int kv_assign_pages(const int32_t* have, const int32_t* add, int64_t B, const in
     if (!aligned16(have) || !aligned16(add) || !aligned16(free_pages) || !aligned4(n_free) || !aligned16(table) || !aligned16(lens) ||
         !aligned16(cu) || !aligned16(positions) || !aligned16(slots) || !aligned16(left))
         return FP8FG_ERR_ALIGN;
-    if (F > kMaxDim || T > kMaxDim) return FP8FG_ERR_UNSUPPORTED;
+    if (F > kMaxDim || T >= int64_t(1) << 23) return FP8FG_ERR_UNSUPPORTED;
     return hip_status(fp8fg::launch_kv_assign(have, add, B, free_pages, n_free, F, page_log(page), table, width, T, lens, cu, positions,
                                               slots, left, static_cast<hipStream_t>(stream)));
 }

@@ -28,7 +28,9 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kTile = 64;                 // tokens of a tile
-constexpr int kMinTiles = kWaves;         // tiles that a split holds at the least: one per wave
+// Tiles that a split holds at the least, and tables that hold no more than kWhole tiles are not
+// split: 1024 tokens are four steps of each wave, and joining takes a second launch
+constexpr int kMinTiles = 8, kWhole = 16;
 constexpr int kSlots = 512;               // workgroups that run at a time: two on each of 256 CUs
 // Probabilities are held times 2^11, relative to a maximum that is raised only when
 // a score passes it by a factor of 2^4: at most 2^15, and FP16 keeps them normal
@@ -107,7 +109,7 @@ __device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
         for (int i = 0; i < R; ++i) work += float(tiles[i]) * float(kt[i]);
     }
     const float want = ceilf(lanes_sum<64>(work) * (1.0f + 0x1p-20f) / float(p.target));    // no less for FP32's roundings
-    const int per = want < float(kMinTiles) ? kMinTiles : want > 0x1p30f ? 1 << 30 : int(want);
+    const int per = !p.parts ? 1 << 30 : want < float(kMinTiles) ? kMinTiles : want > 0x1p30f ? 1 << 30 : int(want);
     // CLASSES: requests whose parts are long come first, in four classes by their share of the
     // longest (where all requests fit one chunk), so that what starts last is short.  Three chunks
     // of 2048 tokens on 1024 to 8192: 528 / 461 us without and with.  Parts of a decode step are
@@ -743,7 +745,7 @@ inline Plan plan_of(const AttendCall& c, int rows) {
     const int64_t rounds = (3 * all / 2 + kSlots - 1) / kSlots;
     r.target = int(((rounds > 1 ? rounds : 1) * kSlots - all / 2 + c.Hkv - 1) / c.Hkv);
     if (rows == kWideRows && all > kSlots / 4) r.target = 1;      // enough row tiles, and many rows to join
-    const bool split = kt > kMinTiles && r.target > 1;
+    const bool split = kt > kWhole && r.target > 1;
     // a tile has one item more than the work's share at the most, a split one twice as many
     // (the work is summed in FP32), and no more than its keys' whole splits
     const int64_t share = r.target + 1, most = split ? r.tiles * ((kt + kMinTiles - 1) / kMinTiles - 1) : 0;

@@ -627,7 +627,7 @@ int fp8_grouped_gemm_wgrad(const uint8_t* a, const float* sa, const uint8_t* b, 
  *   left: int32 [2], the pages that are left free (the first left[0] of free_pages) and
  *     the number that was missing (0 where every request got its pages).
  * `left` and `lens` may not overlap n_free and have.  B = 0 or T = 0 writes the outputs
- * that exist.
+ * that exist.  Requires T < 2^23.
  */
 int kv_assign_pages(const int32_t* have, const int32_t* add, int64_t B, const int32_t* free_pages, const int32_t* n_free,
                     int64_t F, int64_t page, int32_t* table, int64_t width, int64_t T, int32_t* lens, int32_t* cu,

@@ -32,7 +32,7 @@ def test_assign_refusals():
     assert assign(nf=ctypes.c_void_p(0x10002)) == EALIGN
     for bad in (dict(B=-1), dict(width=-1), dict(T=-1), dict(F=-1)):
         assert assign(**bad) == ESHAPE, bad
-    for bad in (dict(page=0), dict(page=8), dict(page=48), dict(page=512), dict(B=65537), dict(F=BIG), dict(T=BIG),
+    for bad in (dict(page=0), dict(page=8), dict(page=48), dict(page=512), dict(B=65537), dict(F=BIG), dict(T=1 << 23),
                 dict(B=65536, width=1 << 15), dict(width=1 << 25), dict(page=-16)):
         assert assign(**bad) == EUNSUP, bad
 
