@@ -197,6 +197,13 @@ __device__ __forceinline__ float groups_sum(float v) {
     return v + __shfl_xor(v, 32, 64);
 }
 
+// max over the two halves of the wave
+__device__ __forceinline__ float halves_max(float v) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    const uint32_t a = s[0], b = s[1];
+    return fmaxf(__uint_as_float(a), __uint_as_float(b));
+}
+
 // the bytes of w (tokens first .. first + 3) that lie before `end`
 __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int first, int end) {
     const int n = end - first;
@@ -322,16 +329,13 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
         }
         if (!kAhead) load_values();
         // O is held in units of `ref`, the largest of the four pages' value scales, but no
-        // less than 2^-40 of the largest so far: FP32 holds the sums in such units
+        // less than 2^-40 of the largest so far (FP32 holds the sums in such units) and 2^-100
         const float top = groups_max(vsc);
         largest = fmaxf(largest, top);
-        const float unit = fmaxf(top, largest * 0x1p-40f);
-        float moved = 1.0f;
-        if (unit != ref) {
-            moved = ref / unit;
-            ref = unit;
-        }
-        const float ratio = ref > 0.0f ? vsc / ref : 0.0f;
+        const float unit = fmaxf(fmaxf(top, largest * 0x1p-40f), 0x1p-100f), inverse = __builtin_amdgcn_rcpf(unit);
+        const float moved = unit == ref ? 1.0f : ref * inverse;
+        ref = unit;
+        const float ratio = vsc * inverse;
         // scores in units of log2; keys out of sight at -inf
         const bool masked = t0 + kTile - 1 > least || !__all(good);
         v8h pf[NR][2];
@@ -482,7 +486,6 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
     const int kt = most < 0 ? 0 : most / kTile + 1;
     const int per = (kt + it.splits - 1) / it.splits, kt0 = it.split * per, kt1 = kt0 + per < kt ? kt0 + per : kt;
     const int32_t* table = p.table + int64_t(it.b) * p.width;
-    const int64_t page_bytes = int64_t(D) << p.page_log;
     const int mask = (1 << p.page_log) - 1;
 
     v8bf qf[D / 16];
@@ -506,18 +509,20 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
         const int token = tile * kTile + 16 * quad;
         return token < it.len ? table[token >> p.page_log] : -1;
     };
-    const auto exists = [&](int32_t id) { return id >= 0 && id < p.n_pages; };
+    const uint32_t n_pages = uint32_t(p.n_pages), tile_bytes = uint32_t(D) << p.page_log;       // n_pages * Hkv < 2^30
+    const auto exists = [&](int32_t id) { return uint32_t(id) < n_pages; };
+    const uint32_t value_row = threadIdx.x / 4;
     u32x4 kraw[KC], vraw[KC];
     float kscale, vscale;
     const auto fetch = [&](int tile, int32_t id) {
         const int32_t kid = __builtin_amdgcn_readlane(id, wave);
-        const uint8_t* kp = p.kc + (int64_t(exists(kid) ? kid : 0) * p.Hkv + kvh) * page_bytes + ((tile * kTile + 16 * wave) & mask) * D;
-        const int64_t at = int64_t(exists(id) ? id : 0) * p.Hkv + kvh;
-        const uint8_t* vp = p.vc + at * page_bytes + ((tile * kTile + 16 * quad) & mask);
+        const uint32_t k_at = (exists(kid) ? kid : 0) * uint32_t(p.Hkv) + kvh, at = (exists(id) ? id : 0) * uint32_t(p.Hkv) + kvh;
+        const uint8_t* kp = p.kc + uint64_t(k_at) * tile_bytes + uint32_t(((tile * kTile + 16 * wave) & mask) * D);
+        const uint8_t* vp = p.vc + (uint64_t(at) * tile_bytes + (uint32_t((tile * kTile + 16 * quad) & mask) + (value_row << p.page_log)));
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
-            kraw[i] = ld<u32x4>(kp + (lane + 64 * i) * 16);
-            vraw[i] = ld<u32x4>(vp + (int64_t(threadIdx.x / 4 + 64 * i) << p.page_log));
+            kraw[i] = ld<u32x4>(kp + uint32_t((lane + 64 * i) * 16));
+            vraw[i] = ld<u32x4>(vp + (uint32_t(64 * i) << p.page_log));
         }
         kscale = p.ks[at];
         vscale = p.vs[at];
@@ -574,12 +579,20 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
             vsc[t] = scales[buf][1][2 * t + h];
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                const v8bf k = ld<v8bf>(&keys[buf][key_at(32 * t + col, 2 * c + h)]);
-                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[c], s[t], 0, 0, 0);
-            }
         }
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ld<v8bf>(&keys[buf][key_at(32 * t + col, 2 * c + h)]), qf[c], s[t], 0, 0, 0);
+        // six keys' pieces ahead of the products: 425 -> 418 us for three chunks of 2048 tokens
+        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+        for (int c = 0; c < D / 8 - 6; ++c) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 6, 0);
         if (t0 + kTile - 1 > least || !__all(vsc[0] >= 0.0f && vsc[1] >= 0.0f)) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -597,32 +610,32 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
             for (int i = 1; i < 16; ++i) top = fmaxf(top, s[t][i]);
             mt = fmaxf(mt, top * ksc[t]);
         }
-        mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+        mt = halves_max(mt);
         const float m_new = mt > m + kSlack ? mt : m, m_use = m_new == -__builtin_inff() ? 0.0f : m_new;
         const float alpha = __builtin_amdgcn_exp2f(m - m_use);
         m = m_new;
-        float top = fmaxf(vsc[0], vsc[1]);
-        top = fmaxf(0.0f, fmaxf(top, __shfl_xor(top, 32, 64)));
+        const float top = halves_max(fmaxf(0.0f, fmaxf(vsc[0], vsc[1])));
         largest = fmaxf(largest, top);
-        const float unit = fmaxf(top, largest * 0x1p-40f);
-        float factor = alpha;
-        if (unit != ref) {
-            factor *= ref / unit;
-            ref = unit;
-        }
-        float sum = 0.0f;
+        const float unit = fmaxf(fmaxf(top, largest * 0x1p-40f), 0x1p-100f);
+        const float factor = unit == ref ? alpha : alpha * (ref * __builtin_amdgcn_rcpf(unit));
+        ref = unit;
+        // Probabilities are formed times their page's value scale over `ref`, as a term of the
+        // exponent (below 2^-60 FP16 has nothing left of them), and summed without it.
         v8h pf[2][2];
+        l *= alpha;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const float ratio = ref > 0.0f ? fmaxf(vsc[t], 0.0f) / ref : 0.0f;
+            const float ratio = fmaxf(vsc[t] * __builtin_amdgcn_rcpf(ref), 0x1p-60f);
+            const float bias = kPBias - m_use + __builtin_amdgcn_logf(ratio);
+            float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], ksc[t], kPBias - m_use));
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], ksc[t], bias));
                 sum += e;
-                pf[t][i >> 3][i & 7] = _Float16(e * ratio);
+                pf[t][i >> 3][i & 7] = _Float16(e);
             }
+            l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(ratio), l);
         }
-        l = __builtin_fmaf(l, alpha, sum);
         if (!__all(factor == 1.0f)) {
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[d] *= factor;
