@@ -204,6 +204,14 @@ __device__ __forceinline__ float halves_max(float v) {
     return fmaxf(__uint_as_float(a), __uint_as_float(b));
 }
 
+// O is held in units of `ref`: the largest of the tile's value scales, while that lies
+// within [ref / 64, ref] the one before, so that the sums are seldom multiplied; but no
+// less than 2^-40 of the largest so far (FP32 holds the sums in such units) and 2^-100
+__device__ __forceinline__ float unit_of(float top, float largest, float ref) {
+    const float want = fmaxf(fmaxf(top, largest * 0x1p-40f), 0x1p-100f);
+    return want > ref || want < ref * 0x1p-6f ? want : ref;
+}
+
 // the bytes of w (tokens first .. first + 3) that lie before `end`
 __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int first, int end) {
     const int n = end - first;
@@ -328,11 +336,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
             }
         }
         if (!kAhead) load_values();
-        // O is held in units of `ref`, the largest of the four pages' value scales, but no
-        // less than 2^-40 of the largest so far (FP32 holds the sums in such units) and 2^-100
         const float top = groups_max(vsc);
         largest = fmaxf(largest, top);
-        const float unit = fmaxf(fmaxf(top, largest * 0x1p-40f), 0x1p-100f), inverse = __builtin_amdgcn_rcpf(unit);
+        const float unit = unit_of(top, largest, ref), inverse = __builtin_amdgcn_rcpf(unit);
         const float moved = unit == ref ? 1.0f : ref * inverse;
         ref = unit;
         const float ratio = vsc * inverse;
@@ -616,7 +622,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
         m = m_new;
         const float top = halves_max(fmaxf(0.0f, fmaxf(vsc[0], vsc[1])));
         largest = fmaxf(largest, top);
-        const float unit = fmaxf(fmaxf(top, largest * 0x1p-40f), 0x1p-100f);
+        const float unit = unit_of(top, largest, ref);
         const float factor = unit == ref ? alpha : alpha * (ref * __builtin_amdgcn_rcpf(unit));
         ref = unit;
         // Probabilities are formed times their page's value scale over `ref`, as a term of the

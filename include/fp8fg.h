@@ -699,10 +699,11 @@ int fp8_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int x_
  * seen.  A token that sees nothing gets 0, and -inf for lse.
  * What lies in the cache past a request's last token has no influence.
  * Scales may be any finite non-negative FP32 values.
- * Accuracy: codes are multiplied exactly and summed in FP32, probabilities are
- * rounded to FP16's 11 bits:  |out - out*| <= 2^-10 * sum_j p_j |v_j| + 2^-50 max |v| + 2^-100 before
- * the one rounding to BF16, where the scores are below 2^6 (larger scores: their FP32
- * rounding, 2^-22 |x|, is the relative error of p).
+ * Accuracy: codes are multiplied exactly and summed in FP32; probabilities are
+ * rounded to FP16's 11 bits, and where they are below 2^-18 of the row's largest, p_max, to 2^-29
+ * of it:  |out - out*| <= 2^-10 * sum_j p_j |v_j| + 2^-28 * p_max * n * max_j |v_j| + 2^-100
+ * over the n keys seen, before the one rounding to BF16, for scores below 2^6 (larger ones: their
+ * FP32 rounding, 2^-22 |x|, is the relative error of p).
  * workspace: fp8_kv_attention_workspace bytes (may be 0, then NULL), contents unspecified before
  * and after; calls that may run at the same time need one each.
  * Requires Hq % Hkv == 0, 0 <= scale <= 2^64, rows of q at least Hq * D elements and
