@@ -725,6 +725,43 @@ def fp8_grouped_gemm_wgrad(a, sa, b, sb, group_offsets, out=None, accumulate=Fal
 
 # Attention over a key/value cache held in 8 bits, in pages.
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+
+
+def _run(fn, index, like, *args):
+    """The call fn on the device `index` of like and its current stream."""
+    call = getattr(load_library(), fn)
+    if index == _current_device():
+        status = call(*args, _stream(like))
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, _stream(like))
+    if status != 0:
+        raise Fp8fgError(fn, status)
+
+
+def _device_of(t, name):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return index
+
+
+def _need_at(index, t, dtype, shape, name):
+    """_need, and that t lies on the device `index`."""
+    if t.get_device() == index and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return
+    _need(t, dtype, shape, name)
+    raise ValueError(f"{name} must be on device {index}, got {t.device}")
+
+
+def _out_at(index, t, shape, dtype, like, name):
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    _need_at(index, t, dtype, shape, name)
+    return t
+
+
 def kv_cache(n_pages, heads, page, dim, device="cuda"):
     """An empty cache of one layer: (k_cache u8 [n_pages][heads][page][dim], k_scale f32
     [n_pages][heads], v_cache u8 [n_pages][heads][dim][page], v_scale f32 [n_pages][heads])."""
@@ -743,20 +780,21 @@ def kv_assign_pages(have, add, table, free_pages, n_free, page, T, out=None):
     [2]: pages left free, pages missing).  out: the five buffers to write."""
     B, width = table.shape
     F = free_pages.shape[0]
-    _need(table, torch.int32, (B, width), "table")
-    _need(have, torch.int32, (B,), "have")
-    _need(add, torch.int32, (B,), "add")
-    _need(free_pages, torch.int32, (F,), "free_pages")
-    _need(n_free, torch.int32, (1,), "n_free")
+    at = _device_of(table, "table")
+    _need_at(at, table, torch.int32, (B, width), "table")
+    _need_at(at, have, torch.int32, (B,), "have")
+    _need_at(at, add, torch.int32, (B,), "add")
+    _need_at(at, free_pages, torch.int32, (F,), "free_pages")
+    _need_at(at, n_free, torch.int32, (1,), "n_free")
     lens, cu, positions, slots, left = (None,) * 5 if out is None else out
-    lens = _out(lens, (B,), torch.int32, table, "lens")
-    cu = _out(cu, (B + 1,), torch.int32, table, "cu")
-    positions = _out(positions, (T,), torch.int32, table, "positions")
-    slots = _out(slots, (T,), torch.int32, table, "slots")
-    left = _out(left, (2,), torch.int32, table, "left")
-    _check("kv_assign_pages", load_library().kv_assign_pages(
-        _ptr(have), _ptr(add), B, _ptr(free_pages), _ptr(n_free), F, page, _ptr(table), width, T, _ptr(lens), _ptr(cu),
-        _ptr(positions), _ptr(slots), _ptr(left), _stream(table)))
+    lens = _out_at(at, lens, (B,), torch.int32, table, "lens")
+    cu = _out_at(at, cu, (B + 1,), torch.int32, table, "cu")
+    positions = _out_at(at, positions, (T,), torch.int32, table, "positions")
+    slots = _out_at(at, slots, (T,), torch.int32, table, "slots")
+    left = _out_at(at, left, (2,), torch.int32, table, "left")
+    _run("kv_assign_pages", at, table,
+         _ptr(have), _ptr(add), B, _ptr(free_pages), _ptr(n_free), F, page, _ptr(table), width, T, _ptr(lens), _ptr(cu),
+         _ptr(positions), _ptr(slots), _ptr(left))
     return lens, cu, positions, slots, left
 
 
@@ -766,27 +804,25 @@ def kv_release_pages(done, lens, table, free_pages, n_free, page, out=None):
     the pages that are free now).  out: the two buffers to write."""
     B, width = table.shape
     F = free_pages.shape[0]
-    _need(table, torch.int32, (B, width), "table")
-    _need(done, torch.int32, (B,), "done")
-    _need(lens, torch.int32, (B,), "lens")
-    _need(free_pages, torch.int32, (F,), "free_pages")
-    _need(n_free, torch.int32, (1,), "n_free")
+    at = _device_of(table, "table")
+    _need_at(at, table, torch.int32, (B, width), "table")
+    _need_at(at, done, torch.int32, (B,), "done")
+    _need_at(at, lens, torch.int32, (B,), "lens")
+    _need_at(at, free_pages, torch.int32, (F,), "free_pages")
+    _need_at(at, n_free, torch.int32, (1,), "n_free")
     lens_out, left = (None, None) if out is None else out
-    lens_out = _out(lens_out, (B,), torch.int32, table, "lens")
-    left = _out(left, (1,), torch.int32, table, "left")
-    _check("kv_release_pages", load_library().kv_release_pages(
-        _ptr(done), _ptr(lens), _ptr(table), B, width, page, _ptr(free_pages), F, _ptr(n_free), _ptr(lens_out), _ptr(left),
-        _stream(table)))
+    lens_out = _out_at(at, lens_out, (B,), torch.int32, table, "lens")
+    left = _out_at(at, left, (1,), torch.int32, table, "left")
+    _run("kv_release_pages", at, table,
+         _ptr(done), _ptr(lens), _ptr(table), B, width, page, _ptr(free_pages), F, _ptr(n_free), _ptr(lens_out), _ptr(left))
     return lens_out, left
 
 
-def _heads(t, dtype, shape, name):
+def _heads(index, t, dtype, shape, name):
     """The distance of the rows of t [T][H][D], whose heads are contiguous."""
     T, H, D = shape
-    if t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
-        return H * D
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on device {index}, got {t.device}" if t.is_cuda else f"{name} must be a GPU tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -818,39 +854,42 @@ def rope(q, k, positions, freqs, interleaved=False, scale=1.0, inverse=False, q_
     rot on are copied; rows with a negative position are not written.  inverse=True: the
     gradient of q and k from that of the outputs.  q_out=q, k_out=k turns in place."""
     T, Hq, D = q.shape
-    ldq = _heads(q, q.dtype, (T, Hq, D), "q")
+    at = _device_of(q, "q")
+    ldq = _heads(at, q, q.dtype, (T, Hq, D), "q")
     bf16 = _f32_or_bf16(q, "q")
-    _need(positions, torch.int32, (T,), "positions")
-    _need(freqs, torch.float32, (freqs.shape[0],), "freqs")
+    _need_at(at, positions, torch.int32, (T,), "positions")
+    _need_at(at, freqs, torch.float32, (freqs.shape[0],), "freqs")
     ldqo = Hq * D
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
-        ldqo = _heads(q_out, q.dtype, (T, Hq, D), "q_out")
+        ldqo = _heads(at, q_out, q.dtype, (T, Hq, D), "q_out")
     Hkv = ldk = ldko = 0
     if k is not None:
         Hkv = k.shape[1]
-        ldk = _heads(k, q.dtype, (T, Hkv, D), "k")
+        ldk = _heads(at, k, q.dtype, (T, Hkv, D), "k")
         ldko = Hkv * D
         if k_out is None:
             k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         else:
-            ldko = _heads(k_out, q.dtype, (T, Hkv, D), "k_out")
+            ldko = _heads(at, k_out, q.dtype, (T, Hkv, D), "k_out")
     elif k_out is not None:
         raise ValueError("k_out needs k")
-    _check("rope", load_library().rope(
-        _ptr(q), ldq, _ptr(q_out), ldqo, Hq, _ptr(k), ldk, _ptr(k_out), ldko, Hkv, bf16, _ptr(positions), _ptr(freqs), T, D,
-        2 * freqs.shape[0], int(bool(interleaved)), scale, int(bool(inverse)), _stream(q)))
+    _run("rope", at, q,
+         _ptr(q), ldq, _ptr(q_out), ldqo, Hq, _ptr(k), ldk, _ptr(k_out), ldko, Hkv, bf16, _ptr(positions), _ptr(freqs), T, D,
+         2 * freqs.shape[0], int(bool(interleaved)), scale, int(bool(inverse)))
     return q_out, k_out
 
 
 def _need_cache(k_cache, k_scale, v_cache, v_scale):
+    """The cache's device and sizes, once its tensors fit together."""
     n, H, page, D = k_cache.shape
-    _need(k_cache, torch.uint8, (n, H, page, D), "k_cache")
-    _need(v_cache, torch.uint8, (n, H, D, page), "v_cache")
-    _need(k_scale, torch.float32, (n, H), "k_scale")
-    _need(v_scale, torch.float32, (n, H), "v_scale")
-    return n, H, page, D
+    at = _device_of(k_cache, "k_cache")
+    _need_at(at, k_cache, torch.uint8, (n, H, page, D), "k_cache")
+    _need_at(at, v_cache, torch.uint8, (n, H, D, page), "v_cache")
+    _need_at(at, k_scale, torch.float32, (n, H), "k_scale")
+    _need_at(at, v_scale, torch.float32, (n, H), "v_scale")
+    return at, n, H, page, D
 
 
 def fp8_kv_append(k, v, slots, k_cache, k_scale, v_cache, v_scale):
@@ -858,13 +897,13 @@ def fp8_kv_append(k, v, slots, k_cache, k_scale, v_cache, v_scale):
     slots int32 [T] of the cache (see kv_cache), in place: E4M3 codes under one power of
     two per page and head.  Rows with a slot outside the cache are skipped; the rows of
     a page are consecutive, with consecutive slots."""
-    n, H, page, D = _need_cache(k_cache, k_scale, v_cache, v_scale)
+    at, n, H, page, D = _need_cache(k_cache, k_scale, v_cache, v_scale)
     T = k.shape[0]
-    ldk, ldv = _heads(k, k.dtype, (T, H, D), "k"), _heads(v, k.dtype, (T, H, D), "v")
-    _need(slots, torch.int32, (T,), "slots")
-    _check("fp8_kv_append", load_library().fp8_kv_append(
-        _ptr(k), ldk, _ptr(v), ldv, _f32_or_bf16(k, "k"), _ptr(slots), T, H, D, page, n, _ptr(k_cache), _ptr(k_scale),
-        _ptr(v_cache), _ptr(v_scale), _stream(k)))
+    ldk, ldv = _heads(at, k, k.dtype, (T, H, D), "k"), _heads(at, v, k.dtype, (T, H, D), "v")
+    _need_at(at, slots, torch.int32, (T,), "slots")
+    _run("fp8_kv_append", at, k,
+         _ptr(k), ldk, _ptr(v), ldv, _f32_or_bf16(k, "k"), _ptr(slots), T, H, D, page, n, _ptr(k_cache), _ptr(k_scale),
+         _ptr(v_cache), _ptr(v_scale))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -882,27 +921,26 @@ def fp8_kv_attention(q, k_cache, k_scale, v_cache, v_scale, table, cu, lens, sca
     scale defaults to D^-0.5.  Returns out bf16 [T][Hq][D], or (out, lse) where lse f32 [T][Hq] is given to be
     written.  Rows from cu[B] on are not written.  workspace: a uint8 tensor of at least
     fp8_kv_attention_workspace bytes, used by one call at a time."""
-    n, Hkv, page, D = _need_cache(k_cache, k_scale, v_cache, v_scale)
+    at, n, Hkv, page, D = _need_cache(k_cache, k_scale, v_cache, v_scale)
     T, Hq, _ = q.shape
     B, width = table.shape
-    ldq = _heads(q, torch.bfloat16, (T, Hq, D), "q")
-    _need(table, torch.int32, (B, width), "table")
-    _need(cu, torch.int32, (B + 1,), "cu")
-    _need(lens, torch.int32, (B,), "lens")
+    ldq = _heads(at, q, torch.bfloat16, (T, Hq, D), "q")
+    _need_at(at, table, torch.int32, (B, width), "table")
+    _need_at(at, cu, torch.int32, (B + 1,), "cu")
+    _need_at(at, lens, torch.int32, (B,), "lens")
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
-        _need(out, torch.bfloat16, (T, Hq, D), "out")
+        _need_at(at, out, torch.bfloat16, (T, Hq, D), "out")
     if lse is not None:
-        _need(lse, torch.float32, (T, Hq), "lse")
+        _need_at(at, lse, torch.float32, (T, Hq), "lse")
     if workspace is None:
         need = fp8_kv_attention_workspace(T, B, Hq, Hkv, D, page, width)
         workspace = q.new_empty(need, dtype=torch.uint8) if need else None
     else:
         need = workspace.numel()
-        _need(workspace, torch.uint8, (need,), "workspace")
-    _check("fp8_kv_attention", load_library().fp8_kv_attention(
-        _ptr(q), ldq, _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), n, page, _ptr(table), width, _ptr(cu),
-        _ptr(lens), B, T, Hq, Hkv, D, D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(workspace),
-        need, _stream(q)))
+        _need_at(at, workspace, torch.uint8, (need,), "workspace")
+    _run("fp8_kv_attention", at, q,
+         _ptr(q), ldq, _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), n, page, _ptr(table), width, _ptr(cu),
+         _ptr(lens), B, T, Hq, Hkv, D, D ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(workspace), need)
     return out if lse is None else (out, lse)

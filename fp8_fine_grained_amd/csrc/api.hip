@@ -639,7 +639,8 @@ static int attend_args(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
     if (T < 0 || Hq < 0 || Hkv < 0 || (Hkv == 0 ? Hq != 0 : Hq % Hkv != 0)) return FP8FG_ERR_SHAPE;
     if (const int e = table_args(B, width, page)) return e;
     if (const int e = cache_args(0, Hkv, page, D)) return e;
-    if (Hq > 65535 || T > kMaxDim || (Hq > 0 && T > kMaxElems / (Hq * D))) return FP8FG_ERR_UNSUPPORTED;
+    // query rows of a key/value head
+    if (Hq > 65535 || T > kMaxDim || (Hkv > 0 && T * (Hq / Hkv) >= int64_t(1) << 24)) return FP8FG_ERR_UNSUPPORTED;
     c.T = T;
     c.B = B;
     c.Hq = Hq;

@@ -118,8 +118,12 @@ __device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
     const auto divide = [&] {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            splits[i] = kt[i] > per ? (kt[i] + per - 1) / per : 1;
-            size[i] = splits[i] > 1 ? (kt[i] + splits[i] - 1) / splits[i] : kt[i];
+            splits[i] = 1;
+            size[i] = kt[i];
+            if (p.parts) {                // (a division costs tens of instructions)
+                splits[i] = kt[i] > per ? (kt[i] + per - 1) / per : 1;
+                if (CLASSES) size[i] = splits[i] > 1 ? (kt[i] + splits[i] - 1) / splits[i] : kt[i];
+            }
             longest = size[i] > longest && tiles[i] > 0 ? size[i] : longest;
         }
     };
@@ -147,22 +151,22 @@ __device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
             const uint64_t who = __ballot(at >= 0 && at < items);
             if (who) {
                 int part = parts0 + p1 - parts;
-                Item mine{};
+                Item mine{};              // tile: the item's place among its request's
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    if (at >= 0 && at < here[i]) {
-                        const int tile = at / splits[i];
-                        mine = Item{int32_t(b0) + lane * R + i, cu[i], n[i], len[i], tile, at - tile * splits[i], splits[i],
-                                    splits[i] > 1 ? part + tile * splits[i] : 0};
-                    }
+                    if (at >= 0 && at < here[i]) mine = Item{int32_t(b0) + lane * R + i, cu[i], n[i], len[i], at, 0, splits[i], part};
                     at -= here[i];
                     part += splits[i] > 1 ? here[i] : 0;
                 }
                 const int src = __builtin_ctzll(who);
-                it = Item{__builtin_amdgcn_readlane(mine.b, src), __builtin_amdgcn_readlane(mine.cu, src), __builtin_amdgcn_readlane(mine.n, src),
-                          __builtin_amdgcn_readlane(mine.len, src), __builtin_amdgcn_readlane(mine.tile, src),
-                          __builtin_amdgcn_readlane(mine.split, src), __builtin_amdgcn_readlane(mine.splits, src),
-                          __builtin_amdgcn_readlane(mine.part, src)};
+                const auto get = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
+                it = Item{get(mine.b), get(mine.cu), get(mine.n), get(mine.len), get(mine.tile), 0, get(mine.splits), get(mine.part)};
+                if (it.splits > 1) {
+                    const int tile = it.tile / it.splits;
+                    it.split = it.tile - tile * it.splits;
+                    it.part += tile * it.splits;
+                    it.tile = tile;
+                }
                 return it.splits == 1 || it.part + it.splits <= p.most_parts;
             }
             items0 += lane63(i1);
@@ -171,6 +175,16 @@ __device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
     }
     return false;
 }
+
+// Token and query head of a row tile's rows: one division for the tile, the rest by a
+// reciprocal in FP32 (exact for quotients' operands below 2^21: they are at most G + 128)
+struct Rows {
+    int token, rest, G;
+    float inverse;
+    __device__ __forceinline__ Rows(int first, int G_) : token(first / G_), rest(first - token * G_), G(G_), inverse(1.0f / float(G_)) {}
+    __device__ __forceinline__ int token_of(int r) const { return token + int((float(rest + r) + 0.5f) * inverse); }
+    __device__ __forceinline__ int head_of(int r, int t) const { return rest + r - (t - token) * G; }
+};
 
 template <bool HI>
 __device__ __forceinline__ uint32_t to_bf16(uint32_t w) {
@@ -232,18 +246,17 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
     const int before = it.len - it.n;
     const auto sees = [&](int t) { return t < it.n ? (before + t < it.len ? before + t : it.len - 1) : -1; };
     // this lane's query rows, and the last key that each sees
+    const Rows rows(it.tile * ROWS, p.G);
     int tq[NR], hq[NR], last[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-        const int row = it.tile * ROWS + 16 * r + col;
-        tq[r] = row / p.G;
-        hq[r] = kvh * p.G + (row - tq[r] * p.G);
+        tq[r] = rows.token_of(16 * r + col);
+        hq[r] = kvh * p.G + rows.head_of(16 * r + col, tq[r]);
         last[r] = sees(tq[r]);
     }
-    const int first_tq = it.tile * ROWS / p.G, end_tq = (it.tile * ROWS + ROWS - 1) / p.G;
-    const int least = sees(first_tq), most = sees(end_tq < it.n ? end_tq : it.n - 1);
+    const int end_tq = rows.token_of(ROWS - 1), least = sees(rows.token), most = sees(end_tq < it.n ? end_tq : it.n - 1);
     const int kt = most < 0 ? 0 : most / kTile + 1;
-    const int per = (kt + it.splits - 1) / it.splits, kt0 = it.split * per, kt1 = kt0 + per < kt ? kt0 + per : kt;
+    const int per = it.splits > 1 ? (kt + it.splits - 1) / it.splits : kt, kt0 = it.split * per, kt1 = kt0 + per < kt ? kt0 + per : kt;
     const int32_t* table = p.table + int64_t(it.b) * p.width;
     const int64_t page_bytes = int64_t(D) << p.page_log;
 
@@ -447,7 +460,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
     __syncthreads();
     for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
         const int r = i / (D / 4), c = i - r * (D / 4);
-        const int rr = it.tile * ROWS + r, t = rr / p.G;
+        const int t = rows.token_of(r);
         if (t >= it.n) continue;
         v4f v = ld<v4f>(&joined[0][r * D + ((c ^ (r & 15)) * 4)]);
 #pragma unroll
@@ -460,7 +473,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
         joint(r, M, L);
         const float inv = L > 0.0f ? 1.0f / L : 0.0f;
         const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-        store_n<4>(p.out + (int64_t(it.cu + t) * p.Hq + kvh * p.G + (rr - t * p.G)) * D + 4 * c, out);
+        store_n<4>(p.out + (int64_t(it.cu + t) * p.Hq + kvh * p.G + rows.head_of(r, t)) * D + 4 * c, out);
     }
 }
 
@@ -485,12 +498,13 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, h = lane >> 5, quad = threadIdx.x & 3;
     const int before = it.len - it.n;
     const auto sees = [&](int t) { return t < it.n ? (before + t < it.len ? before + t : it.len - 1) : -1; };
-    const int row = it.tile * ROWS + 32 * wave + col, tq = row / p.G, hq = kvh * p.G + (row - tq * p.G), last = sees(tq);
+    const Rows rows(it.tile * ROWS, p.G);
+    const int tq = rows.token_of(32 * wave + col), hq = kvh * p.G + rows.head_of(32 * wave + col, tq), last = sees(tq);
     const bool live = tq < it.n;
-    const int end_tq = (it.tile * ROWS + ROWS - 1) / p.G;
-    const int least = sees((it.tile * ROWS + 32 * wave) / p.G), most = sees(end_tq < it.n ? end_tq : it.n - 1);
+    const int end_tq = rows.token_of(ROWS - 1);
+    const int least = sees(rows.token_of(32 * wave)), most = sees(end_tq < it.n ? end_tq : it.n - 1);
     const int kt = most < 0 ? 0 : most / kTile + 1;
-    const int per = (kt + it.splits - 1) / it.splits, kt0 = it.split * per, kt1 = kt0 + per < kt ? kt0 + per : kt;
+    const int per = it.splits > 1 ? (kt + it.splits - 1) / it.splits : kt, kt0 = it.split * per, kt1 = kt0 + per < kt ? kt0 + per : kt;
     const int32_t* table = p.table + int64_t(it.b) * p.width;
     const int mask = (1 << p.page_log) - 1;
 
@@ -512,8 +526,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
     // come by quads of lanes, four groups of a channel side by side.
     // (What is loaded here is looked at only when it is used: a comparison would wait for it.)
     const auto page_of = [&](int tile) {
-        const int token = tile * kTile + 16 * quad;
-        return token < it.len ? table[token >> p.page_log] : -1;
+        const uint32_t token = uint32_t(tile) * kTile + 16 * quad;          // (two tiles past the end, near 2^31)
+        return token < uint32_t(it.len) ? table[token >> p.page_log] : -1;
     };
     const uint32_t n_pages = uint32_t(p.n_pages), tile_bytes = uint32_t(D) << p.page_log;       // n_pages * Hkv < 2^30
     const auto exists = [&](int32_t id) { return uint32_t(id) < n_pages; };
@@ -816,6 +830,10 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
     using namespace attend_detail;
     const int rows = rows_of(c);
     const Plan plan = plan_of(c, rows);
+    // both launches' grids, before the first
+    if (!grid_fits(rows == kWideRows ? plan.items * c.Hkv : plan.items, kThreads) ||
+        (plan.bytes && !grid_fits(c.T * (c.Hq / c.Hkv), kThreads)))
+        return hipErrorInvalidConfiguration;
     Args p{c.q, c.kc, c.vc, c.ks, c.vs, c.table, c.cu, c.lens, c.ldq, c.n_pages, c.width, c.B, c.T, int(c.Hq), int(c.Hkv), int(c.Hq / c.Hkv),
            c.page_log, c.scale * 1.4426950408889634f, c.out, c.lse, nullptr, nullptr, plan.parts, plan.target};
     if (plan.bytes) {

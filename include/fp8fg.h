@@ -706,7 +706,7 @@ int fp8_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int x_
  * FP32 rounding, 2^-22 |x|, is the relative error of p).
  * workspace: fp8_kv_attention_workspace bytes (may be 0, then NULL), contents unspecified before
  * and after; calls that may run at the same time need one each.
- * Requires Hq % Hkv == 0, 0 <= scale <= 2^64, rows of q at least Hq * D elements and
+ * Requires Hq % Hkv == 0, T * (Hq / Hkv) < 2^24, 0 <= scale <= 2^64, rows of q at least Hq * D elements and
  * a multiple of 16 bytes apart, n_pages >= 1 where there is work.
  */
 int fp8_kv_attention_workspace(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t width, int64_t* bytes);

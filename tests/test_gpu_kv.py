@@ -499,3 +499,62 @@ def test_on_another_stream_and_two_at_once():
                 got[i].append(fp8.fp8_kv_attention(*gpu[i]))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[i]) for i in range(2) for o in got[i])
+
+
+@pytest.mark.parametrize("G,add,long", [(1, 1, 0), (3, 1, 3000), (2, 40, 0), (40, 2, 0)])
+def test_many_requests(G, add, long):
+    """More requests than a wave looks at together, most of them short, one long one among them: each kernel."""
+    rng = np.random.default_rng(G)
+    B = 270 if add == 1 else 262
+    held_ = list(rng.integers(0, 40, B))
+    new = [add if i % 5 else 0 for i in range(B)] if add == 1 else [1 + i % add if i % 7 else 0 for i in range(B)]
+    if long:
+        held_[200] = long
+    attention_check(attention_case(rng, held_, new, G, 1, 64, 16, pad=3))
+
+
+def test_offsets_past_32_bits():
+    """Pages far into a cache of more than 4 GB: writes and reads land where the small cache's do."""
+    H, page, D, n = 4, 256, 256, 17000
+    g = torch.Generator(device=DEV).manual_seed(3)
+    big = (torch.empty(n, H, page, D, dtype=torch.uint8, device=DEV), torch.empty(n, H, device=DEV),
+           torch.empty(n, H, D, page, dtype=torch.uint8, device=DEV), torch.empty(n, H, device=DEV))
+    small = fp8.kv_cache(4, H, page, D, DEV)
+    ids = [16999, 1, 16500, 8191]
+    T = 700
+    x = torch.randn(T, 3 * H, D, generator=g, device=DEV).bfloat16()
+    for cache, table in ((big, ids), (small, [0, 1, 2, 3])):
+        slots = [table[i // page] * page + i % page for i in range(600)] + [table[3] * page + i for i in range(100)]
+        fp8.fp8_kv_append(x[:, H:2 * H], x[:, 2 * H:], ints(slots), *cache)
+    for a, b in zip(big, small):
+        assert torch.equal(a[ids[:2]], b[:2])
+    for cu, lens in (([0, 600, 700], [600, 100]), ([0, 1, 2], [600, 100])):
+        out = []
+        for cache, table in ((big, ids), (small, [0, 1, 2, 3])):
+            tab = ints([table[:3], [table[3]] * 3])
+            out.append(fp8.fp8_kv_attention(x[:cu[-1], :H], *cache, tab, ints(cu), ints(lens)))
+        assert torch.equal(*out)
+
+
+def test_two_graphs_with_one_workspace():
+    """Two captured calls that share a workspace, replayed in turn."""
+    rng = np.random.default_rng(14)
+    cases = [attention_case(rng, h, n, 8, 2, 128, 64) for h, n in (([3000, 40], [1, 3]), ([20, 4500, 1000], [2, 1, 1]))]
+    gpu = [(c[0].to(DEV), dev(c[1]), dev(c[2]), dev(c[3]), dev(c[4]), ints(c[5]), ints(c[6]), ints(c[7])) for c in cases]
+    need = max(fp8.fp8_kv_attention_workspace(c[0].shape[0], len(c[7]), 8, 2, 128, 64, c[5].shape[1]) for c in cases)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    want = [fp8.fp8_kv_attention(*c) for c in gpu]
+    graphs, got = [], []
+    for c in gpu:
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(fp8.fp8_kv_attention(*c, workspace=ws))
+        graphs.append(g)
+    for k in range(6):
+        got[k % 2].zero_()
+        graphs[k % 2].replay()
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        assert torch.equal(got[k % 2], want[k % 2]), k

@@ -125,7 +125,8 @@ def test_attention_workspace():
 def test_grids_longer_than_a_launch_are_refused():
     """2^32 threads and more along a grid's axis: refused before anything is enqueued."""
     assert append(T=1 << 30, H=1, D=64, ldk=64, ldv=64) == EUNSUP
-    assert attend(T=1 << 30, B=1, Hq=64, Hkv=1, D=64, ldq=1 << 10, width=1, ws=NUL) in (ESHAPE, EUNSUP)
+    assert attend(T=1 << 20, B=1, Hq=64, Hkv=1, D=64, ldq=1 << 12, width=1) == EUNSUP
+    assert attend(T=1 << 23, B=1, Hq=65535, Hkv=65535, D=64, ldq=1 << 22, width=1) == EUNSUP        # 65,536 tiles x 65,535 heads
 
 
 def test_frequencies():
@@ -148,3 +149,51 @@ def test_binding_refuses_what_it_cannot_pass_on():
               lambda: fp8.fp8_kv_attention(x, *cache, table, i, i)):
         with pytest.raises(ValueError):
             f()
+
+
+class Elsewhere:
+    """A stand-in for a tensor on another device."""
+    is_cuda, dtype, shape, device = True, torch.int32, (4,), "cuda:1"
+
+    def __init__(self, index):
+        self.index = index
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return True
+
+
+def test_tensors_on_different_devices():
+    fp8._need_at(1, Elsewhere(1), torch.int32, (4,), "lens")
+    with pytest.raises(ValueError, match="lens must be on device 0"):
+        fp8._need_at(0, Elsewhere(1), torch.int32, (4,), "lens")
+
+
+def test_calls_run_on_the_tensors_device(monkeypatch):
+    """The call is made with the tensor's device current, on that device's stream."""
+    seen = []
+
+    class Guard:
+        def __init__(self, index):
+            seen.append(("device", index))
+
+        def __enter__(self):
+            seen.append("in")
+
+        def __exit__(self, *a):
+            seen.append("out")
+
+    class Library:
+        def rope(self, *args):
+            seen.append(args)
+            return 0
+
+    monkeypatch.setattr(fp8, "load_library", lambda: Library())
+    monkeypatch.setattr(fp8, "_current_device", lambda: 0)
+    monkeypatch.setattr(fp8, "_stream", lambda t: 70 + t.get_device())
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    fp8._run("rope", 2, Elsewhere(2), 5)
+    fp8._run("rope", 0, Elsewhere(0), 6)
+    assert seen == [("device", 2), "in", (5, 72), "out", (6, 70)]
