@@ -760,6 +760,38 @@ __global__ __launch_bounds__(kThreads) void join(const Args p) {
     if (c == 0 && p.lse) p.lse[at] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
 }
 
+// The same for many rows of few splits: D / 4 threads a row, which take its splits one after
+// another, 1024 / D rows a workgroup
+template <int D, int ROWS>
+__global__ __launch_bounds__(kThreads) void join_rows(const Args p) {
+    constexpr int PER = D / 4, SIDE = kThreads / PER;
+    const int side = threadIdx.x / PER, c = threadIdx.x % PER, kvh = blockIdx.y, used = p.cu[p.B];
+    const int64_t row = int64_t(blockIdx.x) * SIDE + side;
+    if (side >= SIDE || row >= p.T * p.G || row >= int64_t(used) * p.G) return;
+    const int4 d = ld<int4>(p.desc + 4 * row);
+    const int splits = d.x, first = d.y, r = d.z;
+    if (splits <= 1 || first < 0 || splits > p.most_parts - first || r < 0 || r >= ROWS) return;
+    const float* part = p.parts + (int64_t(first) * p.Hkv + kvh) * (ROWS * (D + 2)) + r;
+    const int64_t step = int64_t(p.Hkv) * (ROWS * (D + 2));
+    float M = -__builtin_inff(), L = 0.0f;
+    v4f v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+        const float m = part[s * step], l = part[s * step + ROWS];
+        const v4f o = ld<v4f>(part - r + s * step + 2 * ROWS + r * D + 4 * c);
+        const float top = fmaxf(M, m), use = top == -__builtin_inff() ? 0.0f : top;
+        const float f = __builtin_amdgcn_exp2f(M - use), h = __builtin_amdgcn_exp2f(m - use);
+        M = top;
+        L = L * f + l * h;
+        v = v * f + o * h;
+    }
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const int64_t t = row / p.G, at = t * p.Hq + kvh * p.G + (row - t * p.G);
+    const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+    store_n<4>(p.out + at * D + 4 * c, out);
+    if (c == 0 && p.lse) p.lse[at] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
+}
+
 constexpr int kWideRows = 32 * kWaves;
 struct Plan {
     int64_t tiles, items, parts;          // bounds: row tiles, workgroups, unjoined results, per key/value head
@@ -777,7 +809,10 @@ inline Plan plan_of(const AttendCall& c, int rows) {
     const int64_t all = (c.T * G / rows > seqs ? c.T * G / rows : seqs) * c.Hkv;
     const int64_t rounds = (3 * all / 2 + kSlots - 1) / kSlots;
     r.target = int(((rounds > 1 ? rounds : 1) * kSlots - all / 2 + c.Hkv - 1) / c.Hkv);
-    if (rows == kWideRows && all > kSlots / 4) r.target = 1;      // enough row tiles, and many rows to join
+    // Many rows are split only where their tiles do not fill the chip: two chunks of 1024 tokens on
+    // 16,000 and 2000, 421 us whole, 210 split; one of 2048 on 2000 109 / 84; six of up to 500 on 2000 79 / 85;
+    // of three of 2048 on 8192, 960 tiles, 413 / 437
+    if (rows == kWideRows && all > kSlots) r.target = 1;
     const bool split = kt > kWhole && r.target > 1;
     // a tile has one item more than the work's share at the most, a split one twice as many
     // (the work is summed in FP32), and no more than its keys' whole splits
@@ -810,7 +845,8 @@ hipError_t run_wide(const AttendCall& c, const Args& p, const Plan& plan, hipStr
     // a head's workgroups side by side: with eight heads each XCD reads one head's keys and values
     if (const hipError_t e = launch_kernel(attend_wide<D>, dim3(unsigned(plan.items * c.Hkv)), dim3(kThreads), stream, p)) return e;
     if (plan.bytes == 0) return hipSuccess;
-    return launch_kernel(join<D, kWideRows>, dim3(unsigned(c.T * p.G), unsigned(c.Hkv)), dim3(kThreads), stream, p);
+    constexpr int SIDE = 4 * kThreads / D;
+    return launch_kernel(join_rows<D, kWideRows>, dim3(unsigned((c.T * p.G + SIDE - 1) / SIDE), unsigned(c.Hkv)), dim3(kThreads), stream, p);
 }
 
 template <int D>

@@ -324,6 +324,13 @@ def test_long_axis(held_, new, Hq, Hkv):
     attention_check(attention_case(rng, held_, new, Hq, Hkv, 128, 64, pad=1))
 
 
+@pytest.mark.parametrize("D,page", [(64, 128), (128, 16), (192, 64), (256, 32)])
+def test_long_axis_of_many_rows(D, page):
+    """Many rows over keys that are split: their parts joined row by row, beside requests that are not split."""
+    rng = np.random.default_rng(D)
+    attention_check(attention_case(rng, [2500, 0, 1200, 30], [45, 70, 0, 133], 3, 1, D, page, pad=2))
+
+
 def test_rows_that_see_nothing():
     """Requests shorter than their new rows (refused ones), empty ones, and a batch of nothing else."""
     rng = np.random.default_rng(8)
