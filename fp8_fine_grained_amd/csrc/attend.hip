@@ -551,16 +551,20 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
     // rows of 8 (or an odd multiple) in two
     const auto key_at = [&](int n, int c) { return n * D + ((c ^ (D % 128 == 0 ? n & 15 : (n >> 1) & 7)) * 8); };
     const auto value_at = [&](int d, int c) { return d * kTile + ((c ^ ((d >> 1) & 7)) * 8); };
-    // the fetched tile, widened, into buffer `to`
-    const auto put = [&](int tile, int32_t id, int to) {
+    // the fetched tile's values without what is past the last token: those codes are not numbers
+    const auto cut = [&](int tile, int32_t id) {
         const bool there = exists(id);
-        const int end = !there ? 0 : it.len - (tile * kTile + 16 * quad);     // codes past the last token are not numbers
         if ((tile + 1) * kTile > it.len || !__all(there)) {
+            const int end = !there ? 0 : it.len - (tile * kTile + 16 * quad);
 #pragma unroll
             for (int i = 0; i < KC; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) vraw[i][j] = keep_bytes(vraw[i][j], 4 * j, end);
         }
+    };
+    // the fetched tile, widened, into buffer `to`
+    const auto put = [&](int32_t id, int to) {
+        const bool there = exists(id);
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
             const int at = lane + 64 * i, r = at / (D / 16), c = 2 * (at % (D / 16));
@@ -583,7 +587,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
     int32_t id = page_of(kt0), id2 = page_of(kt0 + 1);
     if (kt0 < kt1) {
         fetch(kt0, id);
-        put(kt0, id, 0);
+        cut(kt0, id);
+        put(id, 0);
     }
     __syncthreads();
     for (int tile = kt0; tile < kt1; ++tile) {
@@ -639,8 +644,15 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
         const float unit = unit_of(top, largest, ref);
         const float factor = unit == ref ? alpha : alpha * (ref * __builtin_amdgcn_rcpf(unit));
         ref = unit;
+        if (!__all(factor == 1.0f)) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] *= factor;
+        }
+        if (tile + 1 < kt1) cut(tile + 1, id);
         // Probabilities are formed times their page's value scale over `ref`, as a term of the
-        // exponent (below 2^-60 FP16 has nothing left of them), and summed without it.
+        // exponent (below 2^-60 FP16 has nothing left of them), and summed without it.  The second
+        // half's run beside the first half's products, and beside its own products the next
+        // tile is widened (what is put past the end is not used).
         v8h pf[2][2];
         l *= alpha;
 #pragma unroll
@@ -656,20 +668,16 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
             }
             l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(ratio), l);
         }
-        if (!__all(factor == 1.0f)) {
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[d] *= factor;
-        }
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int d = 0; d < DT; ++d) {
                     const v8h v = ld<v8h>(&values[buf][value_at(32 * d + col, 4 * t + 2 * h + k)]);
                     o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pf[t][k], o[d], 0, 0, 0);
                 }
-        if (tile + 1 < kt1) put(tile + 1, id, buf ^ 1);
+        put(id, buf ^ 1);
         __syncthreads();
     }
 
