@@ -24,7 +24,6 @@ namespace attend_detail {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kTile = 64;                 // tokens of a tile
@@ -93,10 +92,9 @@ __device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int end = cu[i + 1];
+            const int end = cu[i + 1] < p.T ? cu[i + 1] : int(p.T);
             cu[i] = cu[i] < 0 ? 0 : cu[i];
-            n[i] = cu[i] >= p.T ? 0 : end > p.T ? int(p.T) - cu[i] : end - cu[i];
-            n[i] = n[i] < 0 ? 0 : n[i];
+            n[i] = end > cu[i] ? end - cu[i] : 0;
             len[i] = len[i] < 0 ? 0 : len[i] > room ? room : len[i];
             tiles[i] = int((int64_t(n[i]) * p.G + ROWS - 1) / ROWS);
             kt[i] = (len[i] + kTile - 1) / kTile;
@@ -201,15 +199,18 @@ __device__ __forceinline__ v8h wide_f16(uint32_t a, uint32_t b) {
     return __builtin_bit_cast(v8h, u32x4{to_f16<false>(a), to_f16<true>(a), to_f16<false>(b), to_f16<true>(b)});
 }
 
-// max over the four 16-lane groups
-__device__ __forceinline__ float groups_max(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16, 64));
-    return fmaxf(v, __shfl_xor(v, 32, 64));
+// Over the four 16-lane groups: rows are swapped in pairs, then halves
+template <class Op>
+__device__ __forceinline__ float groups_reduce(float v, Op op) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    const uint32_t a = s[0], b = s[1];
+    v = op(__uint_as_float(a), __uint_as_float(b));
+    const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    const uint32_t c = t[0], d = t[1];
+    return op(__uint_as_float(c), __uint_as_float(d));
 }
-__device__ __forceinline__ float groups_sum(float v) {
-    v += __shfl_xor(v, 16, 64);
-    return v + __shfl_xor(v, 32, 64);
-}
+__device__ __forceinline__ float groups_max(float v) { return groups_reduce(v, MaxOp()); }
+__device__ __forceinline__ float groups_sum(float v) { return groups_reduce(v, SumOp()); }
 
 // max over the two halves of the wave
 __device__ __forceinline__ float halves_max(float v) {
