@@ -553,7 +553,8 @@ static int page_log(int64_t page) {
 // B requests with a block table of `width` entries each
 static int table_args(int64_t B, int64_t width, int64_t page) {
     if (B < 0 || width < 0) return FP8FG_ERR_SHAPE;
-    if (page_log(page) < 0 || B > 65536 || (width > 0 && (B > kMaxDim / width || page > kMaxDim / width))) return FP8FG_ERR_UNSUPPORTED;
+    // (positions are rounded up to whole tiles in 32 bits)
+    if (page_log(page) < 0 || B > 65536 || (width > 0 && (B > kMaxDim / width || page > (kMaxDim - 255) / width))) return FP8FG_ERR_UNSUPPORTED;
     return FP8FG_OK;
 }
 

@@ -28,13 +28,14 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kTile = 64;                 // tokens of a tile
 // Tiles that a split holds at the least, and tables that hold no more than kWhole tiles are not
-// split: 1024 tokens are four steps of each wave, and joining takes a second launch
+// split: 1024 tokens are four steps of each wave, and joining takes a second launch (four requests of up to 601
+// tokens, 32 / 8 heads: 10.4 us whole, 15.9 split)
 constexpr int kMinTiles = 8, kWhole = 16;
 constexpr int kSlots = 512;               // workgroups that run at a time: two on each of 256 CUs
 // Probabilities are held times 2^11, relative to a maximum that is raised only when
 // a score passes it by a factor of 2^4: at most 2^15, and FP16 keeps them normal
-// down to 2^-25.  With every new maximum taken, the wide kernel multiplied its sums by
-// it in most tiles (some row of 32 has one).
+// down to 2^-25.  (Were every new maximum taken, some row of a tile would have one most of
+// the time, and all sums be multiplied.)
 constexpr float kPBias = 11.0f, kSlack = 4.0f;
 
 struct Args {
@@ -47,7 +48,8 @@ struct Args {
     float scale2;                         // softmax scale * log2(e)
     uint16_t* out;
     float* lse;
-    int32_t* desc;                        // workspace: [T][G] x (splits, first part, row of it)
+    int32_t* list;                        // workspace: number of items, and from list + 8 on the items; null: not listed
+    int32_t* desc;                        // [T][G] x (splits, first part, row of it)
     float* parts;                         // unjoined results
     int64_t most_parts;                   // room for them
     int target;                           // workgroups wanted for each key/value head
@@ -73,25 +75,22 @@ __device__ __forceinline__ int wave_scan(int v) {
 }
 __device__ __forceinline__ int lane63(int v) { return __builtin_amdgcn_readlane(v, 63); }
 
-// The requests' row tiles and their splits, numbered in order; every wave
-// finds its workgroup's own from the lengths, four consecutive requests to a
-// lane, without LDS or a barrier.  Splits are of equal numbers of tiles, as long as
-// it takes for about `target` workgroups to do all the work.
-template <int ROWS, bool CLASSES>
-__device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
-    constexpr int R = 4, CHUNK = 64 * R;
-    const int lane = threadIdx.x & 63;
-    const int room = int(p.width << p.page_log);
-    int cu[R + 1], n[R], len[R], tiles[R], kt[R];
-    const auto read = [&](int64_t b0) {
+// Four consecutive requests of a lane: their rows and tokens, with what lies outside
+// the batch and the tables cut off, row tiles and tiles of keys
+constexpr int kPer = 4, kChunk = 64 * kPer;
+template <int ROWS>
+struct Requests {
+    int cu[kPer + 1], n[kPer], len[kPer], tiles[kPer], kt[kPer];
+    __device__ __forceinline__ void read(const Args& p, int64_t b0) {
+        const int room = int(p.width << p.page_log), lane = threadIdx.x & 63;
 #pragma unroll
-        for (int i = 0; i <= R; ++i) {
-            const int64_t b = b0 + lane * R + i;
+        for (int i = 0; i <= kPer; ++i) {
+            const int64_t b = b0 + lane * kPer + i;
             cu[i] = p.cu[b < p.B ? b : p.B];
-            if (i < R) len[i] = b < p.B ? p.lens[b] : 0;
+            if (i < kPer) len[i] = b < p.B ? p.lens[b] : 0;
         }
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
+        for (int i = 0; i < kPer; ++i) {
             const int end = cu[i + 1] < p.T ? cu[i + 1] : int(p.T);
             cu[i] = cu[i] < 0 ? 0 : cu[i];
             n[i] = end > cu[i] ? end - cu[i] : 0;
@@ -99,79 +98,149 @@ __device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
             tiles[i] = int((int64_t(n[i]) * p.G + ROWS - 1) / ROWS);
             kt[i] = (len[i] + kTile - 1) / kTile;
         }
-    };
-    float work = 0.0f;
-    for (int64_t b0 = 0; b0 < p.B; b0 += CHUNK) {
-        read(b0);
-#pragma unroll
-        for (int i = 0; i < R; ++i) work += float(tiles[i]) * float(kt[i]);
     }
-    const float want = ceilf(lanes_sum<64>(work) * (1.0f + 0x1p-20f) / float(p.target));    // no less for FP32's roundings
-    const int per = !p.parts ? 1 << 30 : want < float(kMinTiles) ? kMinTiles : want > 0x1p30f ? 1 << 30 : int(want);
-    // CLASSES: requests whose parts are long come first, in four classes by their share of the
-    // longest (where all requests fit one chunk), so that what starts last is short.  Three chunks
-    // of 2048 tokens on 1024 to 8192: 528 / 461 us without and with.  Parts of a decode step are
-    // alike; there the classes' scans cost 0.7 us and save nothing.
-    int splits[R], size[R], longest = 0;
-    const auto divide = [&] {
+    __device__ __forceinline__ float work() const {
+        float w = 0.0f;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            splits[i] = 1;
-            size[i] = kt[i];
-            if (p.parts) {                // (a division costs tens of instructions)
-                splits[i] = kt[i] > per ? (kt[i] + per - 1) / per : 1;
-                if (CLASSES) size[i] = splits[i] > 1 ? (kt[i] + splits[i] - 1) / splits[i] : kt[i];
-            }
-            longest = size[i] > longest && tiles[i] > 0 ? size[i] : longest;
+        for (int i = 0; i < kPer; ++i) w += float(tiles[i]) * float(kt[i]);
+        return w;
+    }
+};
+
+// Tiles of a part, from the work of all requests: so many that about `target` workgroups do
+// all of it (no less for the roundings of a sum in FP32)
+__device__ __forceinline__ int part_of(const Args& p, float work) {
+    const float want = ceilf(work * (1.0f + 0x1p-20f) / float(p.target));
+    return !p.parts ? 1 << 30 : want < float(kMinTiles) ? kMinTiles : want > 0x1p30f ? 1 << 30 : int(want);
+}
+__device__ __forceinline__ int splits_of(int kt, int per) { return kt > per ? (kt + per - 1) / per : 1; }
+
+// The requests' row tiles and their splits, numbered in order: the me-th.  Up to 256
+// requests every wave finds it from the lengths, four requests to a lane, without
+// LDS or a barrier; more are listed by a launch of their own.
+template <int ROWS, bool CLASSES>
+__device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
+    if (p.list) {
+        const int32_t* at = p.list + 8 + int64_t(me) * 8;
+        const int4 a = ld<int4>(at), b = ld<int4>(at + 4);
+        const auto get = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+        it = Item{get(a.x), get(a.y), get(a.z), get(a.w), get(b.x), get(b.y), get(b.z), get(b.w)};
+        return me < p.list[0];
+    }
+    const int lane = threadIdx.x & 63;
+    Requests<ROWS> r;
+    r.read(p, 0);
+    const int per = part_of(p, lanes_sum<64>(r.work()));
+    // CLASSES: requests whose parts are long come first, in four classes by their share of the
+    // longest, so that what starts last is short.  Three chunks of up to 2048 tokens on 1024 to 8192: 528 / 461 us
+    // without and with.  Parts of a decode step are alike; there the classes' scans cost 0.7 us and save nothing.
+    int splits[kPer], size[kPer], longest = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        splits[i] = 1;
+        size[i] = r.kt[i];
+        if (p.parts) {                    // (a division costs tens of instructions)
+            splits[i] = splits_of(r.kt[i], per);
+            if (CLASSES) size[i] = splits[i] > 1 ? (r.kt[i] + splits[i] - 1) / splits[i] : r.kt[i];
         }
-    };
-    const bool whole = p.B <= CHUNK;
-    if (whole) divide();
+        longest = size[i] > longest && r.tiles[i] > 0 ? size[i] : longest;
+    }
     if (CLASSES) longest = __builtin_amdgcn_readfirstlane(int(lanes_max<64>(uint32_t(longest))));
     int items0 = 0, parts0 = 0;
-    const bool classes = CLASSES && whole;
-    for (int cls = classes ? 3 : 0; cls >= 0; --cls) {
-        const int over = classes && cls > 0 ? int(int64_t(longest) * cls / 4) : -1, upto = classes && cls < 3 ? int(int64_t(longest) * (cls + 1) / 4) : 0x7FFFFFFF;
-        for (int64_t b0 = 0; b0 < p.B; b0 += CHUNK) {
-            if (!whole) {
-                read(b0);
-                divide();
-            }
-            int items = 0, parts = 0, here[R];
+    for (int cls = CLASSES ? 3 : 0; cls >= 0; --cls) {
+        const int over = cls > 0 ? int(int64_t(longest) * cls / 4) : -1, upto = CLASSES && cls < 3 ? int(int64_t(longest) * (cls + 1) / 4) : 0x7FFFFFFF;
+        int items = 0, parts = 0, here[kPer];
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                here[i] = size[i] > over && size[i] <= upto ? tiles[i] * splits[i] : 0;
-                items += here[i];
-                parts += splits[i] > 1 ? here[i] : 0;
-            }
-            const int i1 = wave_scan(items), p1 = wave_scan(parts);
-            int at = me - items0 - (i1 - items);
-            const uint64_t who = __ballot(at >= 0 && at < items);
-            if (who) {
-                int part = parts0 + p1 - parts;
-                Item mine{};              // tile: the item's place among its request's
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    if (at >= 0 && at < here[i]) mine = Item{int32_t(b0) + lane * R + i, cu[i], n[i], len[i], at, 0, splits[i], part};
-                    at -= here[i];
-                    part += splits[i] > 1 ? here[i] : 0;
-                }
-                const int src = __builtin_ctzll(who);
-                const auto get = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
-                it = Item{get(mine.b), get(mine.cu), get(mine.n), get(mine.len), get(mine.tile), 0, get(mine.splits), get(mine.part)};
-                if (it.splits > 1) {
-                    const int tile = it.tile / it.splits;
-                    it.split = it.tile - tile * it.splits;
-                    it.part += tile * it.splits;
-                    it.tile = tile;
-                }
-                return it.splits == 1 || it.part + it.splits <= p.most_parts;
-            }
-            items0 += lane63(i1);
-            parts0 += lane63(p1);
+        for (int i = 0; i < kPer; ++i) {
+            here[i] = size[i] > over && size[i] <= upto ? r.tiles[i] * splits[i] : 0;
+            items += here[i];
+            parts += splits[i] > 1 ? here[i] : 0;
         }
+        const int i1 = wave_scan(items), p1 = wave_scan(parts);
+        int at = me - items0 - (i1 - items);
+        const uint64_t who = __ballot(at >= 0 && at < items);
+        if (who) {
+            int part = parts0 + p1 - parts;
+            Item mine{};                  // tile: the item's place among its request's
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                if (at >= 0 && at < here[i]) mine = Item{lane * kPer + i, r.cu[i], r.n[i], r.len[i], at, 0, splits[i], part};
+                at -= here[i];
+                part += splits[i] > 1 ? here[i] : 0;
+            }
+            const int src = __builtin_ctzll(who);
+            const auto get = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
+            it = Item{get(mine.b), get(mine.cu), get(mine.n), get(mine.len), get(mine.tile), 0, get(mine.splits), get(mine.part)};
+            if (it.splits > 1) {
+                const int tile = it.tile / it.splits;
+                it.split = it.tile - tile * it.splits;
+                it.part += tile * it.splits;
+                it.tile = tile;
+            }
+            return it.splits == 1 || (it.part >= 0 && it.part + it.splits <= p.most_parts);
+        }
+        items0 += lane63(i1);
+        parts0 += lane63(p1);
     }
     return false;
+}
+
+// The same for more than 256 requests, once for all workgroups: a wave for each 256 of them sums
+// the work of all and the items before its own, and writes its own out.  1000 requests of up
+// to 500 tokens, 8 heads: 259 us with every wave finding its item among all, 154 with the list; 300 of up to 8192,
+// one head: 72 / 74.
+template <int ROWS>
+__global__ __launch_bounds__(64) void list_items(const Args p, int64_t room) {
+    const int lane = threadIdx.x & 63;
+    const int64_t own = int64_t(blockIdx.x) * kChunk;
+    Requests<ROWS> r;
+    float work = 0.0f;
+    if (p.parts) {
+#pragma unroll 2
+        for (int64_t b0 = 0; b0 < p.B; b0 += kChunk) {
+            r.read(p, b0);
+            work += r.work();
+        }
+    }
+    const int per = part_of(p, lanes_sum<64>(work));
+    int items0 = 0, parts0 = 0;
+#pragma unroll 2
+    for (int64_t b0 = 0; b0 < own; b0 += kChunk) {
+        r.read(p, b0);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int splits = splits_of(r.kt[i], per), all = r.tiles[i] * splits;
+            items0 += all;
+            parts0 += splits > 1 ? all : 0;
+        }
+    }
+    items0 = lane63(wave_scan(items0));
+    parts0 = lane63(wave_scan(parts0));
+    r.read(p, own);
+    int splits[kPer], items = 0, parts = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        splits[i] = splits_of(r.kt[i], per);
+        items += r.tiles[i] * splits[i];
+        parts += splits[i] > 1 ? r.tiles[i] * splits[i] : 0;
+    }
+    const int i1 = wave_scan(items), p1 = wave_scan(parts);
+    int64_t at = int64_t(items0) + i1 - items;
+    int part = parts0 + p1 - parts;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        // (items and parts that no room was counted for, which sound offsets do not have, are left out or see nothing)
+        for (int tile = 0; tile < r.tiles[i] && at >= 0 && at < room; ++tile) {
+            const bool fits = splits[i] == 1 || (part >= 0 && part + splits[i] <= p.most_parts);
+            for (int split = 0; split < splits[i] && at < room; ++split, ++at) {
+                int32_t* to = p.list + 8 + at * 8;
+                st<int4>(to, int4{int32_t(own) + lane * kPer + i, r.cu[i], fits ? r.n[i] : 0, r.len[i]});
+                st<int4>(to + 4, int4{tile, split, fits ? splits[i] : 1, splits[i] > 1 ? part : 0});
+            }
+            part += splits[i] > 1 ? splits[i] : 0;
+        }
+    }
+    if (own + kChunk >= p.B && lane == 0) p.list[0] = items0 + lane63(i1);
 }
 
 // Token and query head of a row tile's rows: one division for the tile, the rest by a
@@ -234,7 +303,9 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int first, int end) {
 }
 
 // 16 NR query rows of one key/value head and a part of their keys.  The four waves
-// take every fourth tile; a wave widens a tile's codes once for all its rows.
+// take every fourth tile; a wave widens a tile's codes once for all its rows.  Bound by the
+// stream of codes: 607 MB (64 requests of 1025 to 8193 tokens, 64 / 8 heads, D = 128) in 115 us, 5.2 TB/s, what a copy
+// reaches; matrix units busy 0.08, vector instructions 0.34 of the time.
 template <int D, int NR, bool ONCE>
 __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
     constexpr int ROWS = 16 * NR, KC = D / 64, DT = D / 16;
@@ -484,7 +555,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
 // registers.  The products are 32 x 32 x 16, again S^T = K Q^T and O^T = V^T P^T: row n =
 // 8 b + 4 h + i of a 32-token product holds token 16 h + 4 b + i, so that lane half h ends up with
 // tokens 16 h .. 16 h + 15 of a row, one page's, in order.  16-byte pieces of LDS rows are
-// swapped by row, so that eight lanes' pieces meet different banks.
+// swapped by row, so that eight lanes' pieces meet different banks.  Bound by the vector instructions
+// beside the products (9.5 for each): 512 tokens on 30,000, 32 / 8 heads, D = 128, 296 us with the join,
+// 0.85 PFLOP/s; three chunks of 512 to 2048 on 1024 to 8192 348 to 493 us, 0.75 to 0.88 PFLOP/s.
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 template <int D>
@@ -611,7 +684,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
 #pragma unroll
             for (int t = 0; t < 2; ++t)
                 s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ld<v8bf>(&keys[buf][key_at(32 * t + col, 2 * c + h)]), qf[c], s[t], 0, 0, 0);
-        // six keys' pieces ahead of the products: 425 -> 418 us for three chunks of 2048 tokens
+        // six keys' pieces ahead of the products: 425 -> 418 us for three chunks of up to 2048 tokens
         __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
 #pragma unroll
         for (int c = 0; c < D / 8 - 6; ++c) {
@@ -716,7 +789,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
 
 // The splits of a query row joined, a workgroup for each: D / 4 threads of four
 // channels side by side, 1024 / D splits at a time, each with a running maximum of its
-// own; they meet in LDS in a fixed order.
+// own; they meet in LDS in a fixed order.  Bound by latency: 5.1 us for 64 requests of 64 heads, four to ten parts each.
 template <int D, int ROWS>
 __global__ __launch_bounds__(kThreads) void join(const Args p) {
     constexpr int PER = D / 4, SIDE = kThreads / PER;
@@ -770,7 +843,8 @@ __global__ __launch_bounds__(kThreads) void join(const Args p) {
 }
 
 // The same for many rows of few splits: D / 4 threads a row, which take its splits one after
-// another, 1024 / D rows a workgroup
+// another, 1024 / D rows a workgroup (chunk of 2048 tokens on 2000, 16 / 4 heads: the whole call 94 us with a workgroup for each row,
+// 83 so)
 template <int D, int ROWS>
 __global__ __launch_bounds__(kThreads) void join_rows(const Args p) {
     constexpr int PER = D / 4, SIDE = kThreads / PER;
@@ -805,7 +879,7 @@ constexpr int kWideRows = 32 * kWaves;
 struct Plan {
     int64_t tiles, items, parts;          // bounds: row tiles, workgroups, unjoined results, per key/value head
     int target;
-    int64_t bytes;
+    int64_t list, desc, parts_at, bytes;  // places in the workspace, and its size
 };
 inline Plan plan_of(const AttendCall& c, int rows) {
     Plan r;
@@ -818,9 +892,11 @@ inline Plan plan_of(const AttendCall& c, int rows) {
     const int64_t all = (c.T * G / rows > seqs ? c.T * G / rows : seqs) * c.Hkv;
     const int64_t rounds = (3 * all / 2 + kSlots - 1) / kSlots;
     r.target = int(((rounds > 1 ? rounds : 1) * kSlots - all / 2 + c.Hkv - 1) / c.Hkv);
-    // Many rows are split only where their tiles do not fill the chip: two chunks of 1024 tokens on
-    // 16,000 and 2000, 421 us whole, 210 split; one of 2048 on 2000 109 / 84; six of up to 500 on 2000 79 / 85;
-    // of three of 2048 on 8192, 960 tiles, 413 / 437
+    // no part needs to be shorter than half of what one place does in all (and the workspace stays small)
+    if (r.target > (2 * kSlots + c.Hkv - 1) / c.Hkv) r.target = int((2 * kSlots + c.Hkv - 1) / c.Hkv);
+    // Many rows are split only where their tiles do not fill the chip: chunks of 1024 and 256
+    // tokens on 16,000 and 2000, 421 us whole, 210 split; one of 2048 on 2000 109 / 84; six of up to 500 on up
+    // to 2000 79 / 85; three of up to 2048 on up to 8192, 960 tiles, 413 / 437
     if (rows == kWideRows && all > kSlots) r.target = 1;
     const bool split = kt > kWhole && r.target > 1;
     // a tile has one item more than the work's share at the most, a split one twice as many
@@ -828,24 +904,32 @@ inline Plan plan_of(const AttendCall& c, int rows) {
     const int64_t share = r.target + 1, most = split ? r.tiles * ((kt + kMinTiles - 1) / kMinTiles - 1) : 0;
     r.items = r.tiles + (share < most ? share : most);
     r.parts = split ? 2 * int64_t(r.target) + 2 : 0;
-    r.bytes = split ? c.T * G * 16 + r.parts * c.Hkv * rows * (c.D + 2) * 4 : 0;
+    r.list = 0;
+    r.desc = c.B > kChunk ? 32 + r.items * 32 : 0;
+    r.parts_at = r.desc + (split ? c.T * G * 16 : 0);
+    r.bytes = r.parts_at + r.parts * c.Hkv * rows * (c.D + 2) * 4;
     return r;
 }
 
-// Rows of a workgroup, by what the requests bring on average
+// Rows of a workgroup, by what the requests bring on average: sixteen, thirty-two, or four waves' 32
+// over one copy in LDS.  us, on caches of up to 3000 tokens: 64 requests of 8 heads and D = 128 with 16 rows each, 16 and 32
+// a workgroup 56 / 62, with 24 rows 85 / 65; with 40, 50 and 60 rows, 32 and 128 a workgroup 92 / 92, 103 / 93, 116 / 95,
+// with 80 144 / 98; 60 rows of four requests 21 / 26, of 32 requests of two heads at D = 256 48 / 46.
 inline int rows_of(const AttendCall& c) {
     const int64_t seqs = c.B < c.T ? c.B : c.T, rows = c.T * (c.Hq / c.Hkv);
-    return rows > 64 * seqs ? kWideRows : c.D <= 128 && rows > 16 * seqs ? 32 : 16;
+    return rows > 64 * seqs || (rows > 48 * seqs && seqs * c.Hkv >= kSlots) ? kWideRows : c.D <= 128 && rows > 16 * seqs ? 32 : 16;
 }
 
 template <int D, int NR>
 hipError_t run(const AttendCall& c, const Args& p, const Plan& plan, hipStream_t stream) {
-    // values that no other workgroup reads pass the caches by
-    const bool once = c.T * p.G <= 16 * NR * (c.B < c.T ? c.B : c.T);
-    if (const hipError_t e = launch_kernel(once ? attend<D, NR, true> : attend<D, NR, false>, dim3(unsigned(plan.items), unsigned(c.Hkv)),
-                                           dim3(kThreads), stream, p))
-        return e;
-    if (plan.bytes == 0) return hipSuccess;
+    // Values that no other workgroup reads pass the caches by.  Without and with, us: 64 requests of 1025 to 8193
+    // tokens, 8 heads, 128 / 118 (D = 128), 73 / 69 (64); with 24 to 48 rows each, 49 / 51, 50 / 49, 93 / 96
+    auto kernel = attend<D, NR, false>;
+    if constexpr (NR == 1) {
+        if (c.T * p.G <= 16 * (c.B < c.T ? c.B : c.T)) kernel = attend<D, NR, true>;
+    }
+    if (const hipError_t e = launch_kernel(kernel, dim3(unsigned(plan.items), unsigned(c.Hkv)), dim3(kThreads), stream, p)) return e;
+    if (plan.parts == 0) return hipSuccess;
     return launch_kernel(join<D, 16 * NR>, dim3(unsigned(c.T * p.G), unsigned(c.Hkv)), dim3(kThreads), stream, p);
 }
 
@@ -853,7 +937,7 @@ template <int D>
 hipError_t run_wide(const AttendCall& c, const Args& p, const Plan& plan, hipStream_t stream) {
     // a head's workgroups side by side: with eight heads each XCD reads one head's keys and values
     if (const hipError_t e = launch_kernel(attend_wide<D>, dim3(unsigned(plan.items * c.Hkv)), dim3(kThreads), stream, p)) return e;
-    if (plan.bytes == 0) return hipSuccess;
+    if (plan.parts == 0) return hipSuccess;
     constexpr int SIDE = 4 * kThreads / D;
     return launch_kernel(join_rows<D, kWideRows>, dim3(unsigned((c.T * p.G + SIDE - 1) / SIDE), unsigned(c.Hkv)), dim3(kThreads), stream, p);
 }
@@ -877,13 +961,19 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t stream) {
     const Plan plan = plan_of(c, rows);
     // both launches' grids, before the first
     if (!grid_fits(rows == kWideRows ? plan.items * c.Hkv : plan.items, kThreads) ||
-        (plan.bytes && !grid_fits(c.T * (c.Hq / c.Hkv), kThreads)))
+        (plan.parts && !grid_fits(c.T * (c.Hq / c.Hkv), kThreads)))
         return hipErrorInvalidConfiguration;
     Args p{c.q, c.kc, c.vc, c.ks, c.vs, c.table, c.cu, c.lens, c.ldq, c.n_pages, c.width, c.B, c.T, int(c.Hq), int(c.Hkv), int(c.Hq / c.Hkv),
-           c.page_log, c.scale * 1.4426950408889634f, c.out, c.lse, nullptr, nullptr, plan.parts, plan.target};
-    if (plan.bytes) {
-        p.desc = static_cast<int32_t*>(c.workspace);
-        p.parts = reinterpret_cast<float*>(p.desc + 4 * c.T * p.G);
+           c.page_log, c.scale * 1.4426950408889634f, c.out, c.lse, nullptr, nullptr, nullptr, plan.parts, plan.target};
+    uint8_t* w = static_cast<uint8_t*>(c.workspace);
+    if (plan.parts) {
+        p.desc = reinterpret_cast<int32_t*>(w + plan.desc);
+        p.parts = reinterpret_cast<float*>(w + plan.parts_at);
+    }
+    if (c.B > kChunk) {
+        p.list = reinterpret_cast<int32_t*>(w + plan.list);
+        const auto kernel = rows == 16 ? list_items<16> : rows == 32 ? list_items<32> : list_items<kWideRows>;
+        if (const hipError_t e = launch_kernel(kernel, dim3(unsigned((c.B + kChunk - 1) / kChunk)), dim3(64), stream, p, plan.items)) return e;
     }
     switch (c.D) {
         case 64: return run_any<64>(c, p, plan, rows, stream);

@@ -604,8 +604,8 @@ int fp8_grouped_gemm_wgrad(const uint8_t* a, const float* sa, const uint8_t* b, 
  * cu[b] .. cu[b+1] - 1 (int32 [B+1], non-decreasing from 0).  Rows from cu[B] on
  * (a batch padded to a fixed size T) are left as they were by every call.
  * All of them are deterministic: no sum depends on the order of execution.
- * Sizes common to them: B <= 65536 requests, B * width < 2^31, page * width <
- * 2^31, n_pages * page < 2^31, at most 65535 heads.
+ * Sizes common to them: B <= 65536 requests, B * width < 2^31, page * width <=
+ * 2^31 - 256, n_pages * page < 2^31, at most 65535 heads.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -670,7 +670,7 @@ int rope(const void* q, int64_t ldq, void* q_out, int64_t ldqo, int64_t Hq, cons
 
 /*
  * New keys and values into the cache.
- * k, v: [T][H][D], f32 or bf16 (x_bf16), rows ldk and ldv elements apart; slots: int32
+ * k, v: finite [T][H][D], f32 or bf16 (x_bf16), rows ldk and ldv elements apart; slots: int32
  * [T], each row's place; rows whose slot is outside [0, n_pages * page) are skipped.
  * The rows of one page have to be consecutive, with consecutive slots.  Where a
  * page's first new row has offset o > 0, its tokens 0 .. o - 1 are in the cache
@@ -695,8 +695,8 @@ int fp8_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int x_
  * n = cu[b+1] - cu[b] new ones of request b sees the keys j <= lens[b] - n + i (j < lens[b]):
  *   x_j = scale * <q, k_j>,  p = softmax(x),  out = sum_j p_j v_j.
  *   out: bf16 [T][Hq][D];  lse: f32 [T][Hq] = log sum_j exp(x_j), or NULL.
- * Tokens in pages outside [0, n_pages) (and past the table's last entry) are not
- * seen.  A token that sees nothing gets 0, and -inf for lse.
+ * Tokens in pages outside [0, n_pages) are not seen, and a length counts as width * page at
+ * the most.  A token that sees nothing gets 0, and -inf for lse.
  * What lies in the cache past a request's last token has no influence.
  * Scales may be any finite non-negative FP32 values.
  * Accuracy: codes are multiplied exactly and summed in FP32; probabilities are

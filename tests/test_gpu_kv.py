@@ -520,6 +520,39 @@ def test_many_requests(G, add, long):
     attention_check(attention_case(rng, held_, new, G, 1, 64, 16, pad=3))
 
 
+def test_list_across_chunks():
+    """Requests in several chunks of 256, empty, short and split ones in each, replayed from a graph on other lengths."""
+    rng = np.random.default_rng(21)
+    B = 700
+    cases = []
+    for k in range(2):
+        held_ = rng.integers(0, 30, B)
+        held_[[3 + k, 300 + k, 650 + k]] = 2500 + 100 * k
+        cases.append(attention_case(rng, list(held_), [int(i % 4 > 0) for i in range(B)], 2, 1, 64, 16, pad=5, width=170))
+        attention_check(cases[-1])
+    gpu = [(c[0].to(DEV), dev(c[1]), dev(c[2]), dev(c[3]), dev(c[4]), ints(c[5]), ints(c[6]), ints(c[7])) for c in cases]
+    most = max(g[1].shape[0] for g in gpu)
+    at = [torch.zeros((most, *x.shape[1:]) if 1 <= i <= 4 else x.shape, dtype=x.dtype, device=DEV) for i, x in enumerate(gpu[0])]
+
+    def put(g):
+        for a, x in zip(at, g):
+            a[:x.shape[0]].copy_(x)
+
+    put(gpu[0])
+    out = torch.zeros_like(at[0])
+    fp8.fp8_kv_attention(*at, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fp8.fp8_kv_attention(*at, out=out)
+    for k in (1, 0, 1, 0):
+        put(gpu[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        used = int(gpu[k][6][-1])
+        assert torch.equal(out[:used], fp8.fp8_kv_attention(*gpu[k])[:used])
+
+
 def test_offsets_past_32_bits():
     """Pages far into a cache of more than 4 GB: writes and reads land where the small cache's do."""
     H, page, D, n = 4, 256, 256, 17000

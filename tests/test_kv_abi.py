@@ -197,3 +197,12 @@ def test_calls_run_on_the_tensors_device(monkeypatch):
     fp8._run("rope", 2, Elsewhere(2), 5)
     fp8._run("rope", 0, Elsewhere(0), 6)
     assert seen == [("device", 2), "in", (5, 72), "out", (6, 70)]
+
+
+def test_positions_are_rounded_to_tiles():
+    """page * width up to 2^31 - 256, whatever the page."""
+    for page in (16, 64, 256):
+        most = (2 ** 31 - 256) // page
+        for f in (assign, attend):
+            assert f(B=1, page=page, width=most + 1) == EUNSUP
+        assert attend(B=1, page=page, width=most) == OK
