@@ -299,7 +299,8 @@ __global__ __launch_bounds__(kThreads) void rope(const RopeArgs p) {
 // consecutive rows with consecutive slots, and a wave or a workgroup takes one head's run of keys or
 // values.  The scale is the least power of two s with amax <= 448 s (2^-126 at the least), over
 // the run and the page's older tokens; when it grows, older codes are re-encoded by the exact factor.  Bound by
-// latency (slots, scale, data, maximum, stores in turn): 128 tokens x 8 x 128 in BF16 6.0 us in a graph, 5120 14.8.  Thousands of
+// latency (slots, scale, data, maximum, stores in turn): 128 tokens x 8 x 128 in BF16 5.9 us in a graph, 5120
+// 13.2 (with four waves a SIMD, which is a round and a quarter of workgroups, 14.8).  Thousands of
 // single tokens are bound by the bytes that each writes into its value page's rows: 4096 99 us.
 struct AppendArgs {
     const void *k, *v;
@@ -403,15 +404,20 @@ __device__ __forceinline__ void in_two_passes(int pieces, int me, int team, Load
         for (int i = 0; i < HOLD; ++i)
             if (team * i < pieces) look(w[i]);
         const float r = scale();
+        // (held as they came: the compiler would keep the widened values of the first pass, 119 in place of 89 registers)
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i)
+#pragma unroll
+            for (auto& v : w[i].w) asm volatile("" : "+v"(v));
 #pragma unroll
         for (int i = 0; i < HOLD; ++i)
             if (me + team * i < pieces) put(me + team * i, w[i], r);
         return;
     }
-#pragma unroll 2
+#pragma unroll 4
     for (int i = me; i < pieces; i += team) look(load(i));
     const float r = scale();
-#pragma unroll 2
+#pragma unroll 4
     for (int i = me; i < pieces; i += team) put(i, load(i), r);
 }
 
@@ -528,7 +534,7 @@ __device__ __forceinline__ void append_one(const Run<T>& r) {
 // workgroup one after another.  Bit j of a word says that the j-th row continues the run of the
 // row before it.
 template <class T>
-__global__ __launch_bounds__(kThreads, 4) void append(const AppendArgs p, int window) {
+__global__ __launch_bounds__(kThreads, 5) void append(const AppendArgs p, int window) {
     __shared__ float part[kWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = blockIdx.y, page = 1 << p.page_log;
     const bool values = blockIdx.z != 0;
@@ -620,7 +626,7 @@ hipError_t launch_kv_append(const KvAppendCall& c, hipStream_t stream) {
     const AppendArgs p{c.k, c.v, c.ldk, c.ldv, c.T, c.n_pages << c.page_log, int(c.H), int(c.D), c.page_log, c.slots, c.kc, c.vc, c.ks, c.vs};
     // Few rows: each may begin a run of its own; many: most continue one.  About a thousand workgroups: us with windows of
     // 4 / 16 / 64 rows, 8 heads of 128, single tokens: 128 5.9 / 7.5 / 18, 512 12.1 / 11.3 / 20, 2048 46 / 45 / 43 (32 rows: 42);
-    // runs: 5120 rows 36 / 22 / 15
+    // runs: 5120 rows 36 / 22 / 15, 1250 14.0 / 11.1 / 10.1 (32 rows: 9.6)
     int window = 4;
     while (window < 64 && window * 512 < c.T * c.H) window *= 2;
     return launch_kernel(c.bf16 ? append<uint16_t> : append<float>, dim3(unsigned((c.T + window - 1) / window), unsigned(c.H), 2),
