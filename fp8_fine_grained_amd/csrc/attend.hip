@@ -896,8 +896,10 @@ inline Plan plan_of(const AttendCall& c, int rows) {
     if (r.target > (2 * kSlots + c.Hkv - 1) / c.Hkv) r.target = int((2 * kSlots + c.Hkv - 1) / c.Hkv);
     // Many rows are split only where their tiles do not fill the chip: chunks of 1024 and 256
     // tokens on 16,000 and 2000, 421 us whole, 210 split; one of 2048 on 2000 109 / 84; six of up to 500 on up
-    // to 2000 79 / 85; three of up to 2048 on up to 8192, 960 tiles, 413 / 437
-    if (rows == kWideRows && all > kSlots) r.target = 1;
+    // to 2000 79 / 85; three of up to 2048 on up to 8192, 960 tiles, 413 / 437.  Where they do, and each of several requests
+    // brings many, only tiles longer than a place's share are, which the host cannot see: 2048 and 512 tokens on up to
+    // 16,384 484 / 398, five of 512 to 2048 on 1024 to 8192, where none is, 564 / 571 for the empty second launch
+    if (rows == kWideRows && all > kSlots) r.target = seqs > 1 && c.T * G > 512 * seqs ? int((kSlots + c.Hkv - 1) / c.Hkv) : 1;
     const bool split = kt > kWhole && r.target > 1;
     // a tile has one item more than the work's share at the most, a split one twice as many
     // (the work is summed in FP32), and no more than its keys' whole splits

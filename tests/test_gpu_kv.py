@@ -520,6 +520,24 @@ def test_many_requests(G, add, long):
     attention_check(attention_case(rng, held_, new, G, 1, 64, 16, pad=3))
 
 
+def test_only_long_tiles_split():
+    """More row tiles than workgroups run at a time; the few of a long request are split, the others whole."""
+    rng = np.random.default_rng(33)
+    q, k, ks, v, vs, table, cu, lens = attention_case(rng, [0, 3500], [1200, 150], 64, 64, 64, 64)
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out, _ = fp8.fp8_kv_attention(q.to(DEV), dev(k), dev(ks), dev(v), dev(vs), ints(table), ints(cu), ints(lens), lse=lse)
+    for h in (0, 37, 63):
+        part = [a[:, h: h + 1].copy() for a in (k, ks, v, vs)]
+        one = (q[:, h: h + 1].contiguous(), *part, table, cu, lens)
+        n, got = int(lens.max()), host(out[:, h: h + 1])
+        full, flse, size, score = kv.attention(one[0].float().numpy(), *part, table, cu, lens, 64 ** -0.5)
+        x = (64 + 8) * EPS * score + 4 * EPS
+        p = 2.0 ** -11 + 4 * x + (n + 64) * EPS
+        vmax = float(np.nanmax(np.where(np.isfinite(part[3]), np.abs(part[3]), 0))) * 448.0
+        held(got - full, 2.0 ** -8 * np.abs(full) + (1 + 2.0 ** -8) * p[..., None] * size + 2.0 ** -50 * vmax, "out")
+        held(host(lse[:, h: h + 1]) - flse, 2 * x + (n + 64) * EPS + 8 * EPS * np.abs(flse), "lse")
+
+
 def test_list_across_chunks():
     """Requests in several chunks of 256, empty, short and split ones in each, replayed from a graph on other lengths."""
     rng = np.random.default_rng(21)
