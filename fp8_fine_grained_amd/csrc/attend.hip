@@ -125,7 +125,7 @@ __device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
         const int4 a = ld<int4>(at), b = ld<int4>(at + 4);
         const auto get = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
         it = Item{get(a.x), get(a.y), get(a.z), get(a.w), get(b.x), get(b.y), get(b.z), get(b.w)};
-        return me < p.list[0];
+        return me < p.list[0] && it.n > 0;
     }
     const int lane = threadIdx.x & 63;
     Requests<ROWS> r;
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(64) void list_items(const Args p, int64_t room) {
     int part = parts0 + p1 - parts;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        // (items and parts that no room was counted for, which sound offsets do not have, are left out or see nothing)
+        // (items and parts that no room was counted for, which sound offsets do not have, are left out)
         for (int tile = 0; tile < r.tiles[i] && at >= 0 && at < room; ++tile) {
             const bool fits = splits[i] == 1 || (part >= 0 && part + splits[i] <= p.most_parts);
             for (int split = 0; split < splits[i] && at < room; ++split, ++at) {
@@ -557,7 +557,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
 // tokens 16 h .. 16 h + 15 of a row, one page's, in order.  16-byte pieces of LDS rows are
 // swapped by row, so that eight lanes' pieces meet different banks.  Bound by the vector instructions
 // beside the products (9.5 for each): 512 tokens on 30,000, 32 / 8 heads, D = 128, 296 us with the join,
-// 0.85 PFLOP/s; three chunks of 512 to 2048 on 1024 to 8192 348 to 493 us, 0.75 to 0.88 PFLOP/s.
+// 0.85 PFLOP/s; three chunks of 512 to 2048 on 1024 to 8192 293 to 512 us, 0.83 to 0.87 PFLOP/s.
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 template <int D>
@@ -845,34 +845,37 @@ __global__ __launch_bounds__(kThreads) void join(const Args p) {
 // The same for many rows of few splits: D / 4 threads a row, which take its splits one after
 // another, 1024 / D rows a workgroup (chunk of 2048 tokens on 2000, 16 / 4 heads: the whole call 94 us with a workgroup for each row,
 // 83 so)
-template <int D, int ROWS>
+template <int D, int ROWS, bool HEADS>
 __global__ __launch_bounds__(kThreads) void join_rows(const Args p) {
     constexpr int PER = D / 4, SIDE = kThreads / PER;
-    const int side = threadIdx.x / PER, c = threadIdx.x % PER, kvh = blockIdx.y, used = p.cu[p.B];
+    const int side = threadIdx.x / PER, c = threadIdx.x % PER, used = p.cu[p.B];
     const int64_t row = int64_t(blockIdx.x) * SIDE + side;
     if (side >= SIDE || row >= p.T * p.G || row >= int64_t(used) * p.G) return;
     const int4 d = ld<int4>(p.desc + 4 * row);
     const int splits = d.x, first = d.y, r = d.z;
     if (splits <= 1 || first < 0 || splits > p.most_parts - first || r < 0 || r >= ROWS) return;
-    const float* part = p.parts + (int64_t(first) * p.Hkv + kvh) * (ROWS * (D + 2)) + r;
-    const int64_t step = int64_t(p.Hkv) * (ROWS * (D + 2));
-    float M = -__builtin_inff(), L = 0.0f;
-    v4f v{0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t step = int64_t(p.Hkv) * (ROWS * (D + 2)), t = row / p.G;
+    for (int kvh = HEADS ? 0 : blockIdx.y; kvh < p.Hkv; ++kvh) {
+        const float* part = p.parts + (int64_t(first) * p.Hkv + kvh) * (ROWS * (D + 2)) + r;
+        float M = -__builtin_inff(), L = 0.0f;
+        v4f v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-        const float m = part[s * step], l = part[s * step + ROWS];
-        const v4f o = ld<v4f>(part - r + s * step + 2 * ROWS + r * D + 4 * c);
-        const float top = fmaxf(M, m), use = top == -__builtin_inff() ? 0.0f : top;
-        const float f = __builtin_amdgcn_exp2f(M - use), h = __builtin_amdgcn_exp2f(m - use);
-        M = top;
-        L = L * f + l * h;
-        v = v * f + o * h;
+        for (int s = 0; s < splits; ++s) {
+            const float m = part[s * step], l = part[s * step + ROWS];
+            const v4f o = ld<v4f>(part - r + s * step + 2 * ROWS + r * D + 4 * c);
+            const float top = fmaxf(M, m), use = top == -__builtin_inff() ? 0.0f : top;
+            const float f = __builtin_amdgcn_exp2f(M - use), h = __builtin_amdgcn_exp2f(m - use);
+            M = top;
+            L = L * f + l * h;
+            v = v * f + o * h;
+        }
+        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        const int64_t at = t * p.Hq + kvh * p.G + (row - t * p.G);
+        const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+        store_n<4>(p.out + at * D + 4 * c, out);
+        if (c == 0 && p.lse) p.lse[at] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
+        if (!HEADS) break;
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    const int64_t t = row / p.G, at = t * p.Hq + kvh * p.G + (row - t * p.G);
-    const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-    store_n<4>(p.out + at * D + 4 * c, out);
-    if (c == 0 && p.lse) p.lse[at] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
 }
 
 constexpr int kWideRows = 32 * kWaves;
@@ -898,7 +901,7 @@ inline Plan plan_of(const AttendCall& c, int rows) {
     // tokens on 16,000 and 2000, 421 us whole, 210 split; one of 2048 on 2000 109 / 84; six of up to 500 on up
     // to 2000 79 / 85; three of up to 2048 on up to 8192, 960 tiles, 413 / 437.  Where they do, and each of several requests
     // brings many, only tiles longer than a place's share are, which the host cannot see: 2048 and 512 tokens on up to
-    // 16,384 484 / 398, five of 512 to 2048 on 1024 to 8192, where none is, 564 / 571 for the empty second launch
+    // 16,384 494 / 409, five of 512 to 2048 on 1024 to 8192, where none is, 579 / 582 for the empty second launch
     if (rows == kWideRows && all > kSlots) r.target = seqs > 1 && c.T * G > 512 * seqs ? int((kSlots + c.Hkv - 1) / c.Hkv) : 1;
     const bool split = kt > kWhole && r.target > 1;
     // a tile has one item more than the work's share at the most, a split one twice as many
@@ -941,7 +944,10 @@ hipError_t run_wide(const AttendCall& c, const Args& p, const Plan& plan, hipStr
     if (const hipError_t e = launch_kernel(attend_wide<D>, dim3(unsigned(plan.items * c.Hkv)), dim3(kThreads), stream, p)) return e;
     if (plan.parts == 0) return hipSuccess;
     constexpr int SIDE = 4 * kThreads / D;
-    return launch_kernel(join_rows<D, kWideRows>, dim3(unsigned((c.T * p.G + SIDE - 1) / SIDE), unsigned(c.Hkv)), dim3(kThreads), stream, p);
+    // (where most rows have nothing to join, one workgroup sees to all heads: 3 us in place of 6 for nothing)
+    const bool few = c.T * p.G / kWideRows * c.Hkv > kSlots;
+    return launch_kernel(few ? join_rows<D, kWideRows, true> : join_rows<D, kWideRows, false>, dim3(unsigned((c.T * p.G + SIDE - 1) / SIDE), few ? 1 : unsigned(c.Hkv)),
+                         dim3(kThreads), stream, p);
 }
 
 template <int D>
