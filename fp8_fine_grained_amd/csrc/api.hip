@@ -7,6 +7,7 @@
 #include "fp8fg.h"
 #include "launch.hpp"
 
+#include <initializer_list>
 #include <stdint.h>
 
 namespace {
@@ -550,6 +551,21 @@ static int page_log(int64_t page) {
     return -1;
 }
 
+// An int32 buffer, and whether one of those that a call writes shares memory with one that it reads:
+// a workgroup would read what another has written already
+struct Ints {
+    const int32_t* p;
+    int64_t n;
+};
+static bool shared(std::initializer_list<Ints> writes, std::initializer_list<Ints> reads) {
+    for (const Ints& w : writes)
+        for (const Ints& r : reads) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(w.p), b = reinterpret_cast<uintptr_t>(r.p);
+            if (w.n > 0 && r.n > 0 && a < b + 4 * r.n && b < a + 4 * w.n) return true;
+        }
+    return false;
+}
+
 // B requests with a block table of `width` entries each
 static int table_args(int64_t B, int64_t width, int64_t page) {
     if (B < 0 || width < 0) return FP8FG_ERR_SHAPE;
@@ -569,6 +585,9 @@ int kv_assign_pages(const int32_t* have, const int32_t* add, int64_t B, const in
         !aligned16(cu) || !aligned16(positions) || !aligned16(slots) || !aligned16(left))
         return FP8FG_ERR_ALIGN;
     if (F > kMaxDim || T >= int64_t(1) << 23) return FP8FG_ERR_UNSUPPORTED;
+    if (shared({{table, B * width}, {lens, B}, {cu, B + 1}, {positions, T}, {slots, T}, {left, 2}},
+               {{have, B}, {add, B}, {free_pages, F}, {n_free, 1}}))
+        return FP8FG_ERR_UNSUPPORTED;
     return hip_status(fp8fg::launch_kv_assign(have, add, B, free_pages, n_free, F, page_log(page), table, width, T, lens, cu, positions,
                                               slots, left, static_cast<hipStream_t>(stream)));
 }
@@ -582,7 +601,8 @@ int kv_release_pages(const int32_t* done, const int32_t* lens, const int32_t* ta
     if (!aligned16(done) || !aligned16(lens) || !aligned16(table) || !aligned16(free_pages) || !aligned4(n_free) || !aligned16(lens_out) ||
         !aligned16(left))
         return FP8FG_ERR_ALIGN;
-    if (F > kMaxDim) return FP8FG_ERR_UNSUPPORTED;
+    if (F > kMaxDim || shared({{free_pages, F}, {lens_out, B}, {left, 1}}, {{done, B}, {lens, B}, {table, B * width}, {n_free, 1}}))
+        return FP8FG_ERR_UNSUPPORTED;
     return hip_status(fp8fg::launch_kv_release(done, lens, table, B, width, page_log(page), free_pages, F, n_free, lens_out, left,
                                                static_cast<hipStream_t>(stream)));
 }
@@ -607,6 +627,7 @@ int rope(const void* q, int64_t ldq, void* q_out, int64_t ldqo, int64_t Hq, cons
     if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out) || !aligned16(positions) || !aligned16(freqs))
         return FP8FG_ERR_ALIGN;
     if (T == 0 || Hq + Hkv == 0) return FP8FG_OK;
+    if ((Hq > 0 && q == q_out && ldq != ldqo) || (Hkv > 0 && k == k_out && ldk != ldko)) return FP8FG_ERR_UNSUPPORTED;
     return hip_status(fp8fg::launch_rope({q, k, q_out, k_out, ldq, ldk, ldqo, ldko, T, Hq, Hkv, D, rot, x_bf16, interleaved, inverse, scale,
                                           positions, freqs}, static_cast<hipStream_t>(stream)));
 }

@@ -626,7 +626,7 @@ int fp8_grouped_gemm_wgrad(const uint8_t* a, const float* sa, const uint8_t* b, 
  *   slots: int32 [T], the rows' places, -1 from cu[B] on and where refused;
  *   left: int32 [2], the pages that are left free (the first left[0] of free_pages) and
  *     the number that was missing (0 where every request got its pages).
- * `left` and `lens` may not overlap n_free and have.  B = 0 or T = 0 writes the outputs
+ * What is written may not overlap what is only read.  B = 0 or T = 0 writes the outputs
  * that exist.  Requires T < 2^23.
  */
 int kv_assign_pages(const int32_t* have, const int32_t* add, int64_t B, const int32_t* free_pages, const int32_t* n_free,
@@ -642,7 +642,7 @@ int kv_assign_pages(const int32_t* have, const int32_t* add, int64_t B, const in
  *   lens_out: int32 [B] = 0 where done, lens (at least 0) elsewhere;
  *   left: int32 [1], the pages that are free now.
  * The table is not written (entries past a request's length mean nothing).
- * `left` and lens_out may not overlap n_free and lens.
+ * What is written may not overlap what is only read.
  */
 int kv_release_pages(const int32_t* done, const int32_t* lens, const int32_t* table, int64_t B, int64_t width, int64_t page,
                      int32_t* free_pages, int64_t F, const int32_t* n_free, int32_t* lens_out, int32_t* left, void* stream);

@@ -206,3 +206,30 @@ def test_positions_are_rounded_to_tiles():
         for f in (assign, attend):
             assert f(B=1, page=page, width=most + 1) == EUNSUP
         assert attend(B=1, page=page, width=most) == OK
+
+
+def test_buffers_that_overlap():
+    """Outputs on top of inputs are refused: some workgroups would read what others have written."""
+    def at(i):
+        return ctypes.c_void_p(0x100000 * (i + 1))
+
+    names = ("have", "add", "free", "nf", "table", "lens", "cu", "pos", "slots", "left")
+    apart = {k: at(i) for i, k in enumerate(names)}
+    for out, inp in (("lens", "have"), ("lens", "add"), ("left", "nf"), ("cu", "add"), ("slots", "free"), ("table", "have"), ("pos", "have")):
+        assert assign(**dict(apart, **{out: apart[inp]})) == EUNSUP, (out, inp)
+    # the last of four lengths, and of a hundred pages
+    assert assign(**dict(apart, cu=ctypes.c_void_p(apart["have"].value - 16))) == EUNSUP
+    assert assign(**dict(apart, have=ctypes.c_void_p(apart["free"].value + 384), pos=ctypes.c_void_p(apart["free"].value + 384))) == EUNSUP
+    names = ("done", "lens", "table", "free", "nf", "out", "left")
+    apart = {k: at(i) for i, k in enumerate(names)}
+    for out, inp in (("out", "lens"), ("left", "nf"), ("free", "table"), ("out", "done")):
+        got = call("kv_release_pages", "done lens table B width page free F nf out left",
+                   dict(apart, B=4, width=8, page=64, F=100, **{out: apart[inp]}))
+        assert got == EUNSUP, (out, inp)
+
+
+def test_rope_in_place_keeps_its_rows():
+    order = "q ldq qo ldqo Hq k ldk ko ldko Hkv bf16 pos freqs T D rot inter scale inv"
+    good = dict(q=P, ldq=512, qo=P, ldqo=512, Hq=4, k=P, ldk=256, ko=P, ldko=256, Hkv=2, bf16=1, pos=P, freqs=P, T=3, D=128, rot=64, inter=0,
+                scale=1.0, inv=0)
+    assert call("rope", order, good, ldqo=520) == EUNSUP and call("rope", order, good, ldk=264) == EUNSUP
