@@ -777,7 +777,7 @@ def kv_assign_pages(have, add, table, free_pages, n_free, page, T, out=None):
     cache holds of each request, and new ones; table int32 [B][width], to which the new pages are
     added; free_pages int32 [F], of which the first n_free (int32 [1]) are free; T rows
     -> (lens int32 [B], cu int32 [B+1], positions int32 [T], slots int32 [T], left int32
-    [2]: pages left free, pages missing).  out: the five buffers to write."""
+    [2]: pages left free, pages missing).  out: the five buffers to write, none of them an input."""
     B, width = table.shape
     F = free_pages.shape[0]
     at = _device_of(table, "table")
@@ -801,7 +801,7 @@ def kv_assign_pages(have, add, table, free_pages, n_free, page, T, out=None):
 def kv_release_pages(done, lens, table, free_pages, n_free, page, out=None):
     """The pages of the requests that are done (int32 [B], 0 or not) back to the free
     list, which is extended in place -> (lens int32 [B], 0 where done; left int32 [1],
-    the pages that are free now).  out: the two buffers to write."""
+    the pages that are free now).  out: the two buffers to write, neither of them an input."""
     B, width = table.shape
     F = free_pages.shape[0]
     at = _device_of(table, "table")

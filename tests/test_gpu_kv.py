@@ -571,6 +571,58 @@ def test_list_across_chunks():
         assert torch.equal(out[:used], fp8.fp8_kv_attention(*gpu[k])[:used])
 
 
+def test_empty_problems():
+    """No requests, no rows: what exists is written, nothing else."""
+    none, free, n = ints([]), ints([5, 6, 7]), ints([3])
+    table = ints([]).reshape(0, 4)
+    lens, cu, positions, slots, left = fp8.kv_assign_pages(none, none, table, free, n, 16, 3)
+    assert lens.numel() == 0 and cu.tolist() == [0] and positions.tolist() == slots.tolist() == [-1] * 3 and left.tolist() == [3, 0]
+    table = ints([[-1, -1], [4, -1]])
+    lens, cu, positions, slots, left = fp8.kv_assign_pages(ints([0, 9]), ints([2, 0]), table, free, n, 16, 0)
+    assert lens.tolist() == [0, 9] and cu.tolist() == [0, 0, 0] and positions.numel() == slots.numel() == 0 and left.tolist() == [3, 0]
+    assert table.tolist() == [[-1, -1], [4, -1]]
+    lens, left = fp8.kv_release_pages(none, none, ints([]).reshape(0, 4), free, n, 16)
+    assert lens.numel() == 0 and left.tolist() == [3] and free.tolist() == [5, 6, 7]
+    cache = fp8.kv_cache(2, 1, 16, 64, DEV)
+    x = torch.ones(0, 1, 64, dtype=torch.bfloat16, device=DEV)
+    assert fp8.rope(x, x, none, torch.ones(32, device=DEV))[0].shape == x.shape
+    fp8.fp8_kv_append(x, x, none, *cache)
+    assert all(int(t.count_nonzero()) == 0 for t in cache)
+    assert fp8.fp8_kv_attention(x, *cache, ints([[0]]), ints([0, 0]), ints([7])).shape == x.shape
+    out = torch.full((2, 1, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    fp8.fp8_kv_attention(out.clone(), *cache, ints([]).reshape(0, 1), ints([0]), none, out=out)
+    assert bool((out == 3.0).all())
+
+
+def test_most_requests():
+    """65,536 requests of one token each through every call: the token sees itself alone, so that
+    the output is its value as the cache holds it, and lse the one score."""
+    B, page, D = 65536, 16, 64
+    g = torch.Generator(device=DEV).manual_seed(17)
+    free = torch.randperm(B, generator=g, device=DEV).int()
+    have, add = torch.zeros(B, dtype=torch.int32, device=DEV), torch.ones(B, dtype=torch.int32, device=DEV)
+    table = torch.full((B, 1), -1, dtype=torch.int32, device=DEV)
+    lens, cu, positions, slots, left = fp8.kv_assign_pages(have, add, table, free, ints([B]), page, B)
+    assert torch.equal(table[:, 0], free.flip(0)) and torch.equal(slots, table[:, 0] * page) and left.tolist() == [0, 0]
+    assert torch.equal(cu, torch.arange(B + 1, dtype=torch.int32, device=DEV)) and int(positions.abs().max()) == 0
+    cache = fp8.kv_cache(B, 1, page, D, DEV)
+    x = torch.randn(B, 3, D, generator=g, device=DEV).bfloat16()
+    fp8.fp8_kv_append(x[:, 1:2], x[:, 2:], slots, *cache)
+    lse = torch.empty(B, 1, device=DEV)
+    out, _ = fp8.fp8_kv_attention(x[:, :1], *cache, table, cu, lens, lse=lse)
+    at = table[:, 0].long()
+    k = e4m3.decode(host(cache[0][at, 0, 0])) * host(cache[1][at]).astype(np.float64)
+    v = e4m3.decode(host(cache[2][at, 0, :, 0])) * host(cache[3][at]).astype(np.float64)
+    # p = 1 up to FP32 roundings and a power of two as the scale: values of four bits are BF16's own
+    assert np.array_equal(host(out)[:, 0], v)
+    score = D ** -0.5 * (host(x[:, 0]) * k).sum(1)
+    size = D ** -0.5 * np.abs(host(x[:, 0]) * k).sum(1)
+    # as in attention_check, with one token
+    held(host(lse)[:, 0] - score, 2 * ((D + 8) * EPS * size + 4 * EPS) + 65 * EPS + 8 * EPS * np.abs(score), "lse")
+    lens, left = fp8.kv_release_pages(add, lens, table, free, ints([0]), page)
+    assert torch.equal(free, table[:, 0]) and int(lens.abs().max()) == 0 and left.tolist() == [B]
+
+
 def test_offsets_past_32_bits():
     """Pages far into a cache of more than 4 GB: writes and reads land where the small cache's do."""
     H, page, D, n = 4, 256, 256, 17000
