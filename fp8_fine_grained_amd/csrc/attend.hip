@@ -288,9 +288,11 @@ __device__ __forceinline__ float halves_max(float v) {
     return fmaxf(__uint_as_float(a), __uint_as_float(b));
 }
 
-// O is held in units of `ref`: the largest of the tile's value scales, while that lies
-// within [ref / 64, ref] the one before, so that the sums are seldom multiplied; but no
-// less than 2^-40 of the largest so far (FP32 holds the sums in such units) and 2^-100
+// A row of O is held in units of its own `ref`: the largest value scale of the tile's pages that
+// the row sees a token of, while that lies within [ref / 64, ref] the one before, so that the sums
+// are seldom multiplied; but no less than 2^-40 of the largest so far (FP32 holds the sums in such units)
+// and 2^-100.  (A unit from all of the tile's pages would take the probabilities of a row below
+// FP16's range for a page that only later tokens see.)
 __device__ __forceinline__ float unit_of(float top, float largest, float ref) {
     const float want = fmaxf(fmaxf(top, largest * 0x1p-40f), 0x1p-100f);
     return want > ref || want < ref * 0x1p-6f ? want : ref;
@@ -344,11 +346,11 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
                 qf[r][c][h] = __builtin_bit_cast(v8bf, w);
             }
     v4f o[NR][DT];
-    float m[NR], l[NR], ref = 0.0f, largest = 0.0f;
+    float m[NR], l[NR], ref[NR], largest[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         m[r] = -__builtin_inff();
-        l[r] = 0.0f;
+        l[r] = ref[r] = largest[r] = 0.0f;
 #pragma unroll
         for (int i = 0; i < DT; ++i) o[r][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -421,12 +423,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
             }
         }
         if (!kAhead) load_values();
-        const float top = groups_max(vsc);
-        largest = fmaxf(largest, top);
-        const float unit = unit_of(top, largest, ref), inverse = __builtin_amdgcn_rcpf(unit);
-        const float moved = unit == ref ? 1.0f : ref * inverse;
-        ref = unit;
-        const float ratio = vsc * inverse;
+        const float all = groups_max(vsc);
         // scores in units of log2; keys out of sight at -inf
         const bool masked = t0 + kTile - 1 > least || !__all(good);
         v8h pf[NR][2];
@@ -448,7 +445,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
             const float m_new = mt > m[r] + kSlack ? mt : m[r], m_use = m_new == -__builtin_inff() ? 0.0f : m_new;
             const float alpha = __builtin_amdgcn_exp2f(m[r] - m_use);
             m[r] = m_new;
-            factor[r] = alpha * moved;
+            const float top = masked ? groups_max(seen >= 0 ? vsc : 0.0f) : all;
+            largest[r] = fmaxf(largest[r], top);
+            const float unit = unit_of(top, largest[r], ref[r]), inverse = __builtin_amdgcn_rcpf(unit);
+            factor[r] = unit == ref[r] ? alpha : alpha * (ref[r] * inverse);
+            ref[r] = unit;
+            const float ratio = fminf(vsc * inverse, 1.0f);        // (above 1: a page out of sight)
             same = same && factor[r] == 1.0f;
             float sum = 0.0f;
 #pragma unroll
@@ -512,7 +514,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
         const int row = 16 * r + col;
         float M, L;
         joint(row, M, L);
-        const float mine = __builtin_amdgcn_exp2f(m[r] - (M == -__builtin_inff() ? 0.0f : M)) * ref;
+        const float mine = __builtin_amdgcn_exp2f(m[r] - (M == -__builtin_inff() ? 0.0f : M)) * ref[r];
 #pragma unroll
         for (int d = 0; d < DT; ++d)  // [row][channel], the 16-byte pieces of a row swapped by row
             st<v4f>(&joined[wave][row * D + (((4 * d + g) ^ col) * 4)], o[r][d] * mine);
@@ -692,10 +694,13 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
         __builtin_amdgcn_sched_group_barrier(0x008, 6, 0);
+        float vis = fmaxf(vsc[0], vsc[1]);            // of the pages in sight
         if (t0 + kTile - 1 > least || !__all(vsc[0] >= 0.0f && vsc[1] >= 0.0f)) {
+            vis = 0.0f;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int seen = vsc[t] >= 0.0f ? last - (t0 + 32 * t + 16 * h) : -1;
+                vis = seen >= 0 ? fmaxf(vis, vsc[t]) : vis;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (i > seen) s[t][i] = -__builtin_inff();
@@ -713,7 +718,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
         const float m_new = mt > m + kSlack ? mt : m, m_use = m_new == -__builtin_inff() ? 0.0f : m_new;
         const float alpha = __builtin_amdgcn_exp2f(m - m_use);
         m = m_new;
-        const float top = halves_max(fmaxf(0.0f, fmaxf(vsc[0], vsc[1])));
+        const float top = halves_max(vis);
         largest = fmaxf(largest, top);
         const float unit = unit_of(top, largest, ref);
         const float factor = unit == ref ? alpha : alpha * (ref * __builtin_amdgcn_rcpf(unit));
@@ -724,14 +729,15 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
         }
         if (tile + 1 < kt1) cut(tile + 1, id);
         // Probabilities are formed times their page's value scale over `ref`, as a term of the
-        // exponent (below 2^-60 FP16 has nothing left of them), and summed without it.  The second
+        // exponent (below 2^-60 FP16 has nothing left of them, above 1 the page is out of sight), and
+        // summed without it.  The second
         // half's run beside the first half's products, and beside its own products the next
         // tile is widened (what is put past the end is not used).
         v8h pf[2][2];
         l *= alpha;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const float ratio = fmaxf(vsc[t] * __builtin_amdgcn_rcpf(ref), 0x1p-60f);
+            const float ratio = __builtin_amdgcn_fmed3f(vsc[t] * __builtin_amdgcn_rcpf(ref), 0x1p-60f, 1.0f);
             const float bias = kPBias - m_use + __builtin_amdgcn_logf(ratio);
             float sum = 0.0f;
 #pragma unroll

@@ -699,11 +699,13 @@ int fp8_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int x_
  * the most.  A token that sees nothing gets 0, and -inf for lse.
  * What lies in the cache past a request's last token has no influence.
  * Scales may be any finite non-negative FP32 values.
- * Accuracy: codes are multiplied exactly and summed in FP32; probabilities are
- * rounded to FP16's 11 bits, and where they are below 2^-18 of the row's largest, p_max, to 2^-29
- * of it:  |out - out*| <= 2^-10 * sum_j p_j |v_j| + 2^-28 * p_max * n * max_j |v_j| + 2^-100
- * over the n keys seen, before the one rounding to BF16, for scores below 2^6 (larger ones: their
- * FP32 rounding, 2^-22 |x|, is the relative error of p).
+ * Accuracy: codes are multiplied exactly and summed in FP32; a probability times its page's value
+ * scale is rounded to FP16's 11 bits, and where it is below 2^-25 of p_max * S to 2^-36 of it, with p_max the row's
+ * largest probability and S the largest value scale of the pages of which the row sees a token:
+ *   |out - out*| <= (2^-11 + 2^-22 (D + 8) X + 2^-24 (n + 128)) * sum_j p_j |v_j|
+ *                   + 2^-27 * p_max * n * max(S, 2^-100) + 2^-100
+ * over the n keys seen, X the largest scale * sum_d |q_d k_jd|, before the one rounding to BF16.  Pages that a
+ * row sees no token of leave its bits as they are.
  * workspace: fp8_kv_attention_workspace bytes (may be 0, then NULL), contents unspecified before
  * and after; calls that may run at the same time need one each.
  * Requires Hq % Hkv == 0, T * (Hq / Hkv) < 2^24, 0 <= scale <= 2^64, rows of q at least Hq * D elements and

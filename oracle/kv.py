@@ -155,3 +155,30 @@ def attention(q, k_cache, k_scale, v_cache, v_scale, table, cu, lens, scale):
                     out[t, j], lse[t, j] = p @ vv, top + np.log(e.sum())
                     size[t, j], score[t, j] = p @ np.abs(vv), scale * (np.abs(kk) @ np.abs(q[t, j])).max()
     return out, lse, size, score
+
+
+def seen(q, k_cache, k_scale, v_scale, table, cu, lens, scale):
+    """What an error of attention is measured by: (keys [T] that a row sees, p_max [T][Hq], the largest of its
+    probabilities, top [T][Hq], the largest value scale of the pages of which it sees a token); 0 where it sees nothing."""
+    q = np.asarray(q, np.float64)
+    T, Hq, _ = q.shape
+    n, Hkv, page, _ = k_cache.shape
+    G = Hq // Hkv
+    keys, p_max, top = np.zeros(T, np.int64), np.zeros((T, Hq)), np.zeros((T, Hq))
+    for b in range(len(lens)):
+        length = min(max(int(lens[b]), 0), table.shape[1] * page)
+        new = int(cu[b + 1] - cu[b])
+        for h in range(Hkv):
+            k, live = values(k_cache, k_scale, table[b], length, page, h)
+            s = np.zeros(length)
+            for j in np.nonzero(live)[0]:
+                s[j] = float(v_scale[table[b][j // page], h])
+            for i in range(new):
+                t, m = int(cu[b]) + i, max(0, length - new + i + 1)
+                if not live[:m].any():
+                    continue
+                keys[t] = live[:m].sum()
+                x = scale * (k[:m][live[:m]] @ q[t, h * G: (h + 1) * G].T)
+                p_max[t, h * G: (h + 1) * G] = 1.0 / np.exp(x - x.max(0)).sum(0)
+                top[t, h * G: (h + 1) * G] = s[:m][live[:m]].max()
+    return keys, p_max, top
