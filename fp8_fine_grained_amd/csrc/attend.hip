@@ -37,6 +37,9 @@ constexpr int kSlots = 512;               // workgroups that run at a time: two 
 // down to 2^-25.  (Were every new maximum taken, some row of a tile would have one most of
 // the time, and all sums be multiplied.)
 constexpr float kPBias = 11.0f, kSlack = 4.0f;
+// What waves and parts join is a sum of 2^31 values at the most, each below 2^128 and times a probability held as up to
+// 2^15: it is held times 2^-48, so that it stays in FP32's range until the division by the probabilities' sum
+constexpr float kDown = 0x1p-48f, kUp = 0x1p48f;
 
 struct Args {
     const uint16_t* q;
@@ -50,7 +53,7 @@ struct Args {
     float* lse;
     int32_t* list;                        // workspace: number of items, and from list + 8 on the items; null: not listed
     int32_t* desc;                        // [T][G] x (splits, first part, row of it)
-    float* parts;                         // unjoined results
+    float* parts;                         // unjoined results: maxima, sums of probabilities, sums of values times kDown
     int64_t most_parts;                   // room for them
     int target;                           // workgroups wanted for each key/value head
 };
@@ -297,6 +300,8 @@ __device__ __forceinline__ float unit_of(float top, float largest, float ref) {
     const float want = fmaxf(fmaxf(top, largest * 0x1p-40f), 0x1p-100f);
     return want > ref || want < ref * 0x1p-6f ? want : ref;
 }
+// 1 / unit, to 2^-21 of it: from 2^126 on a subnormal number, which the instruction would flush
+__device__ __forceinline__ float per_unit(float unit) { return __builtin_amdgcn_rcpf(unit * 0x1p-8f) * 0x1p-8f; }
 
 // the bytes of w (tokens first .. first + 3) that lie before `end`
 __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int first, int end) {
@@ -447,7 +452,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
             m[r] = m_new;
             const float top = masked ? groups_max(seen >= 0 ? vsc : 0.0f) : all;
             largest[r] = fmaxf(largest[r], top);
-            const float unit = unit_of(top, largest[r], ref[r]), inverse = __builtin_amdgcn_rcpf(unit);
+            const float unit = unit_of(top, largest[r], ref[r]), inverse = per_unit(unit);
             factor[r] = unit == ref[r] ? alpha : alpha * (ref[r] * inverse);
             ref[r] = unit;
             const float ratio = fminf(vsc * inverse, 1.0f);        // (above 1: a page out of sight)
@@ -514,10 +519,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
         const int row = 16 * r + col;
         float M, L;
         joint(row, M, L);
-        const float mine = __builtin_amdgcn_exp2f(m[r] - (M == -__builtin_inff() ? 0.0f : M)) * ref[r];
+        const float mine = __builtin_amdgcn_exp2f(m[r] - (M == -__builtin_inff() ? 0.0f : M)) * kDown;
 #pragma unroll
         for (int d = 0; d < DT; ++d)  // [row][channel], the 16-byte pieces of a row swapped by row
-            st<v4f>(&joined[wave][row * D + (((4 * d + g) ^ col) * 4)], o[r][d] * mine);
+            st<v4f>(&joined[wave][row * D + (((4 * d + g) ^ col) * 4)], o[r][d] * mine * ref[r]);
         if (wave == 0 && g == 0) {
             if (split) {
                 part[row] = M;
@@ -546,7 +551,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
         float M, L;
         joint(r, M, L);
         const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-        const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+        const float out[4] = {v[0] * inv * kUp, v[1] * inv * kUp, v[2] * inv * kUp, v[3] * inv * kUp};
         store_n<4>(p.out + (int64_t(it.cu + t) * p.Hq + kvh * p.G + rows.head_of(r, t)) * D + 4 * c, out);
     }
 }
@@ -721,7 +726,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
         const float top = halves_max(vis);
         largest = fmaxf(largest, top);
         const float unit = unit_of(top, largest, ref);
-        const float factor = unit == ref ? alpha : alpha * (ref * __builtin_amdgcn_rcpf(unit));
+        const float inverse = per_unit(unit), factor = unit == ref ? alpha : alpha * (ref * inverse);
         ref = unit;
         if (!__all(factor == 1.0f)) {
 #pragma unroll
@@ -737,7 +742,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
         l *= alpha;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const float ratio = __builtin_amdgcn_fmed3f(vsc[t] * __builtin_amdgcn_rcpf(ref), 0x1p-60f, 1.0f);
+            const float ratio = __builtin_amdgcn_fmed3f(vsc[t] * inverse, 0x1p-60f, 1.0f);
             const float bias = kPBias - m_use + __builtin_amdgcn_logf(ratio);
             float sum = 0.0f;
 #pragma unroll
@@ -777,14 +782,15 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
 #pragma unroll
             for (int b = 0; b < 4; ++b)
                 st<v4f>(part + 2 * ROWS + r * D + 32 * d + 8 * b + 4 * h,
-                        v4f{o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]} * ref);
+                        v4f{o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]} * kDown * ref);
     } else {
-        const float inv = l > 0.0f ? ref / l : 0.0f;
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                const float out[4] = {o[d][4 * b] * inv, o[d][4 * b + 1] * inv, o[d][4 * b + 2] * inv, o[d][4 * b + 3] * inv};
+                const float out[4] = {o[d][4 * b] * inv * ref, o[d][4 * b + 1] * inv * ref, o[d][4 * b + 2] * inv * ref,
+                                      o[d][4 * b + 3] * inv * ref};
                 store_n<4>(p.out + at * D + 32 * d + 8 * b + 4 * h, out);
             }
         if (h == 0 && p.lse) p.lse[at] = l > 0.0f ? (m + __log2f(l) - kPBias) * 0.6931471805599453f : -__builtin_inff();
@@ -843,7 +849,7 @@ __global__ __launch_bounds__(kThreads) void join(const Args p) {
     }
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     const int64_t t = row / p.G, at = t * p.Hq + kvh * p.G + (row - t * p.G);
-    const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+    const float out[4] = {v[0] * inv * kUp, v[1] * inv * kUp, v[2] * inv * kUp, v[3] * inv * kUp};
     store_n<4>(p.out + at * D + 4 * c, out);
     if (c == 0 && p.lse) p.lse[at] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
 }
@@ -877,7 +883,7 @@ __global__ __launch_bounds__(kThreads) void join_rows(const Args p) {
         }
         const float inv = L > 0.0f ? 1.0f / L : 0.0f;
         const int64_t at = t * p.Hq + kvh * p.G + (row - t * p.G);
-        const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+        const float out[4] = {v[0] * inv * kUp, v[1] * inv * kUp, v[2] * inv * kUp, v[3] * inv * kUp};
         store_n<4>(p.out + at * D + 4 * c, out);
         if (c == 0 && p.lse) p.lse[at] = L > 0.0f ? (M + __log2f(L) - kPBias) * 0.6931471805599453f : -__builtin_inff();
         if (!HEADS) break;

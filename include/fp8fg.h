@@ -698,7 +698,7 @@ int fp8_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int x_
  * Tokens in pages outside [0, n_pages) are not seen, and a length counts as width * page at
  * the most.  A token that sees nothing gets 0, and -inf for lse.
  * What lies in the cache past a request's last token has no influence.
- * Scales may be any finite non-negative FP32 values.
+ * Scales may be any finite non-negative FP32 values with which the values themselves are finite.
  * Accuracy: codes are multiplied exactly and summed in FP32; a probability times its page's value
  * scale is rounded to FP16's 11 bits, and where it is below 2^-25 of p_max * S to 2^-36 of it, with p_max the row's
  * largest probability and S the largest value scale of the pages of which the row sees a token:

@@ -93,3 +93,25 @@ def test_pages_that_a_row_does_not_see_leave_its_bits(page, Hq, Hkv, D, old, new
             assert all(torch.equal(x[cu[b] + i], y[cu[b] + i]) for x, y in zip(*outs)), (b, i)
             rows += 1
     assert rows > 0
+
+
+# value scale, largest code: values up to 3.2e38, and those of the smallest scales, which the bound's last terms cover
+@pytest.mark.parametrize("top,code", [(2.0 ** 110, 0x7E), (2.0 ** 119, 0x7E), (2.0 ** 120, 0x77), (1.9 * 2.0 ** 126, 0x40), (1.9 * 2.0 ** 127, 0x38),
+                                      (1.37 * 2.0 ** -95, 0x7E), (2.0 ** -126, 0x7E)])
+@each_form
+def test_scales_at_the_ends_of_fp32(top, code, Hq, Hkv, D, old, new):
+    """Values up to FP32's largest: no sum on the way leaves its range."""
+    case = spread(np.random.default_rng(D), old, new, Hq, Hkv, D, 32, lambda e, pages: top)
+    v = case[3]
+    v[...] = (v & 0x80) | np.minimum(v & 0x7F, code)
+    bound_check(case)
+
+
+def test_one_token_of_the_largest_values():
+    """Written by the library: a request's only token comes back as it was, up to the cache's rounding."""
+    x = torch.tensor([3.1e38, -3.1e38, 1.0, 2.0 ** 113], device=DEV).repeat(2, 1, 16)           # [2][1][64]
+    cache = fp8.kv_cache(2, 1, 16, 64, DEV)
+    fp8.fp8_kv_append(x * 2.0 ** -127, x, ints([0, 16]), *cache)
+    out = fp8.fp8_kv_attention(torch.ones(2, 1, 64, dtype=torch.bfloat16, device=DEV), *cache, ints([[0], [1]]), ints([0, 1, 2]), ints([1, 1]))
+    want = kv.values(host(cache[2]), host(cache[3]), np.array([0]), 1, 16, 0, turned=True)[0]
+    assert np.abs(want).max() > 3e38 and np.array_equal(host(out)[0], want) and np.array_equal(host(out)[1], want)
