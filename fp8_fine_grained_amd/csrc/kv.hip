@@ -319,8 +319,44 @@ __device__ __forceinline__ float pow2_scale(float amax) {
     e = e < 1 ? 1 : e;
     return __uint_as_float(uint32_t(e) << 23);
 }
-// the power of two that takes values to codes: 1 / s, exact for s in [2^-126, 2^119]
-__device__ __forceinline__ float inverse_of(float s) { return s == 0.0f ? 1.0f : 1.0f / s; }
+// Values to codes' quotients x / s: by the scale's power of two, an exact product, which is all of a scale written here (2^-126
+// to 2^120, or 0).  The older tokens' scale of a cache that was filled otherwise may be any other number; what is left of it,
+// f in (1, 2), divides by a product with its rounded inverse and one remainder step, which rounds as a division does
+// (Markstein's theorem; below 2^-100, where remainders lose bits, the code is 0).  No quotient is above 448, for
+// s is no less than pow2_scale's; a subnormal s has values of 0 alone.
+struct Exact {
+    float r;
+    template <int N>
+    __device__ __forceinline__ void operator()(float (&v)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= r;
+    }
+};
+struct Divide : Exact {
+    float f, rf;
+    bool exact;
+    __device__ __forceinline__ explicit Divide(float s) {
+        const uint32_t two = __float_as_uint(s) & 0x7F800000;
+        exact = two == 0 || two == __float_as_uint(s);
+        r = __uint_as_float(two == 0 ? 0x3F800000 : two == 0x7F000000 ? 0x00400000 : 0x7F000000 - two);       // 1 / 2^127: subnormal
+        f = rf = 1.0f;
+        if (!exact) {
+            f = s * r;
+            rf = 1.0f / f;
+        }
+    }
+    template <int N>
+    __device__ __forceinline__ void operator()(float (&v)[N]) const {
+        Exact::operator()(v);
+        if (!exact) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float q = v[i] * rf;
+                v[i] = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q, f, v[i]), rf, q), q);      // (-0 + 0 is 0)
+            }
+        }
+    }
+};
 
 __device__ __forceinline__ uint32_t shift_codes(uint32_t w, float f) {
     const v2f lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, 1.0f, false), hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, 1.0f, true);
@@ -353,11 +389,11 @@ struct Run {
     float* part;                          // LDS for the workgroup's waves
 };
 
-// The page's scale after a run whose largest magnitude is amax (in any lane), and its
-// inverse; older codes are moved to it, 16 bytes at a time.  VALUES: [channel][token],
+// The page's scale after a run whose largest magnitude is amax (in any lane), and what
+// divides by it; older codes are moved to it, 16 bytes at a time.  VALUES: [channel][token],
 // where only the bytes of the older tokens are changed.
 template <bool VALUES, class T>
-__device__ __forceinline__ float new_scale(const Run<T>& r, float amax) {
+__device__ __forceinline__ Divide new_scale(const Run<T>& r, float amax) {
     float s = fmaxf(r.was, pow2_scale(lanes_max<64>(amax)));
     if (r.team > 64) {                    // (every wave has read the page's scale by now, before one writes it)
         __syncthreads();                  // the last use of part is over
@@ -387,7 +423,7 @@ __device__ __forceinline__ float new_scale(const Run<T>& r, float amax) {
         if (VALUES && r.team > 64) __syncthreads();
         else if (VALUES) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    return inverse_of(s);
+    return Divide(s);
 }
 
 // A run's data are read once: up to HOLD pieces of a thread stay in registers between
@@ -403,7 +439,7 @@ __device__ __forceinline__ void in_two_passes(int pieces, int me, int team, Load
 #pragma unroll
         for (int i = 0; i < HOLD; ++i)
             if (team * i < pieces) look(w[i]);
-        const float r = scale();
+        const Divide r = scale();
         // (held as they came: the compiler would keep the widened values of the first pass, 119 in place of 89 registers)
 #pragma unroll
         for (int i = 0; i < HOLD; ++i)
@@ -416,9 +452,14 @@ __device__ __forceinline__ void in_two_passes(int pieces, int me, int team, Load
     }
 #pragma unroll 4
     for (int i = me; i < pieces; i += team) look(load(i));
-    const float r = scale();
+    const Divide r = scale();
+    if (!r.exact) {
+        for (int i = me; i < pieces; i += team) put(i, load(i), r);
+        return;
+    }
+    // (a branch at each piece would hold up the next ones' loads)
 #pragma unroll 4
-    for (int i = me; i < pieces; i += team) put(i, load(i), r);
+    for (int i = me; i < pieces; i += team) put(i, load(i), Exact(r));
 }
 
 // Keys: eight channels of a token at a time
@@ -437,10 +478,11 @@ __device__ __forceinline__ void append_keys(const Run<T>& r) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(w.get(j)));
         },
-        [&](int i, const Raw<T, 8>& w, float f) {
+        [&](int i, const Raw<T, 8>& w, const auto& by_scale) {
             float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = w.get(j) * f;
+            for (int j = 0; j < 8; ++j) v[j] = w.get(j);
+            by_scale(v);
             st<u32x2_t>(r.codes + r.off * r.D + i * 8, u32x2_t{cvt4(v[0], v[1], v[2], v[3]), cvt4(v[4], v[5], v[6], v[7])});
         },
         [&] { return new_scale<false>(r, amax); });
@@ -477,16 +519,22 @@ __device__ __forceinline__ void append_values(const Run<T>& r) {
                 amax = fmaxf(amax, fmaxf(fabsf(v[0]), fabsf(v[1])));
             }
         },
-        [&](int task, const Group<T>& a, float f) {
+        [&](int task, const Group<T>& a, const auto& by_scale) {
             const int g = task / pairs, first = (g0 + g) * 16 - r.off;
             uint8_t* c = r.codes + 2 * (task - g * pairs) * r.page + (g0 + g) * 16;
             u32x4 x, y;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const v2f v0 = widen2(a.w[4 * i]) * f, v1 = widen2(a.w[4 * i + 1]) * f, v2 = widen2(a.w[4 * i + 2]) * f,
-                          v3 = widen2(a.w[4 * i + 3]) * f;
-                x[i] = cvt4(v0[0], v1[0], v2[0], v3[0]);
-                y[i] = cvt4(v0[1], v1[1], v2[1], v3[1]);
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const v2f two = widen2(a.w[4 * i + j]);
+                    v[j] = two[0];
+                    v[4 + j] = two[1];
+                }
+                by_scale(v);
+                x[i] = cvt4(v[0], v[1], v[2], v[3]);
+                y[i] = cvt4(v[4], v[5], v[6], v[7]);
             }
             if (first >= 0 && first + 16 <= r.count) {
                 st<u32x4>(c, x);
@@ -513,11 +561,12 @@ __device__ __forceinline__ void append_one(const Run<T>& r) {
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(widen2(w[i])[0]), fabsf(widen2(w[i])[1])));
-    const float f = new_scale<VALUES>(r, amax);
+    const Divide by_scale = new_scale<VALUES>(r, amax);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         if (lane + 64 * i < pairs) {
-            const v2f v = widen2(w[i]) * f;
+            float v[2] = {widen2(w[i])[0], widen2(w[i])[1]};
+            by_scale(v);
             const uint32_t two = cvt4(v[0], v[1], 0.0f, 0.0f);
             if constexpr (VALUES) {
                 uint8_t* c = r.codes + 2 * (lane + 64 * i) * r.page + r.off;

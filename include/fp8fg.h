@@ -680,6 +680,8 @@ int rope(const void* q, int64_t ldq, void* q_out, int64_t ldqo, int64_t Hq, cons
  *   code = E4M3 round-to-nearest-even of x / s.  Where the scale grows, the page's older
  *   codes are re-encoded under it (exactly, but for codes that become subnormal):
  *   powers of two, so that no value drifts as a page fills up.
+ *   A page that other code began may have any finite non-negative scale: one that is larger is kept, and codes are of the FP32
+ *   quotient x / s; a smaller one gives way to the power of two, with older codes of the FP32 product of their value and the scales' quotient.
  * Nothing but the pages' codes up to the last new token and their scales is written.  A
  * page named by two separate runs of rows in one call gets unspecified codes.
  * Requires rows as in rope.
