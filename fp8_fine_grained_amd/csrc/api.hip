@@ -566,6 +566,43 @@ static bool shared(std::initializer_list<Ints> writes, std::initializer_list<Int
     return false;
 }
 
+// n rows of `width` bytes, `step` bytes (at least width) apart
+struct Span {
+    const void* p;
+    int64_t n, width, step;
+};
+static Span span(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+// whether two of them share a byte: rows between one another's, as the heads of a fused projection, do not
+static bool meet(Span a, Span b) {
+    if (a.n <= 0 || b.n <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const int64_t d = int64_t(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));      // b's first row, from a's
+    if (d >= (a.n - 1) * a.step + a.width || -d >= (b.n - 1) * b.step + b.width) return false;
+    const auto up = [](int64_t x, int64_t y) { return x <= 0 ? -(-x / y) : (x + y - 1) / y; };
+    if (a.step == b.step) {
+        // row i of a and row i + k of b: k from the first on whose end lies behind a's start
+        int64_t k = up(1 - b.width - d, a.step);
+        if (k < 1 - a.n) k = 1 - a.n;
+        return k < b.n && d + k * a.step < a.width;
+    }
+    if (a.n > b.n) return meet(b, a);
+    for (int64_t i = 0; i < a.n; ++i) {
+        const int64_t at = i * a.step - d;               // a's row, from b's first
+        const int64_t j = at - b.width < 0 ? 0 : (at - b.width) / b.step + 1;
+        if (j < b.n && j * b.step < at + a.width) return true;
+    }
+    return false;
+}
+// one of those that a call writes, on one that it reads or on another that it writes
+static bool overlap(std::initializer_list<Span> writes, std::initializer_list<Span> reads) {
+    for (const Span* w = writes.begin(); w != writes.end(); ++w) {
+        for (const Span& r : reads)
+            if (meet(*w, r)) return true;
+        for (const Span* other = writes.begin(); other != w; ++other)
+            if (meet(*w, *other)) return true;
+    }
+    return false;
+}
+
 // B requests with a block table of `width` entries each
 static int table_args(int64_t B, int64_t width, int64_t page) {
     if (B < 0 || width < 0) return FP8FG_ERR_SHAPE;
@@ -627,7 +664,12 @@ int rope(const void* q, int64_t ldq, void* q_out, int64_t ldqo, int64_t Hq, cons
     if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out) || !aligned16(positions) || !aligned16(freqs))
         return FP8FG_ERR_ALIGN;
     if (T == 0 || Hq + Hkv == 0) return FP8FG_OK;
-    if ((Hq > 0 && q == q_out && ldq != ldqo) || (Hkv > 0 && k == k_out && ldk != ldko)) return FP8FG_ERR_UNSUPPORTED;
+    // in place, or apart
+    const auto heads = [&](const void* p, int64_t H, int64_t ld) { return Span{p, T, H * D * size, ld * size}; };
+    const Span none = span(nullptr, 0), qi = heads(q, Hq, ldq), ki = heads(k, Hkv, ldk), qo = heads(q_out, Hq, ldqo), ko = heads(k_out, Hkv, ldko);
+    if (meet(qo, q == q_out && ldq == ldqo ? none : qi) || meet(ko, k == k_out && ldk == ldko ? none : ki) || meet(qo, ki) || meet(ko, qi) ||
+        overlap({qo, ko}, {span(positions, 4 * T), span(freqs, 2 * rot)}))
+        return FP8FG_ERR_UNSUPPORTED;
     return hip_status(fp8fg::launch_rope({q, k, q_out, k_out, ldq, ldk, ldqo, ldko, T, Hq, Hkv, D, rot, x_bf16, interleaved, inverse, scale,
                                           positions, freqs}, static_cast<hipStream_t>(stream)));
 }

@@ -660,7 +660,7 @@ int kv_release_pages(const int32_t* done, const int32_t* lens, const int32_t* ta
  * and the products in FP32 (an absolute error below 2^-21 of scale * (|a| + |b|)), and
  * rounded once to the outputs' type.  Rows with a negative position are not written.
  * q_out, k_out: as q and k, rows ldqo and ldko apart, or q and k themselves (with
- * the same distance).
+ * the same distance); they may lie between one another's rows, but share no memory with each other or, otherwise, with an input.
  * Requires D % 8 == 0, D <= 1024, rot % 16 == 0, 0 < rot <= min(D, 256), rows at
  * least H * D elements and a multiple of 16 bytes apart.
  */
