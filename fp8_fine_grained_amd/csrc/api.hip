@@ -551,27 +551,13 @@ static int page_log(int64_t page) {
     return -1;
 }
 
-// An int32 buffer, and whether one of those that a call writes shares memory with one that it reads:
-// a workgroup would read what another has written already
-struct Ints {
-    const int32_t* p;
-    int64_t n;
-};
-static bool shared(std::initializer_list<Ints> writes, std::initializer_list<Ints> reads) {
-    for (const Ints& w : writes)
-        for (const Ints& r : reads) {
-            const uintptr_t a = reinterpret_cast<uintptr_t>(w.p), b = reinterpret_cast<uintptr_t>(r.p);
-            if (w.n > 0 && r.n > 0 && a < b + 4 * r.n && b < a + 4 * w.n) return true;
-        }
-    return false;
-}
-
 // n rows of `width` bytes, `step` bytes (at least width) apart
 struct Span {
     const void* p;
     int64_t n, width, step;
 };
 static Span span(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+static Span ints(const void* p, int64_t n) { return span(p, 4 * n); }
 // whether two of them share a byte: rows between one another's, as the heads of a fused projection, do not
 static bool meet(Span a, Span b) {
     if (a.n <= 0 || b.n <= 0 || a.width <= 0 || b.width <= 0) return false;
@@ -592,7 +578,8 @@ static bool meet(Span a, Span b) {
     }
     return false;
 }
-// one of those that a call writes, on one that it reads or on another that it writes
+// one of those that a call writes, on one that it reads (a workgroup would read what another has written) or
+// on another that it writes
 static bool overlap(std::initializer_list<Span> writes, std::initializer_list<Span> reads) {
     for (const Span* w = writes.begin(); w != writes.end(); ++w) {
         for (const Span& r : reads)
@@ -622,8 +609,8 @@ int kv_assign_pages(const int32_t* have, const int32_t* add, int64_t B, const in
         !aligned16(cu) || !aligned16(positions) || !aligned16(slots) || !aligned16(left))
         return FP8FG_ERR_ALIGN;
     if (F > kMaxDim || T >= int64_t(1) << 23) return FP8FG_ERR_UNSUPPORTED;
-    if (shared({{table, B * width}, {lens, B}, {cu, B + 1}, {positions, T}, {slots, T}, {left, 2}},
-               {{have, B}, {add, B}, {free_pages, F}, {n_free, 1}}))
+    if (overlap({ints(table, B * width), ints(lens, B), ints(cu, B + 1), ints(positions, T), ints(slots, T), ints(left, 2)},
+                {ints(have, B), ints(add, B), ints(free_pages, F), ints(n_free, 1)}))
         return FP8FG_ERR_UNSUPPORTED;
     return hip_status(fp8fg::launch_kv_assign(have, add, B, free_pages, n_free, F, page_log(page), table, width, T, lens, cu, positions,
                                               slots, left, static_cast<hipStream_t>(stream)));
@@ -638,7 +625,8 @@ int kv_release_pages(const int32_t* done, const int32_t* lens, const int32_t* ta
     if (!aligned16(done) || !aligned16(lens) || !aligned16(table) || !aligned16(free_pages) || !aligned4(n_free) || !aligned16(lens_out) ||
         !aligned16(left))
         return FP8FG_ERR_ALIGN;
-    if (F > kMaxDim || shared({{free_pages, F}, {lens_out, B}, {left, 1}}, {{done, B}, {lens, B}, {table, B * width}, {n_free, 1}}))
+    if (F > kMaxDim || overlap({ints(free_pages, F), ints(lens_out, B), ints(left, 1)},
+                               {ints(done, B), ints(lens, B), ints(table, B * width), ints(n_free, 1)}))
         return FP8FG_ERR_UNSUPPORTED;
     return hip_status(fp8fg::launch_kv_release(done, lens, table, B, width, page_log(page), free_pages, F, n_free, lens_out, left,
                                                static_cast<hipStream_t>(stream)));
@@ -668,7 +656,7 @@ int rope(const void* q, int64_t ldq, void* q_out, int64_t ldqo, int64_t Hq, cons
     const auto heads = [&](const void* p, int64_t H, int64_t ld) { return Span{p, T, H * D * size, ld * size}; };
     const Span none = span(nullptr, 0), qi = heads(q, Hq, ldq), ki = heads(k, Hkv, ldk), qo = heads(q_out, Hq, ldqo), ko = heads(k_out, Hkv, ldko);
     if (meet(qo, q == q_out && ldq == ldqo ? none : qi) || meet(ko, k == k_out && ldk == ldko ? none : ki) || meet(qo, ki) || meet(ko, qi) ||
-        overlap({qo, ko}, {span(positions, 4 * T), span(freqs, 2 * rot)}))
+        overlap({qo, ko}, {ints(positions, T), span(freqs, 2 * rot)}))
         return FP8FG_ERR_UNSUPPORTED;
     return hip_status(fp8fg::launch_rope({q, k, q_out, k_out, ldq, ldk, ldqo, ldko, T, Hq, Hkv, D, rot, x_bf16, interleaved, inverse, scale,
                                           positions, freqs}, static_cast<hipStream_t>(stream)));
@@ -694,6 +682,10 @@ int fp8_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int x_
         !aligned16(v_scale))
         return FP8FG_ERR_ALIGN;
     if (T == 0 || H == 0 || n_pages == 0) return FP8FG_OK;
+    const int64_t codes = n_pages * H * page * D, scales = 4 * n_pages * H, size = x_bf16 ? 2 : 4;
+    if (overlap({span(k_cache, codes), span(k_scale, scales), span(v_cache, codes), span(v_scale, scales)},
+                {Span{k, T, H * D * size, ldk * size}, Span{v, T, H * D * size, ldv * size}, ints(slots, T)}))
+        return FP8FG_ERR_UNSUPPORTED;
     return hip_status(fp8fg::launch_kv_append({k, v, ldk, ldv, T, H, D, n_pages, x_bf16, page_log(page), slots, k_cache, v_cache, k_scale,
                                                v_scale}, static_cast<hipStream_t>(stream)));
 }
@@ -742,6 +734,13 @@ int fp8_kv_attention(const uint16_t* q, int64_t ldq, const uint8_t* k_cache, con
     const int64_t need = fp8fg::attend_workspace(c);
     if (need > 0 && !workspace) return FP8FG_ERR_NULL;
     if (workspace_bytes < need) return FP8FG_ERR_SHAPE;
+    // (a row's queries are read by the workgroup that writes its output, or by an earlier launch: in place is sound)
+    const int64_t codes = n_pages * Hkv * page * D, scales = 4 * n_pages * Hkv, row = 2 * Hq * D;
+    const Span queries{q, T, row, 2 * ldq}, result = span(out, T * row), sums = span(lse, lse ? 4 * T * Hq : 0), scratch = span(workspace, need);
+    if ((!(out == q && ldq == Hq * D) && meet(result, queries)) || meet(sums, queries) || meet(scratch, queries) ||
+        overlap({result, sums, scratch}, {span(k_cache, codes), span(k_scale, scales), span(v_cache, codes), span(v_scale, scales),
+                                          ints(table, B * width), ints(cu, B + 1), ints(lens, B)}))
+        return FP8FG_ERR_UNSUPPORTED;
     c.q = q;
     c.ldq = ldq;
     c.kc = k_cache;

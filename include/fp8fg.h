@@ -626,8 +626,8 @@ int fp8_grouped_gemm_wgrad(const uint8_t* a, const float* sa, const uint8_t* b, 
  *   slots: int32 [T], the rows' places, -1 from cu[B] on and where refused;
  *   left: int32 [2], the pages that are left free (the first left[0] of free_pages) and
  *     the number that was missing (0 where every request got its pages).
- * What is written may not overlap what is only read.  B = 0 or T = 0 writes the outputs
- * that exist.  Requires T < 2^23.
+ * No output may share memory with an input that is only read, nor with another output.  B = 0 or T = 0 writes the
+ * outputs that exist.  Requires T < 2^23.
  */
 int kv_assign_pages(const int32_t* have, const int32_t* add, int64_t B, const int32_t* free_pages, const int32_t* n_free,
                     int64_t F, int64_t page, int32_t* table, int64_t width, int64_t T, int32_t* lens, int32_t* cu,
@@ -642,7 +642,7 @@ int kv_assign_pages(const int32_t* have, const int32_t* add, int64_t B, const in
  *   lens_out: int32 [B] = 0 where done, lens (at least 0) elsewhere;
  *   left: int32 [1], the pages that are free now.
  * The table is not written (entries past a request's length mean nothing).
- * What is written may not overlap what is only read.
+ * No output may share memory with an input that is only read, nor with another output.
  */
 int kv_release_pages(const int32_t* done, const int32_t* lens, const int32_t* table, int64_t B, int64_t width, int64_t page,
                      int32_t* free_pages, int64_t F, const int32_t* n_free, int32_t* lens_out, int32_t* left, void* stream);
@@ -684,7 +684,7 @@ int rope(const void* q, int64_t ldq, void* q_out, int64_t ldqo, int64_t Hq, cons
  *   quotient x / s; a smaller one gives way to the power of two, with older codes of the FP32 product of their value and the scales' quotient.
  * Nothing but the pages' codes up to the last new token and their scales is written.  A
  * page named by two separate runs of rows in one call gets unspecified codes.
- * Requires rows as in rope.
+ * Requires rows as in rope; the cache's four buffers share no memory with one another or with k, v and slots.
  */
 int fp8_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int x_bf16, const int32_t* slots, int64_t T, int64_t H,
                   int64_t D, int64_t page, int64_t n_pages, uint8_t* k_cache, float* k_scale, uint8_t* v_cache, float* v_scale,
@@ -709,7 +709,8 @@ int fp8_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int x_
  * over the n keys seen, X the largest scale * sum_d |q_d k_jd|, before the one rounding to BF16.  Pages that a
  * row sees no token of leave its bits as they are.
  * workspace: fp8_kv_attention_workspace bytes (may be 0, then NULL), contents unspecified before
- * and after; calls that may run at the same time need one each.
+ * and after; calls that may run at the same time need one each.  out may be q itself, with ldq = Hq * D;
+ * otherwise out, lse and workspace share no memory with one another or with what is read.
  * Requires Hq % Hkv == 0, T * (Hq / Hkv) < 2^24, 0 <= scale <= 2^64, rows of q at least Hq * D elements and
  * a multiple of 16 bytes apart, n_pages >= 1 where there is work.
  */

@@ -1,9 +1,11 @@
 """Buffers that lie between one another's rows, or on one another as the calls allow it, give what separate ones give."""
+import numpy as np
 import pytest
 import torch
 
 import fp8_fine_grained_amd as fp8
-from tests.test_gpu_kv import DEV, ints
+from tests.test_gpu_kv import DEV, attention_case, ints
+from tests.test_gpu_kv_units import FORMS, on_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +29,26 @@ def test_rope_between_rows(T, dtype):
     assert torch.equal(out, q) and torch.equal(y, torch.cat([x[:, :4], k, x[:, 6:]], 1))
     with pytest.raises(fp8.Fp8fgError):
         fp8.rope(y[:, :4], y[:, 4:6], pos, freqs, q_out=y[:, 1:5])
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,old,new", [f[1:] for f in FORMS], ids=[f[0] for f in FORMS])
+def test_attention_in_place(D, Hq, Hkv, old, new):
+    """Outputs on the queries, by every kernel, whole and split."""
+    q, *cache = on_gpu(attention_case(np.random.default_rng(D), [old, 0, old // 2], [new, new, 1], Hq, Hkv, D, 32))
+    lse = torch.empty(q.shape[:2], device=DEV)
+    want, wlse = fp8.fp8_kv_attention(q, *cache, lse=lse)
+    for _ in range(3):
+        x = q.clone()
+        got, glse = fp8.fp8_kv_attention(x, *cache, out=x, lse=torch.empty_like(lse))
+        assert got is x and torch.equal(x, want) and torch.equal(glse, wlse)
+
+
+def test_append_of_columns():
+    """Keys and values as columns of one buffer, as a fused projection leaves them."""
+    x = torch.randn(20, 6, 64, device=DEV).bfloat16()
+    a, b = fp8.kv_cache(3, 2, 16, 64, DEV), fp8.kv_cache(3, 2, 16, 64, DEV)
+    fp8.fp8_kv_append(x[:, 2:4], x[:, 4:], ints(range(20)), *a)
+    fp8.fp8_kv_append(x[:, 2:4].contiguous(), x[:, 4:].contiguous(), ints(range(20)), *b)
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    with pytest.raises(fp8.Fp8fgError):
+        fp8.fp8_kv_append(x[:, 2:4], x[:, 4:], ints(range(20)), a[0], a[1], a[2], a[1])

@@ -43,3 +43,44 @@ def test_rope_of_queries_alone():
     none = dict(k=NUL, ko=NUL, Hkv=0)
     assert rope(qo=at(0, 8), **none) == EUNSUP and rope(qo=at(4), **none) == EUNSUP
     assert rope(T=1, qo=at(0, 3 * D), **none) == EUNSUP
+
+
+def assign(**c):
+    names = "have add free nf table lens cu pos slots left".split()
+    return call("kv_assign_pages", "have add B free nf F page table width T lens cu pos slots left",
+                dict({k: at(i) for i, k in enumerate(names)}, B=4, F=100, page=64, width=8, T=9), **c)
+
+
+def test_outputs_of_the_page_tables_on_one_another():
+    """What one workgroup writes of a buffer another would write as well."""
+    for a, b in (("cu", 5), ("pos", 4), ("left", 8), ("slots", 7), ("cu", 4)):
+        assert assign(**{a: at(b)}) == EUNSUP, (a, b)
+    assert assign(cu=at(7, -8)) == EUNSUP                      # the last of five
+    got = call("kv_release_pages", "done lens table B width page free F nf out left",
+               dict(done=at(0), lens=at(1), table=at(2), free=at(3), nf=at(4), out=at(3, 192), left=at(5), B=4, width=8, page=64, F=100))
+    assert got == EUNSUP
+
+
+def append(**c):
+    return call("fp8_kv_append", "k ldk v ldv bf16 slots T H D page n kc ks vc vs",
+                dict(k=at(0), ldk=2 * D, v=at(1), ldv=2 * D, bf16=1, slots=at(2), T=T, H=2, D=D, page=64, n=10, kc=at(3), ks=at(4), vc=at(5), vs=at(6)), **c)
+
+
+@pytest.mark.parametrize("case", [dict(kc=at(0)), dict(vc=at(1, (T - 1) * 2 * D)), dict(ks=at(0, 2 * D)), dict(vs=at(2)), dict(vc=at(2, -8)),
+                                  dict(vc=at(3)), dict(vs=at(4)), dict(vs=at(4, 32)), dict(ks=at(3, 8)), dict(vc=at(3, 10 * 2 * 64 * D // 2 - 8)),
+                                  dict(v=at(0, 2 * D), ldk=6 * D, ldv=6 * D, kc=at(0, 4 * D))])
+def test_append(case):
+    assert append(**case) == EUNSUP
+
+
+def attend(**c):
+    return call("fp8_kv_attention", "q ldq kc ks vc vs n page table width cu lens B T Hq Hkv D scale out lse ws wb",
+                dict(q=at(0), ldq=8 * D, kc=at(1), ks=at(2), vc=at(3), vs=at(4), n=10, page=64, table=at(5), width=40, cu=at(6), lens=at(7), B=3, T=T,
+                     Hq=8, Hkv=2, D=D, scale=0.1, out=at(8), lse=at(9), ws=at(10), wb=1 << 30), **c)
+
+
+@pytest.mark.parametrize("case", [dict(out=at(0, 8 * D)), dict(out=at(0, -D)), dict(out=at(0), ldq=9 * D), dict(out=at(1)), dict(out=at(2)), dict(out=at(3)),
+                                  dict(out=at(4, 8)), dict(out=at(5)), dict(out=at(6)), dict(out=at(7)), dict(lse=at(0)), dict(lse=at(8)), dict(lse=at(6)),
+                                  dict(ws=at(0)), dict(ws=at(8)), dict(ws=at(9)), dict(ws=at(5, 16)), dict(out=at(10, 64)), dict(lse=at(10, 8)), dict(ws=at(3))])
+def test_attention(case):
+    assert attend(**case) == EUNSUP
