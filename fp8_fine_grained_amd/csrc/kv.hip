@@ -218,8 +218,9 @@ __global__ __launch_bounds__(kThreads) void release(const ReleaseArgs p) {
 // Rotary positions.  A wave takes one token: its lanes form the angles' sines and
 // cosines, one pair each, and pass them through LDS; then a lane turns eight
 // pairs of one head after another.  Angles are position * frequency in
-// revolutions in 64 bits (FP32 would lose them from positions of some
-// thousands on), their fraction in FP32.  Bound by memory: 8192 x 72 heads x 128 in BF16, 302 MB, 59 us, 5.1 TB/s.
+// revolutions, in 64 bits and what those lose (FP32 would lose them from positions of some
+// thousands on, 64 bits alone 2^-21 of a radian at 2^31 radians and more beyond), their fraction, half a turn at the most, its
+// sine and cosine in FP32: 2^-23 of each, below the products' own roundings.  Bound by memory: 8192 x 72 heads x 128 in BF16, 302 MB, 59 us, 5.1 TB/s.
 struct RopeArgs {
     const void *q, *k;
     void *q_out, *k_out;
@@ -230,6 +231,16 @@ struct RopeArgs {
     const float* freqs;
 };
 constexpr int kMaxPairs = 128;
+// position * freq in revolutions, without the whole ones.  (Contracted, the rounded product would
+// be subtracted from without its rounding, which `lost` holds.)
+__device__ __forceinline__ float part_of_turn(int32_t position, float freq) {
+#pragma clang fp contract(off)
+    constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnLost = -0x1.6b01ec5417056p-57;   // 1 / (2 pi)
+    const double p = double(position), f = double(freq), angle = p * f, angle_lost = __builtin_fma(p, f, -angle);
+    const double turns = angle * kTurn, lost = __builtin_fma(angle, kTurn, -turns) + __builtin_fma(angle, kTurnLost, angle_lost * kTurn);
+    const double part = (turns - __builtin_rint(turns)) + lost;     // (lost is below 2^-23, but for angles past 2^31)
+    return float(part - __builtin_rint(part));
+}
 
 template <class T, bool NEXT>
 __global__ __launch_bounds__(kThreads) void rope(const RopeArgs p) {
@@ -239,8 +250,7 @@ __global__ __launch_bounds__(kThreads) void rope(const RopeArgs p) {
     const int32_t pos = t < p.T ? p.positions[t] : -1;
     const int pairs = p.rot / 2, units = pairs / 8;
     for (int i = lane; i < pairs; i += 64) {
-        const double turns = double(pos) * double(p.freqs[i]) * 0.15915494309189535;
-        const float r = float(turns - __builtin_rint(turns));
+        const float r = part_of_turn(pos, p.freqs[i]);
         float s, c;
         sincospif(2.0f * r, &s, &c);
         cs[wave][0][i] = c * p.scale;

@@ -656,8 +656,8 @@ int kv_release_pages(const int32_t* done, const int32_t* lens, const int32_t* ta
  *   (a, b) -> scale * (a cos - b sin, b cos + a sin)
  * of the channel pairs (i, i + rot / 2), or (2 i, 2 i + 1) when interleaved = 1.
  * inverse = 1 turns the other way: with the same scale, the gradient of the
- * inputs from that of the outputs.  The angle is formed in 64 bits, its sine and cosine
- * and the products in FP32 (an absolute error below 2^-21 of scale * (|a| + |b|)), and
+ * inputs from that of the outputs.  The angle is formed in twice 64 bits, its sine and cosine
+ * and the products in FP32 (an absolute error below 2^-21 of scale * (|a| + |b|), for angles below 2^64), and
  * rounded once to the outputs' type.  Rows with a negative position are not written.
  * q_out, k_out: as q and k, rows ldqo and ldko apart, or q and k themselves (with
  * the same distance); they may lie between one another's rows, but share no memory with each other or, otherwise, with an input.
