@@ -837,7 +837,8 @@ def rope_frequencies(rot, base=10000.0, factor=1.0, original=4096, fast=32.0, sl
     """Frequencies f32 [rot/2] for rope, base^(-2 i / rot), and the scale that goes
     with them.  factor > 1 stretches a context of `original` tokens: frequencies that turn
     fewer than `slow` times in it are divided by factor, those that turn more than `fast`
-    times are kept, with a linear ramp between, and the scale is 0.1 ln(factor) + 1."""
+    times are kept, with a ramp between that is linear in the turns (models whose ramp is linear in the channel's
+    number between two rounded ones bring frequencies of their own), and the scale is 0.1 ln(factor) + 1."""
     f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
     if factor > 1.0:
         turns = f * (original / 6.283185307179586)

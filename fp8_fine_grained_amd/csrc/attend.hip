@@ -5,7 +5,9 @@
 // over the keys j that token i sees, in one pass with a running maximum m.
 // Keys and values are E4M3 codes times one scale per page and head.  K's codes
 // are widened exactly to BF16 and multiplied with the BF16 queries, V's exactly
-// to FP16 and multiplied with FP16 probabilities, sums in FP32.
+// to FP16 and multiplied with FP16 probabilities, sums in FP32.  (The matrix units take 16 bits: half a step of FP16 is 2^-11 of a
+// probability, an eighth of the output's own rounding to BF16; as BF16 a probability would cost as much as that.)  Units of the sums,
+// their reciprocals and lse go through the hardware's approximate reciprocal and logarithm: 2^-21 at the most, beside 2^-11.
 //
 // A tile is 64 tokens of one head, S^T = K Q^T of it four 16-token products.
 // The 16 x 16 result of the matrix instruction leaves row 4 g + i of a 16-lane
@@ -135,7 +137,7 @@ __device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
     r.read(p, 0);
     const int per = part_of(p, lanes_sum<64>(r.work()));
     // CLASSES: requests whose parts are long come first, in four classes by their share of the
-    // longest, so that what starts last is short.  Three chunks of up to 2048 tokens on 1024 to 8192: 528 / 461 us
+    // longest, so that what starts last is short.  (The list of more than 256 requests goes without.)  Three chunks of up to 2048 tokens on 1024 to 8192: 528 / 461 us
     // without and with.  Parts of a decode step are alike; there the classes' scans cost 0.7 us and save nothing.
     int splits[kPer], size[kPer], longest = 0;
 #pragma unroll
@@ -312,7 +314,7 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int first, int end) {
 // 16 NR query rows of one key/value head and a part of their keys.  The four waves
 // take every fourth tile; a wave widens a tile's codes once for all its rows.  Bound by the
 // stream of codes: 607 MB (64 requests of 1025 to 8193 tokens, 64 / 8 heads, D = 128) in 115 us, 5.2 TB/s, what a copy
-// reaches; matrix units busy 0.08, vector instructions 0.34 of the time.
+// reaches; matrix units busy 0.08, vector instructions 0.35 of the time.
 template <int D, int NR, bool ONCE>
 __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
     constexpr int ROWS = 16 * NR, KC = D / 64, DT = D / 16;
@@ -563,7 +565,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend(const Args p) {
 // 8 b + 4 h + i of a 32-token product holds token 16 h + 4 b + i, so that lane half h ends up with
 // tokens 16 h .. 16 h + 15 of a row, one page's, in order.  16-byte pieces of LDS rows are
 // swapped by row, so that eight lanes' pieces meet different banks.  Bound by the vector instructions
-// beside the products (9.5 for each): 512 tokens on 30,000, 32 / 8 heads, D = 128, 296 us with the join,
+// beside the products (9.7 for each): 512 tokens on 30,000, 32 / 8 heads, D = 128, 296 us with the join,
 // 0.85 PFLOP/s; three chunks of 512 to 2048 on 1024 to 8192 293 to 512 us, 0.83 to 0.87 PFLOP/s.
 typedef float v16f __attribute__((ext_vector_type(16)));
 
@@ -913,7 +915,8 @@ inline Plan plan_of(const AttendCall& c, int rows) {
     // tokens on 16,000 and 2000, 421 us whole, 210 split; one of 2048 on 2000 109 / 84; six of up to 500 on up
     // to 2000 79 / 85; three of up to 2048 on up to 8192, 960 tiles, 413 / 437.  Where they do, and each of several requests
     // brings many, only tiles longer than a place's share are, which the host cannot see: 2048 and 512 tokens on up to
-    // 16,384 494 / 409, five of 512 to 2048 on 1024 to 8192, where none is, 579 / 582 for the empty second launch
+    // 16,384 494 / 409, five of 512 to 2048 on 1024 to 8192, where none is, 579 / 582 for the empty second launch.
+    // (A single token on a very long context is then one workgroup's: 131,072 tokens beside that chunk take 3.6 ms.)
     if (rows == kWideRows && all > kSlots) r.target = seqs > 1 && c.T * G > 512 * seqs ? int((kSlots + c.Hkv - 1) / c.Hkv) : 1;
     const bool split = kt > kWhole && r.target > 1;
     // a tile has one item more than the work's share at the most, a split one twice as many
@@ -929,7 +932,8 @@ inline Plan plan_of(const AttendCall& c, int rows) {
 }
 
 // Rows of a workgroup, by what the requests bring on average: sixteen, thirty-two, or four waves' 32
-// over one copy in LDS.  us, on caches of up to 3000 tokens: 64 requests of 8 heads and D = 128 with 16 rows each, 16 and 32
+// over one copy in LDS.  (The host knows no more.  Where a few chunks lift the average, single tokens beside them take the wide kernel
+// too: 63 of them on 1024 to 8192 tokens, 116 us alone, with a chunk of 2048 tokens on 4096, 364 alone, 563 in one call, 64 / 8 heads.)  us, on caches of up to 3000 tokens: 64 requests of 8 heads and D = 128 with 16 rows each, 16 and 32
 // a workgroup 56 / 62, with 24 rows 85 / 65; with 40, 50 and 60 rows, 32 and 128 a workgroup 92 / 92, 103 / 93, 116 / 95,
 // with 80 144 / 98; 60 rows of four requests 21 / 26, of 32 requests of two heads at D = 256 48 / 46.
 inline int rows_of(const AttendCall& c) {

@@ -54,7 +54,7 @@ __device__ __forceinline__ int last_not_past(const int32_t* start, int n, int32_
 // A row that is a page's first token writes the page into the table.  Bound by
 // latency: the lengths, a search of eight steps in LDS, the page's number, the stores.
 // 256 requests' decode step 4.8 us in a graph (7.2 with 64-bit sums over the
-// workgroup, shuffled and joined in LDS), 40 prompts' 37,503 rows 6.6.
+// workgroup, shuffled and joined in LDS), 40 prompts' 37,503 rows 6.6.  Every workgroup walks all lengths: 4096 requests 18, 65,536 195.
 struct AssignArgs {
     const int32_t *have, *add, *free_pages, *n_free;
     int64_t B, F, width, T;
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kThreads) void assign(const AssignArgs p) {
 
 // The pages of the requests that are done, back on the free list in the order of
 // the requests and of their entries, by the same sums.  Bound by latency: 96 of 512 requests, 7000 pages, 6.9 us in a graph,
-// of which each chunk of 256 lengths takes two.
+// of which each chunk of 256 lengths takes two; 4096 requests 19, 65,536 374.
 struct ReleaseArgs {
     const int32_t *done, *lens, *table, *n_free;
     int64_t B, F, width;
@@ -310,8 +310,9 @@ __global__ __launch_bounds__(kThreads) void rope(const RopeArgs p) {
 // values.  The scale is the least power of two s with amax <= 448 s (2^-126 at the least), over
 // the run and the page's older tokens; when it grows, older codes are re-encoded by the exact factor.  Bound by
 // latency (slots, scale, data, maximum, stores in turn): 128 tokens x 8 x 128 in BF16 5.9 us in a graph, 5120
-// 13.2 (with four waves a SIMD, which is a round and a quarter of workgroups, 14.8).  Thousands of
-// single tokens are bound by the bytes that each writes into its value page's rows: 4096 99 us.
+// 13.3 (with four waves a SIMD, which is a round and a quarter of workgroups, 14.8).  Thousands of
+// single tokens are bound by the bytes that each writes into its value page's rows, every one a sector of 32: 4096 99 us;
+// where no older code moves 86, and 136 MB written for 8.4 MB of codes (pages of 16, whose rows share sectors, 29 and 70).
 struct AppendArgs {
     const void *k, *v;
     int64_t ldk, ldv, T, n_slots;
@@ -450,7 +451,7 @@ __device__ __forceinline__ void in_two_passes(int pieces, int me, int team, Load
         for (int i = 0; i < HOLD; ++i)
             if (team * i < pieces) look(w[i]);
         const Divide r = scale();
-        // (held as they came: the compiler would keep the widened values of the first pass, 119 in place of 89 registers)
+        // (held as they came: the compiler would keep the widened values of the first pass, 119 in place of 91 registers)
 #pragma unroll
         for (int i = 0; i < HOLD; ++i)
 #pragma unroll

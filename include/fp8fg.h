@@ -712,7 +712,8 @@ int fp8_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int x_
  * and after; calls that may run at the same time need one each.  out may be q itself, with ldq = Hq * D;
  * otherwise out, lse and workspace share no memory with one another or with what is read.
  * Requires Hq % Hkv == 0, T * (Hq / Hkv) < 2^24, 0 <= scale <= 2^64, rows of q at least Hq * D elements and
- * a multiple of 16 bytes apart, n_pages >= 1 where there is work.
+ * a multiple of 16 bytes apart, n_pages >= 1 where there is work; in FP32's range, key scales times `scale`, scores and the
+ * sums of products with the codes, sum_d |q_d code_d|, all below 2^126.
  */
 int fp8_kv_attention_workspace(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t width, int64_t* bytes);
 int fp8_kv_attention(const uint16_t* q, int64_t ldq, const uint8_t* k_cache, const float* k_scale, const uint8_t* v_cache,
