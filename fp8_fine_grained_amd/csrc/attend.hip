@@ -5,9 +5,10 @@
 // over the keys j that token i sees, in one pass with a running maximum m.
 // Keys and values are E4M3 codes times one scale per page and head.  K's codes
 // are widened exactly to BF16 and multiplied with the BF16 queries, V's exactly
-// to FP16 and multiplied with FP16 probabilities, sums in FP32.  (The matrix units take 16 bits: half a step of FP16 is 2^-11 of a
-// probability, an eighth of the output's own rounding to BF16; as BF16 a probability would cost as much as that.)  Units of the sums,
-// their reciprocals and lse go through the hardware's approximate reciprocal and logarithm: 2^-21 at the most, beside 2^-11.
+// to FP16 and multiplied with FP16 probabilities, sums in FP32.  (The matrix units take 16 bits:
+// half a step of FP16 is 2^-11 of a probability, an eighth of the output's own rounding to BF16; as
+// BF16 a probability would cost as much as that.)  Units of the sums and lse go through the
+// hardware's approximate reciprocal and logarithm, which costs a probability 2^-18 at the most.
 //
 // A tile is 64 tokens of one head, S^T = K Q^T of it four 16-token products.
 // The 16 x 16 result of the matrix instruction leaves row 4 g + i of a 16-lane
@@ -137,8 +138,8 @@ __device__ __forceinline__ bool find_item(const Args& p, int me, Item& it) {
     r.read(p, 0);
     const int per = part_of(p, lanes_sum<64>(r.work()));
     // CLASSES: requests whose parts are long come first, in four classes by their share of the
-    // longest, so that what starts last is short.  (The list of more than 256 requests goes without.)  Three chunks of up to 2048 tokens on 1024 to 8192: 528 / 461 us
-    // without and with.  Parts of a decode step are alike; there the classes' scans cost 0.7 us and save nothing.
+    // longest, so that what starts last is short.  (The list of more than 256 requests goes without.)  Three chunks
+    // of up to 2048 tokens on 1024 to 8192: 528 / 461 us without and with.  Parts of a decode step are alike; there the classes' scans cost 0.7 us and save nothing.
     int splits[kPer], size[kPer], longest = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -737,8 +738,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_wide(const 
         if (tile + 1 < kt1) cut(tile + 1, id);
         // Probabilities are formed times their page's value scale over `ref`, as a term of the
         // exponent (below 2^-60 FP16 has nothing left of them, above 1 the page is out of sight), and
-        // summed without it.  The second
-        // half's run beside the first half's products, and beside its own products the next
+        // summed without it.  The second half's run beside the first half's products, and beside its own products the next
         // tile is widened (what is put past the end is not used).
         v8h pf[2][2];
         l *= alpha;
@@ -932,8 +932,9 @@ inline Plan plan_of(const AttendCall& c, int rows) {
 }
 
 // Rows of a workgroup, by what the requests bring on average: sixteen, thirty-two, or four waves' 32
-// over one copy in LDS.  (The host knows no more.  Where a few chunks lift the average, single tokens beside them take the wide kernel
-// too: 63 of them on 1024 to 8192 tokens, 116 us alone, with a chunk of 2048 tokens on 4096, 364 alone, 563 in one call, 64 / 8 heads.)  us, on caches of up to 3000 tokens: 64 requests of 8 heads and D = 128 with 16 rows each, 16 and 32
+// over one copy in LDS.  (The host knows no more.  Where a few chunks lift the average, single tokens beside them take
+// the wide kernel too: 63 of them on 1024 to 8192 tokens, 116 us alone, with a chunk of 2048 tokens on 4096, 364 alone, 563
+// in one call, 64 / 8 heads.)  us, on caches of up to 3000 tokens: 64 requests of 8 heads and D = 128 with 16 rows each, 16 and 32
 // a workgroup 56 / 62, with 24 rows 85 / 65; with 40, 50 and 60 rows, 32 and 128 a workgroup 92 / 92, 103 / 93, 116 / 95,
 // with 80 144 / 98; 60 rows of four requests 21 / 26, of 32 requests of two heads at D = 256 48 / 46.
 inline int rows_of(const AttendCall& c) {
