@@ -115,3 +115,30 @@ def test_one_token_of_the_largest_values():
     out = fp8.fp8_kv_attention(torch.ones(2, 1, 64, dtype=torch.bfloat16, device=DEV), *cache, ints([[0], [1]]), ints([0, 1, 2]), ints([1, 1]))
     want = kv.values(host(cache[2]), host(cache[3]), np.array([0]), 1, 16, 0, turned=True)[0]
     assert np.abs(want).max() > 3e38 and np.array_equal(host(out)[0], want) and np.array_equal(host(out)[1], want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,old,new", [
+    (8, 2, [700, 64, 0, 1300, 33, 500], [1, 1, 1, 4, 2, 400]),                # few rows beside a chunk: 128 rows a workgroup, split
+    (4, 2, [700, 20, 0, 90, 1100] * 6, [1, 1, 3, 1, 2] * 5 + [1, 1, 3, 1, 150])])      # a chunk beside many: 16 rows
+def test_steps_that_mix_single_tokens_and_chunks(Hq, Hkv, old, new):
+    """Single tokens, a few drafted ones and a prompt's chunk in one call."""
+    case = list(attention_case(np.random.default_rng(Hq), old, new, Hq, Hkv, 64, 32, special=False))
+    case[2], case[4] = np.full(case[2].shape, 2.0 ** -8), case[4].astype(np.float64)
+    bound_check(case)
+
+
+def test_a_mixed_step_that_fills_the_chip():
+    """Nothing is split there, a long single token neither: what each request gives in a call of its own."""
+    q, k, ks, v, vs, table, cu, lens = on_gpu(attention_case(np.random.default_rng(5), [1500, 64, 300, 15], [1, 3, 1, 1160], 64, 64, 64, 32, special=False))
+    assert fp8.fp8_kv_attention_workspace(q.shape[0], 4, 64, 64, 64, 32, table.shape[1]) == 0
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out, _ = fp8.fp8_kv_attention(q, k, ks, v, vs, table, cu, lens, lse=lse)
+    at = cu.tolist()
+    for b in range(4):
+        rows = slice(at[b], at[b + 1])
+        alone_lse = torch.empty_like(lse[rows])
+        alone, _ = fp8.fp8_kv_attention(q[rows], k, ks, v, vs, table[b: b + 1].clone(), ints([0, at[b + 1] - at[b]]), lens[b: b + 1].clone(), lse=alone_lse)
+        # either call is within the bound of the exact result (X < 2^4, n < 2^11: 2^-10 of sum_j p_j |v_j|, at most 448 / 64 here), and rounds once
+        lim = 2 * (2.0 ** -10 * 7.0) + 2.0 ** -7 * alone.float().abs()
+        assert bool(((out[rows].float() - alone.float()).abs() <= lim).all()), b
+        assert bool(((lse[rows] - alone_lse).abs() <= 2.0 ** -10).all()), b
